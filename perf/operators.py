@@ -159,20 +159,21 @@ def prepare(case, seed):
         from mixture_experts_ffn_router_gb300 import binding as B
         s["kv"] = B.PagedKV(c["hq"], c["hkv"], c["d"], c["page"], n_pages, c["fmt"], max_tokens=T, max_seqs=c["seqs"])
         s["batch"] = B.KVBatch(s["cu_q"], s["kv_len"], s["pages"], max_new=s["max_new"])
+        s["layer"] = s["kv"].cache(**s["cache"])
     return s
 
 
 def run(state):
     c = state["case"]
     if own:
-        kv, cache, batch = state["kv"], state["cache"], state["batch"]
+        kv, layer, batch = state["kv"], state["layer"], state["batch"]
         if c["op"] == "write":
-            kv.write(cache, batch, state["k"], state["v"])
-            return cache
+            kv.write(layer, batch, state["k"], state["v"])
+            return state["cache"]
         if c["op"] == "read":
-            k, v = kv.read(cache, batch)
+            k, v = kv.read(layer, batch, state["tokens"])
             return {"k": k, "v": v}
-        out, lse = kv.attention(cache, batch, state["q"], window=c["window"], sinks=c["sinks"])
+        out, lse = kv.attention(layer, batch, state["q"], window=c["window"], sinks=c["sinks"])
         return {"out": out, "lse": lse}
     return {"write": _write, "read": _read, "attend": _attend}[c["op"]](state)
 
