@@ -309,6 +309,120 @@ int moe_ffn_quantize_mxfp4(const void* w, long long rows, int cols, uint8_t* cod
  * MOE_FFN_EARCH on a device other than sm_103, MOE_FFN_ECUDA if the launch fails. */
 int moe_ffn_selftest_wait_expiry(uint32_t* status_word, unsigned long long* record, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Paged key/value cache and its attention, the other half of a decoder layer ("Lab 008 — Raw lab
+ * detail", "The model under test": sliding layers of 16 query and 8 key/value heads of width 256
+ * with a window of 1024, global layers with 2 key/value heads of width 512).
+ *
+ * A batch holds the new tokens of n_seqs sequences, one after the other. Sequence b has the token
+ * rows cu_q[b] .. cu_q[b+1]-1 (n_b of them) and kv_len[b] tokens in the cache, the new ones
+ * included and last: new token i is at position kv_len[b] - n_b + i. Position p of sequence b is
+ * kept in slot p % page_size of page pages[b * pages_stride + p / page_size].
+ *   - New tokens at a negative position (kv_len[b] < n_b) and token rows at or after
+ *     cu_q[n_seqs] (padding) belong to no position: they are not written, read back as 0 and attend
+ *     to nothing.
+ *   - cu_q must start at 0 and not decrease, n_b <= max_new, and kv_len[b] <= pages_cols *
+ *     page_size; entries of the page table past a sequence's last token are not read. The kernels
+ *     check these and every page id they use: what lies outside is never accessed, the status word
+ *     gets MOE_FFN_STATUS_BAD_INDEX (moe_ffn_kv_device_status) and the results of the sequences
+ *     concerned are unspecified.
+ * The cache holds keys and values as [n_pages, kv_heads, page_size, head_dim], as bf16, or as e4m3
+ * with one fp32 scale per token and head in [n_pages, kv_heads, page_size]; a value is code * scale.
+ * Calls on one handle share its workspace: they must not overlap in time (one stream, or ordered).
+ */
+#define MOE_FFN_KV_BF16 0
+#define MOE_FFN_KV_E4M3 1
+#define MOE_FFN_KV_MAX_TOKENS_LIMIT 16777216
+#define MOE_FFN_KV_MAX_SEQS_LIMIT 65536
+
+typedef struct moe_ffn_kv_config {
+  int q_heads;     /* a multiple of kv_heads; query head h reads kv head h / (q_heads / kv_heads) */
+  int kv_heads;    /* 1..1024; q_heads / kv_heads at most 64 */
+  int head_dim;    /* 128, 256 or 512 */
+  int page_size;   /* tokens per page: 16, 32, 64 or 128 */
+  int n_pages;     /* pages in the cache; n_pages * kv_heads * page_size < 2^31 */
+  int format;      /* MOE_FFN_KV_BF16 or MOE_FFN_KV_E4M3 */
+  int max_tokens;  /* the most token rows of a batch, 1..MOE_FFN_KV_MAX_TOKENS_LIMIT */
+  int max_seqs;    /* the most sequences of a batch, 1..MOE_FFN_KV_MAX_SEQS_LIMIT */
+} moe_ffn_kv_config;
+
+/* One layer's cache: device pointers, borrowed, 16-byte aligned. */
+typedef struct moe_ffn_kv_cache {
+  void* k;         /* [n_pages, kv_heads, page_size, head_dim] bf16 or e4m3 */
+  void* v;         /* the same */
+  float* k_scale;  /* [n_pages, kv_heads, page_size] fp32 (E4M3; ignored and may be NULL for BF16) */
+  float* v_scale;  /* the same */
+} moe_ffn_kv_cache;
+
+/* One batch. The three arrays are device pointers, 4-byte aligned. */
+typedef struct moe_ffn_kv_batch {
+  const int32_t* cu_q;     /* [n_seqs + 1] first token row of each sequence */
+  const int32_t* kv_len;   /* [n_seqs] tokens in the cache, the new ones included */
+  const int32_t* pages;    /* [n_seqs, pages_cols] page ids, rows pages_stride entries apart */
+  long long pages_stride;  /* >= pages_cols */
+  int pages_cols;          /* >= 0 */
+  int n_seqs;              /* 0..max_seqs */
+  int n_tokens;            /* token rows of the batch's tensors, 0..max_tokens */
+  int max_new;             /* at least the largest n_b */
+} moe_ffn_kv_batch;
+
+/* A bf16 tensor [n_tokens, heads, head_dim] whose last dimension is contiguous: element (t, h, d) is
+ * ptr[t * token_stride + h * head_stride + d]. ptr 16-byte aligned, strides in elements, >= 0 and
+ * multiples of 8 (a slice of a fused projection, a transposed view or an expanded one). */
+typedef struct moe_ffn_kv_rows {
+  const void* ptr;
+  long long token_stride;
+  long long head_stride;
+} moe_ffn_kv_rows;
+
+typedef struct moe_ffn_kv moe_ffn_kv;
+
+/* Bytes of device workspace a handle with this config needs (0 if the config is invalid). */
+size_t moe_ffn_kv_workspace_bytes(const moe_ffn_kv_config* cfg);
+
+/* Creates a handle on CUDA device `device` (which this call makes current). One handle serves every
+ * layer of its shape. `workspace`: device pointer, 256-byte aligned, owned by the caller; its control
+ * words are cleared here, so handles do not share one. Errors as for moe_ffn_init; on failure *kv is
+ * set to NULL. */
+int moe_ffn_kv_init(moe_ffn_kv** kv, const moe_ffn_kv_config* cfg, void* workspace, size_t workspace_bytes,
+                    int device);
+
+/* Writes the batch's new keys and values into the cache, quantising them for MOE_FFN_KV_E4M3. Each
+ * row of head_dim values has scale = max |x| / 448 in fp32 (correctly rounded division) and codes
+ * x / scale in fp32 (correctly rounded) rounded to the nearest e4m3 (ties to even); a row of zeros
+ * gets scale 0 and codes 0, a row that holds an infinity or a NaN scale NaN and codes 0 (it reads back
+ * as NaN). Positions that two sequences of the batch share are written in no particular order.
+ * Asynchronous on `stream`. */
+int moe_ffn_kv_write(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch,
+                     const moe_ffn_kv_rows* k, const moe_ffn_kv_rows* v, void* stream);
+
+/* Reads the batch's "new" tokens back out of the cache: k_out and v_out, device pointers,
+ * [n_tokens, kv_heads, head_dim] bf16 contiguous, code * scale rounded once. With n_b = kv_len[b] that
+ * is the whole of each sequence. Asynchronous on `stream`. */
+int moe_ffn_kv_read(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch, void* k_out,
+                    void* v_out, void* stream);
+
+/* Attention of the batch's new tokens over the cache (which holds them already: moe_ffn_kv_write
+ * first). For the token at position p >= 0 and query head h,
+ *   out = sum_j softmax_j(scale * q . K_j) V_j over the visible positions j <= p,
+ * and with window > 0 only those with j > p - window or j < sinks. Nothing visible: out = 0.
+ *   q      [n_tokens, q_heads, head_dim] bf16;
+ *   out    device pointer, [n_tokens, q_heads, head_dim] bf16 contiguous, not overlapping q;
+ *   lse    device pointer or NULL, [n_tokens, q_heads] fp32: log sum_j exp(scale * q . K_j)
+ *          (-infinity where nothing is visible), for joining with attention over other keys;
+ *   scale  finite, > 0 (head_dim^-1/2 as a rule); window >= 0 (0: none); sinks >= 0.
+ * What is in slots no token sees (NaN included) does not change the result. Deterministic: the same
+ * inputs give bitwise-equal outputs. Asynchronous on `stream`; nothing is allocated or read back. */
+int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch,
+                         const moe_ffn_kv_rows* q, float scale, int window, int sinks, void* out, float* lse,
+                         void* stream);
+
+/* As moe_ffn_device_status, for a handle of the paged cache. */
+int moe_ffn_kv_device_status(moe_ffn_kv* kv, void* stream, uint32_t* word);
+
+/* Releases the handle's host state. Safe on NULL. */
+void moe_ffn_kv_destroy(moe_ffn_kv* kv);
+
 /* A static string naming a status code. */
 const char* moe_ffn_status_string(int status);
 

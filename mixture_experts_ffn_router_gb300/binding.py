@@ -76,6 +76,27 @@ class moe_ffn_views(ctypes.Structure):
     _fields_ = [(f, _vp) for f in VIEW_FIELDS] + [("T", ctypes.c_int)]
 
 
+KV_FORMATS = {"bf16": 0, "e4m3": 1}  # MOE_FFN_KV_BF16, MOE_FFN_KV_E4M3
+
+
+class moe_ffn_kv_config(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("q_heads", "kv_heads", "head_dim", "page_size", "n_pages", "format",
+                                            "max_tokens", "max_seqs")]
+
+
+class moe_ffn_kv_cache(ctypes.Structure):
+    _fields_ = [(f, _vp) for f in ("k", "v", "k_scale", "v_scale")]
+
+
+class moe_ffn_kv_batch(ctypes.Structure):
+    _fields_ = ([(f, _vp) for f in ("cu_q", "kv_len", "pages")] + [("pages_stride", ctypes.c_longlong)]
+                + [(f, ctypes.c_int) for f in ("pages_cols", "n_seqs", "n_tokens", "max_new")])
+
+
+class moe_ffn_kv_rows(ctypes.Structure):
+    _fields_ = [("ptr", _vp), ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
 _LIB = None
 
 
@@ -121,6 +142,23 @@ def lib():
         L.moe_ffn_quantize_int8.argtypes = [_vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp, _vp]
         L.moe_ffn_quantize_mxfp4.restype = ctypes.c_int
         L.moe_ffn_quantize_mxfp4.argtypes = [_vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp, _vp]
+        cfg_p, cache_p, batch_p, rows_p = (ctypes.POINTER(t) for t in (moe_ffn_kv_config, moe_ffn_kv_cache,
+                                                                       moe_ffn_kv_batch, moe_ffn_kv_rows))
+        L.moe_ffn_kv_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_ffn_kv_workspace_bytes.argtypes = [cfg_p]
+        L.moe_ffn_kv_init.restype = ctypes.c_int
+        L.moe_ffn_kv_init.argtypes = [ctypes.POINTER(_vp), cfg_p, _vp, ctypes.c_size_t, ctypes.c_int]
+        L.moe_ffn_kv_write.restype = ctypes.c_int
+        L.moe_ffn_kv_write.argtypes = [_vp, cache_p, batch_p, rows_p, rows_p, _vp]
+        L.moe_ffn_kv_read.restype = ctypes.c_int
+        L.moe_ffn_kv_read.argtypes = [_vp, cache_p, batch_p, _vp, _vp, _vp]
+        L.moe_ffn_kv_attention.restype = ctypes.c_int
+        L.moe_ffn_kv_attention.argtypes = [_vp, cache_p, batch_p, rows_p, ctypes.c_float, ctypes.c_int, ctypes.c_int,
+                                           _vp, _vp, _vp]
+        L.moe_ffn_kv_device_status.restype = ctypes.c_int
+        L.moe_ffn_kv_device_status.argtypes = [_vp, _vp, ctypes.POINTER(ctypes.c_uint32)]
+        L.moe_ffn_kv_destroy.restype = None
+        L.moe_ffn_kv_destroy.argtypes = [_vp]
         L.moe_ffn_destroy.restype = None
         L.moe_ffn_destroy.argtypes = [_vp]
         _LIB = L
@@ -273,6 +311,49 @@ def moe_ffn_destroy(ctx: int) -> None:
     lib().moe_ffn_destroy(_vp(ctx))
 
 
+def make_kv_config(q_heads: int, kv_heads: int, head_dim: int, page_size: int, n_pages: int, fmt: str,
+                   max_tokens: int, max_seqs: int) -> moe_ffn_kv_config:
+    return moe_ffn_kv_config(int(q_heads), int(kv_heads), int(head_dim), int(page_size), int(n_pages),
+                             KV_FORMATS.get(fmt, -1), int(max_tokens), int(max_seqs))
+
+
+def moe_ffn_kv_workspace_bytes(cfg: moe_ffn_kv_config) -> int:
+    return lib().moe_ffn_kv_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_ffn_kv_init(cfg: moe_ffn_kv_config, workspace: int, workspace_bytes: int, device: int) -> int:
+    """Returns the handle (an int)."""
+    h = _vp()
+    _check("moe_ffn_kv_init", lib().moe_ffn_kv_init(ctypes.byref(h), ctypes.byref(cfg), _vp(workspace),
+                                                     workspace_bytes, int(device)))
+    return h.value
+
+
+def moe_ffn_kv_write(kv: int, cache: moe_ffn_kv_cache, batch: moe_ffn_kv_batch, k: moe_ffn_kv_rows,
+                     v: moe_ffn_kv_rows, stream: int) -> int:
+    return lib().moe_ffn_kv_write(kv, cache, batch, k, v, stream)
+
+
+def moe_ffn_kv_read(kv: int, cache: moe_ffn_kv_cache, batch: moe_ffn_kv_batch, k_out: int, v_out: int,
+                    stream: int) -> int:
+    return lib().moe_ffn_kv_read(kv, cache, batch, k_out, v_out, stream)
+
+
+def moe_ffn_kv_attention(kv: int, cache: moe_ffn_kv_cache, batch: moe_ffn_kv_batch, q: moe_ffn_kv_rows, scale: float,
+                         window: int, sinks: int, out: int, lse: int, stream: int) -> int:
+    return lib().moe_ffn_kv_attention(kv, cache, batch, q, scale, window, sinks, out, lse, stream)
+
+
+def moe_ffn_kv_device_status(kv: int, stream: int):
+    w = ctypes.c_uint32(0)
+    rc = lib().moe_ffn_kv_device_status(_vp(kv), _vp(stream), ctypes.byref(w))
+    return rc, w.value
+
+
+def moe_ffn_kv_destroy(kv: int) -> None:
+    lib().moe_ffn_kv_destroy(_vp(kv))
+
+
 # ------------------------------------------------------------------ torch convenience layer
 
 def _field_specs():
@@ -409,6 +490,195 @@ class MoeFFN:
     def close(self):
         if self.ctx:
             moe_ffn_destroy(self.ctx)
+            self.ctx = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVBatch:
+    """The new tokens of a step, for PagedKV: device int32 tensors cu_q [n_seqs + 1] (first token row
+    of each sequence), kv_len [n_seqs] (cached tokens, the new ones included) and pages [n_seqs, cols]
+    (page ids; rows may be strided), and max_new, at least the largest number of new tokens of one
+    sequence. The tensors may be rewritten between calls (a captured graph reads them anew); their
+    values are checked on the device."""
+
+    def __init__(self, cu_q, kv_len, pages, max_new: int):
+        import torch
+        if kv_len.dim() != 1 or cu_q.dim() != 1 or pages.dim() != 2:
+            raise ValueError("cu_q and kv_len must have one dimension and pages two")
+        n = kv_len.shape[0]
+        if cu_q.shape[0] != n + 1 or pages.shape[0] != n:
+            raise ValueError("kv_len has %d sequences, cu_q %d and pages %d" % (n, cu_q.shape[0] - 1, pages.shape[0]))
+        for name, t in (("cu_q", cu_q), ("kv_len", kv_len), ("pages", pages)):
+            if t.dtype != torch.int32:
+                raise ValueError("%s must be torch.int32, got %s" % (name, t.dtype))
+        if max_new < 0:
+            raise ValueError("max_new must not be negative")
+        for name, t in (("cu_q", cu_q), ("kv_len", kv_len)):
+            _check_placement(name, t)
+        cols = pages.shape[1]
+        if not pages.is_cuda or (cols > 1 and pages.stride(1) != 1) or (n > 1 and pages.stride(0) < cols):
+            raise ValueError("pages must be a CUDA tensor with contiguous rows")
+        if kv_len.device != cu_q.device or pages.device != cu_q.device:
+            raise ValueError("cu_q, kv_len and pages must be on one device")
+        self.tensors = (cu_q, kv_len, pages)
+        self.device = cu_q.device
+        self.struct = moe_ffn_kv_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(),
+                                       pages.stride(0) if n > 1 else cols, cols, n, 0, int(max_new))
+
+    def of(self, n_tokens: int) -> moe_ffn_kv_batch:
+        self.struct.n_tokens = n_tokens
+        return self.struct
+
+
+class KVCache:
+    """One layer's cache tensors, checked once (PagedKV.cache and PagedKV.new_cache make it)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.struct = moe_ffn_kv_cache(*(t.data_ptr() if t is not None else None for t in (k, v, k_scale, v_scale)))
+
+
+class PagedKV:
+    """A paged key/value cache's shape, its handle and workspace; one serves all layers of that shape.
+
+    fmt "bf16", or "e4m3" with an fp32 scale per token and head. Calls go to the current stream; a call
+    on another stream than the last one's first waits for that one (not while a graph is captured:
+    order the replays yourself)."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, n_pages: int, fmt: str = "bf16",
+                 max_tokens: int = 8192, max_seqs: int = 256, device: int = 0):
+        import torch
+        self.ctx = 0
+        if fmt not in KV_FORMATS:
+            raise ValueError("fmt must be one of %s, got %r" % (sorted(KV_FORMATS), fmt))
+        self.cfg = make_kv_config(q_heads, kv_heads, head_dim, page_size, n_pages, fmt, max_tokens, max_seqs)
+        self.nbytes = moe_ffn_kv_workspace_bytes(self.cfg)
+        if self.nbytes == 0:
+            raise ValueError("invalid configuration")
+        self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        self.shape = (int(n_pages), self.kv_heads, int(page_size), self.head_dim)
+        self.fmt = fmt
+        self.dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+        self.default_scale = self.head_dim ** -0.5
+        self.device = torch.device("cuda", int(device))
+        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+        self.ctx = moe_ffn_kv_init(self.cfg, self.workspace.data_ptr(), self.nbytes, int(device))
+        self._handle = _vp(self.ctx)
+        self._last = None
+
+    def new_cache(self) -> KVCache:
+        """A zeroed cache of one layer."""
+        import torch
+        k, v = (torch.zeros(self.shape, dtype=self.dtype, device=self.device) for _ in range(2))
+        if self.fmt == "bf16":
+            return KVCache(k, v)
+        return KVCache(k, v, *(torch.zeros(self.shape[:3], device=self.device) for _ in range(2)))
+
+    def cache(self, k, v, k_scale=None, v_scale=None) -> KVCache:
+        """A cache over existing tensors, checked against this shape."""
+        import torch
+        wanted = [("k", k, self.dtype, self.shape), ("v", v, self.dtype, self.shape)]
+        if self.fmt == "e4m3":
+            wanted += [(n, t, torch.float32, self.shape[:3]) for n, t in (("k_scale", k_scale), ("v_scale", v_scale))]
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        for name, t, dtype, shape in wanted:
+            if t is None:
+                raise ValueError("%s is required" % name)
+            if t.dtype != dtype or tuple(t.shape) != shape:
+                raise ValueError("%s must be %s of shape %s, got %s of shape %s" % (name, dtype, shape, t.dtype,
+                                                                                    tuple(t.shape)))
+        for name, t, _, _ in wanted:
+            _check_placement(name, t)
+            if t.device != self.device:
+                raise ValueError("%s must be on %s" % (name, self.device))
+        return KVCache(k, v, k_scale, v_scale)
+
+    def _rows(self, what, t, heads):
+        import torch
+        if t.dtype != torch.bfloat16:
+            raise ValueError("%s must be torch.bfloat16, got %s" % (what, t.dtype))
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
+            raise ValueError("%s must have shape [tokens, %d, %d], got %s" % (what, heads, self.head_dim,
+                                                                              tuple(t.shape)))
+        if not t.is_cuda or t.device != self.device:
+            raise ValueError("%s must be on %s" % (what, self.device))
+        ts, hs, es = t.stride()
+        # A dimension of one element has no stride that matters.
+        ts, hs = ts if t.shape[0] > 1 else 0, hs if heads > 1 else 0
+        if es != 1 or ts % 8 or hs % 8:
+            raise ValueError("%s must have a contiguous last dimension and strides that are multiples of 8" % what)
+        return moe_ffn_kv_rows(t.data_ptr(), ts, hs)
+
+    def _begin(self, cache, batch):
+        import torch
+        if not isinstance(cache, KVCache):
+            cache = self.cache(**cache)
+        if batch.device != self.device:
+            raise ValueError("the batch must be on %s" % self.device)
+        stream = torch.cuda.current_stream(self.device)
+        if self._last is None or self._last.cuda_stream != stream.cuda_stream:
+            if not torch.cuda.is_current_stream_capturing():
+                if self._last is not None:
+                    stream.wait_stream(self._last)
+                self._last = stream
+        return cache.struct, _vp(stream.cuda_stream)
+
+    def write(self, cache, batch: KVBatch, k, v) -> None:
+        """Writes the new tokens' keys and values, bf16 [tokens, kv_heads, head_dim] each, into `cache`
+        (a KVCache, or a dict of its tensors)."""
+        kr, vr = self._rows("k", k, self.kv_heads), self._rows("v", v, self.kv_heads)
+        if k.shape[0] != v.shape[0]:
+            raise ValueError("k has %d tokens, v %d" % (k.shape[0], v.shape[0]))
+        c, s = self._begin(cache, batch)
+        _check("moe_ffn_kv_write", moe_ffn_kv_write(self._handle, c, batch.of(k.shape[0]), kr, vr, s))
+
+    def read(self, cache, batch: KVBatch, n_tokens=None):
+        """The batch's tokens read back: (k, v), bf16 [tokens, kv_heads, head_dim]. n_tokens: the token
+        rows of the batch, cu_q's last value (which is read from the device if it is not given)."""
+        import torch
+        if n_tokens is None:
+            n_tokens = int(batch.tensors[0][-1])
+        k, v = (torch.empty((n_tokens, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+                for _ in range(2))
+        c, s = self._begin(cache, batch)
+        _check("moe_ffn_kv_read", moe_ffn_kv_read(self._handle, c, batch.of(n_tokens), k.data_ptr(), v.data_ptr(), s))
+        return k, v
+
+    def attention(self, cache, batch: KVBatch, q, window: int = 0, sinks: int = 0, scale=None, out=None):
+        """Attention of the new tokens' queries, bf16 [tokens, q_heads, head_dim], over the cache, causal,
+        with an optional sliding window and first positions that stay visible: (out, lse), bf16 like q
+        (contiguous) and fp32 [tokens, q_heads]. scale: head_dim ** -0.5 if not given."""
+        import torch
+        qr = self._rows("q", q, self.q_heads)
+        T = q.shape[0]
+        if out is None:
+            out = torch.empty((T, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+        else:
+            if tuple(out.shape) != tuple(q.shape):
+                raise ValueError("out must have the shape of q %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+            _check_type_size("out", out, torch.bfloat16, q.numel())
+            _check_placement("out", out)
+        lse = torch.empty((T, self.q_heads), dtype=torch.float32, device=self.device)
+        c, s = self._begin(cache, batch)
+        _check("moe_ffn_kv_attention",
+               moe_ffn_kv_attention(self._handle, c, batch.of(T), qr, self.default_scale if scale is None else scale,
+                                    window, sinks, out.data_ptr(), lse.data_ptr(), s))
+        return out, lse
+
+    def status(self, stream=None):
+        import torch
+        s = stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
+        return moe_ffn_kv_device_status(self.ctx, s)
+
+    def close(self):
+        if self.ctx:
+            moe_ffn_kv_destroy(self.ctx)
             self.ctx = 0
 
     def __del__(self):

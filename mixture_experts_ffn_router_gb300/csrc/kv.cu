@@ -1,0 +1,445 @@
+// kv.cu — the paged key/value cache: the host side of its C ABI, and the kernels that write new
+// tokens into it and read cached ones back.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <cmath>
+#include <new>
+
+#include "internal.h"
+#include "kv.h"
+#include "moe_ffn.h"
+
+namespace moe {
+
+namespace {
+
+// Writing and reading back. A row is one head's key or value of one token, D bf16 values in
+// registers as 16-byte vectors, D / 8 lanes (or D / 16 with two vectors) to a row. A warp takes
+// 2 KB of one token's rows, keys and values of all heads counted together: four loads per lane in
+// flight before the first is used, and enough warps for a single decode step's tokens to spread over
+// the SMs. Both kernels only move bytes; HBM bounds them.
+constexpr int kMoveWarps = 8;
+constexpr int kVecs = 4;  // 16-byte bf16 vectors per lane
+
+// The sequence a token row belongs to, found by the whole warp: 32 probes per step, so two steps for
+// up to 1023 sequences instead of ten of a binary search, each a dependent load.
+__device__ __forceinline__ int find_sequence(const KvBatch& b, int row, int lane) {
+  int lo = 0, hi = b.n_seqs;  // the answer's last sequence with cu_q <= row is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && b.cu_q[min(at, hi - 1)] <= row);
+    const int last = 31 - __clz(le | 1u);
+    lo += last * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// Where token row `row` is kept: {page, slot}, page -1 if nowhere.
+__device__ __forceinline__ int2 find_place(const KvBatch& b, const KvCache& c, int row, int lane,
+                                           unsigned int* status) {
+  if (b.n_seqs == 0) return make_int2(-1, 0);
+  const int seq = find_sequence(b, row, lane);
+  const KvSeq s = kv_sequence(b, c, seq, status);
+  const int i = row - s.row0;
+  if (i < 0 || i >= s.n) return make_int2(-1, 0);
+  const int pos = s.len - s.n + i;
+  if (pos < 0) return make_int2(-1, 0);
+  return make_int2(kv_page(b, c, seq, pos >> c.page_log2, status), pos & ((1 << c.page_log2) - 1));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kMoveWarps * 32)
+    kv_write_kernel(KvBatch b, KvCache c, KvRows k, KvRows v, int parts, unsigned int* status) {
+  constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;  // lanes of a row
+  constexpr int kRowVecs = D / 8 / kLanes;         // vectors of a row per lane
+  constexpr int kRows = kVecs / kRowVecs;          // rows per lane
+  constexpr int kWarpRows = kRows * 32 / kLanes;
+  const int lane = threadIdx.x & 31;
+  const long long w = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+  const int row = static_cast<int>(w / parts);
+  if (row >= b.n_tokens) return;
+  const int r0 = static_cast<int>(w % parts) * kWarpRows + lane / kLanes;
+  const int sub = lane % kLanes, n_rows = 2 * c.kv_heads;
+  uint4 x[kRows][kRowVecs];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = r0 + i * (32 / kLanes);
+    if (r >= n_rows) continue;
+    const KvRows& src = r < c.kv_heads ? k : v;
+    const int h = r < c.kv_heads ? r : r - c.kv_heads;
+    const uint16_t* p = src.ptr + row * src.token_stride + h * src.head_stride;
+#pragma unroll
+    for (int j = 0; j < kRowVecs; ++j) x[i][j] = *reinterpret_cast<const uint4*>(p + (sub + j * kLanes) * 8);
+  }
+  const int2 at = find_place(b, c, row, lane, status);
+  if (at.x < 0) return;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = r0 + i * (32 / kLanes);
+    const bool key = r < c.kv_heads;
+    const int h = key ? r : r - c.kv_heads;
+    const long long to = (((static_cast<long long>(at.x) * c.kv_heads + h) << c.page_log2) + at.y);
+    if constexpr (!E4M3) {
+      if (r >= n_rows) continue;
+      uint16_t* dst = reinterpret_cast<uint16_t*>(key ? c.k : c.v) + to * D;
+#pragma unroll
+      for (int j = 0; j < kRowVecs; ++j) *reinterpret_cast<uint4*>(dst + (sub + j * kLanes) * 8) = x[i][j];
+    } else {
+      // fmaxf drops a NaN, so the largest magnitude is taken on the bits: they order as the values
+      // do, with infinities and NaNs above every finite one.
+      uint32_t top = 0;
+      if (r < n_rows) {
+#pragma unroll
+        for (int j = 0; j < kRowVecs; ++j) {
+          const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) top = max(top, max((u[q] << 16) & 0x7fffffffu, u[q] & 0x7fff0000u));
+        }
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (r >= n_rows) continue;
+      const bool finite = top < 0x7f800000u;
+      const float s = finite ? __fdiv_rn(__uint_as_float(top), 448.0f) : __uint_as_float(0x7fffffffu);
+      if (sub == 0) (key ? c.k_scale : c.v_scale)[to] = s;
+      uint8_t* dst = (key ? c.k : c.v) + to * D;
+#pragma unroll
+      for (int j = 0; j < kRowVecs; ++j) {
+        float f[8];
+        unpack8(x[i][j], f);
+        uint32_t code[2] = {0u, 0u};
+        if (finite && s > 0.0f) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 y = make_float2(__fdiv_rn(f[2 * q], s), __fdiv_rn(f[2 * q + 1], s));
+            code[q >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3))
+                            << (16 * (q & 1));
+          }
+        }
+        *reinterpret_cast<uint2*>(dst + (sub + j * kLanes) * 8) = make_uint2(code[0], code[1]);
+      }
+    }
+  }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kMoveWarps * 32)
+    kv_read_kernel(KvBatch b, KvCache c, uint16_t* k_out, uint16_t* v_out, int parts, unsigned int* status) {
+  constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;
+  constexpr int kRowVecs = D / 8 / kLanes;
+  constexpr int kRows = kVecs / kRowVecs;
+  constexpr int kWarpRows = kRows * 32 / kLanes;
+  const int lane = threadIdx.x & 31;
+  const long long w = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+  const int row = static_cast<int>(w / parts);
+  if (row >= b.n_tokens) return;
+  const int r0 = static_cast<int>(w % parts) * kWarpRows + lane / kLanes;
+  const int sub = lane % kLanes, n_rows = 2 * c.kv_heads;
+  const int2 at = find_place(b, c, row, lane, status);
+  uint4 x[kRows][kRowVecs];
+  float s[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = r0 + i * (32 / kLanes);
+    s[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kRowVecs; ++j) x[i][j] = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= n_rows || at.x < 0) continue;
+    const bool key = r < c.kv_heads;
+    const int h = key ? r : r - c.kv_heads;
+    const long long from = (((static_cast<long long>(at.x) * c.kv_heads + h) << c.page_log2) + at.y);
+#pragma unroll
+    for (int j = 0; j < kRowVecs; ++j) {
+      const long long e = from * D + (sub + j * kLanes) * 8;
+      if constexpr (E4M3) {
+        const uint2 code = *reinterpret_cast<const uint2*>((key ? c.k : c.v) + e);
+        x[i][j].x = code.x;
+        x[i][j].y = code.y;
+      } else {
+        x[i][j] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(key ? c.k : c.v) + e);
+      }
+    }
+    if constexpr (E4M3) s[i] = (key ? c.k_scale : c.v_scale)[from];
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = r0 + i * (32 / kLanes);
+    if (r >= n_rows) continue;
+    const bool key = r < c.kv_heads;
+    const int h = key ? r : r - c.kv_heads;
+    uint16_t* dst = (key ? k_out : v_out) + (static_cast<long long>(row) * c.kv_heads + h) * D;
+#pragma unroll
+    for (int j = 0; j < kRowVecs; ++j) {
+      uint4 y = x[i][j];
+      if constexpr (E4M3) {
+        const uint32_t code[2] = {x[i][j].x, x[i][j].y};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const __half2_raw hr =
+              __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(code[q >> 1] >> (16 * (q & 1))), __NV_E4M3);
+          const float2 f = __half22float2(__half2(hr));
+          const __nv_bfloat162 p = __floats2bfloat162_rn(f.x * s[i], f.y * s[i]);
+          o[q] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        y = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      *reinterpret_cast<uint4*>(dst + (sub + j * kLanes) * 8) = y;
+    }
+  }
+}
+
+int move_parts(const KvCache& c) { return (2 * c.kv_heads * c.head_dim + 1023) / 1024; }
+
+unsigned move_blocks(const KvBatch& b, const KvCache& c) {
+  return static_cast<unsigned>((static_cast<long long>(b.n_tokens) * move_parts(c) + kMoveWarps - 1) / kMoveWarps);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvBatch& b, const KvCache& c, const KvRows& k, const KvRows& v, unsigned int* status,
+                            cudaStream_t s) {
+  const unsigned grid = move_blocks(b, c), block = kMoveWarps * 32;
+  const int parts = move_parts(c);
+  switch (c.head_dim * 2 + c.e4m3) {
+    case 256: kv_write_kernel<128, false><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
+    case 257: kv_write_kernel<128, true><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
+    case 512: kv_write_kernel<256, false><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
+    case 513: kv_write_kernel<256, true><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
+    case 1024: kv_write_kernel<512, false><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
+    default: kv_write_kernel<512, true><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_read(const KvBatch& b, const KvCache& c, uint16_t* k_out, uint16_t* v_out, unsigned int* status,
+                           cudaStream_t s) {
+  const unsigned grid = move_blocks(b, c), block = kMoveWarps * 32;
+  const int parts = move_parts(c);
+  switch (c.head_dim * 2 + c.e4m3) {
+    case 256: kv_read_kernel<128, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
+    case 257: kv_read_kernel<128, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
+    case 512: kv_read_kernel<256, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
+    case 513: kv_read_kernel<256, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
+    case 1024: kv_read_kernel<512, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
+    default: kv_read_kernel<512, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace moe
+
+// ------------------------------------------------------------------ the C ABI
+
+using namespace moe;
+
+struct moe_ffn_kv {
+  moe_ffn_kv_config cfg;
+  int device;
+  int num_sms;
+  uint8_t* ws;
+  size_t ws_bytes;
+  unsigned int* status;
+};
+
+namespace {
+
+bool kv_config_ok(const moe_ffn_kv_config* c) {
+  return c && c->kv_heads >= 1 && c->kv_heads <= 1024 && c->q_heads >= c->kv_heads && c->q_heads % c->kv_heads == 0 &&
+         c->q_heads / c->kv_heads <= 64 && (c->head_dim == 128 || c->head_dim == 256 || c->head_dim == 512) &&
+         (c->page_size == 16 || c->page_size == 32 || c->page_size == 64 || c->page_size == 128) && c->n_pages >= 1 &&
+         static_cast<long long>(c->n_pages) * c->kv_heads * c->page_size < (1LL << 31) &&
+         (c->format == MOE_FFN_KV_BF16 || c->format == MOE_FFN_KV_E4M3) && c->max_tokens >= 1 &&
+         c->max_tokens <= MOE_FFN_KV_MAX_TOKENS_LIMIT && c->max_seqs >= 1 && c->max_seqs <= MOE_FFN_KV_MAX_SEQS_LIMIT;
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+bool meet(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
+// Checks a call's cache and batch and gives them in the kernels' form. Returns MOE_FFN_OK, an error,
+// or 1 if there is nothing to do.
+int kv_arguments(const moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch, KvBatch* b,
+                 KvCache* c) {
+  if (!kv || !cache || !batch) return MOE_FFN_EINVAL;
+  if (batch->n_tokens < 0 || batch->n_seqs < 0 || batch->pages_cols < 0 || batch->max_new < 0 ||
+      batch->pages_stride < batch->pages_cols)
+    return MOE_FFN_EINVAL;
+  if (batch->n_tokens > kv->cfg.max_tokens || batch->n_seqs > kv->cfg.max_seqs) return MOE_FFN_ETOOBIG;
+  if (batch->n_tokens == 0) return 1;
+  const bool q8 = kv->cfg.format == MOE_FFN_KV_E4M3;
+  if (!cache->k || !cache->v || (q8 && (!cache->k_scale || !cache->v_scale))) return MOE_FFN_EINVAL;
+  if (batch->n_seqs > 0 && (!batch->cu_q || !batch->kv_len || (batch->pages_cols > 0 && !batch->pages)))
+    return MOE_FFN_EINVAL;
+  if (off16(cache->k) || off16(cache->v) || (q8 && (off16(cache->k_scale) || off16(cache->v_scale))) ||
+      off4(batch->cu_q) || off4(batch->kv_len) || off4(batch->pages))
+    return MOE_FFN_EALIGN;
+  b->cu_q = batch->cu_q;
+  b->kv_len = batch->kv_len;
+  b->pages = batch->pages;
+  b->pages_stride = batch->pages_stride;
+  b->pages_cols = batch->pages_cols;
+  b->n_seqs = batch->n_seqs;
+  b->n_tokens = batch->n_tokens;
+  b->max_new = batch->max_new;
+  c->k = static_cast<uint8_t*>(cache->k);
+  c->v = static_cast<uint8_t*>(cache->v);
+  c->k_scale = cache->k_scale;
+  c->v_scale = cache->v_scale;
+  c->n_pages = kv->cfg.n_pages;
+  c->kv_heads = kv->cfg.kv_heads;
+  c->page_log2 = kv->cfg.page_size == 16 ? 4 : kv->cfg.page_size == 32 ? 5 : kv->cfg.page_size == 64 ? 6 : 7;
+  c->head_dim = kv->cfg.head_dim;
+  c->e4m3 = q8 ? 1 : 0;
+  return MOE_FFN_OK;
+}
+
+int kv_rows(const moe_ffn_kv_rows* r, KvRows* o) {
+  if (!r || !r->ptr || r->token_stride < 0 || r->head_stride < 0) return MOE_FFN_EINVAL;
+  if (off16(r->ptr) || r->token_stride % 8 != 0 || r->head_stride % 8 != 0) return MOE_FFN_EALIGN;
+  o->ptr = static_cast<const uint16_t*>(r->ptr);
+  o->token_stride = r->token_stride;
+  o->head_stride = r->head_stride;
+  return MOE_FFN_OK;
+}
+
+size_t kv_rows_bytes(const KvRows& r, int tokens, int heads, int d) {
+  return static_cast<size_t>((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + d) * 2;
+}
+
+int on_device(const moe_ffn_kv* kv) {
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) return MOE_FFN_ECUDA;
+  return cur == kv->device || cudaSetDevice(kv->device) == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_ffn_kv_workspace_bytes(const moe_ffn_kv_config* cfg) {
+  if (!kv_config_ok(cfg)) return 0;
+  return 256;
+}
+
+int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* workspace, size_t workspace_bytes,
+                    int device) {
+  if (!out) return MOE_FFN_EINVAL;
+  *out = nullptr;
+  if (!kv_config_ok(cfg) || !workspace) return MOE_FFN_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_FFN_EALIGN;
+  if (workspace_bytes < moe_ffn_kv_workspace_bytes(cfg)) return MOE_FFN_ETOOBIG;
+  if (cudaSetDevice(device) != cudaSuccess) return MOE_FFN_ECUDA;
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return MOE_FFN_ECUDA;
+  if (major != 10 || minor != 3) return MOE_FFN_EARCH;
+  moe_ffn_kv* kv = new (std::nothrow) moe_ffn_kv();
+  if (!kv) return MOE_FFN_ECUDA;
+  kv->cfg = *cfg;
+  kv->device = device;
+  kv->num_sms = sms;
+  kv->ws = static_cast<uint8_t*>(workspace);
+  kv->ws_bytes = workspace_bytes;
+  kv->status = reinterpret_cast<unsigned int*>(kv->ws);
+  if (cudaMemset(kv->ws, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    delete kv;
+    return MOE_FFN_ECUDA;
+  }
+  *out = kv;
+  return MOE_FFN_OK;
+}
+
+int moe_ffn_kv_write(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch,
+                     const moe_ffn_kv_rows* k, const moe_ffn_kv_rows* v, void* stream) {
+  KvBatch b;
+  KvCache c;
+  KvRows kr, vr;
+  int rc = kv_arguments(kv, cache, batch, &b, &c);
+  if (rc != MOE_FFN_OK) return rc > 0 ? MOE_FFN_OK : rc;
+  if ((rc = kv_rows(k, &kr)) != MOE_FFN_OK || (rc = kv_rows(v, &vr)) != MOE_FFN_OK) return rc;
+  if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
+  return launch_kv_write(b, c, kr, vr, kv->status, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_FFN_OK
+                                                                                                     : MOE_FFN_ECUDA;
+}
+
+int moe_ffn_kv_read(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch, void* k_out,
+                    void* v_out, void* stream) {
+  KvBatch b;
+  KvCache c;
+  int rc = kv_arguments(kv, cache, batch, &b, &c);
+  if (rc != MOE_FFN_OK) return rc > 0 ? MOE_FFN_OK : rc;
+  if (!k_out || !v_out) return MOE_FFN_EINVAL;
+  if (off16(k_out) || off16(v_out)) return MOE_FFN_EALIGN;
+  const size_t bytes = static_cast<size_t>(b.n_tokens) * c.kv_heads * c.head_dim * 2;
+  if (meet(k_out, bytes, v_out, bytes) || meet(k_out, bytes, kv->ws, kv->ws_bytes) ||
+      meet(v_out, bytes, kv->ws, kv->ws_bytes))
+    return MOE_FFN_EINVAL;
+  if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
+  return launch_kv_read(b, c, static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out), kv->status,
+                        static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_FFN_OK
+             : MOE_FFN_ECUDA;
+}
+
+int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch,
+                         const moe_ffn_kv_rows* q, float scale, int window, int sinks, void* out, float* lse,
+                         void* stream) {
+  KvAttn a;
+  int rc = kv_arguments(kv, cache, batch, &a.b, &a.c);
+  if (rc < 0) return rc;
+  if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0 || sinks < 0) return MOE_FFN_EINVAL;
+  if (rc > 0) return MOE_FFN_OK;
+  if ((rc = kv_rows(q, &a.q)) != MOE_FFN_OK) return rc;
+  if (!out) return MOE_FFN_EINVAL;
+  if (off16(out) || off4(lse)) return MOE_FFN_EALIGN;
+  const moe_ffn_kv_config& f = kv->cfg;
+  const size_t rows = static_cast<size_t>(a.b.n_tokens) * f.q_heads, bytes = rows * f.head_dim * 2;
+  if (meet(out, bytes, a.q.ptr, kv_rows_bytes(a.q, a.b.n_tokens, f.q_heads, f.head_dim)) ||
+      meet(out, bytes, kv->ws, kv->ws_bytes) ||
+      (lse && (meet(lse, rows * 4, out, bytes) || meet(lse, rows * 4, kv->ws, kv->ws_bytes))))
+    return MOE_FFN_EINVAL;
+  a.group = f.q_heads / f.kv_heads;
+  a.q_heads = f.q_heads;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.status = kv->status;
+  if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
+  return launch_kv_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
+}
+
+int moe_ffn_kv_device_status(moe_ffn_kv* kv, void* stream, uint32_t* word) {
+  if (!kv) return MOE_FFN_EINVAL;
+  if (cudaSetDevice(kv->device) != cudaSuccess) return MOE_FFN_ECUDA;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOE_FFN_ECUDA;
+  uint32_t v = 0;
+  if (cudaMemcpy(&v, kv->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_FFN_ECUDA;
+  if (v != 0 && cudaMemset(kv->status, 0, 4) != cudaSuccess) return MOE_FFN_ECUDA;
+  if (word) *word = v;
+  return v ? MOE_FFN_EDEVICE : MOE_FFN_OK;
+}
+
+void moe_ffn_kv_destroy(moe_ffn_kv* kv) { delete kv; }
+
+}  // extern "C"

@@ -1,0 +1,88 @@
+// kv.h — declarations shared by the paged key/value cache's translation units (not part of the ABI).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace moe {
+
+// The batch and the cache as the kernels see them.
+struct KvBatch {
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* pages;
+  long long pages_stride;
+  int pages_cols;
+  int n_seqs;
+  int n_tokens;
+  int max_new;
+};
+
+struct KvCache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int n_pages;
+  int kv_heads;
+  int page_log2;
+  int head_dim;
+  int e4m3;
+};
+
+struct KvRows {
+  const uint16_t* ptr;
+  long long token_stride;
+  long long head_stride;
+};
+
+struct KvAttn {
+  KvBatch b;
+  KvCache c;
+  KvRows q;
+  int group;    // query heads per kv head
+  int q_heads;
+  float scale;
+  int window;   // 0: none
+  int sinks;
+  uint16_t* out;
+  float* lse;   // or NULL
+  unsigned int* status;
+};
+
+cudaError_t launch_kv_write(const KvBatch& b, const KvCache& c, const KvRows& k, const KvRows& v, unsigned int* status,
+                            cudaStream_t s);
+cudaError_t launch_kv_read(const KvBatch& b, const KvCache& c, uint16_t* k_out, uint16_t* v_out, unsigned int* status,
+                           cudaStream_t s);
+cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t s);
+
+#ifdef __CUDACC__
+// What a batch says of one sequence, with every value brought into range.
+struct KvSeq {
+  int row0;    // first token row
+  int n;       // new tokens
+  int len;     // tokens in the cache
+};
+
+__device__ __forceinline__ KvSeq kv_sequence(const KvBatch& b, const KvCache& c, int seq, unsigned int* status) {
+  const int r0 = b.cu_q[seq], r1 = b.cu_q[seq + 1], len = b.kv_len[seq];
+  KvSeq s;
+  s.row0 = min(max(r0, 0), b.n_tokens);
+  s.n = min(max(r1 - s.row0, 0), min(b.n_tokens - s.row0, b.max_new));
+  const long long room = static_cast<long long>(b.pages_cols) << c.page_log2;
+  s.len = static_cast<int>(min(static_cast<long long>(max(len, 0)), min(room, 0x7fffff00LL)));
+  if (s.row0 != r0 || s.row0 + s.n != r1 || s.len != len) atomicOr(status, 0x10u);
+  return s;
+}
+
+// The page that holds page `i` of sequence `seq`, or -1 (and the status bit) if its id is no page.
+__device__ __forceinline__ int kv_page(const KvBatch& b, const KvCache& c, int seq, int i, unsigned int* status) {
+  const int page = b.pages[seq * b.pages_stride + i];
+  if (static_cast<unsigned>(page) < static_cast<unsigned>(c.n_pages)) return page;
+  atomicOr(status, 0x10u);
+  return -1;
+}
+#endif
+
+}  // namespace moe

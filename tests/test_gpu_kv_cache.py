@@ -1,0 +1,372 @@
+"""The paged key/value cache and its attention on a GB300, against their definitions in 64 bits
+(tests/kv_util.py, which derives the tolerances)."""
+import math
+
+import pytest
+import torch
+
+import tests.kv_util as U
+from mixture_experts_ffn_router_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [("bf16", 128), ("bf16", 256), ("bf16", 512), ("e4m3", 128), ("e4m3", 256), ("e4m3", 512)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.lib()
+
+
+def _ok(kv):
+    torch.cuda.synchronize()
+    assert kv.status() == (B.MOE_FFN_OK, 0)
+
+
+# ------------------------------------------------------------------ writing and reading back
+
+def _expected_cache(case, kv, c):
+    """The cache's tensors after case.filled, in the same order: values, and scales."""
+    want = case.empty_cache(kv)
+    for b, n in enumerate(case.kv):
+        for p in range(n):
+            page, slot = int(case.pages[b, p // case.page]), p % case.page
+            for name, x in (("k", case.k[b][p]), ("v", case.v[b][p])):
+                t = getattr(want, name)
+                if case.fmt == "bf16":
+                    t[page, :, slot] = x.cuda()
+                else:
+                    codes, scale = U.quantised(x)
+                    t.view(torch.uint8)[page, :, slot] = codes.view(torch.uint8).cuda()
+                    getattr(want, name + "_scale")[page, :, slot] = scale.cuda()
+    return want
+
+
+def _same_bits(a, b):
+    kind = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[a.element_size()]
+    a, b = a.view(kind), b.view(kind)
+    assert torch.equal(a, b), "%d of %d values differ" % ((a != b).sum(), a.numel())
+
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("page,hkv", [(16, 1), (32, 3), (64, 8), (128, 2)])
+def test_written_bits(fmt, d, page, hkv):
+    case = U.Case(fmt, hkv, hkv, d, page, [0] * 4, [1, page, page + 1, 2 * page + 5], seed=d + page, garbage="zero")
+    case.k[3][7] = 0.0                       # a row of zeros
+    case.k[3][8] *= 2.0 ** -120              # near the bottom of bf16's range
+    case.v[3][9] *= 2.0 ** 120
+    kv = case.handle()
+    c = case.filled(kv)
+    _ok(kv)
+    want = _expected_cache(case, kv, c)
+    for n in ("k", "v") + (("k_scale", "v_scale") if fmt == "e4m3" else ()):
+        _same_bits(getattr(c, n), getattr(want, n))
+
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+def test_round_trip(fmt, d):
+    case = U.Case(fmt, 4, 2, d, 16, [3, 0, 17, 1], [3, 40, 30, 100], seed=d, pad_rows=2)
+    kv = case.handle()
+    c = case.filled(kv)
+    k, v = kv.read(c, case.batch(), n_tokens=case.T)
+    _ok(kv)
+    for name, got in (("k", k), ("v", v)):
+        want = torch.cat([case.stored(name, b)[case.kv[b] - n:] for b, n in enumerate(case.new)]
+                         + [torch.zeros(2, case.hkv, d, dtype=torch.float64)])
+        U.check_close(got, want, (U.BF + U.F32) * want.abs() if fmt == "e4m3" else torch.zeros_like(want), name)
+    assert torch.equal(kv.read(c, case.batch())[0], k[:case.cu[-1]])
+
+
+def test_rows_with_infinities_read_back_as_nan_in_e4m3():
+    case = U.Case("e4m3", 2, 2, 256, 32, [0], [9], seed=1)
+    case.k[0][3, 1, 17] = math.inf
+    case.v[0][5, 0, 255] = math.nan
+    kv = case.handle()
+    c = case.filled(kv)
+    k, v = kv.read(c, case.batch([9]), n_tokens=9)
+    _ok(kv)
+    for got, at in ((k, (3, 1)), (v, (5, 0))):
+        nan = torch.isnan(got).all(-1)
+        assert nan[at] and nan.sum() == 1 and torch.isnan(got).any(-1).sum() == 1
+
+
+def test_strided_views_write_the_same():
+    case = U.Case("e4m3", 4, 4, 256, 32, [0, 0], [37, 20], seed=2)
+    kv = case.handle()
+    base = case.filled(kv)
+    k, v = torch.cat(case.k).cuda(), torch.cat(case.v).cuda()
+    T = k.shape[0]
+    fused = torch.zeros(T, 3, 4, 256, dtype=torch.bfloat16, device="cuda")
+    fused[:, 1], fused[:, 2] = k, v
+    other = case.empty_cache(kv)
+    kv.write(other, case.batch([37, 20]), fused[:, 1], v.transpose(0, 1).contiguous().transpose(0, 1))
+    _ok(kv)
+    for n in ("k", "v", "k_scale", "v_scale"):
+        _same_bits(getattr(base, n), getattr(other, n))
+
+
+def test_tokens_of_no_position_write_nothing():
+    # Three new tokens of a sequence whose cache holds two, and padding rows.
+    case = U.Case("bf16", 2, 2, 128, 16, [3, 1], [2, 1], seed=3, pad_rows=3, garbage="zero")
+    kv = case.handle()
+    c = kv.new_cache()
+    x = torch.randn(7, 2, 128, device="cuda").to(torch.bfloat16)
+    kv.write(c, case.batch(), x, -x)
+    _ok(kv)
+    assert (c.k != 0).any(-1).sum() == 3 * 2
+    page = int(case.pages[0, 0])
+    assert torch.equal(c.k[page, :, :2].transpose(0, 1), x[1:3])
+    k, _ = kv.read(c, case.batch(), n_tokens=7)
+    assert torch.equal(k[1:4], x[1:4]) and not k[0].any() and not k[4:].any()
+
+
+@pytest.mark.parametrize("n_seqs", [1, 31, 33, 300, 1100])
+def test_many_sequences_find_their_places(n_seqs):
+    new = [(7 * b) % 3 for b in range(n_seqs)]
+    case = U.Case("bf16", 1, 1, 128, 16, new, [n + (5 * b) % 40 for b, n in enumerate(new)], seed=4, pad_rows=1)
+    kv = case.handle()
+    c = case.filled(kv)
+    k, v = kv.read(c, case.batch(), n_tokens=case.T)
+    _ok(kv)
+    for got, have in ((k, case.k), (v, case.v)):
+        want = torch.cat([have[b][case.kv[b] - n:] for b, n in enumerate(new)] + [torch.zeros(1, 1, 128).bfloat16()])
+        assert torch.equal(got.cpu(), want)
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("page", [16, 128])
+def test_single_tokens(fmt, d, page):
+    kv_len = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300]
+    U.check_attention(U.Case(fmt, 4, 2, d, page, [1] * len(kv_len), kv_len, seed=d))
+
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("group", [1, 3, 8, 11])
+def test_head_groups(fmt, d, group):
+    U.check_attention(U.Case(fmt, 2 * group, 2, d, 32, [1, 1, 1], [40, 1, 150], seed=group))
+    U.check_attention(U.Case(fmt, 2 * group, 2, d, 32, [5, 1, 30], [40, 1, 130], seed=group))
+
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+def test_chunks(fmt, d):
+    U.check_attention(U.Case(fmt, 4, 2, d, 16, [1, 64, 65, 7, 0, 130], [1, 64, 200, 263, 90, 131], seed=d))
+
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (20, 0), (64, 4), (100, 40), (100, 1000), (1000, 4)])
+def test_windows_and_sinks(fmt, d, window, sinks):
+    U.check_attention(U.Case(fmt, 2, 1, d, 16, [1, 1, 1, 1], [1, 20, 21, 333], seed=window), window, sinks)
+    U.check_attention(U.Case(fmt, 2, 1, d, 16, [130, 3, 77], [130, 300, 211], seed=window), window, sinks)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,kv", [([1, 1, 1], [0, 5, 0]), ([4, 1, 70], [2, 0, 33]), ([0, 0], [7, 0])])
+def test_rows_that_see_nothing(fmt, new, kv):
+    case = U.Case(fmt, 4, 2, 256, 16, new, kv, seed=5, pad_rows=3)
+    out, lse = U.check_attention(case, window=9)
+    assert not out[case.cu[-1]:].any() and torch.isinf(lse[case.cu[-1]:]).all()
+
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 2)])
+def test_hidden_values_do_not_matter(fmt, d, window, sinks):
+    """NaN and infinities in keys and values change only the rows that see them."""
+    case = U.Case(fmt, 2, 1, d, 16, [90, 1], [150, 200], seed=6)
+    case.v[0][130, 0, 5] = math.nan
+    case.v[0][100, 0, d - 1] = math.inf
+    case.k[0][145, 0, 3] = math.nan
+    case.v[0][30, 0, 40] = math.nan       # outside every window but the first rows'
+    case.k[1][20, 0, 3] = math.nan        # hidden by the window
+    U.check_attention(case, window, sinks)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_queries_with_nan_stay_alone(fmt):
+    case = U.Case(fmt, 4, 2, 256, 32, [20, 1], [50, 77], seed=7)
+    case.q[3, 1, 0] = math.nan
+    case.q[20, 2, 9] = math.nan
+    U.check_attention(case)
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 256), ("e4m3", 512)])
+def test_large_scores(fmt, d):
+    # Scores of some hundreds: the running maximum moves far and often.
+    case = U.Case(fmt, 2, 1, d, 16, [60, 1], [200, 500], seed=8)
+    for k in case.k:
+        k.mul_(torch.linspace(0.2, 8, k.shape[0]).view(-1, 1, 1))
+    case.q.mul_(6)
+    U.check_attention(case)
+
+
+def test_scale_and_strided_queries():
+    case = U.Case("bf16", 6, 2, 128, 32, [9, 1], [40, 60], seed=9)
+    fused = torch.zeros(10, 10, 128, dtype=torch.bfloat16, device="cuda")
+    fused[:, 2:8] = case.q.cuda()
+    U.check_attention(case, scale=0.3, q=fused[:, 2:8])
+    by_head = case.q.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+    U.check_attention(case, scale=0.01, q=by_head)
+
+
+def _large(fmt, hq, hkv, d, page, new, kv, seed):
+    """A case too large for the row-by-row definition, and its result by 64-bit products on the GPU."""
+    case = U.Case(fmt, hq, hkv, d, page, new, kv, seed=seed)
+    h = case.handle()
+    c = case.filled(h)
+    g = hq // hkv
+
+    def want(window, sinks):
+        out, lse = [], []
+        for b, n in enumerate(new):
+            k, v = case.stored("k", b).cuda(), case.stored("v", b).cuda()
+            q = case.q[case.cu[b]:case.cu[b + 1]].double().cuda()
+            s = torch.einsum("thd,jhd->htj", q, k.repeat_interleave(g, 1)) * d ** -0.5
+            j, p = torch.arange(kv[b], device="cuda"), torch.arange(kv[b] - n, kv[b], device="cuda")[:, None]
+            see = j <= p
+            if window:
+                see = see & ((j > p - window) | (j < sinks))
+            s = s.masked_fill(~see, -math.inf)
+            out.append(torch.einsum("htj,jhd->thd", torch.softmax(s, -1), v.repeat_interleave(g, 1)))
+            lse.append(torch.logsumexp(s, -1).T)
+        return torch.cat(out).cpu(), torch.cat(lse).cpu()
+
+    return case, h, c, want
+
+
+@pytest.mark.parametrize("fmt,hq,hkv,d,page,new,kv", [
+    ("bf16", 16, 2, 512, 64, [1, 1], [20011, 3]), ("e4m3", 16, 8, 256, 16, [1] * 5, [5000, 1, 900, 2048, 4097]),
+    ("bf16", 8, 2, 128, 128, [40, 3], [9000, 30]), ("e4m3", 4, 1, 512, 32, [300], [5000]),
+    ("bf16", 16, 8, 256, 64, [700, 1, 129], [2000, 1999, 129])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1024, 4)])
+def test_long_caches(fmt, hq, hkv, d, page, new, kv, window, sinks):
+    case, h, c, want = _large(fmt, hq, hkv, d, page, new, kv, seed=10)
+    out, lse = h.attention(c, case.batch(), case.q.cuda(), window=window, sinks=sinks)
+    _ok(h)
+    w, wl = want(window, sinks)
+    # Values of order 1 under softmax weights that sum to 1: one rounding of the weights, one of the
+    # result, each 2^-8 of magnitudes up to 6, and 2^-10 for everything held in fp32.
+    U.check_close(lse, wl, torch.full_like(wl, 2.0 ** -10), "lse")
+    U.check_close(out, w, 2 * U.BF * w.abs() + (U.BF + 2.0 ** -10) * 6 * torch.ones_like(w) / 6, "out")
+    out2, lse2 = h.attention(c, case.batch(), case.q.cuda(), window=window, sinks=sinks)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_captured_step_replays_with_new_lengths():
+    """Write and attention of a decode step in a graph; the batch's tensors change between replays."""
+    case = U.Case("e4m3", 4, 2, 256, 16, [1, 1], [30, 51], seed=11)
+    kv = case.handle()
+    batch = case.batch()
+    q = case.q.cuda()
+    k = torch.stack([case.k[b][-1] for b in range(2)]).cuda()
+    v = torch.stack([case.v[b][-1] for b in range(2)]).cuda()
+    c = case.filled(kv)
+    kv.write(c, batch, k, v)
+    want, wlse = kv.attention(c, batch, q)
+    torch.cuda.synchronize()
+    c2 = case.filled(kv)
+    for b in range(2):
+        page, slot = int(case.pages[b, (case.kv[b] - 1) // 16]), (case.kv[b] - 1) % 16
+        c2.v.view(torch.uint8)[page, :, slot] = 0
+    batch.tensors[1].fill_(1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.write(c2, batch, k, v)
+        out, lse = kv.attention(c2, batch, q)
+    batch.tensors[1].copy_(torch.tensor(case.kv, dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    _ok(kv)
+
+
+def test_calls_on_two_streams_are_ordered():
+    case = U.Case("bf16", 4, 2, 256, 16, [64], [640], seed=12)
+    kv = case.handle()
+    c = case.filled(kv)
+    q = case.q.cuda()
+    want, _ = kv.attention(c, case.batch(), q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    batch = case.batch()
+    for _ in range(4):
+        c2 = case.filled(kv)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got, _ = kv.attention(c2, batch, q)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want)
+
+
+def test_bad_tables_set_the_status_word():
+    """Page ids and lengths out of range: nothing out of the cache is touched, and the status says so."""
+    case = U.Case("bf16", 4, 2, 256, 16, [1, 1, 20], [40, 20, 33], seed=13)
+    kv = case.handle()
+    c = case.filled(kv)
+    for change in ("page", "negative", "kv_len", "cu_q"):
+        batch = case.batch()
+        cu, kv_len, pages = batch.tensors
+        if change == "page":
+            pages[1, 0] = case.n_pages
+        elif change == "negative":
+            pages[1, 1] = -1
+        elif change == "kv_len":
+            kv_len[1] = pages.shape[1] * 16 + 1
+        else:
+            cu[2] = 40
+        out, _ = kv.attention(c, batch, case.q.cuda())
+        torch.cuda.synchronize()
+        assert kv.status() == (B.MOE_FFN_EDEVICE, B.STATUS_BITS["BAD_INDEX"]), change
+        kv.read(c, batch, n_tokens=case.T)
+        assert kv.status()[1] in (0, B.STATUS_BITS["BAD_INDEX"])
+    want, _ = U.check_attention(case, kv=kv, cache=c)
+
+
+def test_empty_batches_do_nothing():
+    case = U.Case("bf16", 4, 2, 256, 16, [], [], seed=14)
+    kv = case.handle()
+    c = kv.new_cache()
+    x = torch.zeros(0, 2, 256, dtype=torch.bfloat16, device="cuda")
+    kv.write(c, case.batch(), x, x)
+    out, lse = kv.attention(c, case.batch(), torch.zeros(0, 4, 256, dtype=torch.bfloat16, device="cuda"))
+    assert out.shape == (0, 4, 256) and lse.shape == (0, 4)
+    # Rows but no sequences: all padding.
+    out, lse = kv.attention(c, case.batch(), torch.ones(1, 4, 256, dtype=torch.bfloat16, device="cuda"))
+    _ok(kv)
+    assert not out.any() and torch.isinf(lse).all()
+
+
+def test_refusals():
+    case = U.Case("bf16", 4, 2, 256, 16, [2], [5], seed=15)
+    kv = case.handle()
+    c, batch, q = case.filled(kv), case.batch(), case.q.cuda()
+    for kw in (dict(window=-1), dict(sinks=-1), dict(scale=0.0), dict(scale=math.inf), dict(scale=-1.0)):
+        with pytest.raises(B.MoeFFNError) as e:
+            kv.attention(c, batch, q, **kw)
+        assert e.value.status == B.MOE_FFN_EINVAL
+    with pytest.raises(B.MoeFFNError) as e:
+        kv.attention(c, batch, q, out=q)
+    assert e.value.status == B.MOE_FFN_EINVAL
+    big = torch.zeros(kv.cfg.max_tokens + 1, 4, 256, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(B.MoeFFNError) as e:
+        kv.attention(c, batch, big)
+    assert e.value.status == B.MOE_FFN_ETOOBIG
+    flat = torch.zeros(4 * 256 * 2 + 4, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(B.MoeFFNError) as e:
+        kv.attention(c, batch, flat[4:].view(2, 4, 256))
+    assert e.value.status == B.MOE_FFN_EALIGN
+    with pytest.raises(ValueError, match="multiples of 8"):
+        kv.attention(c, batch, torch.zeros(2, 4, 257, dtype=torch.bfloat16, device="cuda")[:, :, :256])
+    L = B.lib()
+    rows = kv._rows("q", q, 4)
+    st = batch.of(2)
+    args = (rows, 0.1, 0, 0, q.data_ptr() + (1 << 20), None, None)
+    assert L.moe_ffn_kv_attention(kv._handle, B.moe_ffn_kv_cache(), st, *args) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_attention(kv._handle, c.struct, st, rows, 0.1, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
+    st.n_seqs = kv.cfg.max_seqs + 1
+    assert L.moe_ffn_kv_attention(kv._handle, c.struct, st, *args) == B.MOE_FFN_ETOOBIG
+    st.n_seqs = 1
+    st.pages_stride = 0
+    assert L.moe_ffn_kv_attention(kv._handle, c.struct, st, *args) == B.MOE_FFN_EINVAL

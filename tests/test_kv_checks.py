@@ -1,0 +1,129 @@
+"""The paged cache's refusals, and its structures' layout, without a GPU."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+from mixture_experts_ffn_router_gb300 import binding as B
+from mixture_experts_ffn_router_gb300 import build as cuda_build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+GOOD = dict(q_heads=16, kv_heads=8, head_dim=256, page_size=64, n_pages=10, fmt="bf16", max_tokens=64, max_seqs=4)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    cuda_build.build()
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    names = ("moe_ffn_kv_config", "moe_ffn_kv_cache", "moe_ffn_kv_batch", "moe_ffn_kv_rows")
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "moe_ffn.h"', "int main(void){"]
+    for st in names:
+        lines.append('printf("%s %%zu\\n", sizeof(%s));' % (st, st))
+        for f, _ in getattr(B, st)._fields_:
+            lines.append('printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (st, f, st, f))
+    lines.append('printf("formats %d %d\\n", MOE_FFN_KV_BF16, MOE_FFN_KV_E4M3);return 0;}')
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines))
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    got = dict(l.split(" ", 1) for l in out.strip().split("\n"))
+    for st in names:
+        cls = getattr(B, st)
+        assert int(got[st]) == ctypes.sizeof(cls), st
+        for f, _ in cls._fields_:
+            assert int(got["%s.%s" % (st, f)]) == getattr(cls, f).offset, (st, f)
+    assert got["formats"] == "%d %d" % (B.KV_FORMATS["bf16"], B.KV_FORMATS["e4m3"])
+
+
+def test_workspace_of_a_good_configuration():
+    assert B.moe_ffn_kv_workspace_bytes(B.make_kv_config(**GOOD)) >= 256
+
+
+@pytest.mark.parametrize("change", [
+    dict(q_heads=0), dict(kv_heads=0), dict(q_heads=12), dict(q_heads=8 * 65), dict(head_dim=64), dict(head_dim=192),
+    dict(page_size=8), dict(page_size=48), dict(page_size=256), dict(n_pages=0), dict(n_pages=1 << 22),
+    dict(fmt="int4"), dict(max_tokens=0), dict(max_tokens=(1 << 24) + 1), dict(max_seqs=0), dict(max_seqs=65537)])
+def test_bad_configurations_have_no_workspace(change):
+    assert B.moe_ffn_kv_workspace_bytes(B.make_kv_config(**{**GOOD, **change})) == 0
+
+
+def test_calls_without_a_handle():
+    L = B.lib()
+    c, b, r = B.moe_ffn_kv_cache(), B.moe_ffn_kv_batch(), B.moe_ffn_kv_rows()
+    assert L.moe_ffn_kv_write(None, c, b, r, r, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_read(None, c, b, None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_attention(None, c, b, r, 1.0, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_device_status(None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_init(None, None, None, 0, 0) == B.MOE_FFN_EINVAL
+    h = ctypes.c_void_p(4096)
+    cfg = B.make_kv_config(**GOOD)
+    assert L.moe_ffn_kv_init(ctypes.byref(h), ctypes.byref(cfg), None, 1 << 30, 0) == B.MOE_FFN_EINVAL
+    assert not h.value
+    assert L.moe_ffn_kv_init(ctypes.byref(h), ctypes.byref(cfg), ctypes.c_void_p(4096 + 16), 1 << 30,
+                             0) == B.MOE_FFN_EALIGN
+    assert L.moe_ffn_kv_init(ctypes.byref(h), ctypes.byref(cfg), ctypes.c_void_p(4096), 16, 0) == B.MOE_FFN_ETOOBIG
+    L.moe_ffn_kv_destroy(None)
+
+
+def test_format_and_configuration_are_named():
+    with pytest.raises(ValueError, match="fmt"):
+        B.PagedKV(16, 8, 256, 64, 10, "fp8")
+    with pytest.raises(ValueError, match="invalid configuration"):
+        B.PagedKV(16, 8, 100, 64, 10)
+
+
+def _stub(fmt="bf16"):
+    """A PagedKV without a device: what its argument checks read."""
+    kv = B.PagedKV.__new__(B.PagedKV)
+    kv.ctx, kv.fmt, kv.device = 0, fmt, torch.device("cuda", 0)
+    kv.q_heads, kv.kv_heads, kv.head_dim, kv.shape = 16, 8, 256, (10, 8, 64, 256)
+    kv.dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    return kv
+
+
+@pytest.mark.parametrize("shape,dtype,match", [
+    ((3, 16, 256), torch.float32, "bfloat16"), ((3, 8, 256), torch.bfloat16, "shape"),
+    ((3, 16, 128), torch.bfloat16, "shape"), ((3, 4096), torch.bfloat16, "shape"),
+    ((3, 16, 256), torch.bfloat16, "must be on")])
+def test_queries_are_checked(shape, dtype, match):
+    with pytest.raises(ValueError, match=match):
+        _stub()._rows("q", torch.empty(shape, dtype=dtype, device="meta"), 16)
+
+
+@pytest.mark.parametrize("fmt,change,match", [
+    ("bf16", dict(k=None), "required"), ("bf16", dict(v_scale="scale"), "no scales"),
+    ("bf16", dict(v=torch.float8_e4m3fn), "v must be"), ("e4m3", dict(k_scale=None), "k_scale is required"),
+    ("e4m3", dict(v_scale=torch.float64), "v_scale must be"), ("e4m3", dict(k="short"), "k must be"),
+    ("e4m3", dict(), "CUDA tensor")])
+def test_caches_are_checked(fmt, change, match):
+    dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    given = {n: torch.empty((10, 8, 64, 256), dtype=dtype, device="meta") for n in ("k", "v")}
+    if fmt == "e4m3":
+        given.update({n: torch.empty((10, 8, 64), device="meta") for n in ("k_scale", "v_scale")})
+    for n, what in change.items():
+        if isinstance(what, torch.dtype):
+            given[n] = torch.empty(given[n].shape, dtype=what, device="meta")
+        elif what == "short":
+            given[n] = given[n][:, :, :32]
+        elif what == "scale":
+            given[n] = torch.empty((10, 8, 64), device="meta")
+        else:
+            given[n] = None
+    with pytest.raises(ValueError, match=match):
+        _stub(fmt).cache(**given)
+
+
+@pytest.mark.parametrize("cu,kv,pages,new,match", [
+    ((4,), (4,), (4, 2), 1, "sequences"), ((5,), (4,), (3, 2), 1, "sequences"), ((5,), (4, 1), (4, 2), 1, "dimension"),
+    ((5,), (4,), (4,), 1, "dimension"), ((5,), (4,), (4, 2), -1, "max_new"), ((5,), (4,), (4, 2), 1, "CUDA tensor")])
+def test_batches_are_checked(cu, kv, pages, new, match):
+    t = [torch.empty(s, dtype=torch.int32, device="meta") for s in (cu, kv, pages)]
+    with pytest.raises(ValueError, match=match):
+        B.KVBatch(*t, max_new=new)
+    if match == "CUDA tensor":
+        with pytest.raises(ValueError, match="int32"):
+            B.KVBatch(t[0].long(), *t[1:], max_new=new)
