@@ -252,6 +252,8 @@ struct moe_ffn_kv {
   uint8_t* ws;
   size_t ws_bytes;
   unsigned int* status;
+  int* counters;
+  float* partial;
 };
 
 namespace {
@@ -323,6 +325,26 @@ size_t kv_rows_bytes(const KvRows& r, int tokens, int heads, int d) {
   return static_cast<size_t>((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + d) * 2;
 }
 
+// The workspace: control words (zeroed when the handle is made), then the kernels' pieces.
+struct KvLayout {
+  size_t status, counters, partial, total;
+};
+
+KvLayout make_kv_layout(const moe_ffn_kv_config& c) {
+  KvLayout l;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 255) / 256 * 256;
+    return at;
+  };
+  l.status = take(4);
+  l.counters = take(static_cast<size_t>(c.max_seqs) * c.kv_heads * 4);
+  l.partial = take(static_cast<size_t>(2 * kDecodeMaxCtas * decode_piece_floats(c.head_dim)) * 4);
+  l.total = o;
+  return l;
+}
+
 int on_device(const moe_ffn_kv* kv) {
   int cur = -1;
   if (cudaGetDevice(&cur) != cudaSuccess) return MOE_FFN_ECUDA;
@@ -335,7 +357,7 @@ extern "C" {
 
 size_t moe_ffn_kv_workspace_bytes(const moe_ffn_kv_config* cfg) {
   if (!kv_config_ok(cfg)) return 0;
-  return 256;
+  return make_kv_layout(*cfg).total;
 }
 
 int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* workspace, size_t workspace_bytes,
@@ -344,7 +366,8 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   *out = nullptr;
   if (!kv_config_ok(cfg) || !workspace) return MOE_FFN_EINVAL;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_FFN_EALIGN;
-  if (workspace_bytes < moe_ffn_kv_workspace_bytes(cfg)) return MOE_FFN_ETOOBIG;
+  const KvLayout l = make_kv_layout(*cfg);
+  if (workspace_bytes < l.total) return MOE_FFN_ETOOBIG;
   if (cudaSetDevice(device) != cudaSuccess) return MOE_FFN_ECUDA;
   int major = 0, minor = 0, sms = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
@@ -359,8 +382,10 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   kv->num_sms = sms;
   kv->ws = static_cast<uint8_t*>(workspace);
   kv->ws_bytes = workspace_bytes;
-  kv->status = reinterpret_cast<unsigned int*>(kv->ws);
-  if (cudaMemset(kv->ws, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  kv->status = reinterpret_cast<unsigned int*>(kv->ws + l.status);
+  kv->counters = reinterpret_cast<int*>(kv->ws + l.counters);
+  kv->partial = reinterpret_cast<float*>(kv->ws + l.partial);
+  if (kv_decode_setup() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     delete kv;
     return MOE_FFN_ECUDA;
   }
@@ -425,8 +450,14 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = kv->status;
+  a.counters = kv->counters;
+  a.partial = kv->partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
-  return launch_kv_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int ctas = 2 * kv->num_sms < kDecodeMaxCtas ? 2 * kv->num_sms : kDecodeMaxCtas;
+  const cudaError_t e = a.b.max_new <= 1 && a.group <= kDecodeHeads ? launch_kv_decode(a, ctas, s)
+                                                                    : launch_kv_attention(a, s);
+  return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
 }
 
 int moe_ffn_kv_device_status(moe_ffn_kv* kv, void* stream, uint32_t* word) {

@@ -49,13 +49,28 @@ struct KvAttn {
   uint16_t* out;
   float* lse;   // or NULL
   unsigned int* status;
+  int* counters;    // [max_seqs * kv_heads] pieces finished of each item, zero between calls
+  float* partial;   // pieces of items that several CTAs share
 };
+
+// The single-token kernel: CTAs (two to an SM), and the floats of a piece: eight heads' outputs, then
+// their running maxima and sums.
+constexpr int kDecodeMaxCtas = 304;
+constexpr int kDecodeHeads = 8;
+__host__ __device__ constexpr long long decode_piece_floats(int head_dim) {
+  return static_cast<long long>(kDecodeHeads) * head_dim + 2 * kDecodeHeads;
+}
+
+bool encode_row_chunks(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
+                       uint32_t box_chunks);
 
 cudaError_t launch_kv_write(const KvBatch& b, const KvCache& c, const KvRows& k, const KvRows& v, unsigned int* status,
                             cudaStream_t s);
 cudaError_t launch_kv_read(const KvBatch& b, const KvCache& c, uint16_t* k_out, uint16_t* v_out, unsigned int* status,
                            cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t s);
+cudaError_t kv_decode_setup();
+cudaError_t launch_kv_decode(const KvAttn& a, int ctas, cudaStream_t s);
 
 #ifdef __CUDACC__
 // What a batch says of one sequence, with every value brought into range.
@@ -73,6 +88,21 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvBatch& b, const KvCache& c,
   const long long room = static_cast<long long>(b.pages_cols) << c.page_log2;
   s.len = static_cast<int>(min(static_cast<long long>(max(len, 0)), min(room, 0x7fffff00LL)));
   if (s.row0 != r0 || s.row0 + s.n != r1 || s.len != len) atomicOr(status, 0x10u);
+  return s;
+}
+
+// The positions one token sees: [0, sinks) and [lo, p], p < 0 for none.
+struct KvSpan {
+  int p;
+  int lo;
+  int sinks;  // at most lo
+};
+
+__device__ __forceinline__ KvSpan kv_span(int p, int window, int sinks) {
+  KvSpan s;
+  s.p = p;
+  s.lo = window > 0 ? max(0, p - window + 1) : 0;
+  s.sinks = min(sinks, s.lo);
   return s;
 }
 
