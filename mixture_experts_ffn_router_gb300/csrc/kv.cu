@@ -253,6 +253,7 @@ struct moe_ffn_kv {
   size_t ws_bytes;
   unsigned int* status;
   int* counters;
+  int* counters_in;
   float* partial;
 };
 
@@ -327,7 +328,7 @@ size_t kv_rows_bytes(const KvRows& r, int tokens, int heads, int d) {
 
 // The workspace: control words (zeroed when the handle is made), then the kernels' pieces.
 struct KvLayout {
-  size_t status, counters, partial, total;
+  size_t status, counters, counters_in, partial, total;
 };
 
 KvLayout make_kv_layout(const moe_ffn_kv_config& c) {
@@ -340,6 +341,7 @@ KvLayout make_kv_layout(const moe_ffn_kv_config& c) {
   };
   l.status = take(4);
   l.counters = take(static_cast<size_t>(c.max_seqs) * c.kv_heads * 4);
+  l.counters_in = take(2 * kDecodeMaxCtas * 4);
   l.partial = take(static_cast<size_t>(2 * kDecodeMaxCtas * decode_piece_floats(c.head_dim)) * 4);
   l.total = o;
   return l;
@@ -384,6 +386,7 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   kv->ws_bytes = workspace_bytes;
   kv->status = reinterpret_cast<unsigned int*>(kv->ws + l.status);
   kv->counters = reinterpret_cast<int*>(kv->ws + l.counters);
+  kv->counters_in = reinterpret_cast<int*>(kv->ws + l.counters_in);
   kv->partial = reinterpret_cast<float*>(kv->ws + l.partial);
   if (kv_decode_setup() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     delete kv;
@@ -451,6 +454,7 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   a.lse = lse;
   a.status = kv->status;
   a.counters = kv->counters;
+  a.counters_in = kv->counters_in;
   a.partial = kv->partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

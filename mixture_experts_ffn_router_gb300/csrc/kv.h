@@ -50,6 +50,7 @@ struct KvAttn {
   float* lse;   // or NULL
   unsigned int* status;
   int* counters;    // [max_seqs * kv_heads] pieces finished of each item, zero between calls
+  int* counters_in; // [2 * kDecodeMaxCtas] the same, of groups of an item's pieces
   float* partial;   // pieces of items that several CTAs share
 };
 

@@ -123,6 +123,11 @@ __device__ __forceinline__ uint32_t e4m3_part(float (&x)[4]) {
   return codes;
 }
 
+// The four computing warps.
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+constexpr int kJoin = 24;  // pieces joined at once, at most 32
+
 // Where a CTA's share of the tiles begins, and how a sequence's tiles lie.
 struct SeqTiles {
   int row;     // the token's row
@@ -161,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* empty = full + C::kUnits;
   __shared__ volatile int abort_flag;
   __shared__ int s_last;
+  __shared__ float s_weight[kDecodeHeads][32], s_join[kDecodeHeads][2];
   __shared__ long long s_sum[kThreads / 32], s_total, s_before;
   __shared__ int s_seq;
 
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[unit]);
       next_unit();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      compute_sync();
 
       // P of every key, for head r8: this lane the keys 16 k + 2 c4 + {0, 1, 8, 9}.
       float p[KT / 16][4];
@@ -582,60 +588,112 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (a.lse && warp == 0 && c4 == 0 && r8 < a.group)
         a.lse[to + r8] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147181f;
     } else {
-      // A piece: its place is this CTA's first if the item began before the CTA's share.
-      const long long piece_floats = decode_piece_floats(D);
-      float* piece = a.partial + (2LL * blockIdx.x + (item_start < begin || i0 > 0 || pos == begin ? 0 : 1)) * piece_floats;
+      // A piece. Its place is this CTA's first if the item began before the CTA's share or with it, as
+      // it did for all of the item's CTAs but its first.
+      const int first = static_cast<int>(((item_start + 1) * ctas - 1) / total);
+      const int count = static_cast<int>(((item_start + t.count) * ctas - 1) / total) - first + 1;
+      const int first_place = 2 * first + (first * total / ctas >= item_start ? 0 : 1);
+      auto place = [&](int x) { return x == 0 ? first_place : 2 * (first + x); };  // of the item's piece x
+      constexpr long long piece_floats = decode_piece_floats(D);
+      const int me = static_cast<int>(blockIdx.x) - first;
+      {
+        float* piece = a.partial + place(me) * piece_floats;
 #pragma unroll
-      for (int v = 0; v < C::VT; ++v)
+        for (int v = 0; v < C::VT; ++v)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int h = x & 1 ? h1 : h0;
-          if (h < a.group) piece[h * D + dim0 + v * 16 + (x >> 1) * apart] = o[v][x];
-        }
-      if (warp == 0 && c4 == 0) {
-        piece[kDecodeHeads * D + r8] = m;
-        piece[kDecodeHeads * D + kDecodeHeads + r8] = l;
-      }
-      __threadfence();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      const long long first = ((item_start + 1) * ctas - 1) / total;
-      const long long last = ((item_start + t.count) * ctas - 1) / total;
-      if (tid == 0) {
-        int* counter = a.counters + static_cast<long long>(seq) * heads + head;
-        const int done = atomicAdd(counter, 1);
-        s_last = done == last - first;
-        if (done == last - first) *counter = 0;
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (s_last) {
-        __threadfence();
-        auto place = [&](long long x) {
-          // CTA x's first piece, unless the item begins after the CTA's share does.
-          return a.partial + (2 * x + (x * total / ctas >= item_start ? 0 : 1)) * piece_floats;
-        };
-        for (int e = tid; e < a.group * (D / 4); e += kComputeWarps * 32) {
-          const int h = e / (D / 4), d4 = e % (D / 4) * 4;
-          float top = -INFINITY;
-          for (long long x = first; x <= last; ++x) top = fmaxf(top, __ldcg(place(x) + kDecodeHeads * D + h));
-          const float base = top == -INFINITY ? 0.0f : top;
-          float sum = 0.0f;
-          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (long long x = first; x <= last; ++x) {
-            const float* from = place(x);
-            const float w = exp2_approx(__ldcg(from + kDecodeHeads * D + h) - base);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(from + h * D + d4));
-            sum = fmaf(w, __ldcg(from + kDecodeHeads * D + kDecodeHeads + h), sum);
-            acc.x = fmaf(w, y.x, acc.x);
-            acc.y = fmaf(w, y.y, acc.y);
-            acc.z = fmaf(w, y.z, acc.z);
-            acc.w = fmaf(w, y.w, acc.w);
+          for (int x = 0; x < 4; ++x) {
+            const int h = x & 1 ? h1 : h0;
+            if (h < a.group) piece[h * D + dim0 + v * 16 + (x >> 1) * apart] = o[v][x];
           }
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          *reinterpret_cast<uint2*>(a.out + (to + h) * D + d4) =
-              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-          if (a.lse && d4 == 0) a.lse[to + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147181f;
+        if (warp == 0 && c4 == 0) {
+          piece[kDecodeHeads * D + r8] = m;
+          piece[kDecodeHeads * D + kDecodeHeads + r8] = l;
         }
+      }
+      // Up to kJoin pieces are joined at once; more in groups first, by each group's last CTA into the
+      // group's first piece, and then the groups: 152 pieces in one go were 25 us at the end of a
+      // long sequence's 80.
+      const int span = count <= kJoin ? count : static_cast<int>(ceilf(sqrtf(static_cast<float>(count))));
+      const int groups = (count + span - 1) / span;
+      int from = me / span * span, n_in = min(span, count - from), apart_in = 1;
+      int* counter = groups == 1 ? a.counters + static_cast<long long>(seq) * heads + head : a.counters_in + place(from);
+      for (;;) {
+        __threadfence();
+        compute_sync();
+        if (tid == 0) {
+          const int done = atomicAdd(counter, 1);
+          s_last = done == n_in - 1;
+          if (done == n_in - 1) *counter = 0;
+        }
+        compute_sync();
+        if (!s_last) break;
+        __threadfence();
+        const bool final = apart_in > 1 || groups == 1;
+        // The pieces' weights, a warp for every other head, a lane for each piece.
+        for (int h = warp; h < a.group; h += kComputeWarps) {
+          const float* at = a.partial + place(from + min(lane, n_in - 1) * apart_in) * piece_floats + kDecodeHeads * D + h;
+          const float pm = lane < n_in ? __ldcg(at) : -INFINITY;
+          float top = pm;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          const float w = lane < n_in ? exp2_approx(pm - (top == -INFINITY ? 0.0f : top)) : 0.0f;
+          float sum = lane < n_in ? w * __ldcg(at + kDecodeHeads) : 0.0f;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          s_weight[h][lane] = w;
+          if (lane == 0) {
+            s_join[h][0] = top;
+            s_join[h][1] = sum;
+          }
+        }
+        compute_sync();
+        constexpr int kE = kDecodeHeads * D / 4 / (kComputeWarps * 32);
+        float4 acc[kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+        for (int x = 0; x < n_in; ++x) {
+          const float* at = a.partial + place(from + x * apart_in) * piece_floats;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const int i = tid + e * kComputeWarps * 32, h = i / (D / 4);
+            if (h >= a.group) continue;
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(at + 4 * i));
+            const float w = s_weight[h][x];
+            acc[e].x = fmaf(w, y.x, acc[e].x);
+            acc[e].y = fmaf(w, y.y, acc[e].y);
+            acc[e].z = fmaf(w, y.z, acc[e].z);
+            acc[e].w = fmaf(w, y.w, acc[e].w);
+          }
+        }
+        float* group_piece = a.partial + place(from) * piece_floats;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const int i = tid + e * kComputeWarps * 32, h = i / (D / 4);
+          if (h >= a.group) continue;
+          if (final) {
+            const float sum = s_join[h][1], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            *reinterpret_cast<uint2*>(a.out + to * D + 4 * i) = make_uint2(
+                pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
+          } else {
+            *reinterpret_cast<float4*>(group_piece + 4 * i) = acc[e];
+          }
+        }
+        if (tid < a.group) {
+          const float top = s_join[tid][0], sum = s_join[tid][1];
+          if (!final) {
+            group_piece[kDecodeHeads * D + tid] = top;
+            group_piece[kDecodeHeads * D + kDecodeHeads + tid] = sum;
+          } else if (a.lse) {
+            a.lse[to + tid] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147181f;
+          }
+        }
+        compute_sync();
+        if (final) break;
+        counter = a.counters + static_cast<long long>(seq) * heads + head;
+        from = 0;
+        n_in = groups;
+        apart_in = span;
       }
     }
     pos += n;
