@@ -10,21 +10,26 @@
 // that finishes it last, from fp32 pieces (unnormalised output, maximum, sum) in the order of the tiles:
 // whichever CTA that is, the sums are the same.
 //
-// A CTA: warp 4 loads, TMA boxes of one page's rows (128-byte swizzle) into a ring of units, one unit the
-// keys or the values of a tile; warps 0..3 compute with mma.sync, the keys as the rows of the products
+// A CTA: warp 8 loads, TMA boxes of one page's rows (128-byte swizzle) into a ring of units, one unit the
+// keys or the values of a tile; warps 0..7 compute with mma.sync, the keys as the rows of the products
 // (S^T = K Q^T, then O^T = V^T P^T), so the eight heads are the narrow side and nothing is padded to
-// 16 query rows. Each warp takes S of its own keys (of half the width where a tile has only 32 or the
-// width is 512), all exchange S through shared memory, and each forms all of P in the layout the second
-// product reads, and multiplies its own quarter of V's width: one barrier per tile, no output to be
-// joined between warps, and P^T needs no transpose.
+// 16 query rows. For S the tile's keys are shared out over the warps, 16 to a warp; where a tile has
+// fewer than 128, several warps take a part of the width each and add their S in shared memory. P goes
+// through shared memory to all warps, each of which multiplies its own eighth of V's width: no output
+// is joined between warps.
 //
-// Softmax: one pass, running maximum m and sum l in fp32 and base 2; P is rounded to bf16 for the product
-// with V (half a step is 2^-8 of each weight; l adds the unrounded ones).
+// Softmax: one pass in base 2. The weights are exp2(s - M) with a reference M that all warps share and
+// that moves (to the maximum so far, with the outputs and sums rescaled) only when a score passes it
+// by more than 8: a tile then costs one barrier, which also tells every warp whether a score did.
+// Weights are so at most 2^8, kept in fp32 for the sum l, and rounded to 16 bits for the product with V.
 //
-// e4m3: the keys meet the queries as e4m3, each query value as the sum of two e4m3 numbers (its leading
-// and next four bits; the row is scaled by a power of two to at most 256, so what two numbers lose lies
-// 2^-18 below the row's largest magnitude). The key's scale multiplies S, the value's scale P. Value codes
-// become bf16 by moving their bits and a multiplication by 2^120, exactly.
+// e4m3: codes are exact in fp16, so both products run in fp16. A row of queries is scaled by a power of
+// two to at most 2^15, where fp16 holds all of bf16's bits down to 2^-29 below the row's largest
+// magnitude; the key's scale multiplies S. The weights carry the value's scale in their exponent,
+// exp2(s + log2(scale) - R) with a reference R of their own that keeps the largest between 2^7 and 2^15:
+// fp16's half step (2^-11)
+// holds down to 2^-21 below that, and what is lost under it is at most 2^-32 of the largest per key.
+// (mma.sync on e4m3 itself, with queries split in two e4m3 parts, was slower: 100 us against XX.)
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -36,7 +41,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kComputeWarps = 4;
+constexpr int kComputeWarps = 8;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 
 template <int D, bool E4M3>
@@ -45,18 +50,19 @@ struct Dec {
   // Positions per tile: a unit of 32 KB (16 KB for e4m3 rows of 128), three of them (six) per CTA, so
   // that 64 KB and more per CTA are on their way while a tile is computed.
   static constexpr int KT = E4M3 ? (D == 512 ? 64 : 128) : 16384 / D;
-  static constexpr int KG = D == 512 ? 2 : 4;                        // warps along the keys, for S
+  static constexpr int KG = KT / 16 < kComputeWarps ? KT / 16 : kComputeWarps;  // warps along the keys, for S
   static constexpr int DS = kComputeWarps / KG;                      // warps along the width, for S
-  static constexpr int MT = KT / (16 * KG);                          // 16-key blocks per warp, for S
   static constexpr int kUnit = KT * kRow;
   static constexpr int kUnits = 98304 / kUnit;
   static constexpr int kSteps = kRow / 32 / DS;                      // 32-byte steps of a key row per warp
-  static constexpr int kQRegs = kSteps * 2 * (E4M3 ? 2 : 1);
-  static constexpr int VT = D / 64;                                  // 16-wide blocks of V per warp
+  static constexpr int kQRegs = D / DS / 8;
+  static constexpr int VT = D / (16 * kComputeWarps);                // 16-wide blocks of V per warp
   static constexpr int SP = KT + 4;                                  // row pitch of S, in floats
-  static constexpr int kSBytes = 2 * DS * kDecodeHeads * SP * 4;
+  static constexpr int PP = KT + 8;                                  // row pitch of P, in 16-bit values
+  static constexpr int kSBytes = DS > 1 ? DS * kDecodeHeads * SP * 4 : 0;
+  static constexpr int kPBytes = 2 * kDecodeHeads * PP * 2;
   static constexpr int kScaleBytes = E4M3 ? kUnits * KT * 4 : 0;
-  static constexpr int kSmem = 1024 + kUnits * kUnit + kSBytes + kScaleBytes + 256;
+  static constexpr int kSmem = 1024 + kUnits * kUnit + kSBytes + kPBytes + kScaleBytes + 256;
   static_assert(kSmem <= 115712, "two CTAs to an SM");
 };
 
@@ -80,6 +86,10 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ void ldsm2_trans(uint32_t addr, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr) : "memory");
+}
+
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -87,11 +97,9 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -99,32 +107,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// Two e4m3 codes in the high bytes of w's halves, as bf16: sign, exponent and fraction move to bf16's
-// fields, where the exponent reads 120 too low.
-__device__ __forceinline__ uint32_t widen_e4m3(uint32_t w) {
-  const uint32_t t = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-  __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&t);
-  const uint32_t f = 0x7b807b80u;  // 2^120
-  v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&f));
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The leading (or, with the leading part taken off, the next) e4m3 parts of four values.
-__device__ __forceinline__ uint32_t e4m3_part(float (&x)[4]) {
-  uint32_t codes = 0;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * j], x[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-    codes |= static_cast<uint32_t>(c) << (16 * j);
-    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-    x[2 * j] -= back.x;
-    x[2 * j + 1] -= back.y;
-  }
-  return codes;
+// Four e4m3 codes as two pairs of fp16, exactly.
+__device__ __forceinline__ void widen_e4m3(uint32_t y, uint32_t& even, uint32_t& odd) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(even), "=r"(odd)
+      : "r"(y));
 }
 
-// The four computing warps.
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The computing warps.
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The same, with the disjunction of a condition.
+__device__ __forceinline__ bool compute_sync_or(bool c) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(c ? 1 : 0)
+      : "memory");
+  return r != 0;
+}
 
 constexpr int kJoin = 24;  // pieces joined at once, at most 32
 
@@ -161,11 +171,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* s_buf = reinterpret_cast<float*>(ring + C::kUnits * C::kUnit);
-  float* scale_buf = s_buf + C::kSBytes / 4;
+  uint16_t* p_buf = reinterpret_cast<uint16_t*>(s_buf + C::kSBytes / 4);
+  float* scale_buf = reinterpret_cast<float*>(p_buf + C::kPBytes / 2);
   uint64_t* full = reinterpret_cast<uint64_t*>(scale_buf + C::kScaleBytes / 4);
   uint64_t* empty = full + C::kUnits;
   __shared__ volatile int abort_flag;
   __shared__ int s_last;
+  __shared__ float s_top[kComputeWarps][kDecodeHeads], s_vtop[kComputeWarps][kDecodeHeads];
   __shared__ float s_weight[kDecodeHeads][32], s_join[kDecodeHeads][2];
   __shared__ long long s_sum[kThreads / 32], s_total, s_before;
   __shared__ int s_seq;
@@ -373,18 +385,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // A power of two that brings the largest magnitude into [128, 256); NaN for a row with one.
+        // A power of two that brings the largest magnitude into [2^14, 2^15); NaN for a row with one.
         const int e = static_cast<int>(top >> 23);
-        const float up = e == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(min(261 - e, 254)) << 23);
-        const float down = in_log2 * (e == 255 ? up : __uint_as_float(static_cast<uint32_t>(max(e - 7, 0)) << 23));
-        const float undo = e < 8 ? in_log2 / up : down;
+        const float up = e == 255 ? __uint_as_float(0x7fffffffu)
+                                  : __uint_as_float(static_cast<uint32_t>(min(268 - e, 254)) << 23);
+        const float undo = in_log2 / up;
+        // The products' 16 dimensions per step: this lane's four in a row, as a key's bytes are loaded.
 #pragma unroll
         for (int s = 0; s < 2 * C::kSteps; ++s) {
           const uint2 w = *reinterpret_cast<const uint2*>(qp + 16 * s + 4 * c4);
-          float x[4] = {__uint_as_float(w.x << 16) * up, __uint_as_float(w.x & 0xffff0000u) * up,
-                        __uint_as_float(w.y << 16) * up, __uint_as_float(w.y & 0xffff0000u) * up};
-          q[s] = e4m3_part(x);
-          q[2 * C::kSteps + s] = e4m3_part(x);
+          q[2 * s] = pack_f16(__uint_as_float(w.x << 16) * up, __uint_as_float(w.x & 0xffff0000u) * up);
+          q[2 * s + 1] = pack_f16(__uint_as_float(w.y << 16) * up, __uint_as_float(w.y & 0xffff0000u) * up);
         }
         qs[0] = __shfl_sync(0xffffffffu, undo, 8 * c4);
         qs[1] = __shfl_sync(0xffffffffu, undo, 8 * c4 + 4);
@@ -393,171 +404,233 @@ __global__ void __launch_bounds__(kThreads, 2)
     float o[C::VT][4];
 #pragma unroll
     for (int v = 0; v < C::VT; ++v) o[v][0] = o[v][1] = o[v][2] = o[v][3] = 0.0f;
-    float m = -INFINITY, l = 0.0f;  // of head r8; l of this lane's keys
+    // Of heads 2 c4 and 2 c4 + 1: the references, and this lane's part of the sums.
+    float ref[2] = {-INFINITY, -INFINITY}, vref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
     for (int i = i0; i < i0 + n; ++i) {
       const int tile = i < t.front ? i : i + t.skip;
       const bool masked = !(tile * KT + KT - 1 <= t.span.p &&
                             (tile * KT >= t.span.lo || tile * KT + KT <= t.span.sinks));
-      // S^T of this warp's keys.
-      float s[C::MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[mt][0][x] = s[mt][1][x] = 0.0f;
+      // S^T of this warp's 16 keys, over its part of the width.
+      float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
       mbar_wait_bounded(&full[unit], phase, &abort_flag, a.status, kStatusWaitFull);
       {
-        const uint32_t base = smem_u32(ring + unit * C::kUnit);
+        const int key = kg * 16 + (lane & 15);
+        const uint32_t row = smem_u32(ring + unit * C::kUnit) + (key >> rows_log2) * (C::kRow << rows_log2) +
+                             (key & (R - 1)) * 128;
+        const uint32_t swz = (key & 7) << 4;
 #pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt) {
-          const int key = (kg * C::MT + mt) * 16 + (lane & 15);
-          const uint32_t row = base + (key >> rows_log2) * (C::kRow << rows_log2) + (key & (R - 1)) * 128;
-          const uint32_t swz = (key & 7) << 4;
-#pragma unroll
-          for (int st = 0; st < C::kSteps; ++st) {
-            const uint32_t x = ds * (C::kRow / C::DS) + st * 32;
-            uint32_t f[4];
-            ldsm4(row + ((x >> 7) << (7 + rows_log2)) + (((x & 127) + ((lane >> 4) << 4)) ^ swz), f);
-            if constexpr (E4M3) {
-              mma_e4m3(s[mt][0], f, q[2 * st], q[2 * st + 1]);
-              mma_e4m3(s[mt][1], f, q[2 * C::kSteps + 2 * st], q[2 * C::kSteps + 2 * st + 1]);
-            } else {
-              mma_bf16(s[mt][st & 1], f, q[2 * st], q[2 * st + 1]);
-            }
+        for (int st = 0; st < C::kSteps; ++st) {
+          const uint32_t x = ds * (C::kRow / C::DS) + st * 32;
+          uint32_t f[4];
+          ldsm4(row + ((x >> 7) << (7 + rows_log2)) + (((x & 127) + ((lane >> 4) << 4)) ^ swz), f);
+          if constexpr (E4M3) {
+            uint32_t f0[4], f1[4];
+            widen_e4m3(f[0], f0[0], f0[2]);
+            widen_e4m3(f[1], f0[1], f0[3]);
+            widen_e4m3(f[2], f1[0], f1[2]);
+            widen_e4m3(f[3], f1[1], f1[3]);
+            mma_f16(s[0], f0, q[4 * st], q[4 * st + 1]);
+            mma_f16(s[1], f1, q[4 * st + 2], q[4 * st + 3]);
+          } else {
+            mma_bf16(s[st & 1], f, q[2 * st], q[2 * st + 1]);
           }
         }
       }
-      float* sb = s_buf + flip * (C::DS * kDecodeHeads * C::SP);
-#pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt) {
-        const int key = (kg * C::MT + mt) * 16 + r8;
-        float f0 = 1.0f, f1 = 1.0f;
-        if constexpr (E4M3) {
-          f0 = scale_buf[unit * KT + key];
-          f1 = scale_buf[unit * KT + key + 8];
-        }
-        float* to = sb + (ds * kDecodeHeads + 2 * c4) * C::SP + key;
-        to[0] = (s[mt][0][0] + s[mt][1][0]) * (qs[0] * f0);
-        to[C::SP] = (s[mt][0][1] + s[mt][1][1]) * (qs[1] * f0);
-        to[8] = (s[mt][0][2] + s[mt][1][2]) * (qs[0] * f1);
-        to[C::SP + 8] = (s[mt][0][3] + s[mt][1][3]) * (qs[1] * f1);
+      // The scores this lane weighs: of two heads, keys k0 and k0 + 8, or k0 alone where S is joined.
+      constexpr int kMine = C::DS > 1 ? 1 : 2;
+      const int k0 = C::DS > 1 ? warp * 8 + r8 : kg * 16 + r8;
+      const bool active = C::DS == 1 || warp * 8 < KT;
+      float f0 = 1.0f, f1 = 1.0f;
+      if constexpr (E4M3) {
+        f0 = scale_buf[unit * KT + kg * 16 + r8];
+        f1 = scale_buf[unit * KT + kg * 16 + r8 + 8];
       }
+      float x[kMine][2];  // scores in base 2
+      const float x00 = (s[0][0] + s[1][0]) * (qs[0] * f0), x01 = (s[0][1] + s[1][1]) * (qs[1] * f0);
+      const float x10 = (s[0][2] + s[1][2]) * (qs[0] * f1), x11 = (s[0][3] + s[1][3]) * (qs[1] * f1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[unit]);
       next_unit();
-      compute_sync();
-
-      // P of every key, for head r8: this lane the keys 16 k + 2 c4 + {0, 1, 8, 9}.
-      float p[KT / 16][4];
-      float mx = -INFINITY;
+      if constexpr (C::DS > 1) {
+        float* to = s_buf + (ds * kDecodeHeads + 2 * c4) * C::SP + kg * 16 + r8;
+        to[0] = x00;
+        to[C::SP] = x01;
+        to[8] = x10;
+        to[C::SP + 8] = x11;
+        compute_sync();
+        x[0][0] = x[0][1] = 0.0f;
+        if (active) {
 #pragma unroll
-      for (int k = 0; k < KT / 16; ++k) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float* from = sb + r8 * C::SP + 16 * k + 8 * half + 2 * c4;
-          float2 v = *reinterpret_cast<const float2*>(from);
-          if constexpr (C::DS == 2) {
-            const float2 w = *reinterpret_cast<const float2*>(from + kDecodeHeads * C::SP);
-            v.x += w.x;
-            v.y += w.y;
+          for (int part = 0; part < C::DS; ++part) {
+            x[0][0] += s_buf[(part * kDecodeHeads + 2 * c4) * C::SP + k0];
+            x[0][1] += s_buf[(part * kDecodeHeads + 2 * c4 + 1) * C::SP + k0];
           }
-          if (masked) {
-            const int at = tile * KT + 16 * k + 8 * half + 2 * c4;
-            if (at > t.span.p || (at < t.span.lo && at >= t.span.sinks)) v.x = -INFINITY;
-            if (at + 1 > t.span.p || (at + 1 < t.span.lo && at + 1 >= t.span.sinks)) v.y = -INFINITY;
-          }
-          p[k][2 * half] = v.x;
-          p[k][2 * half + 1] = v.y;
-          mx = fmaxf(mx, fmaxf(v.x, v.y));
         }
+      } else {
+        x[0][0] = x00;
+        x[0][1] = x01;
+        x[1][0] = x10;
+        x[1][1] = x11;
       }
+      // The values' scales, in base 2.
+      float lv[kMine];
+      if constexpr (E4M3) {
+        mbar_wait_bounded(&full[unit], phase, &abort_flag, a.status, kStatusWaitFull);
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) lv[r] = active ? log2f(scale_buf[unit * KT + k0 + 8 * r]) : 0.0f;
+      }
+      bool hidden[kMine];
+#pragma unroll
+      for (int r = 0; r < kMine; ++r) {
+        const int at = tile * KT + k0 + 8 * r;
+        hidden[r] = !active || (masked && (at > t.span.p || (at < t.span.lo && at >= t.span.sinks)));
+        if (hidden[r]) x[r][0] = x[r][1] = -INFINITY;
+        if (E4M3 && hidden[r]) lv[r] = 0.0f;
+      }
+      uint16_t* pb = p_buf + flip * (kDecodeHeads * C::PP);
       flip ^= 1;
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // The maximum drops a NaN, and stays -inf where no score is a number yet; 0 stands in for it.
-      const float m1 = fmaxf(m, mx), base = m1 == -INFINITY ? 0.0f : m1;
-      const float f = exp2_approx(m - base);
-      m = m1;
-      l *= f;
-      float sum = 0.0f;
+      // A reference of -inf (nothing but NaN or -inf so far) counts as 0.
+      auto weigh = [&](float (&sum)[2]) {
+        const float base[2] = {ref[0] == -INFINITY ? 0.0f : ref[0], ref[1] == -INFINITY ? 0.0f : ref[1]};
+        const float vbase[2] = {vref[0] == -INFINITY ? 0.0f : vref[0], vref[1] == -INFINITY ? 0.0f : vref[1]};
+        sum[0] = sum[1] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < KT / 16; ++k)
+        for (int r = 0; r < kMine; ++r)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          p[k][x] = exp2_approx(p[k][x] - base);
-          sum += p[k][x];
+          for (int h = 0; h < 2; ++h) {
+            const float w = exp2_approx(x[r][h] - base[h]);
+            sum[h] += w;
+            uint16_t bits;
+            if constexpr (E4M3) bits = __half_as_ushort(__float2half_rn(exp2_approx(x[r][h] + lv[r] - vbase[h])));
+            else bits = f32_to_bf16_rn(w);
+            if (active) pb[(2 * c4 + h) * C::PP + k0 + 8 * r] = bits;
+          }
+      };
+      bool over = false;
+#pragma unroll
+      for (int r = 0; r < kMine; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          over |= x[r][h] > ref[h] + 8.0f;
+          if constexpr (E4M3) over |= x[r][h] + lv[r] > vref[h] + 15.0f;
         }
-      l += sum;
-      if (__any_sync(0xffffffffu, f != 1.0f)) {
-        const float f0 = __shfl_sync(0xffffffffu, f, 8 * c4), f1 = __shfl_sync(0xffffffffu, f, 8 * c4 + 4);
+      float sum[2];
+      weigh(sum);
+      if (compute_sync_or(over)) {
+        float top[2] = {x[0][0], x[0][1]}, vtop[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (kMine > 1) top[h] = fmaxf(top[h], x[kMine - 1][h]);
+          if constexpr (E4M3)
+#pragma unroll
+            for (int r = 0; r < kMine; ++r) vtop[h] = fmaxf(vtop[h], x[r][h] + lv[r]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], d));
+            if constexpr (E4M3) vtop[h] = fmaxf(vtop[h], __shfl_xor_sync(0xffffffffu, vtop[h], d));
+          }
+          if (r8 == 0) {
+            s_top[warp][2 * c4 + h] = top[h];
+            if constexpr (E4M3) s_vtop[warp][2 * c4 + h] = vtop[h];
+          }
+        }
+        compute_sync();
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float m = ref[h], vm = vref[h] + 7.0f;
+          for (int w = 0; w < kComputeWarps; ++w) {
+            m = fmaxf(m, s_top[w][2 * c4 + h]);
+            if constexpr (E4M3) vm = fmaxf(vm, s_vtop[w][2 * c4 + h]);
+          }
+          f[h] = exp2_approx(ref[h] - (m == -INFINITY ? 0.0f : m));
+          l[h] *= f[h];
+          ref[h] = m;
+          if constexpr (E4M3) {
+            vm -= 7.0f;
+            f[h] = exp2_approx(vref[h] - (vm == -INFINITY ? 0.0f : vm));
+            vref[h] = vm;
+          }
+        }
 #pragma unroll
         for (int v = 0; v < C::VT; ++v) {
-          o[v][0] *= f0;
-          o[v][1] *= f1;
-          o[v][2] *= f0;
-          o[v][3] *= f1;
+          o[v][0] *= f[0];
+          o[v][1] *= f[1];
+          o[v][2] *= f[0];
+          o[v][3] *= f[1];
         }
+        weigh(sum);
+        compute_sync();
       }
+      l[0] += sum[0];
+      l[1] += sum[1];
 
-      // O^T += V^T P^T over this warp's quarter of the width.
-      mbar_wait_bounded(&full[unit], phase, &abort_flag, a.status, kStatusWaitFull);
+      // O^T += V^T P^T over this warp's part of the width.
+      if constexpr (!E4M3) mbar_wait_bounded(&full[unit], phase, &abort_flag, a.status, kStatusWaitFull);
       const uint32_t vbase = smem_u32(ring + unit * C::kUnit);
+      const uint32_t paddr = smem_u32(pb) + ((lane & 7) * C::PP + (lane >> 3) * 8) * 2;
 #pragma unroll
-      for (int k = 0; k < KT / 16; ++k) {
-        uint32_t b0, b1, keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if constexpr (E4M3) {
-          const float* vs = scale_buf + unit * KT + 16 * k + 2 * c4;
-          // Hidden keys: a weight of 0 whatever the scale that lies there.
-          float w[4];
+      for (int k2 = 0; k2 < KT / 32; ++k2) {
+        uint32_t pr[4];
+        ldsm4(paddr + k2 * 64, pr);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = p[k][x] == 0.0f ? 0.0f : p[k][x] * vs[(x & 1) + 8 * (x >> 1)];
-          b0 = pack_bf16(w[0], w[1]);
-          b1 = pack_bf16(w[2], w[3]);
-        } else {
-          b0 = pack_bf16(p[k][0], p[k][1]);
-          b1 = pack_bf16(p[k][2], p[k][3]);
+        for (int kk = 0; kk < 2; ++kk) {
+          const int k = 2 * k2 + kk;
+          const uint32_t b0 = pr[2 * kk], b1 = pr[2 * kk + 1];
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (masked) {
             // Hidden values may be anything, NaN included: they become 0.
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int at = tile * KT + 16 * k + 2 * c4 + (x & 1) + 8 * (x >> 1);
-              const uint32_t gone = at > t.span.p || (at < t.span.lo && at >= t.span.sinks) ? 0xffffu << (16 * (x & 1)) : 0u;
-              if (x < 2) keep0 &= ~gone;
+            for (int y = 0; y < 4; ++y) {
+              const int at = tile * KT + 16 * k + 2 * c4 + (y & 1) + 8 * (y >> 1);
+              const uint32_t gone = at > t.span.p || (at < t.span.lo && at >= t.span.sinks) ? 0xffffu << (16 * (y & 1)) : 0u;
+              if (y < 2) keep0 &= ~gone;
               else keep1 &= ~gone;
             }
           }
-        }
-        const int key = 16 * k + (lane & 7) + (E4M3 ? (lane & 8) : (lane & 16) >> 1);
-        const uint32_t row = vbase + (key >> rows_log2) * (C::kRow << rows_log2) + (key & (R - 1)) * 128;
-        const uint32_t swz = (key & 7) << 4;
-        if constexpr (E4M3) {
-          // A 16-byte piece is 16 dimensions; as 16-bit pairs the transposed load gives a lane the
-          // dimensions 2 r8 and 2 r8 + 1, which become the rows r8 and r8 + 8 of the block.
+          const int key = 16 * k + (lane & 7) + (E4M3 ? (lane & 8) : (lane & 16) >> 1);
+          const uint32_t row = vbase + (key >> rows_log2) * (C::kRow << rows_log2) + (key & (R - 1)) * 128;
+          const uint32_t swz = (key & 7) << 4;
+          if constexpr (E4M3) {
+            // A 16-byte piece is 16 dimensions; as 16-bit pairs the transposed load gives a lane the
+            // dimensions 2 r8 and 2 r8 + 1, which become the rows r8 and r8 + 8 of the block.
 #pragma unroll
-          for (int v = 0; v < C::VT; v += 2) {
-            const uint32_t x = warp * (D / 4) + v * 16;
-            uint32_t w[4];
-            ldsm4_trans(row + ((x >> 7) << (7 + rows_log2)) + (((x & 127) + (lane & 16)) ^ swz), w);
+            for (int v = 0; v < C::VT; v += 2) {
+              const uint32_t xb = warp * (D / kComputeWarps) + v * 16;
+              uint32_t w[4];
+              const uint32_t at = row + ((xb >> 7) << (7 + rows_log2));
+              if constexpr (C::VT > 1) ldsm4_trans(at + (((xb & 127) + (lane & 16)) ^ swz), w);
+              else ldsm2_trans(at + ((xb & 127) ^ swz), w[0], w[1]);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t fr[4] = {widen_e4m3(w[2 * y] << 8), widen_e4m3(w[2 * y]), widen_e4m3(w[2 * y + 1] << 8),
-                                      widen_e4m3(w[2 * y + 1])};
-              mma_bf16(o[v + y], fr, b0, b1);
+              for (int y = 0; y < (C::VT > 1 ? 2 : 1); ++y) {
+                uint32_t fr[4];
+                // Bytes: d and d + 1 of one key, then of the next.
+                widen_e4m3(__byte_perm(w[2 * y], 0, 0x3120), fr[0], fr[1]);
+                widen_e4m3(__byte_perm(w[2 * y + 1], 0, 0x3120), fr[2], fr[3]);
+                if (masked) {
+                  fr[0] &= keep0;
+                  fr[1] &= keep0;
+                  fr[2] &= keep1;
+                  fr[3] &= keep1;
+                }
+                mma_f16(o[v + y], fr, b0, b1);
+              }
             }
-          }
-        } else {
+          } else {
 #pragma unroll
-          for (int v = 0; v < C::VT; ++v) {
-            const uint32_t x = (warp * (D / 4) + v * 16) * 2;
-            uint32_t w[4];
-            ldsm4_trans(row + ((x >> 7) << (7 + rows_log2)) + (((x & 127) + ((lane & 8) << 1)) ^ swz), w);
-            if (masked) {
-              w[0] &= keep0;
-              w[1] &= keep0;
-              w[2] &= keep1;
-              w[3] &= keep1;
+            for (int v = 0; v < C::VT; ++v) {
+              const uint32_t xb = (warp * (D / kComputeWarps) + v * 16) * 2;
+              uint32_t w[4];
+              ldsm4_trans(row + ((xb >> 7) << (7 + rows_log2)) + (((xb & 127) + ((lane & 8) << 1)) ^ swz), w);
+              if (masked) {
+                w[0] &= keep0;
+                w[1] &= keep0;
+                w[2] &= keep1;
+                w[3] &= keep1;
+              }
+              mma_bf16(o[v], w, b0, b1);
             }
-            mma_bf16(o[v], w, b0, b1);
           }
         }
       }
@@ -566,17 +639,37 @@ __global__ void __launch_bounds__(kThreads, 2)
       next_unit();
     }
 
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    // The sums of all lanes and warps, and the outputs relative to the scores' reference.
+    float m[2] = {ref[0], ref[1]};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+      if (r8 == 0) s_top[warp][2 * c4 + h] = l[h];
+    }
+    compute_sync();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] = 0.0f;
+      for (int w = 0; w < kComputeWarps; ++w) l[h] += s_top[w][2 * c4 + h];
+      if constexpr (E4M3) {
+        const float f = vref[h] == -INFINITY ? 1.0f : exp2f(vref[h] - (m[h] == -INFINITY ? 0.0f : m[h]));
+#pragma unroll
+        for (int v = 0; v < C::VT; ++v) {
+          o[v][h] *= f;
+          o[v][2 + h] *= f;
+        }
+      }
+    }
+    compute_sync();
     const long long item_start = pos - i0;
     const long long to = static_cast<long long>(t.row) * a.q_heads + head * a.group;  // the first head's output row
     const int h0 = 2 * c4, h1 = h0 + 1;
     // The dimension of o[v][0]; o[v][2] is `apart` further.
     constexpr int apart = E4M3 ? 1 : 8;
-    const int dim0 = warp * (D / 4) + (E4M3 ? 2 * r8 : r8);
+    const int dim0 = warp * (D / kComputeWarps) + (E4M3 ? 2 * r8 : r8);
     if (i0 == 0 && n == t.count) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const float f0 = __shfl_sync(0xffffffffu, inv, 4 * h0), f1 = __shfl_sync(0xffffffffu, inv, 4 * h1);
+      const float f0 = l[0] == 0.0f ? 0.0f : 1.0f / l[0], f1 = l[1] == 0.0f ? 0.0f : 1.0f / l[1];
 #pragma unroll
       for (int v = 0; v < C::VT; ++v)
 #pragma unroll
@@ -585,8 +678,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (h < a.group)
             a.out[(to + h) * D + dim0 + v * 16 + (x >> 1) * apart] = f32_to_bf16_rn(o[v][x] * (x & 1 ? f1 : f0));
         }
-      if (a.lse && warp == 0 && c4 == 0 && r8 < a.group)
-        a.lse[to + r8] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147181f;
+      if (a.lse && warp == 0 && r8 == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (h0 + h < a.group) a.lse[to + h0 + h] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * 0.693147181f;
+      }
     } else {
       // A piece. Its place is this CTA's first if the item began before the CTA's share or with it, as
       // it did for all of the item's CTAs but its first.
@@ -605,9 +701,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int h = x & 1 ? h1 : h0;
             if (h < a.group) piece[h * D + dim0 + v * 16 + (x >> 1) * apart] = o[v][x];
           }
-        if (warp == 0 && c4 == 0) {
-          piece[kDecodeHeads * D + r8] = m;
-          piece[kDecodeHeads * D + kDecodeHeads + r8] = l;
+        if (warp == 0 && r8 == 0) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            piece[kDecodeHeads * D + h0 + h] = m[h];
+            piece[kDecodeHeads * D + kDecodeHeads + h0 + h] = l[h];
+          }
         }
       }
       // Up to kJoin pieces are joined at once; more in groups first, by each group's last CTA into the
