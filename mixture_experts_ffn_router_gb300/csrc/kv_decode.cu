@@ -136,9 +136,13 @@ __device__ __forceinline__ bool compute_sync_or(bool c) {
   return r != 0;
 }
 
+// What an item costs beside its tiles (its queries, its end), in tiles: shares are equal in units, an
+// item being kItemCost units and one for each tile. XXITEM
+constexpr int kItemCost = 2;
+
 constexpr int kJoin = 24;  // pieces joined at once, at most 32
 
-// Where a CTA's share of the tiles begins, and how a sequence's tiles lie.
+// How a sequence's tiles lie.
 struct SeqTiles {
   int row;     // the token's row
   KvSpan span;
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_wait();
   pdl_launch_dependents();
 
-  // The tiles of all sequences, and the sequence this CTA's share begins in.
+  // The units of all sequences, and the sequence this CTA's share begins in.
   const int heads = a.c.kv_heads, n_seqs = a.b.n_seqs;
   auto block_sum = [&](long long v) {  // inclusive sum over the threads; s_total: over the block
 #pragma unroll
@@ -215,12 +219,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     return before + v;
   };
-  int own = 0;  // tiles of sequence tid
+  auto units_of = [](int tiles) { return tiles > 0 ? tiles + kItemCost : 0; };
+  int own = 0;  // units of sequence tid's items, each
   long long mine = 0;
   for (int b = tid; b < n_seqs; b += kThreads) {
     const SeqTiles t = seq_tiles<KT>(a, b);
-    if (b == tid) own = t.count;
-    mine += t.count;
+    if (b == tid) own = units_of(t.count);
+    mine += units_of(t.count);
     if (t.span.p < 0 && b % gridDim.x == blockIdx.x && t.row < a.b.n_tokens && a.b.cu_q[b + 1] > t.row) {
       // A token that sees nothing.
       for (int h = 0; h < a.q_heads; ++h) {
@@ -241,8 +246,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   long long upto = block_sum(mine);
   const long long total = s_total * heads;
-  // A share is at least two tiles: below that the joining of pieces costs more than the tiles.
-  const long long ctas = min(static_cast<long long>(gridDim.x), (total + 1) / 2);
+  // A share is at least one item of one tile: below that pieces cost more than they save.
+  constexpr int kShare = kItemCost + 1;
+  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kShare - 1) / kShare);
   if (blockIdx.x >= ctas) return;
   const long long begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
   for (int base = 0;; base += kThreads) {
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (base == 0 && n_seqs <= kThreads) {
       before = 0;
     } else {
-      if (base > 0) own = base + tid < n_seqs ? seq_tiles<KT>(a, base + tid).count : 0;
+      if (base > 0) own = base + tid < n_seqs ? units_of(seq_tiles<KT>(a, base + tid).count) : 0;
       if (tid == 0 && base == 0) s_before = 0;
       upto = block_sum(own);
       before = s_before;
@@ -269,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   int seq = s_seq;
   const long long seq_start = s_sum[0];
   SeqTiles t = seq_tiles<KT>(a, seq);
-  int head = static_cast<int>((begin - seq_start) / t.count);
-  int i0 = static_cast<int>((begin - seq_start) % t.count);
+  int head = static_cast<int>((begin - seq_start) / units_of(t.count));
+  int u0 = static_cast<int>((begin - seq_start) % units_of(t.count));  // where the item goes on, in units
 
   const int rows_log2 = min(a.c.page_log2, KT == 128 ? 7 : KT == 64 ? 6 : 5);
   const int R = 1 << rows_log2;  // rows of a box
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   // Goes on to the next item, of the same sequence or of the next that has tiles.
   auto next_item = [&] {
-    i0 = 0;
+    u0 = 0;
     if (++head < heads) return;
     head = 0;
     do t = seq_tiles<KT>(a, ++seq);
@@ -297,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool alive = true;
     int issued = 0;
     for (long long pos = begin; pos < end && alive;) {
-      const int n = static_cast<int>(min(static_cast<long long>(t.count - i0), end - pos));
+      const int un = static_cast<int>(min(static_cast<long long>(units_of(t.count) - u0), end - pos));
+      const int i0 = max(u0 - kItemCost, 0), n = max(u0 + un - kItemCost, 0) - i0;
       for (int i = i0; i < i0 + n && alive; ++i) {
         const int tile = i < t.front ? i : i + t.skip;
         const int p0 = tile * KT + (lane << rows_log2);  // the first position of this lane's page part
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           next_unit();
         }
       }
-      pos += n;
+      pos += un;
       if (pos < end) next_item();
     }
     if (!alive && lane == 0) {
@@ -360,8 +367,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int kg = warp % C::KG, ds = warp / C::KG;
   const int c4 = lane & 3, r8 = lane >> 2;
   int flip = 0;
+  // Where 16 keys begin in a unit, and this lane's swizzled places in them: for S rows of keys, four
+  // 32-byte steps of a 128-byte chunk; for P V its pieces of V's rows.
+  auto block = [&](int k) {
+    return static_cast<uint32_t>(((16 * k) >> rows_log2) * (C::kRow << rows_log2) + ((16 * k) & (R - 1)) * 128);
+  };
+  constexpr int kVLoads = E4M3 && C::VT > 1 ? C::VT / 2 : C::VT;
+  uint32_t koff[4], voff[kVLoads];
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    koff[x] = block(kg) + ((ds * (C::kSteps / 4)) << (7 + rows_log2)) + (lane & 15) * 128 +
+              ((x * 32 + ((lane >> 4) << 4)) ^ ((lane & 7) << 4));
+#pragma unroll
+  for (int v = 0; v < kVLoads; ++v) {
+    const int byte = warp * (C::kRow / kComputeWarps) + v * 32;
+    const int key = (lane & 7) + (E4M3 ? lane & 8 : (lane & 16) >> 1);
+    const int piece = E4M3 ? (C::VT > 1 ? lane & 16 : 0) : (lane & 8) << 1;
+    voff[v] = ((byte >> 7) << (7 + rows_log2)) + key * 128 + (((byte & 127) + piece) ^ ((lane & 7) << 4));
+  }
   for (long long pos = begin; pos < end;) {
-    const int n = static_cast<int>(min(static_cast<long long>(t.count - i0), end - pos));
+    const int un = static_cast<int>(min(static_cast<long long>(units_of(t.count) - u0), end - pos));
+    const int i0 = max(u0 - kItemCost, 0), n = max(u0 + un - kItemCost, 0) - i0;
+    if (n == 0) break;  // the share ends in front of the item's first tile
     // The queries as the second operand of S^T = K Q^T: lane holds head r8.
     uint32_t q[C::kQRegs];
     float qs[2];  // what S of heads 2 c4 and 2 c4 + 1 is multiplied by
@@ -415,15 +442,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
       mbar_wait_bounded(&full[unit], phase, &abort_flag, a.status, kStatusWaitFull);
       {
-        const int key = kg * 16 + (lane & 15);
-        const uint32_t row = smem_u32(ring + unit * C::kUnit) + (key >> rows_log2) * (C::kRow << rows_log2) +
-                             (key & (R - 1)) * 128;
-        const uint32_t swz = (key & 7) << 4;
+        const uint32_t base = smem_u32(ring + unit * C::kUnit);
 #pragma unroll
         for (int st = 0; st < C::kSteps; ++st) {
-          const uint32_t x = ds * (C::kRow / C::DS) + st * 32;
           uint32_t f[4];
-          ldsm4(row + ((x >> 7) << (7 + rows_log2)) + (((x & 127) + ((lane >> 4) << 4)) ^ swz), f);
+          ldsm4(base + ((st >> 2) << (7 + rows_log2)) + koff[st & 3], f);
           if constexpr (E4M3) {
             uint32_t f0[4], f1[4];
             widen_e4m3(f[0], f0[0], f0[2]);
@@ -589,19 +612,15 @@ __global__ void __launch_bounds__(kThreads, 2)
               else keep1 &= ~gone;
             }
           }
-          const int key = 16 * k + (lane & 7) + (E4M3 ? (lane & 8) : (lane & 16) >> 1);
-          const uint32_t row = vbase + (key >> rows_log2) * (C::kRow << rows_log2) + (key & (R - 1)) * 128;
-          const uint32_t swz = (key & 7) << 4;
+          const uint32_t vk = vbase + block(k);
           if constexpr (E4M3) {
             // A 16-byte piece is 16 dimensions; as 16-bit pairs the transposed load gives a lane the
             // dimensions 2 r8 and 2 r8 + 1, which become the rows r8 and r8 + 8 of the block.
 #pragma unroll
             for (int v = 0; v < C::VT; v += 2) {
-              const uint32_t xb = warp * (D / kComputeWarps) + v * 16;
               uint32_t w[4];
-              const uint32_t at = row + ((xb >> 7) << (7 + rows_log2));
-              if constexpr (C::VT > 1) ldsm4_trans(at + (((xb & 127) + (lane & 16)) ^ swz), w);
-              else ldsm2_trans(at + ((xb & 127) ^ swz), w[0], w[1]);
+              if constexpr (C::VT > 1) ldsm4_trans(vk + voff[v / 2], w);
+              else ldsm2_trans(vk + voff[0], w[0], w[1]);
 #pragma unroll
               for (int y = 0; y < (C::VT > 1 ? 2 : 1); ++y) {
                 uint32_t fr[4];
@@ -620,9 +639,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           } else {
 #pragma unroll
             for (int v = 0; v < C::VT; ++v) {
-              const uint32_t xb = (warp * (D / kComputeWarps) + v * 16) * 2;
               uint32_t w[4];
-              ldsm4_trans(row + ((xb >> 7) << (7 + rows_log2)) + (((xb & 127) + ((lane & 8) << 1)) ^ swz), w);
+              ldsm4_trans(vk + voff[v], w);
               if (masked) {
                 w[0] &= keep0;
                 w[1] &= keep0;
@@ -662,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     compute_sync();
-    const long long item_start = pos - i0;
+    const long long item_start = pos - u0;
     const long long to = static_cast<long long>(t.row) * a.q_heads + head * a.group;  // the first head's output row
     const int h0 = 2 * c4, h1 = h0 + 1;
     // The dimension of o[v][0]; o[v][2] is `apart` further.
@@ -686,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
       // A piece. Its place is this CTA's first if the item began before the CTA's share or with it, as
       // it did for all of the item's CTAs but its first.
-      const int first = static_cast<int>(((item_start + 1) * ctas - 1) / total);
-      const int count = static_cast<int>(((item_start + t.count) * ctas - 1) / total) - first + 1;
+      const int first = static_cast<int>(((item_start + kItemCost + 1) * ctas - 1) / total);
+      const int count = static_cast<int>(((item_start + kItemCost + t.count) * ctas - 1) / total) - first + 1;
       const int first_place = 2 * first + (first * total / ctas >= item_start ? 0 : 1);
       auto place = [&](int x) { return x == 0 ? first_place : 2 * (first + x); };  // of the item's piece x
       constexpr long long piece_floats = decode_piece_floats(D);
@@ -795,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         apart_in = span;
       }
     }
-    pos += n;
+    pos += un;
     if (pos < end) next_item();
   }
 }
