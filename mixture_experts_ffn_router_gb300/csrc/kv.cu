@@ -255,6 +255,8 @@ struct moe_ffn_kv {
   int* counters;
   int* counters_in;
   float* partial;
+  KvChunkList list;
+  float* chunk_partial;
 };
 
 namespace {
@@ -328,8 +330,12 @@ size_t kv_rows_bytes(const KvRows& r, int tokens, int heads, int d) {
 
 // The workspace: control words (zeroed when the handle is made), then the kernels' pieces.
 struct KvLayout {
-  size_t status, counters, counters_in, partial, total;
+  size_t status, counters, counters_in, n_tiles, partial, first_tile, tiles, first_unit, chunk_partial, total;
 };
+
+size_t max_row_tiles(const moe_ffn_kv_config& c) {
+  return static_cast<size_t>(c.max_tokens) / chunk_tokens(c.q_heads / c.kv_heads) + c.max_seqs;
+}
 
 KvLayout make_kv_layout(const moe_ffn_kv_config& c) {
   KvLayout l;
@@ -342,7 +348,13 @@ KvLayout make_kv_layout(const moe_ffn_kv_config& c) {
   l.status = take(4);
   l.counters = take(static_cast<size_t>(c.max_seqs) * c.kv_heads * 4);
   l.counters_in = take(2 * kDecodeMaxCtas * 4);
+  l.n_tiles = take(4);
   l.partial = take(static_cast<size_t>(2 * kDecodeMaxCtas * decode_piece_floats(c.head_dim)) * 4);
+  const size_t tiles = max_row_tiles(c);
+  l.first_tile = take(static_cast<size_t>(c.max_seqs) * 4);
+  l.tiles = take(tiles * sizeof(KvRowTile));
+  l.first_unit = take((tiles + 1) * 8);
+  l.chunk_partial = take(static_cast<size_t>(2 * kChunkMaxCtas * kChunkPieceFloats) * 4);
   l.total = o;
   return l;
 }
@@ -388,7 +400,13 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   kv->counters = reinterpret_cast<int*>(kv->ws + l.counters);
   kv->counters_in = reinterpret_cast<int*>(kv->ws + l.counters_in);
   kv->partial = reinterpret_cast<float*>(kv->ws + l.partial);
-  if (kv_decode_setup() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  kv->list.first_tile = reinterpret_cast<int*>(kv->ws + l.first_tile);
+  kv->list.tiles = reinterpret_cast<KvRowTile*>(kv->ws + l.tiles);
+  kv->list.first_unit = reinterpret_cast<long long*>(kv->ws + l.first_unit);
+  kv->list.n_tiles = reinterpret_cast<int*>(kv->ws + l.n_tiles);
+  kv->list.max_tiles = static_cast<int>(max_row_tiles(*cfg));
+  kv->chunk_partial = reinterpret_cast<float*>(kv->ws + l.chunk_partial);
+  if (kv_decode_setup() != cudaSuccess || kv_chunk_setup() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     delete kv;
     return MOE_FFN_ECUDA;
   }
@@ -456,11 +474,15 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   a.counters = kv->counters;
   a.counters_in = kv->counters_in;
   a.partial = kv->partial;
+  a.list = kv->list;
+  a.chunk_partial = kv->chunk_partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int ctas = 2 * kv->num_sms < kDecodeMaxCtas ? 2 * kv->num_sms : kDecodeMaxCtas;
-  const cudaError_t e = a.b.max_new <= 1 && a.group <= kDecodeHeads ? launch_kv_decode(a, ctas, s)
-                                                                    : launch_kv_attention(a, s);
+  const int sms = kv->num_sms < kChunkMaxCtas ? kv->num_sms : kChunkMaxCtas;
+  cudaError_t e;
+  if (a.b.max_new <= 1 && a.group <= kDecodeHeads) e = launch_kv_decode(a, 2 * sms, s);
+  else if (!a.c.e4m3) e = launch_kv_chunk(a, sms, s);
+  else e = launch_kv_attention(a, s);
   return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
 }
 

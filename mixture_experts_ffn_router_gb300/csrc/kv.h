@@ -37,6 +37,27 @@ struct KvRows {
   long long head_stride;
 };
 
+// Up to 128 (token, query head) rows of one sequence and kv head, and the tiles of 128 keys they see.
+struct KvRowTile {
+  int seq;
+  int row0;   // first token row
+  int nt;     // tokens
+  int p0;     // position of the first (below 0: it sees nothing)
+  int front;  // tiles of the sinks, before the window's
+  int skip;   // tiles between the two
+  int count;  // tiles in all
+  int unused;
+};
+
+// The row tiles of a call, in the workspace.
+struct KvChunkList {
+  int* first_tile;        // [max_seqs] of each sequence
+  KvRowTile* tiles;
+  long long* first_unit;  // [row tiles + 1] shares of the work are counted in units, see kv_chunk.cu
+  int* n_tiles;
+  int max_tiles;          // the list's room
+};
+
 struct KvAttn {
   KvBatch b;
   KvCache c;
@@ -52,6 +73,8 @@ struct KvAttn {
   int* counters;    // [max_seqs * kv_heads] pieces finished of each item, zero between calls
   int* counters_in; // [2 * kDecodeMaxCtas] the same, of groups of an item's pieces
   float* partial;   // pieces of items that several CTAs share
+  KvChunkList list;      // the same for chunks of tokens
+  float* chunk_partial;
 };
 
 // The single-token kernel: CTAs (two to an SM), and the floats of a piece: eight heads' outputs, then
@@ -61,6 +84,12 @@ constexpr int kDecodeHeads = 8;
 __host__ __device__ constexpr long long decode_piece_floats(int head_dim) {
   return static_cast<long long>(kDecodeHeads) * head_dim + 2 * kDecodeHeads;
 }
+
+// The kernel for chunks: CTAs (one to an SM), tokens of a row tile, and the floats of a piece: 128 rows of
+// 256 (or 128) outputs, then their maxima and sums.
+constexpr int kChunkMaxCtas = 152;
+constexpr long long kChunkPieceFloats = 128 * 258;
+inline int chunk_tokens(int group) { return 128 / group; }
 
 bool encode_row_chunks(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
                        uint32_t box_chunks);
@@ -72,6 +101,8 @@ cudaError_t launch_kv_read(const KvBatch& b, const KvCache& c, uint16_t* k_out, 
 cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t s);
 cudaError_t kv_decode_setup();
 cudaError_t launch_kv_decode(const KvAttn& a, int ctas, cudaStream_t s);
+cudaError_t kv_chunk_setup();
+cudaError_t launch_kv_chunk(const KvAttn& a, int ctas, cudaStream_t s);
 
 #ifdef __CUDACC__
 // What a batch says of one sequence, with every value brought into range.

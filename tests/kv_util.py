@@ -157,7 +157,8 @@ def check_attention(case, window=0, sinks=0, scale=None, kv=None, cache=None, q=
     out, lse = kv.attention(cache, case.batch(), case.q.cuda() if q is None else q, window=window, sinks=sinks,
                             scale=scale)
     torch.cuda.synchronize()
-    assert kv.status() == (B.MOE_FFN_OK, 0)
+    rc, word = kv.status()
+    assert rc == B.MOE_FFN_OK, B.decode_status(word)
     want, wl, tol, ltol = attention(case, scale, window, sinks)
     check_close(lse, wl, ltol, "lse")
     check_close(out, want, tol, "out")
