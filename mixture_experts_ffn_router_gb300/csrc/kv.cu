@@ -257,6 +257,7 @@ struct moe_ffn_kv {
   float* partial;
   KvChunkList list;
   float* chunk_partial;
+  int chunk_pairs;  // SM pairs of the kernel for chunks
 };
 
 namespace {
@@ -354,7 +355,7 @@ KvLayout make_kv_layout(const moe_ffn_kv_config& c) {
   l.first_tile = take(static_cast<size_t>(c.max_seqs) * 4);
   l.tiles = take(tiles * sizeof(KvRowTile));
   l.first_unit = take((tiles + 1) * 8);
-  l.chunk_partial = take(static_cast<size_t>(2 * kChunkMaxCtas * kChunkPieceFloats) * 4);
+  l.chunk_partial = take(static_cast<size_t>(2 * kChunkMaxPairs * kChunkPieceFloats) * 4);
   l.total = o;
   return l;
 }
@@ -406,7 +407,7 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   kv->list.n_tiles = reinterpret_cast<int*>(kv->ws + l.n_tiles);
   kv->list.max_tiles = static_cast<int>(max_row_tiles(*cfg));
   kv->chunk_partial = reinterpret_cast<float*>(kv->ws + l.chunk_partial);
-  if (kv_decode_setup() != cudaSuccess || kv_chunk_setup() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (kv_decode_setup() != cudaSuccess || kv_chunk_setup(&kv->chunk_pairs) != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     delete kv;
     return MOE_FFN_ECUDA;
   }
@@ -478,11 +479,9 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   a.chunk_partial = kv->chunk_partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = kv->num_sms < kChunkMaxCtas ? kv->num_sms : kChunkMaxCtas;
-  cudaError_t e;
-  if (a.b.max_new <= 1 && a.group <= kDecodeHeads) e = launch_kv_decode(a, 2 * sms, s);
-  else if (!a.c.e4m3) e = launch_kv_chunk(a, sms, s);
-  else e = launch_kv_attention(a, s);
+  const int ctas = 2 * kv->num_sms < kDecodeMaxCtas ? 2 * kv->num_sms : kDecodeMaxCtas;
+  const cudaError_t e = a.b.max_new <= 1 && a.group <= kDecodeHeads ? launch_kv_decode(a, ctas, s)
+                                                                    : launch_kv_chunk(a, kv->chunk_pairs, s);
   return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
 }
 

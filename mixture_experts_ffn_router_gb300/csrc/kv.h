@@ -37,7 +37,7 @@ struct KvRows {
   long long head_stride;
 };
 
-// Up to 128 (token, query head) rows of one sequence and kv head, and the tiles of 128 keys they see.
+// Up to 256 (token, query head) rows of one sequence and kv head, and the tiles of 128 keys they see.
 struct KvRowTile {
   int seq;
   int row0;   // first token row
@@ -85,14 +85,14 @@ __host__ __device__ constexpr long long decode_piece_floats(int head_dim) {
   return static_cast<long long>(kDecodeHeads) * head_dim + 2 * kDecodeHeads;
 }
 
-// The kernel for chunks: CTAs (one to an SM), tokens of a row tile, and the floats of a piece: 128 rows of
-// 256 (or 128) outputs, then their maxima and sums.
-constexpr int kChunkMaxCtas = 152;
-constexpr long long kChunkPieceFloats = 128 * 258;
-inline int chunk_tokens(int group) { return 128 / group; }
+// The kernel for chunks: pairs of CTAs (one to an SM), tokens of a row tile, and the floats of a piece:
+// 256 rows of 256 (or 128) outputs, then their maxima and sums.
+constexpr int kChunkMaxPairs = 76;
+constexpr long long kChunkPieceFloats = 256 * 258;
+inline int chunk_tokens(int group) { return 256 / group; }
 
 bool encode_row_chunks(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
-                       uint32_t box_chunks);
+                       uint32_t box_chunks, uint32_t chunk_bytes = 128, bool swizzle = true);
 
 cudaError_t launch_kv_write(const KvBatch& b, const KvCache& c, const KvRows& k, const KvRows& v, unsigned int* status,
                             cudaStream_t s);
@@ -101,8 +101,8 @@ cudaError_t launch_kv_read(const KvBatch& b, const KvCache& c, uint16_t* k_out, 
 cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t s);
 cudaError_t kv_decode_setup();
 cudaError_t launch_kv_decode(const KvAttn& a, int ctas, cudaStream_t s);
-cudaError_t kv_chunk_setup();
-cudaError_t launch_kv_chunk(const KvAttn& a, int ctas, cudaStream_t s);
+cudaError_t kv_chunk_setup(int* pairs);
+cudaError_t launch_kv_chunk(const KvAttn& a, int pairs, cudaStream_t s);
 
 #ifdef __CUDACC__
 // What a batch says of one sequence, with every value brought into range.

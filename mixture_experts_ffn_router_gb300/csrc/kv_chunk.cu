@@ -1,12 +1,15 @@
 // kv_chunk.cu — attention of chunks of new tokens over the paged cache, on the 5th-generation tensor
 // cores (tcgen05).
 //
-// A row tile is up to 128 (token, query head) rows of one sequence that share a kv head: the group's
+// A row tile is up to 256 (token, query head) rows of one sequence that share a kv head: the group's
 // heads of a token lie next to each other, so a tile of keys and values read once serves all of them.
-// Its keys fall into tiles of 128 positions. For each:
-//   S = Q K^T    128 x 128 x D, operands in shared memory, fp32 accumulator in TMEM (two of them);
-//   P = exp2(scaled S - M) by eight warps, written over S in TMEM with 16 bits;
-//   O += P V     128 x 128 x (width), P from TMEM, V as it lies in the cache (its width is the
+// A cluster of two CTAs works on it as an SM pair (cta_group::2), 128 rows each; a key tile, 128
+// positions, is loaded by halves: each CTA holds 64 keys of K and half of the width of V, so the pair
+// reads it once. (One CTA for 128 rows, with whole tiles, was bound by its loads and by the shared
+// memory that its products read: XXPAIR.) For each key tile:
+//   S = Q K^T    256 x 128 x D, operands in shared memory, fp32 accumulator in TMEM (two of them);
+//   P = exp2(scaled S - M) by eight warps of each CTA, written over S in TMEM with 16 bits;
+//   O += P V     256 x (width) x 128, P from TMEM, V as it lies in the cache (its width is the
 //                contiguous dimension, which the MMA reads transposed), accumulator in TMEM.
 // S of the next tile is issued before P V of this one, so the tensor cores work while the softmax does.
 // O takes 256 TMEM columns beside the two S, so a head of width 512 is two items that each take
@@ -17,14 +20,15 @@
 // in fp32 and rounded to bf16 (2^-8 of each weight) for the product with V.
 //
 // Work. An item is a row tile, a kv head and a half of V's width where it has two. The key tiles of all
-// items, one after the other with kItemCost more for each item, are shared out evenly over one CTA per
-// SM, so that ragged batches, causal triangles and a few rows over a long cache all end together. Items
+// items, one after the other with kItemCost more for each item, are shared out evenly over the pairs
+// of SMs, so that ragged batches, causal triangles and a few rows over a long cache all end together. Items
 // cut by the shares leave fp32 pieces (unnormalised output, maximum, sum) that kv_chunk_join_kernel
 // adds in the order of the tiles.
 //
-// Warps: 0 loads K and V by TMA (boxes of one page's rows, 128-byte swizzle), 1 issues the MMAs, 4..11
-// are the softmax (two warps per 32 rows, each half the columns) and write the output, 12..15 bring
-// the queries into shared memory, gathered by row.
+// Warps: 0 loads K and V by TMA (boxes of one page's rows, 128-byte swizzle), 1 issues the MMAs (in the
+// pair's first CTA), 4..11 are the softmax (two warps per 32 rows, each half the columns) and write the
+// output, 12..15 bring the queries into shared memory, gathered by row. What the MMA thread waits for
+// is counted on barriers of the first CTA, which the other's warps and copies reach over the cluster.
 //
 // Hidden values. P is 0 for a key a row does not see, but 0 times a NaN or an infinity is not 0, so in
 // key tiles with hidden keys the softmax warps clear V's rows that no row of the tile sees, and
@@ -49,8 +53,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRows = 128;   // rows of a row tile
+constexpr int kRows = 128;   // rows of a row tile in a CTA
 constexpr int KT = 128;      // positions of a key tile
+constexpr int kHalfKeys = 64;  // of which a CTA holds the keys of 64
 constexpr int kChunk = 16384;  // 128 rows of 128 bytes
 constexpr int kSoftmaxWarp0 = 4, kSoftmaxWarps = 8, kAuxWarp0 = 12, kAuxWarps = 4;
 // What an item costs beside its key tiles, in key tiles.
@@ -62,16 +67,25 @@ struct Chk {
   static constexpr int DV = D < 256 ? D : 256;            // V's width of an item
   static constexpr int kHalves = D / DV;
   static constexpr int kQBytes = kRows * D * 2;           // bf16, or two e4m3 parts
-  static constexpr int kKStages = D / 128;                // stages of a key tile's K
-  static constexpr int kVStages = DV / 128;               // and V
-  static constexpr int kStage = E4M3 ? kChunk : 2 * kChunk;  // 128 dimensions of 128 rows
-  static constexpr int kStages = E4M3 ? (D == 512 ? 2 : D == 256 ? 5 : 6) : (D == 512 ? 3 : D == 256 ? 5 : 6);
-  static constexpr int kWide = E4M3 ? (D == 128 ? 3 : 2) : 0;    // stages of widened V, 32 KB each
+  // K: stages of up to two chunks of 64 rows of 128 bytes.
+  static constexpr int kKChunks = kRow == 128 || (E4M3 && D == 512) ? 1 : 2;
+  static constexpr int kKStage = kKChunks * kHalfKeys * 128;
+  static constexpr int kKTile = kRow / 128 / kKChunks;    // stages of a key tile
+  static constexpr int NK = E4M3 ? (D == 128 ? 6 : D == 256 ? 3 : 5) : (D == 512 ? 4 : 6);
+  // V: 128 rows of this CTA's half of the width. bf16: chunks of 64 dimensions; e4m3: rows of codes as
+  // they lie, and chunks of widened ones.
+  static constexpr int kVTile = DV / 128;                 // chunks of a key tile
+  static constexpr int kVBytes = E4M3 ? DV / 2 : 128;     // bytes of a loaded row
+  static constexpr int kVStage = KT * kVBytes;
+  static constexpr int kVLoads = E4M3 ? 1 : kVTile;       // loaded stages of a key tile
+  static constexpr int NV = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : (D == 512 ? 2 : D == 256 ? 4 : 6);
+  static constexpr int NW = E4M3 ? (D == 512 ? 2 : 4) : 0;
   static constexpr int kScaleBytes = E4M3 ? 2 * 2 * KT * 4 : 0;
-  static constexpr int kBarBytes = 384;
-  static constexpr int kSmem = kQBytes + kStages * kStage + kWide * 2 * kChunk + kScaleBytes + kRows * 4 + kBarBytes;
+  static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 15) + 24 + (E4M3 ? 32 : 96) + 15) / 16 * 16;
+  static constexpr int kSmem =
+      kQBytes + NK * kKStage + NV * kVStage + NW * kChunk + kScaleBytes + kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(8 * (2 * kStages + 2 * kWide + 2 + 2 + 8) + 40 + 64 <= kBarBytes, "barriers");
+  static_assert(E4M3 ? NW % kVTile == 0 : NV % kVTile == 0, "the chunks of a key tile's V lie next to each other");
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -104,14 +118,36 @@ __device__ __forceinline__ uint32_t e4m3_part(float (&x)[4]) {
   return codes;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 operands, both K-major, 32 K elements.
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// D (both CTAs' TMEM) (+)= A * B^T over 32 K elements of e4m3, A and B in shared memory, K-major.
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same over 16 K elements of 16 bits, A in each CTA's TMEM.
+__device__ __forceinline__ void umma_16_ta_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A box of one 128-byte (or narrower) chunk of rows into this CTA's shared memory, counted on the
+// barrier at shared::cluster address `bar`, which may be the other CTA's.
+__device__ __forceinline__ void tma_rows_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int row,
+                                              int chunk) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(chunk), "r"(bar)
       : "memory");
 }
 
@@ -149,6 +185,11 @@ __device__ __forceinline__ bool pair_sync_or(int pair, bool c) {
       : "memory");
   return r != 0;
 }
+// Sets bits at a shared::cluster address.
+__device__ __forceinline__ void or_shared(uint32_t addr, uint32_t bits) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(bits) : "memory");
+}
+
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 __device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 6, 128;" ::: "memory"); }
 
@@ -255,84 +296,101 @@ __device__ __forceinline__ int find_tile(const KvChunkList& l, int n_tiles, long
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_chunk_kernel(const KvAttn a, int tokens, const __grid_constant__ CUtensorMap map_k,
+    kv_chunk_kernel(const KvAttn a, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v) {
   using C = Chk<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sq = smem;
-  uint8_t* ring = sq + C::kQBytes;
-  uint8_t* wide = ring + C::kStages * C::kStage;
-  float* scales = reinterpret_cast<float*>(wide + C::kWide * 2 * kChunk);  // [2][2][KT]
-  float* exch = scales + C::kScaleBytes / 4;                              // [kRows]
-  uint64_t* full = reinterpret_cast<uint64_t*>(exch + kRows);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* wide_full = empty + C::kStages;
-  uint64_t* wide_empty = wide_full + C::kWide;
-  uint64_t* s_full = wide_empty + C::kWide;  // [2]
-  uint64_t* scale_full = s_full + 2;         // [2]
-  uint64_t* p_ready = scale_full + 2;        // [2]: a fast pair of warps may be a tile ahead of a slow one
+  uint8_t* k_ring = sq + C::kQBytes;
+  uint8_t* v_ring = k_ring + C::NK * C::kKStage;
+  uint8_t* w_ring = v_ring + C::NV * C::kVStage;
+  float* scales = reinterpret_cast<float*>(w_ring + C::NW * kChunk);  // [2][2][KT]
+  float* exch = scales + C::kScaleBytes / 4;                          // [kRows]
+  uint8_t* q_exp = reinterpret_cast<uint8_t*>(exch + kRows);          // [2][kRows] (e4m3), of alternate items
+  uint64_t* full_k = reinterpret_cast<uint64_t*>(q_exp + (E4M3 ? 2 * kRows : 0));  // first CTA's: both CTAs' keys
+  uint64_t* empty_k = full_k + C::NK;
+  uint64_t* full_v = empty_k + C::NK;    // this CTA's part
+  uint64_t* empty_v = full_v + C::NV;
+  uint64_t* full_w = empty_v + C::NV;
+  uint64_t* empty_w = full_w + C::NW;
+  uint64_t* s_full = empty_w + C::NW;    // [2]
+  uint64_t* scale_full = s_full + 2;     // [2]
+  uint64_t* scale_free = scale_full + 2;  // [2]
+  uint64_t* p_ready = scale_free + 2;    // [2], first CTA's: a fast pair of warps may be a tile ahead of a slow one
   uint64_t* o_done = p_ready + 2;
-  uint64_t* o_free = o_done + 1;
-  uint64_t* q_full = o_free + 1;
+  uint64_t* o_free = o_done + 1;         // first CTA's
+  uint64_t* q_full = o_free + 1;         // first CTA's
   uint64_t* q_free = q_full + 1;
-  uint64_t* v_loaded = q_free + 1;
-  uint64_t* drain = v_loaded + 1;
+  uint64_t* q_scaled = q_free + 1;       // [2]: the softmax may be an item behind the queries
+  uint64_t* drain = q_scaled + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* scale_step = reinterpret_cast<float*>(tmem_slot + 2);  // [2] what O is multiplied by before a tile
   float* scale_ref = scale_step + 2;  // [2] what the values' scales of a tile are relative to
-  uint32_t* aux_top = tmem_slot + 6;  // [4]
-  uint32_t* odd = tmem_slot + 10;     // [2][8] keys with values that were cleared, of alternate items
+  uint32_t* aux_top = tmem_slot + 6;  // [2][4], the tile's largest scale by warps
+  uint32_t* odd = aux_top;            // [3][8] (bf16) keys with values that either CTA cleared, of items in turn
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if ((smem_u32(smem) & 1023u) != 0) {  // what the swizzle's address bits and the descriptors rely on
+  const uint32_t rank = cluster_ctarank();
+  // What the swizzle's address bits and the descriptors rely on (the same in both CTAs).
+  const bool aligned = (smem_u32(smem) & 1023u) == 0;
+  if (!aligned) {
     if (tid == 0) atomicOr(a.status, kStatusBadSchedule);
     return;
   }
   if (tid == 0) {
     *abort_flag = 0;
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(&full_k[s], 1);
+      mbar_init(&empty_k[s], 1);
     }
-    for (int s = 0; s < C::kWide; ++s) {
-      mbar_init(&wide_full[s], kAuxWarps);
-      mbar_init(&wide_empty[s], 1);
+    for (int s = 0; s < C::NV; ++s) {
+      mbar_init(&full_v[s], 1);
+      mbar_init(&empty_v[s], E4M3 ? kAuxWarps : 1);
+    }
+    for (int s = 0; s < C::NW; ++s) {
+      mbar_init(&full_w[s], kAuxWarps);
+      mbar_init(&empty_w[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&scale_full[s], kAuxWarps);
-      mbar_init(&p_ready[s], kSoftmaxWarps);
+      mbar_init(&scale_free[s], kSoftmaxWarps);
+      mbar_init(&q_scaled[s], kAuxWarps);
+      mbar_init(&p_ready[s], 2 * kSoftmaxWarps);
     }
     mbar_init(o_done, 1);
-    mbar_init(o_free, kSoftmaxWarps);
-    mbar_init(q_full, kAuxWarps);
+    mbar_init(o_free, 2 * kSoftmaxWarps);
+    mbar_init(q_full, 2 * kAuxWarps);
     mbar_init(q_free, 1);
-    mbar_init(v_loaded, 1);
     mbar_init(drain, 1);
-    fence_barrier_init();
-    for (int i = 0; i < 16; ++i) odd[i] = 0;
+    fence_barrier_init_cluster();
+    for (int i = 0; i < (E4M3 ? 8 : 24); ++i) odd[i] = 0;
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
 
+  // Waits look at the CTA's flag first, so that all of them end soon after one has given up.
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t why) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     if (*abort_flag) return false;
-    return mbar_wait_bounded(bar, parity, abort_flag, a.status, why);
+    return mbar_wait_bounded_cluster(bar, parity, abort_flag, a.status, why);
   };
+  auto arrive_first = [&](uint64_t* bar) { mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0)); };
 
   const int n_tiles = *a.list.n_tiles;
   const int parts = a.c.kv_heads * C::kHalves;
@@ -353,11 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   constexpr int kShare = kItemCost + 1;
-  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kShare - 1) / kShare);
-  const bool busy = blockIdx.x < ctas;
-  const long long begin = busy ? blockIdx.x * total / ctas : 0, end = busy ? (blockIdx.x + 1) * total / ctas : 0;
+  const long long pairs = min(static_cast<long long>(gridDim.x / 2), (total + kShare - 1) / kShare);
+  const int me = blockIdx.x / 2;
+  const bool busy = me < pairs;
+  const long long begin = busy ? me * total / pairs : 0, end = busy ? (me + 1) * total / pairs : 0;
 
-  // The walk over this CTA's items, the same for every role.
+  // The walk over this pair's items, the same for every role.
   int entry = 0, part = 0, u0 = 0;
   long long pos = begin;
   KvRowTile t;
@@ -405,10 +464,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
-    const uint64_t policy = policy_evict_last();
-    const int np = KT >> a.c.page_log2;  // pages of a tile
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
+    // Boxes are one page's rows, or 64 of them: lane i holds the page of the tile's box i.
+    const int rows_log2 = min(a.c.page_log2, 6);
+    const int boxes = KT >> rows_log2;
+    const int box = lane & (boxes - 1);
+    const uint32_t full_k0 = mapa_shared(smem_u32(&full_k[0]), 0);
+    int ks = 0, vs = 0, k_issued = 0, v_issued = 0;
+    uint32_t k_phase = 0, v_phase = 0;
     bool alive = true;
     for (bool more = start(); more && alive; more = next()) {
       const int head = part / C::kHalves, half = part % C::kHalves;
@@ -416,97 +478,122 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int step = 0; step < 2 * n && alive; ++step) {
         const bool is_v = step == 2 * n - 1 || (step > 0 && !(step & 1));
         const int j = is_v ? step / 2 - (step & 1 ? 0 : 1) : (step + 1) / 2;
-        const int tile = tile_at(i0 + j);
-        const int first = tile * KT + ((lane & (np - 1)) << a.c.page_log2);  // first position of this lane's page
-        const bool need = lane < np && first <= t.p0 + t.nt - 1 &&
-                          (a.window == 0 || first + R - 1 > max(t.p0, 0) - a.window || first < a.sinks);
+        const int first = tile_at(i0 + j) * KT + (box << rows_log2);  // first position of the box
+        const bool need = lane < boxes && first <= t.p0 + t.nt - 1 &&
+                          (a.window == 0 || first + (1 << rows_log2) - 1 > max(t.p0, 0) - a.window || first < a.sinks);
         int page = -1;
         if (need) page = kv_page(a.b, a.c, t.seq, first >> a.c.page_log2, a.status);
         const unsigned who = __ballot_sync(0xffffffffu, page >= 0);
-        const int row = page < 0 ? 0 : (page * a.c.kv_heads + head) << a.c.page_log2;
-        constexpr int kBoxes = C::kStage / kChunk;  // chunks of a stage
-        const int from = __shfl_sync(0xffffffffu, row, lane & (np - 1));
-        const bool mine = lane < np * kBoxes && ((who >> (lane & (np - 1))) & 1);
-        const int chunk = lane / np;
-        const int stages = is_v ? C::kVStages : C::kKStages;
-        for (int st = 0; st < stages && alive; ++st) {
-          if (issued >= C::kStages) {
-            bool ok = true;
-            if (lane == 0) ok = wait(&empty[stage], phase ^ 1, kStatusWaitEmpty);
-            alive = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!alive) break;
+        int row = page < 0 ? 0 : ((page * a.c.kv_heads + head) << a.c.page_log2) + (first & (R - 1));
+        row = __shfl_sync(0xffffffffu, row, box);
+        const bool have = (who >> box) & 1;
+        if (!is_v) {
+          // This CTA's boxes, of each chunk; the first CTA's barrier counts both CTAs'.
+          const int own = boxes / 2, chunk = lane / boxes;
+          const bool mine = have && box / own == static_cast<int>(rank) && chunk < C::kKChunks;
+          for (int st = 0; st < C::kKTile; ++st) {
+            if (k_issued >= C::NK) {
+              bool ok = true;
+              if (lane == 0) ok = wait(&empty_k[ks], k_phase ^ 1, kStatusWaitEmpty);
+              alive = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+              if (!alive) break;
+            }
+            if (lane == 0 && rank == 0)
+              mbar_arrive_expect_tx(&full_k[ks], __popc(who) * static_cast<uint32_t>((128 << rows_log2) * C::kKChunks));
+            __syncwarp();
+            if (mine)
+              tma_rows_pair(smem_u32(k_ring + ks * C::kKStage + chunk * (kHalfKeys * 128) + (((box % own) << rows_log2) * 128)),
+                            &map_k, full_k0 + 8u * ks, 0, row, st * C::kKChunks + chunk);
+            ++k_issued;
+            if (++ks == C::NK) {
+              ks = 0;
+              k_phase ^= 1;
+            }
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(who) * static_cast<uint32_t>(R * 128 * kBoxes));
-          __syncwarp();
-          if (mine) {
-            const int c = (is_v ? half * C::kVStages * kBoxes : 0) + st * kBoxes + chunk;
-            asm volatile(
-                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-                " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(
-                    smem_u32(ring + stage * C::kStage + chunk * kChunk + ((lane & (np - 1)) << a.c.page_log2) * 128)),
-                "l"(reinterpret_cast<uint64_t>(is_v ? &map_v : &map_k)), "r"(0), "r"(from), "r"(c),
-                "r"(smem_u32(&full[stage])), "l"(policy)
-                : "memory");
-          }
-          ++issued;
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1;
+        } else {
+          const bool mine = have && lane < boxes;
+          for (int st = 0; st < C::kVLoads; ++st) {
+            if (v_issued >= C::NV) {
+              bool ok = true;
+              if (lane == 0) ok = wait(&empty_v[vs], v_phase ^ 1, kStatusWaitEmpty);
+              alive = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+              if (!alive) break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full_v[vs], __popc(who) * static_cast<uint32_t>(C::kVBytes << rows_log2));
+            __syncwarp();
+            if (mine) {
+              // The CTA's half of the item's width begins at this byte of the row.
+              const int byte = (half * C::DV + static_cast<int>(rank) * (C::DV / 2)) * (E4M3 ? 1 : 2) + st * 128;
+              tma_rows_pair(smem_u32(v_ring + vs * C::kVStage + (box << rows_log2) * C::kVBytes), &map_v,
+                            mapa_shared(smem_u32(&full_v[vs]), rank), byte & 127, row, byte >> 7);
+            }
+            ++v_issued;
+            if (++vs == C::NV) {
+              vs = 0;
+              v_phase ^= 1;
+            }
           }
         }
       }
     }
     if (!alive && lane == 0) {
-      for (int s = 0; s < min(issued, C::kStages); ++s) {
-        if (stage == 0) {
-          stage = C::kStages;
-          phase ^= 1;
+      // Given up: the copies on their way land before the CTA's shared memory goes.
+      for (int s = 0; s < min(v_issued, C::NV); ++s) {
+        if (vs == 0) {
+          vs = C::NV;
+          v_phase ^= 1;
         }
-        --stage;
-        mbar_wait_timeout(&full[stage], phase, 1000000ull, a.status);
+        --vs;
+        mbar_wait_timeout(&full_v[vs], v_phase, 1000000ull, a.status);
+      }
+      for (int s = 0; rank == 0 && s < min(k_issued, C::NK); ++s) {
+        if (ks == 0) {
+          ks = C::NK;
+          k_phase ^= 1;
+        }
+        --ks;
+        mbar_wait_timeout(&full_k[ks], k_phase, 1000000ull, a.status);
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_of(E4M3 ? 0u : 1u, false, 128, KT);
-      constexpr uint32_t kIdescV = idesc_of(E4M3 ? 0u : 1u, true, 128, 128);
-      int stage = 0, w_stage = 0, tile_no = 0, item_no = 0;
-      uint32_t phase = 0, w_phase = 0;
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t kIdescS = idesc_of(E4M3 ? 0u : 1u, false, 256, KT);
+      constexpr uint32_t kIdescV = idesc_of(E4M3 ? 0u : 1u, true, 256, C::DV);
+      constexpr int NVW = E4M3 ? C::NW : C::NV;
+      uint8_t* const v_chunks = E4M3 ? w_ring : v_ring;
+      uint64_t* const v_empty = E4M3 ? empty_w : empty_v;
+      int ks = 0, vs = 0, tile_no = 0, item_no = 0;
+      uint32_t k_phase = 0;
       bool alive = true;
-      auto advance = [&] {
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      };
-      auto scores = [&](int no) {  // S of the item's next tile, the CTA's tile `no`
+      auto scores = [&](int no) {  // S of the item's next tile, the pair's tile `no`
         const uint32_t d = tmem + 256 + (no & 1) * KT;
-        for (int st = 0; st < C::kKStages && alive; ++st) {
-          alive = wait(&full[stage], phase, kStatusWaitFull);
-          if (!alive) break;
+        for (int st = 0; st < C::kKTile; ++st) {
+          alive = wait(&full_k[ks], k_phase, kStatusWaitFull);
+          if (!alive) return;
           tc_fence_after();
-          const uint64_t kb = smem_desc_sw128(smem_u32(ring + stage * C::kStage));
-          if constexpr (E4M3) {
+          const uint64_t kb = smem_desc_sw128(smem_u32(k_ring + ks * C::kKStage));
 #pragma unroll
-            for (int piece = 0; piece < 2; ++piece) {
-              const uint64_t qb = smem_desc_sw128(smem_u32(sq + (piece * (D / 128) + st) * kChunk));
+          for (int c = 0; c < C::kKChunks; ++c) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) umma_e4m3(d, qb + 2 * k, kb + 2 * k, kIdescS, st > 0 || piece > 0 || k > 0);
-            }
-          } else {
+            for (int piece = 0; piece < (E4M3 ? 2 : 1); ++piece) {
+              const uint64_t qb = smem_desc_sw128(smem_u32(sq + (piece * (C::kRow / 128) + st * C::kKChunks + c) * kChunk));
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint64_t qb = smem_desc_sw128(smem_u32(sq + (2 * st + c) * kChunk));
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_bf16(d, qb + 2 * k, kb + c * (kChunk >> 4) + 2 * k, kIdescS, st > 0 || c > 0 || k > 0);
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t ad = qb + 2 * k, bd = kb + c * (kHalfKeys * 128 >> 4) + 2 * k;
+                const uint32_t more = st > 0 || c > 0 || piece > 0 || k > 0;
+                if constexpr (E4M3) umma_e4m3_pair(d, ad, bd, kIdescS, more);
+                else umma_bf16_pair(d, ad, bd, kIdescS, more);
+              }
             }
           }
-          umma_commit(&empty[stage]);
-          advance();
+          umma_commit_pair(&empty_k[ks], 3);
+          if (++ks == C::NK) {
+            ks = 0;
+            k_phase ^= 1;
+          }
         }
-        if (alive) umma_commit(&s_full[no & 1]);
+        umma_commit_pair(&s_full[no & 1], 3);
       };
       for (bool more = start(); more && alive; more = next(), ++item_no) {
         alive = wait(q_full, item_no & 1, kStatusWaitItem);
@@ -515,47 +602,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         scores(tile_no);
         for (int j = 0; j < n && alive; ++j, ++tile_no) {
           if (j + 1 < n) scores(tile_no + 1);
-          if (j + 1 >= n && alive) umma_commit(q_free);  // the item's last S has read the queries
           if (!alive) break;
+          if (j + 1 >= n) umma_commit_pair(q_free, 3);  // the item's last S has read the queries
           if (j == 0 && item_no > 0) alive = wait(o_free, (item_no - 1) & 1, kStatusWaitAccEmpty);
-          if constexpr (!E4M3) {
-            // The softmax may have to look at V first, and could not tell an earlier use of the ring's
-            // stages from this one.
-            for (int st = 0; st < C::kVStages && alive; ++st) {
-              const int at = stage + st;
-              alive = wait(&full[at < C::kStages ? at : at - C::kStages], at < C::kStages ? phase : phase ^ 1, kStatusWaitFull);
-            }
-            if (alive) mbar_arrive(v_loaded);
-          }
+          // (The softmax has seen V's arrival.)
           alive = alive && wait(&p_ready[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitAccFull);
           if (!alive) break;
           tc_fence_after();
           const uint32_t p = tmem + 256 + (tile_no & 1) * KT;
-          for (int st = 0; st < C::kVStages && alive; ++st) {
-            alive = E4M3 ? wait(&wide_full[w_stage], w_phase, kStatusWaitFull) : wait(&full[stage], phase, kStatusWaitFull);
-            if (!alive) break;
-            tc_fence_after();
-            const uint64_t vb = smem_desc_v(smem_u32(E4M3 ? wide + w_stage * 2 * kChunk : ring + stage * C::kStage));
+          const uint64_t vb = smem_desc_v(smem_u32(v_chunks + vs * kChunk));
 #pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-              umma_bf16_ta(tmem + st * 128, p + 8 * k, vb + k * (2048 >> 4), kIdescV, j > 0 || k > 0);
-            if constexpr (E4M3) {
-              umma_commit(&wide_empty[w_stage]);
-              if (++w_stage == C::kWide) {
-                w_stage = 0;
-                w_phase ^= 1;
-              }
-              advance();  // the raw stage, which the widening warps release
-            } else {
-              umma_commit(&empty[stage]);
-              advance();
-            }
-          }
-          if (alive) umma_commit(o_done);
+          for (int k = 0; k < KT / 16; ++k) umma_16_ta_pair(tmem, p + 8 * k, vb + k * (2048 >> 4), kIdescV, j > 0 || k > 0);
+          for (int st = 0; st < C::kVTile; ++st) umma_commit_pair(&v_empty[vs + st], 3);
+          vs = vs + C::kVTile == NVW ? 0 : vs + C::kVTile;
+          umma_commit_pair(o_done, 3);
         }
       }
       if (!alive) {
-        umma_commit(drain);
+        umma_commit_pair(drain, 1);
         mbar_wait_timeout(drain, 0, 1000000ull, a.status);
       }
     }
@@ -563,20 +627,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- softmax and output
     const int quarter = warp & 3, half = (warp - kSoftmaxWarp0) >> 2;  // 32 rows, 64 of the columns
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const int r = quarter * 32 + lane;
+    const int r = quarter * 32 + lane;              // row of the CTA
+    const int rr = static_cast<int>(rank) * kRows + r;  // and of the pair
     const int stid = tid - kSoftmaxWarp0 * 32;
-    int tile_no = 0, item_no = 0, stage_no = 0;  // tiles, items and ring stages before this item
+    uint64_t* const v_full = E4M3 ? full_w : full_v;
+    constexpr int NVW = E4M3 ? C::NW : C::NV;
+    int tile_no = 0, item_no = 0, vs = 0;
+    uint32_t v_phase = 0;
     for (bool more = start(); more; more = next(), ++item_no) {
       const int head = part / C::kHalves, vhalf = part % C::kHalves;
-      const int tok = r / a.group;
+      const int tok = rr / a.group;
       const bool live = tok < t.nt;
       const int p = live ? t.p0 + tok : -1;
       const int lo = a.window > 0 ? p - a.window + 1 : 0;  // first position in the window
       float qs = a.scale * 1.44269504f;
       if constexpr (E4M3) {
-        wait(q_full, item_no & 1, kStatusWaitItem);
-        qs *= exch[r];
-        pair_sync(quarter);  // exch is used for more below
+        // The power of two that the row was multiplied by (a NaN for a row with one).
+        wait(&q_scaled[item_no & 1], (item_no >> 1) & 1, kStatusWaitItem);
+        const int e = q_exp[(item_no & 1) * kRows + r];
+        if (p >= 0) qs = e == 255 ? __uint_as_float(0x7fffffffu) : qs / __uint_as_float(static_cast<uint32_t>(e) << 23);
       }
       float ref = -INFINITY, l = 0.0f, vref = 0.0f;
       // P V of the tile before is complete.
@@ -686,53 +755,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l += sum0 + sum1;
+        if constexpr (E4M3) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scale_free[tile_no & 1]);
+        }
         tmem_st32(s_at + half * 32, w);
+        // V of this tile has arrived (what the MMA thread knows of it, it knows from here).
+        for (int st = 0; st < C::kVTile; ++st) wait(&v_full[vs + st], v_phase, kStatusWaitFull);
         if constexpr (!E4M3) {
           if (masked) {
             // V's rows that no row sees, and non-finite values that only some rows see.
             const int p1 = t.p0 + t.nt - 1;
-            wait_pv();  // (the barrier's phase of the tile before is over)
-            wait(v_loaded, tile_no & 1, kStatusWaitFull);
-            const int v_no = stage_no + min(j + 2, n) * C::kKStages + j * C::kVStages;
-            for (int st = 0; st < C::kVStages; ++st) {
-              const int sno = v_no + st;
-              wait(&full[sno % C::kStages], (sno / C::kStages) & 1, kStatusWaitFull);
-              uint8_t* v = ring + sno % C::kStages * C::kStage;
-              for (int i = stid; i < C::kStage / 16; i += kSoftmaxWarps * 32) {
-                const int key = tile * KT + ((i >> 3) & (KT - 1));
-                const bool all = key <= t.p0 && (a.window == 0 || key > p1 - a.window || key < a.sinks);
-                if (all) continue;
-                uint4* at = reinterpret_cast<uint4*>(v) + i;
-                if (!any_sees(key)) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                  continue;
-                }
-                const uint4 x = *at;
-                uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                bool found = false;
+            uint4* v = reinterpret_cast<uint4*>(v_ring + vs * C::kVStage);
+            for (int i = stid; i < C::kVTile * C::kVStage / 16; i += kSoftmaxWarps * 32) {
+              const int key = tile * KT + ((i >> 3) & (KT - 1));
+              const bool all = key <= t.p0 && (a.window == 0 || key > p1 - a.window || key < a.sinks);
+              if (all) continue;
+              if (!any_sees(key)) {
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+              }
+              uint32_t xs[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              bool found = false;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  if ((xs[q] & 0x7f80u) == 0x7f80u) xs[q] &= 0xffff0000u, found = true;
-                  if ((xs[q] & 0x7f800000u) == 0x7f800000u) xs[q] &= 0xffffu, found = true;
-                }
-                if (found) {
-                  *at = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-                  // Keys only some rows see: after the first token, or leaving the first tokens' windows.
-                  const int bit = key > t.p0 ? key - t.p0 - 1 : 128 + key - (max(t.p0, 0) - a.window + 1);
-                  atomicOr(&odd[(item_no & 1) * 8 + (bit >> 5)], 1u << (bit & 31));
-                }
+              for (int q = 0; q < 4; ++q) {
+                if ((xs[q] & 0x7f80u) == 0x7f80u) xs[q] &= 0xffff0000u, found = true;
+                if ((xs[q] & 0x7f800000u) == 0x7f800000u) xs[q] &= 0xffffu, found = true;
+              }
+              if (found) {
+                v[i] = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+                // The pair's row tile has up to 256 tokens; keys only some of them see lie after the first
+                // token, or leave the first tokens' windows: 256 bits by the distance, of either kind.
+                const int bit = (key > t.p0 ? key - t.p0 - 1 : key - (max(t.p0, 0) - a.window + 1)) & 255;
+                const uint32_t at = smem_u32(&odd[item_no % 3 * 8 + (bit >> 5)]), mark = 1u << (bit & 31);
+                or_shared(mapa_shared(at, 0), mark);
+                or_shared(mapa_shared(at, 1), mark);
               }
             }
             fence_proxy_async_shared();
           }
         }
+        vs += C::kVTile;
+        if (vs == NVW) {
+          vs = 0;
+          v_phase ^= 1;
+        }
         wait_pv();  // a barrier's phases are told apart by their parity: none may be passed over
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[tile_no & 1]);
+        if (lane == 0) arrive_first(&p_ready[tile_no & 1]);
       }
-      stage_no += n * (C::kKStages + C::kVStages);
 
       // The item's output: its row sums, then O.
       pair_sync(quarter);  // (exch may still be read for the last tile's reference)
@@ -745,23 +818,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       pair_sync(quarter);
       l = exch[r];
       if constexpr (!E4M3) {
-        if (stid < 8) odd[((item_no + 1) & 1) * 8 + stid] = 0;
+        // The marks of the item after the next: the other CTA may be in the next one already.
+        if (stid < 8) odd[(item_no + 2) % 3 * 8 + stid] = 0;
       }
       wait(o_done, (tile_no - 1) & 1, kStatusWaitAccFull);
       tc_fence_after();
       softmax_sync();
       uint32_t cleared = 0;
       if constexpr (!E4M3) {
-        for (int i = 0; i < 8; ++i) cleared |= odd[(item_no & 1) * 8 + i];
+        for (int i = 0; i < 8; ++i) cleared |= odd[item_no % 3 * 8 + i];
       }
       const bool whole = i0 == 0 && n == t.count;
       float vs = 1.0f;
       if constexpr (E4M3) vs = vref * 0.0078125f;
       const float f = whole ? (l == 0.0f ? 0.0f : vs / l) : vs;
-      const long long row = static_cast<long long>(t.row0 + tok) * a.q_heads + head * a.group + r % a.group;
+      const long long row = static_cast<long long>(t.row0 + tok) * a.q_heads + head * a.group + rr % a.group;
       const long long item_start = pos - u0;
-      // A piece's place: this CTA's first if the item began before the CTA's share or with it.
-      float* piece = a.chunk_partial + (2LL * blockIdx.x + (begin >= item_start ? 0 : 1)) * kChunkPieceFloats;
+      // A piece's place: this pair's first if the item began before the pair's share or with it.
+      float* piece = a.chunk_partial + (2LL * me + (begin >= item_start ? 0 : 1)) * kChunkPieceFloats;
 #pragma unroll 1
       for (int c = 0; c < C::DV / 2; c += 32) {
         uint32_t o[32];
@@ -771,10 +845,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_fence32(o);
         if constexpr (!E4M3) {
           if (cleared) {
-            for (int b = 0; b < 256; ++b) {
-              if (!(odd[(item_no & 1) * 8 + (b >> 5)] >> (b & 31) & 1)) continue;
-              const int key = b < 128 ? t.p0 + 1 + b : max(t.p0, 0) - a.window + 1 + b - 128;
-              if (key > p || (key < lo && key >= a.sinks)) continue;
+            // Each set bit stands for up to two keys; a key that is not hidden from some row of the
+            // tile was not cleared.
+            for (int b = 0; b < 512; ++b) {
+              if (!(odd[item_no % 3 * 8 + ((b & 255) >> 5)] >> (b & 31) & 1)) continue;
+              const int p1 = t.p0 + t.nt - 1;
+              const int key = b < 256 ? t.p0 + 1 + b : max(t.p0, 0) - a.window + 1 + b - 256;
+              if (b >= 256 && (a.window == 0 || key < 0 || key > t.p0)) continue;
+              if (key < 0 || key > p || (key < lo && key >= a.sinks)) continue;
+              if (key <= t.p0 && (a.window == 0 || key > p1 - a.window || key < a.sinks)) continue;
               const int page = kv_page(a.b, a.c, t.seq, key >> a.c.page_log2, a.status);
               if (page < 0) continue;
               const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) +
@@ -799,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  pack_bf16(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f));
           }
         } else if (live) {
-          float4* to = reinterpret_cast<float4*>(piece + r * C::DV + col);
+          float4* to = reinterpret_cast<float4*>(piece + rr * C::DV + col);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             to[i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
@@ -808,11 +887,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) arrive_first(o_free);
       if (half == 0) {
         if (!whole) {
-          piece[kRows * 256 + r] = ref;
-          piece[kRows * 257 + r] = l;
+          piece[256 * 256 + rr] = ref;
+          piece[256 * 257 + rr] = l;
         } else if (live && a.lse && vhalf == 0) {
           a.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.693147181f;
         }
@@ -821,11 +900,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kAuxWarp0) {
     // ---------------------------------------------------------------- queries; e4m3: V and the scales
     const int awarp = warp - kAuxWarp0;
-    int item_no = 0;
+    int item_no = 0, tile_no = 0, vs = 0, ws = 0;
+    uint32_t v_phase = 0, w_phase = 0;
     for (bool more = start(); more; more = next(), ++item_no) {
       const int head = part / C::kHalves;
       if (item_no > 0) wait(q_free, (item_no - 1) & 1, kStatusWaitEmpty);
-      // A warp takes 32 rows, four at a time; a lane 16 bytes of a row and every 512 bytes on.
+      // A warp takes 32 rows, some at a time; a lane 16 bytes of a row and every 512 bytes on.
       constexpr int kVecs = D / 8 < 32 ? 1 : D / 256;            // 16-byte vectors of a row per lane
       constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;            // lanes of a row
       constexpr int kRowsAtOnce = 32 / kLanes;
@@ -835,14 +915,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 x[kBatch][kVecs];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          const int r = awarp * 32 + g + b * kRowsAtOnce + lane / kLanes;
-          const int tok = r / a.group;
+          const int rr = static_cast<int>(rank) * kRows + awarp * 32 + g + b * kRowsAtOnce + lane / kLanes;
+          const int tok = rr / a.group;
 #pragma unroll
           for (int v = 0; v < kVecs; ++v) {
             x[b][v] = make_uint4(0u, 0u, 0u, 0u);
             if (tok < t.nt)
               x[b][v] = *reinterpret_cast<const uint4*>(a.q.ptr + static_cast<long long>(t.row0 + tok) * a.q.token_stride +
-                                                        (head * a.group + r % a.group) * a.q.head_stride +
+                                                        (head * a.group + rr % a.group) * a.q.head_stride +
                                                         (lane % kLanes + v * 32) * 8);
           }
         }
@@ -850,22 +930,139 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < kBatch; ++b) {
           const int r = awarp * 32 + g + b * kRowsAtOnce + lane / kLanes;
           const uint32_t swz = (r & 7) << 4;
+          if constexpr (!E4M3) {
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) {
-            const uint32_t byte = (lane % kLanes + v * 32) * 16;
-            *reinterpret_cast<uint4*>(sq + (byte >> 7) * kChunk + r * 128 + ((byte & 127) ^ swz)) = x[b][v];
+            for (int v = 0; v < kVecs; ++v) {
+              const uint32_t byte = (lane % kLanes + v * 32) * 16;
+              *reinterpret_cast<uint4*>(sq + (byte >> 7) * kChunk + r * 128 + ((byte & 127) ^ swz)) = x[b][v];
+            }
+          } else {
+            // A power of two that brings the row's largest magnitude into [128, 256).
+            uint32_t top = 0;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+              const uint32_t u[4] = {x[b][v].x, x[b][v].y, x[b][v].z, x[b][v].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) top = max(top, max((u[q] << 16) & 0x7fffffffu, u[q] & 0x7fffffffu));
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = static_cast<int>(top >> 23), up_exp = e == 255 ? 255 : min(261 - e, 254);
+            const float up = e == 255 ? 1.0f : __uint_as_float(static_cast<uint32_t>(up_exp) << 23);
+            if (lane % kLanes == 0) q_exp[(item_no & 1) * kRows + r] = static_cast<uint8_t>(up_exp);
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+              const uint32_t u[4] = {x[b][v].x, x[b][v].y, x[b][v].z, x[b][v].w};
+              uint32_t hi[2], lo[2];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                float f[4] = {__uint_as_float(u[2 * q] << 16) * up, __uint_as_float(u[2 * q] & 0xffff0000u) * up,
+                              __uint_as_float(u[2 * q + 1] << 16) * up, __uint_as_float(u[2 * q + 1] & 0xffff0000u) * up};
+                hi[q] = e4m3_part(f);
+                lo[q] = e4m3_part(f);
+              }
+              const uint32_t byte = (lane % kLanes + v * 32) * 8;
+              uint8_t* to = sq + (byte >> 7) * kChunk + r * 128 + ((byte & 127) ^ swz);
+              *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(to + (C::kRow / 128) * kChunk) = make_uint2(lo[0], lo[1]);
+            }
           }
         }
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) {
+        arrive_first(q_full);
+        if (E4M3) mbar_arrive(&q_scaled[item_no & 1]);
+      }
+      if constexpr (E4M3) {
+        const int key = awarp * 32 + lane;
+        float vref = __uint_as_float(0x00800000u);  // at least the values' largest scale so far, a power of two
+        for (int j = 0; j < n; ++j, ++tile_no) {
+          const int tile = tile_at(i0 + j);
+          const bool masked = is_masked(tile);
+          // The scales of this thread's key: for the keys as they are, for the values relative to vref.
+          float sk = 0.0f, sv = 0.0f;
+          const int pos_k = tile * KT + key;
+          if (!masked || any_sees(pos_k)) {
+            const int page = kv_page(a.b, a.c, t.seq, pos_k >> a.c.page_log2, a.status);
+            if (page >= 0) {
+              const long long at = ((static_cast<long long>(page) * a.c.kv_heads + head) << a.c.page_log2) + (pos_k & (R - 1));
+              sk = a.c.k_scale[at];
+              sv = a.c.v_scale[at];
+            }
+          }
+          const uint32_t bits = __float_as_uint(sv);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
+          if (lane == 0) aux_top[(tile_no & 1) * 4 + awarp] = top;
+          aux_sync();
+          uint32_t most = 0;
+#pragma unroll
+          for (int w = 0; w < kAuxWarps; ++w) most = max(most, aux_top[(tile_no & 1) * 4 + w]);
+          const float want = __uint_as_float(min((most >> 23) + 1u, 254u) << 23);
+          const float before = vref;
+          if (most > 0) vref = fmaxf(vref, want);
+          if (tile_no >= 2) wait(&scale_free[tile_no & 1], ((tile_no >> 1) - 1) & 1, kStatusWaitEmpty);
+          float* to = scales + (tile_no & 1) * 2 * KT;
+          to[key] = sk;
+          to[KT + key] = __fdiv_rn(sv, vref) * 128.0f;
+          if (awarp == 0 && lane == 0) {
+            scale_step[tile_no & 1] = j == 0 ? 1.0f : before / vref;
+            scale_ref[tile_no & 1] = vref;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scale_full[tile_no & 1]);
+          // V's codes to fp16, 16 at a time; rows no row sees to 0.
+          wait(&full_v[vs], v_phase, kStatusWaitFull);
+          for (int c = 0; c < C::kVTile; ++c) {
+            if (tile_no * C::kVTile + c >= C::NW) wait(&empty_w[ws + c], w_phase ^ 1, kStatusWaitEmpty);
+          }
+          constexpr int kParts = C::kVBytes / 16;
+#pragma unroll 4
+          for (int i = awarp * 32 + lane; i < KT * kParts; i += kAuxWarps * 32) {
+            const int k = i / kParts, piece = i % kParts;
+            const uint4 x = *reinterpret_cast<const uint4*>(v_ring + vs * C::kVStage + i * 16);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                  "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                  : "=r"(w[2 * q]), "=r"(w[2 * q + 1])
+                  : "r"(u[q]));
+            if (masked && !any_sees(tile * KT + k)) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) w[q] = 0;
+            }
+            uint8_t* to_w = w_ring + (ws + piece / 4) * kChunk + k * 128;
+            const uint32_t byte = (piece % 4) * 32, swz = (k & 7) << 4;
+            *reinterpret_cast<uint4*>(to_w + (byte ^ swz)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(to_w + ((byte + 16) ^ swz)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&empty_v[vs]);
+            for (int c = 0; c < C::kVTile; ++c) mbar_arrive(&full_w[ws + c]);
+          }
+          if (++vs == C::NV) {
+            vs = 0;
+            v_phase ^= 1;
+          }
+          ws += C::kVTile;
+          if (ws == C::NW) {
+            ws = 0;
+            w_phase ^= 1;
+          }
+        }
+      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  cluster_sync_all();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 // ------------------------------------------------------------------ joining an item's pieces
@@ -873,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A block for each place where a share begins (x) and each 8 rows: if that is the first cut in an item,
 // a warp joins a row of the item's pieces.
 template <int D>
-__global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int tokens, int grid) {
+__global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int shares) {
   constexpr int DV = D < 256 ? D : 256, kHalves = D / DV;
   pdl_wait();
   pdl_launch_dependents();
@@ -881,7 +1078,7 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int 
   const int parts = a.c.kv_heads * kHalves;
   const long long total = a.list.first_unit[n_tiles] * parts;
   constexpr int kShare = kItemCost + 1;
-  const long long ctas = min(static_cast<long long>(grid), (total + kShare - 1) / kShare);
+  const long long ctas = min(static_cast<long long>(shares), (total + kShare - 1) / kShare);
   const long long x = blockIdx.x + 1;
   if (x >= ctas) return;
   const long long cut = x * total / ctas;
@@ -891,7 +1088,7 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int 
   const long long off = cut - a.list.first_unit[entry] * parts;
   const int part = static_cast<int>(off / units);
   const long long item_start = cut - off % units;
-  // The CTAs with the item's first and last key tiles.
+  // The pairs with the item's first and last key tiles.
   const long long first = ((item_start + kItemCost + 1) * ctas - 1) / total;
   const long long last = ((item_start + units) * ctas - 1) / total;
   if (first == last || first + 1 != x) return;
@@ -902,7 +1099,7 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int 
     return a.chunk_partial + (2 * c + (c > first || c * total / ctas >= item_start ? 0 : 1)) * kChunkPieceFloats;
   };
   float top = -INFINITY;
-  for (long long c = first; c <= last; ++c) top = fmaxf(top, __ldcg(place(c) + kRows * 256 + r));
+  for (long long c = first; c <= last; ++c) top = fmaxf(top, __ldcg(place(c) + 256 * 256 + r));
   const float base = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
   float4 acc[DV / 128];
@@ -911,8 +1108,8 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int 
 #pragma unroll 4
   for (long long c = first; c <= last; ++c) {
     const float* from = place(c);
-    const float w = exp2_approx(__ldcg(from + kRows * 256 + r) - base);
-    sum = fmaf(w, __ldcg(from + kRows * 257 + r), sum);
+    const float w = exp2_approx(__ldcg(from + 256 * 256 + r) - base);
+    sum = fmaf(w, __ldcg(from + 256 * 257 + r), sum);
 #pragma unroll
     for (int v = 0; v < DV / 128; ++v) {
       const float4 y = __ldcg(reinterpret_cast<const float4*>(from + r * DV + v * 128 + lane * 4));
@@ -933,40 +1130,67 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int 
 }
 
 template <int D, bool E4M3>
-cudaError_t launch(const KvAttn& a, int ctas, cudaStream_t s) {
+cudaError_t launch(const KvAttn& a, int pairs, cudaStream_t s) {
   using C = Chk<D, E4M3>;
   CUtensorMap mk, mv;
   const uint64_t rows = (static_cast<uint64_t>(a.c.n_pages) * a.c.kv_heads) << a.c.page_log2;
-  const uint32_t box = 1u << a.c.page_log2;
-  if (!encode_row_chunks(&mk, a.c.k, rows, C::kRow, box, 1) || !encode_row_chunks(&mv, a.c.v, rows, C::kRow, box, 1))
+  const uint32_t box = 1u << (a.c.page_log2 < 6 ? a.c.page_log2 : 6);
+  if (!encode_row_chunks(&mk, a.c.k, rows, C::kRow, box, 1, 128, true) ||
+      !encode_row_chunks(&mv, a.c.v, rows, C::kRow, box, 1, C::kVBytes, !E4M3))
     return cudaErrorInvalidValue;
   const int tokens = chunk_tokens(a.group);
   cudaError_t e = launch_pdl(kv_chunk_list_kernel, dim3(1), dim3(kListThreads), 0, s, a, tokens);
-  if (e == cudaSuccess) e = launch_pdl(kv_chunk_kernel<D, E4M3>, dim3(ctas), dim3(kThreads), C::kSmem, s, a, tokens, mk, mv);
-  if (e == cudaSuccess && ctas > 1)
-    e = launch_pdl(kv_chunk_join_kernel<D>, dim3(ctas - 1, kRows / 8), dim3(256), 0, s, a, tokens, ctas);
+  if (e == cudaSuccess)
+    e = launch_pdl_pair(kv_chunk_kernel<D, E4M3>, dim3(2 * pairs), dim3(kThreads), C::kSmem, s, a, mk, mv);
+  if (e == cudaSuccess && pairs > 1)
+    e = launch_pdl(kv_chunk_join_kernel<D>, dim3(pairs - 1, 256 / 8), dim3(256), 0, s, a, pairs);
   return e;
 }
 
+// Sets the shared memory limit and lowers *pairs to the pairs that can be resident at once.
 template <int D, bool E4M3>
-cudaError_t setup() {
-  return cudaFuncSetAttribute(kv_chunk_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, Chk<D, E4M3>::kSmem);
+cudaError_t setup(int* pairs) {
+  using C = Chk<D, E4M3>;
+  cudaError_t e = cudaFuncSetAttribute(kv_chunk_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * kChunkMaxPairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, kv_chunk_kernel<D, E4M3>, &cfg);
+  if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && n < *pairs) *pairs = n;
+  return e;
 }
 
 }  // namespace
 
-cudaError_t kv_chunk_setup() {
-  cudaError_t e = setup<128, false>();
-  if (e == cudaSuccess) e = setup<256, false>();
-  if (e == cudaSuccess) e = setup<512, false>();
+cudaError_t kv_chunk_setup(int* pairs) {
+  *pairs = kChunkMaxPairs;
+  cudaError_t e = setup<128, false>(pairs);
+  if (e == cudaSuccess) e = setup<256, false>(pairs);
+  if (e == cudaSuccess) e = setup<512, false>(pairs);
+  if (e == cudaSuccess) e = setup<128, true>(pairs);
+  if (e == cudaSuccess) e = setup<256, true>(pairs);
+  if (e == cudaSuccess) e = setup<512, true>(pairs);
   return e;
 }
 
-cudaError_t launch_kv_chunk(const KvAttn& a, int ctas, cudaStream_t s) {
-  switch (a.c.head_dim) {
-    case 128: return launch<128, false>(a, ctas, s);
-    case 256: return launch<256, false>(a, ctas, s);
-    default: return launch<512, false>(a, ctas, s);
+cudaError_t launch_kv_chunk(const KvAttn& a, int pairs, cudaStream_t s) {
+  switch (a.c.head_dim * 2 + a.c.e4m3) {
+    case 256: return launch<128, false>(a, pairs, s);
+    case 257: return launch<128, true>(a, pairs, s);
+    case 512: return launch<256, false>(a, pairs, s);
+    case 513: return launch<256, true>(a, pairs, s);
+    case 1024: return launch<512, false>(a, pairs, s);
+    default: return launch<512, true>(a, pairs, s);
   }
 }
 

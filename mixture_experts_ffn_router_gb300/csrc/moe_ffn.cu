@@ -20,6 +20,7 @@
 
 #include "moe_ffn.h"
 #include "internal.h"
+#include "kv.h"
 
 using namespace moe;
 
@@ -174,18 +175,19 @@ bool encode_bf16_tensor_map(CUtensorMap* map, const void* ptr, uint64_t rows, ui
 }
 
 // Rows of `row_bytes` (a multiple of 128), contiguous, seen as [row_bytes / 128][rows][128 bytes]: a
-// box is `box_chunks` 128-byte chunks of `box_rows` rows, chunk after chunk, 128-byte swizzle.
+// box is the first `chunk_bytes` bytes (or the bytes from any multiple of 16 in a chunk on) of
+// `box_chunks` chunks of `box_rows` rows, chunk after chunk, with the 128-byte swizzle or as they lie.
 bool encode_row_chunks(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
-                       uint32_t box_chunks) {
+                       uint32_t box_chunks, uint32_t chunk_bytes, bool swizzle) {
   EncodeTiledFn fn = get_encode();
   if (!fn) return false;
   cuuint64_t dims[3] = {128, rows, row_bytes / 128};
   cuuint64_t strides[2] = {row_bytes, 128};
-  cuuint32_t box[3] = {128, box_rows, box_chunks};
+  cuuint32_t box[3] = {chunk_bytes, box_rows, box_chunks};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 }  // namespace moe
