@@ -118,25 +118,46 @@ __device__ __forceinline__ uint32_t e4m3_part(float (&x)[4]) {
   return codes;
 }
 
-// D (both CTAs' TMEM) (+)= A * B^T over 32 K elements of e4m3, A and B in shared memory, K-major.
-__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// The MMA warp issues with all its lanes together, one of them elected per instruction: what the
+// instructions take (descriptors, addresses) then stays in uniform registers. Under a branch on the
+// lane, moving it there for every instruction took about 100 cycles where an MMA takes 64.
+
+// D (both CTAs' TMEM) (+)= A * B^T, A and B in shared memory, K-major: 16 K elements of bf16, or 32 of e4m3.
+template <bool E4M3>
+__device__ __forceinline__ void umma_pair_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  if constexpr (E4M3) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
 }
 
 // The same over 16 K elements of 16 bits, A in each CTA's TMEM.
-__device__ __forceinline__ void umma_16_ta_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate) {
+__device__ __forceinline__ void umma_ta_pair_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                   uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives on `bar` of both CTAs when the MMAs issued before have completed.
+__device__ __forceinline__ void commit_pair_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
       : "memory");
 }
 
@@ -185,6 +206,13 @@ __device__ __forceinline__ bool pair_sync_or(int pair, bool c) {
       : "memory");
   return r != 0;
 }
+// Arrives on a barrier at a shared::cluster address. What the arrival announces lies in this CTA's own
+// TMEM and shared memory, for its own tensor core, so nothing is released to the cluster: with
+// .release.cluster the arrival took 1200 cycles of a key tile's 3500.
+__device__ __forceinline__ void arrive_at(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
 // Sets bits at a shared::cluster address.
 __device__ __forceinline__ void or_shared(uint32_t addr, uint32_t bits) {
   asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(bits) : "memory");
@@ -386,11 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Waits look at the CTA's flag first, so that all of them end soon after one has given up.
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t why) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    return mbar_wait_bounded_cluster(bar, parity, abort_flag, a.status, why);
+    return mbar_wait_bounded(bar, parity, abort_flag, a.status, why);
   };
-  auto arrive_first = [&](uint64_t* bar) { mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0)); };
+  auto arrive_first = [&](uint64_t* bar) { arrive_at(mapa_shared(smem_u32(bar), 0)); };
 
   const int n_tiles = *a.list.n_tiles;
   const int parts = a.c.kv_heads * C::kHalves;
@@ -464,46 +492,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
-    // Boxes are one page's rows, or 64 of them: lane i holds the page of the tile's box i.
+    // Boxes are one page's rows, or 64 of them: lane i holds the cache row of the tile's box i (and of
+    // box i - boxes, ...). A tile's page ids are fetched a tile ahead, and serve its K and then its V.
     const int rows_log2 = min(a.c.page_log2, 6);
     const int boxes = KT >> rows_log2;
     const int box = lane & (boxes - 1);
+    const int own = boxes / 2;  // boxes of this CTA's keys
+    const int chunk = lane / boxes;
+    const bool k_lane = box / own == static_cast<int>(rank) && chunk < C::kKChunks, v_lane = lane < boxes;
     const uint32_t full_k0 = mapa_shared(smem_u32(&full_k[0]), 0);
+    const uint32_t k_to = smem_u32(k_ring) + chunk * (kHalfKeys * 128) + (((box % own) << rows_log2) * 128);
+    const uint32_t v_to = smem_u32(v_ring) + (box << rows_log2) * C::kVBytes;
     int ks = 0, vs = 0, k_issued = 0, v_issued = 0;
     uint32_t k_phase = 0, v_phase = 0;
     bool alive = true;
+    struct Boxes {
+      int row;       // of this lane's box
+      unsigned who;  // boxes to load
+    };
     for (bool more = start(); more && alive; more = next()) {
       const int head = part / C::kHalves, half = part % C::kHalves;
-      // K of tile 0; then K of tile j + 1 and V of tile j.
-      for (int step = 0; step < 2 * n && alive; ++step) {
-        const bool is_v = step == 2 * n - 1 || (step > 0 && !(step & 1));
-        const int j = is_v ? step / 2 - (step & 1 ? 0 : 1) : (step + 1) / 2;
-        const int first = tile_at(i0 + j) * KT + (box << rows_log2);  // first position of the box
-        const bool need = lane < boxes && first <= t.p0 + t.nt - 1 &&
+      // The position a box begins at, and the page table's entry of it (or a refusal).
+      auto fetch = [&](int j, int& first) {
+        first = j < n ? tile_at(i0 + j) * KT + (box << rows_log2) : 0x7fffffff;
+        const bool need = first <= t.p0 + t.nt - 1 &&
                           (a.window == 0 || first + (1 << rows_log2) - 1 > max(t.p0, 0) - a.window || first < a.sinks);
-        int page = -1;
-        if (need) page = kv_page(a.b, a.c, t.seq, first >> a.c.page_log2, a.status);
-        const unsigned who = __ballot_sync(0xffffffffu, page >= 0);
-        int row = page < 0 ? 0 : ((page * a.c.kv_heads + head) << a.c.page_log2) + (first & (R - 1));
-        row = __shfl_sync(0xffffffffu, row, box);
-        const bool have = (who >> box) & 1;
-        if (!is_v) {
-          // This CTA's boxes, of each chunk; the first CTA's barrier counts both CTAs'.
-          const int own = boxes / 2, chunk = lane / boxes;
-          const bool mine = have && box / own == static_cast<int>(rank) && chunk < C::kKChunks;
-          for (int st = 0; st < C::kKTile; ++st) {
-            if (k_issued >= C::NK) {
-              bool ok = true;
-              if (lane == 0) ok = wait(&empty_k[ks], k_phase ^ 1, kStatusWaitEmpty);
-              alive = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-              if (!alive) break;
-            }
-            if (lane == 0 && rank == 0)
-              mbar_arrive_expect_tx(&full_k[ks], __popc(who) * static_cast<uint32_t>((128 << rows_log2) * C::kKChunks));
+        return need ? a.b.pages[t.seq * a.b.pages_stride + (first >> a.c.page_log2)] : -2;
+      };
+      auto boxes_of = [&](int page, int first) {
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
+        if (page != -2 && !ok) atomicOr(a.status, kStatusBadIndex);
+        Boxes o;
+        o.who = __ballot_sync(0xffffffffu, ok) & ((1u << boxes) - 1);
+        o.row = ok ? ((page * a.c.kv_heads + head) << a.c.page_log2) + (first & (R - 1)) : 0;
+        return o;
+      };
+      int first;
+      int page = fetch(0, first);
+      Boxes cur = boxes_of(page, first), last = cur;
+      page = fetch(1, first);
+      // K of tile 0; then K of tile j + 1 and V of tile j.
+      for (int j = -1; j < n && alive; ++j) {
+        if (j + 1 < n) {
+          if (j >= 0) {
+            last = cur;
+            cur = boxes_of(page, first);
+            page = fetch(j + 2, first);
+          }
+          const bool mine = k_lane && ((cur.who >> box) & 1);
+          const uint32_t bytes = __popc(cur.who) * static_cast<uint32_t>((128 << rows_log2) * C::kKChunks);
+          for (int st = 0; st < C::kKTile && alive; ++st) {
+            if (k_issued >= C::NK) alive = __all_sync(0xffffffffu, wait(&empty_k[ks], k_phase ^ 1, kStatusWaitEmpty));
+            if (!alive) break;
+            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full_k[ks], bytes);
             __syncwarp();
-            if (mine)
-              tma_rows_pair(smem_u32(k_ring + ks * C::kKStage + chunk * (kHalfKeys * 128) + (((box % own) << rows_log2) * 128)),
-                            &map_k, full_k0 + 8u * ks, 0, row, st * C::kKChunks + chunk);
+            if (mine) tma_rows_pair(k_to + ks * C::kKStage, &map_k, full_k0 + 8u * ks, 0, cur.row, st * C::kKChunks + chunk);
             ++k_issued;
             if (++ks == C::NK) {
               ks = 0;
@@ -511,27 +554,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          const bool mine = have && lane < boxes;
-          for (int st = 0; st < C::kVLoads; ++st) {
-            if (v_issued >= C::NV) {
-              bool ok = true;
-              if (lane == 0) ok = wait(&empty_v[vs], v_phase ^ 1, kStatusWaitEmpty);
-              alive = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-              if (!alive) break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&full_v[vs], __popc(who) * static_cast<uint32_t>(C::kVBytes << rows_log2));
-            __syncwarp();
-            if (mine) {
-              // The CTA's half of the item's width begins at this byte of the row.
-              const int byte = (half * C::DV + static_cast<int>(rank) * (C::DV / 2)) * (E4M3 ? 1 : 2) + st * 128;
-              tma_rows_pair(smem_u32(v_ring + vs * C::kVStage + (box << rows_log2) * C::kVBytes), &map_v,
-                            mapa_shared(smem_u32(&full_v[vs]), rank), byte & 127, row, byte >> 7);
-            }
-            ++v_issued;
-            if (++vs == C::NV) {
-              vs = 0;
-              v_phase ^= 1;
-            }
+          last = cur;
+        }
+        if (j < 0 || !alive) continue;
+        const bool mine = v_lane && ((last.who >> box) & 1);
+        const uint32_t bytes = __popc(last.who) * static_cast<uint32_t>(C::kVBytes << rows_log2);
+        for (int st = 0; st < C::kVLoads; ++st) {
+          if (v_issued >= C::NV) alive = __all_sync(0xffffffffu, wait(&empty_v[vs], v_phase ^ 1, kStatusWaitEmpty));
+          if (!alive) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full_v[vs], bytes);
+          __syncwarp();
+          if (mine) {
+            // The CTA's half of the item's width begins at this byte of the row.
+            const int byte = (half * C::DV + static_cast<int>(rank) * (C::DV / 2)) * (E4M3 ? 1 : 2) + st * 128;
+            tma_rows_pair(v_to + vs * C::kVStage, &map_v, mapa_shared(smem_u32(&full_v[vs]), rank), byte & 127, last.row,
+                          byte >> 7);
+          }
+          ++v_issued;
+          if (++vs == C::NV) {
+            vs = 0;
+            v_phase ^= 1;
           }
         }
       }
@@ -557,69 +599,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t kIdescS = idesc_of(E4M3 ? 0u : 1u, false, 256, KT);
       constexpr uint32_t kIdescV = idesc_of(E4M3 ? 0u : 1u, true, 256, C::DV);
       constexpr int NVW = E4M3 ? C::NW : C::NV;
       uint8_t* const v_chunks = E4M3 ? w_ring : v_ring;
       uint64_t* const v_empty = E4M3 ? empty_w : empty_v;
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
       int ks = 0, vs = 0, tile_no = 0, item_no = 0;
       uint32_t k_phase = 0;
       bool alive = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity, uint32_t why) {
+        alive = uniform(wait(bar, parity, why) ? 1 : 0) != 0 && alive;
+        return alive;
+      };
       auto scores = [&](int no) {  // S of the item's next tile, the pair's tile `no`
-        const uint32_t d = tmem + 256 + (no & 1) * KT;
+        const uint32_t d = tm + 256 + (uniform(no) & 1) * KT;
         for (int st = 0; st < C::kKTile; ++st) {
-          alive = wait(&full_k[ks], k_phase, kStatusWaitFull);
-          if (!alive) return;
+          if (!wait_all(&full_k[ks], k_phase, kStatusWaitFull)) return;
           tc_fence_after();
-          const uint64_t kb = smem_desc_sw128(smem_u32(k_ring + ks * C::kKStage));
+          const int u = uniform(ks);
+          const uint64_t kb = smem_desc_sw128(smem_u32(k_ring) + u * C::kKStage);
 #pragma unroll
           for (int c = 0; c < C::kKChunks; ++c) {
 #pragma unroll
             for (int piece = 0; piece < (E4M3 ? 2 : 1); ++piece) {
-              const uint64_t qb = smem_desc_sw128(smem_u32(sq + (piece * (C::kRow / 128) + st * C::kKChunks + c) * kChunk));
+              const uint64_t qb = smem_desc_sw128(smem_u32(sq) + (piece * (C::kRow / 128) + st * C::kKChunks + c) * kChunk);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint64_t ad = qb + 2 * k, bd = kb + c * (kHalfKeys * 128 >> 4) + 2 * k;
-                const uint32_t more = st > 0 || c > 0 || piece > 0 || k > 0;
-                if constexpr (E4M3) umma_e4m3_pair(d, ad, bd, kIdescS, more);
-                else umma_bf16_pair(d, ad, bd, kIdescS, more);
-              }
+              for (int k = 0; k < 4; ++k)
+                umma_pair_elect<E4M3>(d, qb + 2 * k, kb + c * (kHalfKeys * 128 >> 4) + 2 * k, kIdescS,
+                                      st > 0 || c > 0 || piece > 0 || k > 0);
             }
           }
-          umma_commit_pair(&empty_k[ks], 3);
+          commit_pair_elect(&empty_k[u]);
           if (++ks == C::NK) {
             ks = 0;
             k_phase ^= 1;
           }
         }
-        umma_commit_pair(&s_full[no & 1], 3);
+        commit_pair_elect(&s_full[no & 1]);
       };
       for (bool more = start(); more && alive; more = next(), ++item_no) {
-        alive = wait(q_full, item_no & 1, kStatusWaitItem);
-        if (!alive) break;
+        const int tiles = uniform(n);
+        if (!wait_all(q_full, item_no & 1, kStatusWaitItem)) break;
         tc_fence_after();
         scores(tile_no);
-        for (int j = 0; j < n && alive; ++j, ++tile_no) {
-          if (j + 1 < n) scores(tile_no + 1);
+        for (int j = 0; j < tiles && alive; ++j, ++tile_no) {
+          if (j + 1 < tiles) scores(tile_no + 1);
           if (!alive) break;
-          if (j + 1 >= n) umma_commit_pair(q_free, 3);  // the item's last S has read the queries
-          if (j == 0 && item_no > 0) alive = wait(o_free, (item_no - 1) & 1, kStatusWaitAccEmpty);
+          if (j + 1 >= tiles) commit_pair_elect(q_free);  // the item's last S has read the queries
+          if (j == 0 && item_no > 0) wait_all(o_free, (item_no - 1) & 1, kStatusWaitAccEmpty);
           // (The softmax has seen V's arrival.)
-          alive = alive && wait(&p_ready[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitAccFull);
-          if (!alive) break;
+          if (!alive || !wait_all(&p_ready[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitAccFull)) break;
           tc_fence_after();
-          const uint32_t p = tmem + 256 + (tile_no & 1) * KT;
-          const uint64_t vb = smem_desc_v(smem_u32(v_chunks + vs * kChunk));
+          const uint32_t p = tm + 256 + (uniform(tile_no) & 1) * KT;
+          const int u = uniform(vs);
+          const uint64_t vb = smem_desc_v(smem_u32(v_chunks) + u * kChunk);
+          const uint32_t add = uniform(j > 0 ? 1 : 0);
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k) umma_16_ta_pair(tmem, p + 8 * k, vb + k * (2048 >> 4), kIdescV, j > 0 || k > 0);
-          for (int st = 0; st < C::kVTile; ++st) umma_commit_pair(&v_empty[vs + st], 3);
+          for (int k = 0; k < KT / 16; ++k)
+            umma_ta_pair_elect(tm, p + 8 * k, vb + k * (2048 >> 4), kIdescV, k > 0 ? 1u : add);
+          for (int st = 0; st < C::kVTile; ++st) commit_pair_elect(&v_empty[u + st]);
           vs = vs + C::kVTile == NVW ? 0 : vs + C::kVTile;
-          umma_commit_pair(o_done, 3);
+          commit_pair_elect(o_done);
         }
       }
       if (!alive) {
-        umma_commit_pair(drain, 1);
+        commit_pair_elect(drain);
         mbar_wait_timeout(drain, 0, 1000000ull, a.status);
       }
     }
@@ -766,30 +813,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked) {
             // V's rows that no row sees, and non-finite values that only some rows see.
             const int p1 = t.p0 + t.nt - 1;
-            uint4* v = reinterpret_cast<uint4*>(v_ring + vs * C::kVStage);
-            for (int i = stid; i < C::kVTile * C::kVStage / 16; i += kSoftmaxWarps * 32) {
-              const int key = tile * KT + ((i >> 3) & (KT - 1));
+            // A thread's vectors are the same 16 bytes of four keys, in each chunk.
+            uint4* v = reinterpret_cast<uint4*>(v_ring + vs * C::kVStage) + stid;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const int key = tile * KT + (stid >> 3) + 32 * m;
               const bool all = key <= t.p0 && (a.window == 0 || key > p1 - a.window || key < a.sinks);
               if (all) continue;
-              if (!any_sees(key)) {
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-              }
-              uint32_t xs[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-              bool found = false;
+              const bool none = !any_sees(key);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if ((xs[q] & 0x7f80u) == 0x7f80u) xs[q] &= 0xffff0000u, found = true;
-                if ((xs[q] & 0x7f800000u) == 0x7f800000u) xs[q] &= 0xffffu, found = true;
-              }
-              if (found) {
-                v[i] = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+              for (int c = 0; c < C::kVTile; ++c) {
+                uint4* at = v + m * 256 + c * (kChunk / 16);
+                if (none) {
+                  *at = make_uint4(0u, 0u, 0u, 0u);
+                  continue;
+                }
+                const uint4 x = *at;
+                // Whether some exponent is all ones: a carry out of its field after adding one to it.
+                const uint32_t even = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                      ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+                if ((even & 0x80008000u) == 0) continue;
+                uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if ((xs[q] & 0x7f80u) == 0x7f80u) xs[q] &= 0xffff0000u;
+                  if ((xs[q] & 0x7f800000u) == 0x7f800000u) xs[q] &= 0xffffu;
+                }
+                *at = make_uint4(xs[0], xs[1], xs[2], xs[3]);
                 // The pair's row tile has up to 256 tokens; keys only some of them see lie after the first
                 // token, or leave the first tokens' windows: 256 bits by the distance, of either kind.
                 const int bit = (key > t.p0 ? key - t.p0 - 1 : key - (max(t.p0, 0) - a.window + 1)) & 255;
-                const uint32_t at = smem_u32(&odd[item_no % 3 * 8 + (bit >> 5)]), mark = 1u << (bit & 31);
-                or_shared(mapa_shared(at, 0), mark);
-                or_shared(mapa_shared(at, 1), mark);
+                const uint32_t to = smem_u32(&odd[item_no % 3 * 8 + (bit >> 5)]), mark = 1u << (bit & 31);
+                or_shared(mapa_shared(to, 0), mark);
+                or_shared(mapa_shared(to, 1), mark);
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
               }
             }
             fence_proxy_async_shared();
@@ -836,9 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long item_start = pos - u0;
       // A piece's place: this pair's first if the item began before the pair's share or with it.
       float* piece = a.chunk_partial + (2LL * me + (begin >= item_start ? 0 : 1)) * kChunkPieceFloats;
-#pragma unroll 1
-      for (int c = 0; c < C::DV / 2; c += 32) {
-        uint32_t o[32];
+      // 32 columns of O at a time, with what was cleared of V put back.
+      auto columns = [&](int c, uint32_t (&o)[32]) {
         const int col = half * (C::DV / 2) + c;
         tmem_ld32_nowait(tmem + lanes + col, o);
         tmem_wait_ld();
@@ -867,27 +923,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (whole) {
-          if (live) {
-            uint4* to = reinterpret_cast<uint4*>(a.out + row * D + vhalf * C::DV + col);
+      };
+      auto o_is_free = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first(o_free);
+      };
+      if (whole) {
+        // All of the row's columns as bf16 first, so that O is free for the next item.
+        constexpr int kGroups = C::DV / 64;  // of 32 columns
+        uint32_t w[kGroups][16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              to[i] = make_uint4(pack_bf16(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f),
-                                 pack_bf16(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f),
-                                 pack_bf16(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f),
-                                 pack_bf16(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f));
+        for (int c = 0; c < kGroups; ++c) {
+          uint32_t o[32];
+          columns(32 * c, o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[c][i] = pack_bf16(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
+        }
+        o_is_free();
+        // Four lanes trade their rows' four 16-byte pieces of 64, so that a store writes 64 bytes of a row
+        // from neighbouring lanes: lane i of the four has piece i of each row.
+        uint16_t* to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned long long own = live ? reinterpret_cast<unsigned long long>(a.out + row * D + vhalf * C::DV + half * (C::DV / 2)) : 0ull;
+          to[k] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, own, (lane & ~3) + k)) ;
+        }
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) {
+#pragma unroll
+          for (int d = 1; d <= 2; d <<= 1) {
+            const bool up = lane & d;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k & d) continue;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t &lo_w = w[c][4 * k + i], &hi_w = w[c][4 * (k | d) + i];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo_w : hi_w, d);
+                if (up) lo_w = got;
+                else hi_w = got;
+              }
+            }
           }
-        } else if (live) {
-          float4* to = reinterpret_cast<float4*>(piece + rr * C::DV + col);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (to[k])
+              *reinterpret_cast<uint4*>(to[k] + 32 * c + (lane & 3) * 8) =
+                  make_uint4(w[c][4 * k], w[c][4 * k + 1], w[c][4 * k + 2], w[c][4 * k + 3]);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < C::DV / 2; c += 32) {
+          uint32_t o[32];
+          columns(c, o);
+          float4* to = reinterpret_cast<float4*>(piece + rr * C::DV + half * (C::DV / 2) + c);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            to[i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+            if (live) to[i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
                                 __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
         }
+        o_is_free();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_first(o_free);
       if (half == 0) {
         if (!whole) {
           piece[256 * 256 + rr] = ref;
@@ -905,38 +1002,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (bool more = start(); more; more = next(), ++item_no) {
       const int head = part / C::kHalves;
       if (item_no > 0) wait(q_free, (item_no - 1) & 1, kStatusWaitEmpty);
-      // A warp takes 32 rows, some at a time; a lane 16 bytes of a row and every 512 bytes on.
+      // A warp brings 32 rows; each lane knows where one of them is, or that there is none.
       constexpr int kVecs = D / 8 < 32 ? 1 : D / 256;            // 16-byte vectors of a row per lane
       constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;            // lanes of a row
       constexpr int kRowsAtOnce = 32 / kLanes;
-      constexpr int kBatch = 8 / kVecs;
-#pragma unroll 1
-      for (int g = 0; g < 32; g += kBatch * kRowsAtOnce) {
-        uint4 x[kBatch][kVecs];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int rr = static_cast<int>(rank) * kRows + awarp * 32 + g + b * kRowsAtOnce + lane / kLanes;
-          const int tok = rr / a.group;
+      const int rr = static_cast<int>(rank) * kRows + awarp * 32 + lane, tok = rr / a.group;
+      const unsigned long long own_row =
+          tok >= t.nt ? 0ull
+                      : reinterpret_cast<unsigned long long>(a.q.ptr + static_cast<long long>(t.row0 + tok) * a.q.token_stride +
+                                                             (head * a.group + rr % a.group) * a.q.head_stride);
+      if constexpr (!E4M3) {
+#pragma unroll 8
+        for (int g = 0; g < 32; g += kRowsAtOnce) {
+          const unsigned long long from = __shfl_sync(0xffffffffu, own_row, g + lane / kLanes);
+          const int r = awarp * 32 + g + lane / kLanes;
 #pragma unroll
           for (int v = 0; v < kVecs; ++v) {
-            x[b][v] = make_uint4(0u, 0u, 0u, 0u);
-            if (tok < t.nt)
-              x[b][v] = *reinterpret_cast<const uint4*>(a.q.ptr + static_cast<long long>(t.row0 + tok) * a.q.token_stride +
-                                                        (head * a.group + rr % a.group) * a.q.head_stride +
-                                                        (lane % kLanes + v * 32) * 8);
+            const uint32_t byte = (lane % kLanes + v * 32) * 16;
+            // (A row that is none reads nothing and leaves zeros; any address will do.)
+            const unsigned long long at = from ? from + byte : reinterpret_cast<unsigned long long>(a.q.ptr);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             smem_u32(sq) + (byte >> 7) * kChunk + r * 128 + ((byte & 127) ^ ((r & 7) << 4))),
+                         "l"(at), "r"(from ? 16 : 0)
+                         : "memory");
           }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      } else {
+        constexpr int kBatch = 8 / kVecs;
+#pragma unroll 1
+        for (int g = 0; g < 32; g += kBatch * kRowsAtOnce) {
+          uint4 x[kBatch][kVecs];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int r = awarp * 32 + g + b * kRowsAtOnce + lane / kLanes;
-          const uint32_t swz = (r & 7) << 4;
-          if constexpr (!E4M3) {
+          for (int b = 0; b < kBatch; ++b) {
+            const unsigned long long from = __shfl_sync(0xffffffffu, own_row, g + b * kRowsAtOnce + lane / kLanes);
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
-              const uint32_t byte = (lane % kLanes + v * 32) * 16;
-              *reinterpret_cast<uint4*>(sq + (byte >> 7) * kChunk + r * 128 + ((byte & 127) ^ swz)) = x[b][v];
+              x[b][v] = make_uint4(0u, 0u, 0u, 0u);
+              if (from) x[b][v] = *reinterpret_cast<const uint4*>(from + (lane % kLanes + v * 32) * 16);
             }
-          } else {
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int r = awarp * 32 + g + b * kRowsAtOnce + lane / kLanes;
+            const uint32_t swz = (r & 7) << 4;
             // A power of two that brings the row's largest magnitude into [128, 256).
             uint32_t top = 0;
 #pragma unroll
