@@ -81,9 +81,9 @@ struct Chk {
   static constexpr int NV = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : (D == 512 ? 2 : D == 256 ? 4 : 6);
   static constexpr int NW = E4M3 ? (D == 512 ? 2 : 4) : 0;
   static constexpr int kScaleBytes = E4M3 ? 2 * 2 * KT * 4 : 0;
-  static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 15) + 24 + (E4M3 ? 32 : 96) + 15) / 16 * 16;
+  static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 18) + 24 + (E4M3 ? 32 : 96) + 15) / 16 * 16;
   static constexpr int kSmem =
-      kQBytes + NK * kKStage + NV * kVStage + NW * kChunk + kScaleBytes + kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
+      kQBytes + NK * kKStage + NV * kVStage + NW * kChunk + kScaleBytes + 3 * kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(E4M3 ? NW % kVTile == 0 : NV % kVTile == 0, "the chunks of a key tile's V lie next to each other");
 };
@@ -218,7 +218,6 @@ __device__ __forceinline__ void or_shared(uint32_t addr, uint32_t bits) {
   asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(bits) : "memory");
 }
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 __device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 6, 128;" ::: "memory"); }
 
 // ------------------------------------------------------------------ the list of row tiles
@@ -334,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* w_ring = v_ring + C::NV * C::kVStage;
   float* scales = reinterpret_cast<float*>(w_ring + C::NW * kChunk);  // [2][2][KT]
   float* exch = scales + C::kScaleBytes / 4;                          // [kRows]
-  uint8_t* q_exp = reinterpret_cast<uint8_t*>(exch + kRows);          // [2][kRows] (e4m3), of alternate items
+  float* fin = exch + kRows;  // [2][kRows] what an item's O is multiplied by, of alternate items
+  uint8_t* q_exp = reinterpret_cast<uint8_t*>(fin + 2 * kRows);          // [2][kRows] (e4m3), of alternate items
   uint64_t* full_k = reinterpret_cast<uint64_t*>(q_exp + (E4M3 ? 2 * kRows : 0));  // first CTA's: both CTAs' keys
   uint64_t* empty_k = full_k + C::NK;
   uint64_t* full_v = empty_k + C::NK;    // this CTA's part
@@ -350,7 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = o_free + 1;         // first CTA's
   uint64_t* q_free = q_full + 1;
   uint64_t* q_scaled = q_free + 1;       // [2]: the softmax may be an item behind the queries
-  uint64_t* drain = q_scaled + 2;
+  uint64_t* o_full = q_scaled + 2;       // an item's last P V is complete
+  uint64_t* fin_full = o_full + 1;       // [2]
+  uint64_t* drain = fin_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* scale_step = reinterpret_cast<float*>(tmem_slot + 2);  // [2] what O is multiplied by before a tile
@@ -388,7 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_ready[s], 2 * kSoftmaxWarps);
     }
     mbar_init(o_done, 1);
-    mbar_init(o_free, 2 * kSoftmaxWarps);
+    mbar_init(o_free, 2 * kAuxWarps);
+    mbar_init(o_full, 1);
+    mbar_init(&fin_full[0], kSoftmaxWarps / 2);
+    mbar_init(&fin_full[1], kSoftmaxWarps / 2);
     mbar_init(q_full, 2 * kAuxWarps);
     mbar_init(q_free, 1);
     mbar_init(drain, 1);
@@ -477,6 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     look();
     return n > 0;
   };
+  // An item's piece: this pair's first if the item began before the pair's share or with it.
+  auto piece_of = [&](long long item_start) {
+    return a.chunk_partial + (2LL * me + (begin >= item_start ? 0 : 1)) * kChunkPieceFloats;
+  };
   const int R = 1 << a.c.page_log2;
   // Whether every row of the item sees every key of the tile.
   auto tile_at = [&](int i) { return i < t.front ? i : i + t.skip; };
@@ -488,6 +497,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto any_sees = [&](int j) {
     const int p1 = t.p0 + t.nt - 1;
     return j <= p1 && (a.window == 0 || j > max(t.p0, 0) - a.window || j < a.sinks);
+  };
+
+  // Adds the values that were cleared of V (bf16) back to 32 columns of the row of the token at p.
+  auto put_back = [&](const KvRowTile& it, int head, int col, int p, int no, uint32_t (&o)[32]) {
+    const int p1 = it.p0 + it.nt - 1, lo = a.window > 0 ? p - a.window + 1 : 0;
+    // Each set bit stands for up to two keys; a key that every row of the tile sees was not cleared.
+    for (int b = 0; b < 512; ++b) {
+      if (!(odd[no % 3 * 8 + ((b & 255) >> 5)] >> (b & 31) & 1)) continue;
+      const int key = b < 256 ? it.p0 + 1 + b : max(it.p0, 0) - a.window + 1 + b - 256;
+      if (b >= 256 && (a.window == 0 || key > it.p0)) continue;
+      if (key < 0 || key > p || (key < lo && key >= a.sinks)) continue;
+      if (key <= it.p0 && (a.window == 0 || key > p1 - a.window || key < a.sinks)) continue;
+      const int page = kv_page(a.b, a.c, it.seq, key >> a.c.page_log2, a.status);
+      if (page < 0) continue;
+      const uint16_t* v =
+          reinterpret_cast<const uint16_t*>(a.c.v) +
+          ((((static_cast<long long>(page) * a.c.kv_heads + head) << a.c.page_log2) + (key & (R - 1))) * D + col);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t x = static_cast<uint32_t>(v[i]) << 16;
+        if ((x & 0x7f800000u) == 0x7f800000u) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(x));
+      }
+    }
   };
 
   if (warp == 0) {
@@ -663,6 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int st = 0; st < C::kVTile; ++st) commit_pair_elect(&v_empty[u + st]);
           vs = vs + C::kVTile == NVW ? 0 : vs + C::kVTile;
           commit_pair_elect(o_done);
+          if (j + 1 >= tiles) commit_pair_elect(o_full);
         }
       }
       if (!alive) {
@@ -864,133 +897,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive_first(&p_ready[tile_no & 1]);
       }
 
-      // The item's output: its row sums, then O.
+      // The rows' sums, and what the output is multiplied by; warps 12..15 write it.
       pair_sync(quarter);  // (exch may still be read for the last tile's reference)
       if (half == 1) exch[r] = l;
       pair_sync(quarter);
       if (half == 0) {
         l += exch[r];
-        exch[r] = l;
-      }
-      pair_sync(quarter);
-      l = exch[r];
-      if constexpr (!E4M3) {
-        // The marks of the item after the next: the other CTA may be in the next one already.
-        if (stid < 8) odd[(item_no + 2) % 3 * 8 + stid] = 0;
-      }
-      wait(o_done, (tile_no - 1) & 1, kStatusWaitAccFull);
-      tc_fence_after();
-      softmax_sync();
-      uint32_t cleared = 0;
-      if constexpr (!E4M3) {
-        for (int i = 0; i < 8; ++i) cleared |= odd[item_no % 3 * 8 + i];
-      }
-      const bool whole = i0 == 0 && n == t.count;
-      float vs = 1.0f;
-      if constexpr (E4M3) vs = vref * 0.0078125f;
-      const float f = whole ? (l == 0.0f ? 0.0f : vs / l) : vs;
-      const long long row = static_cast<long long>(t.row0 + tok) * a.q_heads + head * a.group + rr % a.group;
-      const long long item_start = pos - u0;
-      // A piece's place: this pair's first if the item began before the pair's share or with it.
-      float* piece = a.chunk_partial + (2LL * me + (begin >= item_start ? 0 : 1)) * kChunkPieceFloats;
-      // 32 columns of O at a time, with what was cleared of V put back.
-      auto columns = [&](int c, uint32_t (&o)[32]) {
-        const int col = half * (C::DV / 2) + c;
-        tmem_ld32_nowait(tmem + lanes + col, o);
-        tmem_wait_ld();
-        reg_fence32(o);
-        if constexpr (!E4M3) {
-          if (cleared) {
-            // Each set bit stands for up to two keys; a key that is not hidden from some row of the
-            // tile was not cleared.
-            for (int b = 0; b < 512; ++b) {
-              if (!(odd[item_no % 3 * 8 + ((b & 255) >> 5)] >> (b & 31) & 1)) continue;
-              const int p1 = t.p0 + t.nt - 1;
-              const int key = b < 256 ? t.p0 + 1 + b : max(t.p0, 0) - a.window + 1 + b - 256;
-              if (b >= 256 && (a.window == 0 || key < 0 || key > t.p0)) continue;
-              if (key < 0 || key > p || (key < lo && key >= a.sinks)) continue;
-              if (key <= t.p0 && (a.window == 0 || key > p1 - a.window || key < a.sinks)) continue;
-              const int page = kv_page(a.b, a.c, t.seq, key >> a.c.page_log2, a.status);
-              if (page < 0) continue;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) +
-                                  ((((static_cast<long long>(page) * a.c.kv_heads + head) << a.c.page_log2) + (key & (R - 1))) * D +
-                                   vhalf * C::DV + col);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint32_t x = static_cast<uint32_t>(v[i]) << 16;
-                if ((x & 0x7f800000u) == 0x7f800000u) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(x));
-              }
-            }
-          }
-        }
-      };
-      auto o_is_free = [&] {
-        tc_fence_before();
+        const bool whole = i0 == 0 && n == t.count;
+        float vs_f = 1.0f;
+        if constexpr (E4M3) vs_f = vref * 0.0078125f;
+        fin[(item_no & 1) * kRows + r] = whole ? (l == 0.0f ? 0.0f : vs_f / l) : vs_f;
         __syncwarp();
-        if (lane == 0) arrive_first(o_free);
-      };
-      if (whole) {
-        // All of the row's columns as bf16 first, so that O is free for the next item.
-        constexpr int kGroups = C::DV / 64;  // of 32 columns
-        uint32_t w[kGroups][16];
-#pragma unroll
-        for (int c = 0; c < kGroups; ++c) {
-          uint32_t o[32];
-          columns(32 * c, o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[c][i] = pack_bf16(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
-        }
-        o_is_free();
-        // Four lanes trade their rows' four 16-byte pieces of 64, so that a store writes 64 bytes of a row
-        // from neighbouring lanes: lane i of the four has piece i of each row.
-        uint16_t* to[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const unsigned long long own = live ? reinterpret_cast<unsigned long long>(a.out + row * D + vhalf * C::DV + half * (C::DV / 2)) : 0ull;
-          to[k] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, own, (lane & ~3) + k)) ;
-        }
-#pragma unroll
-        for (int c = 0; c < kGroups; ++c) {
-#pragma unroll
-          for (int d = 1; d <= 2; d <<= 1) {
-            const bool up = lane & d;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (k & d) continue;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t &lo_w = w[c][4 * k + i], &hi_w = w[c][4 * (k | d) + i];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo_w : hi_w, d);
-                if (up) lo_w = got;
-                else hi_w = got;
-              }
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (to[k])
-              *reinterpret_cast<uint4*>(to[k] + 32 * c + (lane & 3) * 8) =
-                  make_uint4(w[c][4 * k], w[c][4 * k + 1], w[c][4 * k + 2], w[c][4 * k + 3]);
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < C::DV / 2; c += 32) {
-          uint32_t o[32];
-          columns(c, o);
-          float4* to = reinterpret_cast<float4*>(piece + rr * C::DV + half * (C::DV / 2) + c);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (live) to[i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
-                                __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
-        }
-        o_is_free();
-      }
-      if (half == 0) {
+        if (lane == 0) mbar_arrive(&fin_full[item_no & 1]);
         if (!whole) {
+          float* piece = piece_of(pos - u0);
           piece[256 * 256 + rr] = ref;
           piece[256 * 257 + rr] = l;
         } else if (live && a.lse && vhalf == 0) {
-          a.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.693147181f;
+          a.lse[static_cast<long long>(t.row0 + tok) * a.q_heads + head * a.group + rr % a.group] =
+              l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.693147181f;
         }
       }
     }
@@ -999,6 +924,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int awarp = warp - kAuxWarp0;
     int item_no = 0, tile_no = 0, vs = 0, ws = 0;
     uint32_t v_phase = 0, w_phase = 0;
+
+    // The output of item `no`: lane by lane a row, 32 columns at a time.
+    auto output = [&](const KvRowTile& it, int it_part, bool whole, long long item_start, int no) {
+      const int head = it_part / C::kHalves, vhalf = it_part % C::kHalves;
+      const int r = awarp * 32 + lane, rr = static_cast<int>(rank) * kRows + r;
+      const int tok = rr / a.group;
+      const bool live = tok < it.nt;
+      const uint32_t at = tmem + (static_cast<uint32_t>(awarp * 32) << 16);
+      const unsigned long long own =
+          !live ? 0ull
+          : whole
+              ? reinterpret_cast<unsigned long long>(
+                    a.out + (static_cast<long long>(it.row0 + tok) * a.q_heads + head * a.group + rr % a.group) * D + vhalf * C::DV)
+              : reinterpret_cast<unsigned long long>(piece_of(item_start) + rr * C::DV);
+      // Four lanes trade their rows' pieces, so that a store writes 64 bytes of a row from neighbouring
+      // lanes (lane i of the four has piece i of each of their rows): a lane writing its own row alone
+      // touches 32 lines per instruction, and took three times as long.
+      unsigned long long to[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, own, (lane & ~3) + k);
+      auto trade = [&](uint32_t (&w)[16]) {
+#pragma unroll
+        for (int d = 1; d <= 2; d <<= 1) {
+          const bool up = lane & d;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k & d) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t &lo_w = w[4 * k + i], &hi_w = w[4 * (k | d) + i];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo_w : hi_w, d);
+              if (up) lo_w = got;
+              else hi_w = got;
+            }
+          }
+        }
+      };
+      if constexpr (!E4M3) {
+        // The marks of the item after the next (the softmax of either CTA may be in the next one already):
+        // the last output is done with them, and that item is reached only through this one's o_free.
+        aux_sync();
+        if (awarp == 0 && lane < 8) odd[(no + 2) % 3 * 8 + lane] = 0;
+        __syncwarp();
+      }
+      wait(&fin_full[no & 1], (no >> 1) & 1, kStatusWaitAccFull);
+      const float f = fin[(no & 1) * kRows + r];
+      wait(o_full, no & 1, kStatusWaitAccFull);
+      tc_fence_after();
+      uint32_t cleared = 0;
+      if constexpr (!E4M3) {
+        for (int i = 0; i < 8; ++i) cleared |= odd[no % 3 * 8 + i];
+      }
+#pragma unroll 1
+      for (int col = 0; col < C::DV; col += 32) {
+        uint32_t o[32];
+        tmem_ld32_nowait(at + col, o);
+        tmem_wait_ld();
+        reg_fence32(o);
+        if (col + 32 == C::DV) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first(o_free);
+        }
+        if constexpr (!E4M3) {
+          if (cleared && live) put_back(it, head, vhalf * C::DV + col, it.p0 + tok, no, o);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        if (whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          trade(w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (to[k])
+              *reinterpret_cast<uint4*>(to[k] + col * 2 + (lane & 3) * 16) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = o[16 * h + i];
+            trade(w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (to[k])
+                *reinterpret_cast<uint4*>(to[k] + (col + 16 * h) * 4 + (lane & 3) * 16) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+        }
+      }
+    };
+    KvRowTile was = {};
+    int was_part = 0;
+    bool was_whole = false;
+    long long was_start = 0;
     for (bool more = start(); more; more = next(), ++item_no) {
       const int head = part / C::kHalves;
       if (item_no > 0) wait(q_free, (item_no - 1) & 1, kStatusWaitEmpty);
@@ -1084,6 +1107,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive_first(q_full);
         if (E4M3) mbar_arrive(&q_scaled[item_no & 1]);
       }
+      // The item before is written once this one's queries (and first V) are on their way.
+      auto output_last = [&] {
+        if (item_no > 0) output(was, was_part, was_whole, was_start, item_no - 1);
+        was = t;
+        was_part = part;
+        was_whole = i0 == 0 && n == t.count;
+        was_start = pos - u0;
+      };
+      if constexpr (!E4M3) output_last();
       if constexpr (E4M3) {
         const int key = awarp * 32 + lane;
         float vref = __uint_as_float(0x00800000u);  // at least the values' largest scale so far, a power of two
@@ -1163,9 +1195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ws = 0;
             w_phase ^= 1;
           }
+          if (j == 0) output_last();
         }
       }
     }
+    if (item_no > 0) output(was, was_part, was_whole, was_start, item_no - 1);
   }
   __syncwarp();
   tc_fence_before();
