@@ -94,6 +94,31 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Two fp32 numbers in a register pair, and operations on both at once.
+__device__ __forceinline__ unsigned long long two(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -760,11 +785,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           vref = scale_ref[tile_no & 1];
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sk + i);
-            y[i] *= f.x;
-            y[i + 1] *= f.y;
-            y[i + 2] *= f.z;
-            y[i + 3] *= f.w;
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sk + i);
+            split(mul2(two(y[i], y[i + 1]), f.x), y[i], y[i + 1]);
+            split(mul2(two(y[i + 2], y[i + 3]), f.y), y[i + 2], y[i + 3]);
           }
         }
         if (masked) {
@@ -813,28 +836,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float base = ref == -INFINITY ? 0.0f : ref;
-        float sum0 = 0.0f, sum1 = 0.0f;
+        const unsigned long long qs2 = two(qs, qs), base2 = two(-base, -base);
+        unsigned long long sum2 = 0ull, sum3 = 0ull;  // two zeros each
         uint32_t w[32];
+        auto weigh = [&](bool hidden) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float e0 = exp2_approx(fmaf(y[2 * i], qs, -base)), e1 = exp2_approx(fmaf(y[2 * i + 1], qs, -base));
-          sum0 += e0;
-          sum1 += e1;
-          if constexpr (E4M3) {
-            const float2 v = *reinterpret_cast<const float2*>(sk + KT + 2 * i);
-            if (masked) {  // a hidden key's scale may be anything
-              e0 = e0 == 0.0f ? 0.0f : e0 * v.x;
-              e1 = e1 == 0.0f ? 0.0f : e1 * v.y;
+          for (int i = 0; i < 32; i += 2) {
+            float e[4];
+            split(fma2(two(y[2 * i], y[2 * i + 1]), qs2, base2), e[0], e[1]);
+            split(fma2(two(y[2 * i + 2], y[2 * i + 3]), qs2, base2), e[2], e[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[k] = exp2_approx(e[k]);
+            sum2 = add2(sum2, two(e[0], e[1]));
+            sum3 = add2(sum3, two(e[2], e[3]));
+            if constexpr (E4M3) {
+              const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sk + KT + 2 * i);
+              float x[4];
+              split(mul2(two(e[0], e[1]), v.x), x[0], x[1]);
+              split(mul2(two(e[2], e[3]), v.y), x[2], x[3]);
+              if (hidden) {  // a hidden key's scale may be anything
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = e[k] == 0.0f ? 0.0f : x[k];
+              }
+              w[i] = pack_f16(x[0], x[1]);
+              w[i + 1] = pack_f16(x[2], x[3]);
             } else {
-              e0 *= v.x;
-              e1 *= v.y;
+              w[i] = pack_bf16(e[0], e[1]);
+              w[i + 1] = pack_bf16(e[2], e[3]);
             }
-            w[i] = pack_f16(e0, e1);
-          } else {
-            w[i] = pack_bf16(e0, e1);
           }
-        }
-        l += sum0 + sum1;
+        };
+        if (E4M3 && masked) weigh(true);
+        else weigh(false);
+        float sums[4];
+        split(sum2, sums[0], sums[1]);
+        split(sum3, sums[2], sums[3]);
+        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         if constexpr (E4M3) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&scale_free[tile_no & 1]);
@@ -1024,6 +1061,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long was_start = 0;
     for (bool more = start(); more; more = next(), ++item_no) {
       const int head = part / C::kHalves;
+      // e4m3: this thread's key of the item's tiles. Its page id is fetched two tiles ahead, its scales one.
+      const int key = awarp * 32 + lane;
+      auto page_of = [&](int j) {
+        const int at = j < n ? tile_at(i0 + j) * KT + key : 0;
+        return j < n && any_sees(at) ? a.b.pages[t.seq * a.b.pages_stride + (at >> a.c.page_log2)] : -1;
+      };
+      auto scales_of = [&](int j, int page) {
+        float2 s = make_float2(0.0f, 0.0f);
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages)) {
+          const int at = tile_at(i0 + j) * KT + key;
+          const long long i = ((static_cast<long long>(page) * a.c.kv_heads + head) << a.c.page_log2) + (at & (R - 1));
+          s = make_float2(a.c.k_scale[i], a.c.v_scale[i]);
+        }
+        return s;
+      };
+      int next_page = -1;
+      float2 next_scales = make_float2(0.0f, 0.0f);
+      if constexpr (E4M3) {
+        const int page = page_of(0);
+        next_page = page_of(1);
+        next_scales = scales_of(0, page);
+      }
       if (item_no > 0) wait(q_free, (item_no - 1) & 1, kStatusWaitEmpty);
       // A warp brings 32 rows; each lane knows where one of them is, or that there is none.
       constexpr int kVecs = D / 8 < 32 ? 1 : D / 256;            // 16-byte vectors of a row per lane
@@ -1117,22 +1176,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if constexpr (!E4M3) output_last();
       if constexpr (E4M3) {
-        const int key = awarp * 32 + lane;
         float vref = __uint_as_float(0x00800000u);  // at least the values' largest scale so far, a power of two
         for (int j = 0; j < n; ++j, ++tile_no) {
           const int tile = tile_at(i0 + j);
           const bool masked = is_masked(tile);
           // The scales of this thread's key: for the keys as they are, for the values relative to vref.
-          float sk = 0.0f, sv = 0.0f;
-          const int pos_k = tile * KT + key;
-          if (!masked || any_sees(pos_k)) {
-            const int page = kv_page(a.b, a.c, t.seq, pos_k >> a.c.page_log2, a.status);
-            if (page >= 0) {
-              const long long at = ((static_cast<long long>(page) * a.c.kv_heads + head) << a.c.page_log2) + (pos_k & (R - 1));
-              sk = a.c.k_scale[at];
-              sv = a.c.v_scale[at];
-            }
-          }
+          const float sk = next_scales.x, sv = next_scales.y;
+          next_scales = scales_of(j + 1, next_page);
+          next_page = page_of(j + 2);
           const uint32_t bits = __float_as_uint(sv);
           const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
           if (lane == 0) aux_top[(tile_no & 1) * 4 + awarp] = top;
