@@ -331,7 +331,8 @@ size_t kv_rows_bytes(const KvRows& r, int tokens, int heads, int d) {
 
 // The workspace: control words (zeroed when the handle is made), then the kernels' pieces.
 struct KvLayout {
-  size_t status, counters, counters_in, n_tiles, partial, first_tile, tiles, first_unit, chunk_partial, total;
+  size_t status, counters, counters_in, n_tiles, partial, first_tile, tiles, first_unit, shares, joins, chunk_partial,
+      total;
 };
 
 size_t max_row_tiles(const moe_ffn_kv_config& c) {
@@ -354,7 +355,9 @@ KvLayout make_kv_layout(const moe_ffn_kv_config& c) {
   const size_t tiles = max_row_tiles(c);
   l.first_tile = take(static_cast<size_t>(c.max_seqs) * 4);
   l.tiles = take(tiles * sizeof(KvRowTile));
-  l.first_unit = take((tiles + 1) * 8);
+  l.first_unit = take(tiles * 8);
+  l.shares = take(kChunkMaxPairs * sizeof(KvShare));
+  l.joins = take(kChunkMaxPairs * sizeof(KvJoin));
   l.chunk_partial = take(static_cast<size_t>(2 * kChunkMaxPairs * kChunkPieceFloats) * 4);
   l.total = o;
   return l;
@@ -405,6 +408,8 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   kv->list.tiles = reinterpret_cast<KvRowTile*>(kv->ws + l.tiles);
   kv->list.first_unit = reinterpret_cast<long long*>(kv->ws + l.first_unit);
   kv->list.n_tiles = reinterpret_cast<int*>(kv->ws + l.n_tiles);
+  kv->list.shares = reinterpret_cast<KvShare*>(kv->ws + l.shares);
+  kv->list.joins = reinterpret_cast<KvJoin*>(kv->ws + l.joins);
   kv->list.max_tiles = static_cast<int>(max_row_tiles(*cfg));
   kv->chunk_partial = reinterpret_cast<float*>(kv->ws + l.chunk_partial);
   if (kv_decode_setup() != cudaSuccess || kv_chunk_setup(&kv->chunk_pairs) != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
@@ -476,6 +481,7 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   a.counters_in = kv->counters_in;
   a.partial = kv->partial;
   a.list = kv->list;
+  a.item_cost = a.c.e4m3 ? 5 : 3;
   a.chunk_partial = kv->chunk_partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -49,13 +49,31 @@ struct KvRowTile {
   int unused;
 };
 
+// A pair's share of the work: units [begin, end), and the item it begins in.
+struct KvShare {
+  long long begin, end;
+  int entry, part, u0;  // the row tile, the kv head (and half of V's width) and the unit of the item
+  int unused;
+};
+
+// An item that shares cut into pieces, to be joined.
+struct KvJoin {
+  int row0, nt;     // its tokens; nt 0: nothing to join
+  int part;
+  int first, count; // the pairs that have pieces of it
+  int first_place;  // where the first one's is
+  int unused[2];
+};
+
 // The row tiles of a call, in the workspace.
 struct KvChunkList {
   int* first_tile;        // [max_seqs] of each sequence
   KvRowTile* tiles;
-  long long* first_unit;  // [row tiles + 1] shares of the work are counted in units, see kv_chunk.cu
+  long long* first_unit;  // [row tiles] shares of the work are counted in units, see kv_chunk.cu
   int* n_tiles;
   int max_tiles;          // the list's room
+  KvShare* shares;        // [kChunkMaxPairs]
+  KvJoin* joins;          // [kChunkMaxPairs], by the share that begins inside the item
 };
 
 struct KvAttn {
@@ -74,6 +92,7 @@ struct KvAttn {
   int* counters_in; // [2 * kDecodeMaxCtas] the same, of groups of an item's pieces
   float* partial;   // pieces of items that several CTAs share
   KvChunkList list;      // the same for chunks of tokens
+  int item_cost;         // what an item costs beside its key tiles, in key tiles (chunks of tokens)
   float* chunk_partial;
 };
 

@@ -20,7 +20,7 @@
 // in fp32 and rounded to bf16 (2^-8 of each weight) for the product with V.
 //
 // Work. An item is a row tile, a kv head and a half of V's width where it has two. The key tiles of all
-// items, one after the other with kItemCost more for each item, are shared out evenly over the pairs
+// items, one after the other with item_cost more for each item, are shared out evenly over the pairs
 // of SMs, so that ragged batches, causal triangles and a few rows over a long cache all end together. Items
 // cut by the shares leave fp32 pieces (unnormalised output, maximum, sum) that kv_chunk_join_kernel
 // adds in the order of the tiles.
@@ -58,8 +58,6 @@ constexpr int KT = 128;      // positions of a key tile
 constexpr int kHalfKeys = 64;  // of which a CTA holds the keys of 64
 constexpr int kChunk = 16384;  // 128 rows of 128 bytes
 constexpr int kSoftmaxWarp0 = 4, kSoftmaxWarps = 8, kAuxWarp0 = 12, kAuxWarps = 4;
-// What an item costs beside its key tiles, in key tiles.
-constexpr int kItemCost = 2;
 
 template <int D, bool E4M3>
 struct Chk {
@@ -72,20 +70,20 @@ struct Chk {
   static constexpr int kKStage = kKChunks * kHalfKeys * 128;
   static constexpr int kKTile = kRow / 128 / kKChunks;    // stages of a key tile
   static constexpr int NK = E4M3 ? (D == 128 ? 6 : D == 256 ? 3 : 5) : (D == 512 ? 4 : 6);
-  // V: 128 rows of this CTA's half of the width. bf16: chunks of 64 dimensions; e4m3: rows of codes as
-  // they lie, and chunks of widened ones.
-  static constexpr int kVTile = DV / 128;                 // chunks of a key tile
-  static constexpr int kVBytes = E4M3 ? DV / 2 : 128;     // bytes of a loaded row
-  static constexpr int kVStage = KT * kVBytes;
-  static constexpr int kVLoads = E4M3 ? 1 : kVTile;       // loaded stages of a key tile
-  static constexpr int NV = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : (D == 512 ? 2 : D == 256 ? 4 : 6);
-  static constexpr int NW = E4M3 ? (D == 512 ? 2 : 4) : 0;
+  // V: 128 rows of this CTA's half of the width, a slot for a key tile. bf16: chunks of 64 dimensions;
+  // e4m3: rows of codes, as they lie where they are narrower than 128 bytes, and slots of widened ones.
+  static constexpr int kVTile = DV / 128;                 // chunks of 64 dimensions
+  static constexpr int kVBytes = E4M3 ? DV / 2 : 128;     // bytes of a loaded row (of a chunk)
+  static constexpr int kVLoads = E4M3 ? 1 : kVTile;
+  static constexpr int kVSlot = kVLoads * KT * kVBytes;
+  static constexpr int kWSlot = kVTile * kChunk;
+  static constexpr int NV = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : (D == 512 ? 1 : D == 256 ? 2 : 6);
+  static constexpr int NW = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : 0;
   static constexpr int kScaleBytes = E4M3 ? 2 * 2 * KT * 4 : 0;
   static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 18) + 24 + (E4M3 ? 32 : 96) + 15) / 16 * 16;
   static constexpr int kSmem =
-      kQBytes + NK * kKStage + NV * kVStage + NW * kChunk + kScaleBytes + 3 * kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
+      kQBytes + NK * kKStage + NV * kVSlot + NW * kWSlot + kScaleBytes + 3 * kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(E4M3 ? NW % kVTile == 0 : NV % kVTile == 0, "the chunks of a key tile's V lie next to each other");
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -216,6 +214,22 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t format, bool b_transpos
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Whether the phase of the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The lowest n bits, of all n below 0 or above 64 too.
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+  return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+}
+
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -291,7 +305,9 @@ __device__ long long block_scan(long long v, long long* warp_sums, long long* to
   return v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kListThreads) kv_chunk_list_kernel(const KvAttn a, int tokens) {
+__global__ void __launch_bounds__(kListThreads) kv_chunk_list_kernel(const KvAttn a, int tokens, int parts, int max_pairs) {
+  constexpr int kNear = 1024;  // row tiles whose first units are at hand in shared memory
+  __shared__ long long near_unit[kNear];
   __shared__ long long sums[32];
   pdl_wait();
   pdl_launch_dependents();
@@ -321,27 +337,52 @@ __global__ void __launch_bounds__(kListThreads) kv_chunk_list_kernel(const KvAtt
       }
       const KvRowTile t = row_tile(a, lo, kv_sequence(a.b, a.c, lo, a.status), (e - l.first_tile[lo]) * tokens, tokens);
       l.tiles[e] = t;
-      units = t.count > 0 ? t.count + kItemCost : 0;
+      units = t.count > 0 ? t.count + a.item_cost : 0;
     }
     const long long upto = block_scan(units, sums, &total);
     if (e < n_tiles) l.first_unit[e] = before + upto - units;
+    if (e < min(n_tiles, kNear)) near_unit[e] = before + upto - units;
     before += total;
   }
-  if (threadIdx.x == 0) {
-    l.first_unit[n_tiles] = before;
-    *l.n_tiles = n_tiles;
+  if (threadIdx.x == 0) *l.n_tiles = n_tiles;
+  __syncthreads();
+  // Where each pair's share begins, and the item it begins in if others have part in it: the first cut in
+  // an item stands for the item's join.
+  const int x = threadIdx.x;
+  if (x >= max_pairs) return;
+  const long long all = before * parts;
+  const int share = a.item_cost + 1;
+  const long long pairs = min(static_cast<long long>(max_pairs), (all + share - 1) / share);
+  KvShare s = {};
+  KvJoin j = {};
+  if (x < pairs) {
+    s.begin = x * all / pairs;
+    s.end = (x + 1) * all / pairs;
+    int lo = 0, hi = n_tiles;  // the last row tile with first unit * parts <= begin
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if ((mid < kNear ? near_unit[mid] : l.first_unit[mid]) * parts <= s.begin) lo = mid;
+      else hi = mid;
+    }
+    const KvRowTile t = l.tiles[lo];
+    const int units = t.count + a.item_cost;
+    const long long off = s.begin - (lo < kNear ? near_unit[lo] : l.first_unit[lo]) * parts;
+    s.entry = lo;
+    s.part = static_cast<int>(off / units);
+    s.u0 = static_cast<int>(off % units);
+    const long long item_start = s.begin - s.u0;
+    const long long first = ((item_start + share) * pairs - 1) / all, last = ((item_start + units) * pairs - 1) / all;
+    if (first + 1 == x && last > first) {
+      j.row0 = t.row0;
+      j.nt = t.nt;
+      j.part = s.part;
+      j.first = static_cast<int>(first);
+      j.count = static_cast<int>(last - first) + 1;
+      j.first_place = 2 * j.first + (first * all / pairs >= item_start ? 0 : 1);
+    }
   }
-}
-
-// The row tile whose units (times `parts`) hold unit `at`.
-__device__ __forceinline__ int find_tile(const KvChunkList& l, int n_tiles, long long at, int parts) {
-  int lo = 0, hi = n_tiles;  // the last with first_unit * parts <= at that has units
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (l.first_unit[mid] * parts <= at) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+  l.shares[x] = s;
+  l.joins[x] = j;
 }
 
 // ------------------------------------------------------------------ the attention
@@ -355,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sq = smem;
   uint8_t* k_ring = sq + C::kQBytes;
   uint8_t* v_ring = k_ring + C::NK * C::kKStage;
-  uint8_t* w_ring = v_ring + C::NV * C::kVStage;
-  float* scales = reinterpret_cast<float*>(w_ring + C::NW * kChunk);  // [2][2][KT]
+  uint8_t* w_ring = v_ring + C::NV * C::kVSlot;
+  float* scales = reinterpret_cast<float*>(w_ring + C::NW * C::kWSlot);  // [2][2][KT]
   float* exch = scales + C::kScaleBytes / 4;                          // [kRows]
   float* fin = exch + kRows;  // [2][kRows] what an item's O is multiplied by, of alternate items
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(fin + 2 * kRows);          // [2][kRows] (e4m3), of alternate items
@@ -452,7 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int n_tiles = *a.list.n_tiles;
   const int parts = a.c.kv_heads * C::kHalves;
-  const long long total = a.list.first_unit[n_tiles] * parts;
   {  // Rows of no sequence, and of tokens that see nothing.
     const int used = a.b.n_seqs > 0 ? min(max(a.b.cu_q[a.b.n_seqs], 0), a.b.n_tokens) : 0;
     auto clear = [&](long long to) {
@@ -468,11 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = tid; i < t.nt * a.q_heads; i += kThreads) clear(static_cast<long long>(t.row0) * a.q_heads + i);
     }
   }
-  constexpr int kShare = kItemCost + 1;
-  const long long pairs = min(static_cast<long long>(gridDim.x / 2), (total + kShare - 1) / kShare);
   const int me = blockIdx.x / 2;
-  const bool busy = me < pairs;
-  const long long begin = busy ? me * total / pairs : 0, end = busy ? (me + 1) * total / pairs : 0;
+  const KvShare my_share = a.list.shares[me];
+  const long long begin = my_share.begin, end = my_share.end;
 
   // The walk over this pair's items, the same for every role.
   int entry = 0, part = 0, u0 = 0;
@@ -480,18 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   KvRowTile t;
   int un = 0, i0 = 0, n = 0;  // of the item: units in the share, first key tile and key tiles
   auto look = [&] {
-    const int units = t.count + kItemCost;
+    const int units = t.count + a.item_cost;
     un = static_cast<int>(min(static_cast<long long>(units - u0), end - pos));
-    i0 = max(u0 - kItemCost, 0);
-    n = max(u0 + un - kItemCost, 0) - i0;
+    i0 = max(u0 - a.item_cost, 0);
+    n = max(u0 + un - a.item_cost, 0) - i0;
   };
   auto start = [&] {
-    if (!busy) return false;
-    entry = find_tile(a.list, n_tiles, begin, parts);
+    if (begin >= end) return false;
+    entry = my_share.entry;
+    part = my_share.part;
+    u0 = my_share.u0;
     t = a.list.tiles[entry];
-    const long long off = begin - a.list.first_unit[entry] * parts;
-    part = static_cast<int>(off / (t.count + kItemCost));
-    u0 = static_cast<int>(off % (t.count + kItemCost));
     look();
     return n > 0;
   };
@@ -614,24 +651,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           last = cur;
         }
         if (j < 0 || !alive) continue;
-        const bool mine = v_lane && ((last.who >> box) & 1);
-        const uint32_t bytes = __popc(last.who) * static_cast<uint32_t>(C::kVBytes << rows_log2);
-        for (int st = 0; st < C::kVLoads; ++st) {
-          if (v_issued >= C::NV) alive = __all_sync(0xffffffffu, wait(&empty_v[vs], v_phase ^ 1, kStatusWaitEmpty));
-          if (!alive) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full_v[vs], bytes);
-          __syncwarp();
-          if (mine) {
-            // The CTA's half of the item's width begins at this byte of the row.
-            const int byte = (half * C::DV + static_cast<int>(rank) * (C::DV / 2)) * (E4M3 ? 1 : 2) + st * 128;
-            tma_rows_pair(v_to + vs * C::kVStage, &map_v, mapa_shared(smem_u32(&full_v[vs]), rank), byte & 127, last.row,
-                          byte >> 7);
-          }
-          ++v_issued;
-          if (++vs == C::NV) {
-            vs = 0;
-            v_phase ^= 1;
-          }
+        if (v_issued >= C::NV) alive = __all_sync(0xffffffffu, wait(&empty_v[vs], v_phase ^ 1, kStatusWaitEmpty));
+        if (!alive) break;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full_v[vs], __popc(last.who) * static_cast<uint32_t>((C::kVBytes << rows_log2) * C::kVLoads));
+        __syncwarp();
+        if (v_lane && ((last.who >> box) & 1)) {
+          // The CTA's half of the item's width begins at this byte of the row.
+          const int byte = (half * C::DV + static_cast<int>(rank) * (C::DV / 2)) * (E4M3 ? 1 : 2);
+          const uint32_t bar = mapa_shared(smem_u32(&full_v[vs]), rank);
+#pragma unroll
+          for (int c = 0; c < C::kVLoads; ++c)
+            tma_rows_pair(v_to + vs * C::kVSlot + c * kChunk, &map_v, bar, byte & 127, last.row, (byte >> 7) + c);
+        }
+        ++v_issued;
+        if (++vs == C::NV) {
+          vs = 0;
+          v_phase ^= 1;
         }
       }
     }
@@ -712,13 +748,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t p = tm + 256 + (uniform(tile_no) & 1) * KT;
           const int u = uniform(vs);
-          const uint64_t vb = smem_desc_v(smem_u32(v_chunks) + u * kChunk);
+          const uint64_t vb = smem_desc_v(smem_u32(v_chunks) + u * (E4M3 ? C::kWSlot : C::kVSlot));
           const uint32_t add = uniform(j > 0 ? 1 : 0);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
             umma_ta_pair_elect(tm, p + 8 * k, vb + k * (2048 >> 4), kIdescV, k > 0 ? 1u : add);
-          for (int st = 0; st < C::kVTile; ++st) commit_pair_elect(&v_empty[u + st]);
-          vs = vs + C::kVTile == NVW ? 0 : vs + C::kVTile;
+          commit_pair_elect(&v_empty[u]);
+          if (++vs == NVW) vs = 0;
           commit_pair_elect(o_done);
           if (j + 1 >= tiles) commit_pair_elect(o_full);
         }
@@ -763,83 +799,99 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* sk = scales + (tile_no & 1) * 2 * KT + half * 64;
         wait(&s_full[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitAccFull);
         tc_fence_after();
-        const uint32_t s_at = tmem + lanes + 256 + (tile_no & 1) * KT;
-        float y[64];
-        {
-          uint32_t b0[32], b1[32];
-          tmem_ld32_nowait(s_at + half * 64, b0);
-          tmem_ld32_nowait(s_at + half * 64 + 32, b1);
-          tmem_wait_ld();
-          reg_fence32(b0);
-          reg_fence32(b1);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            y[i] = __uint_as_float(b0[i]);
-            y[32 + i] = __uint_as_float(b1[i]);
-          }
-        }
         float step = 1.0f;
         if constexpr (E4M3) {
           wait(&scale_full[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitFull);
           step = scale_step[tile_no & 1];
           vref = scale_ref[tile_no & 1];
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sk + i);
-            split(mul2(two(y[i], y[i + 1]), f.x), y[i], y[i + 1]);
-            split(mul2(two(y[i + 2], y[i + 3]), f.y), y[i + 2], y[i + 3]);
-          }
         }
+        // What the end of the tile waits for has mostly happened by now.
+        const bool v_here = mbar_test(&v_full[vs], v_phase), pv_done = tile_no == 0 || mbar_test(o_done, (tile_no - 1) & 1);
+        const uint32_t s_at = tmem + lanes + 256 + (tile_no & 1) * KT;
+        // The keys of this half that the row sees, by bits.
+        unsigned long long seen = ~0ull;
         if (masked) {
           const int k0 = tile * KT + half * 64;
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (k0 + i > p || (k0 + i < lo && k0 + i >= a.sinks)) y[i] = -INFINITY;
+          seen = low_bits(p + 1 - k0) & ~(low_bits(lo - k0) & ~low_bits(a.sinks - k0));
         }
-        float top0 = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          top0 = fmaxf(top0, fmaxf(y[i], y[i + 1]));
-          top1 = fmaxf(top1, fmaxf(y[i + 2], y[i + 3]));
-        }
-        // (A row scale that is NaN makes no maximum.)
-        float top = fmaxf(top0, top1) * qs;
-        if (pair_sync_or(quarter, top > ref + 8.0f || step != 1.0f)) {
-          // The reference moves to the maximum so far, of both halves.
-          if (half == 1) exch[r] = top;
-          pair_sync(quarter);
-          if (half == 0) {
-            top = fmaxf(top, exch[r]);
-            exch[r] = top;
-          }
-          pair_sync(quarter);
-          top = fmaxf(ref, exch[r]);
-          const float f = exp2_approx(ref - (top == -INFINITY ? 0.0f : top));
-          ref = top;
-          l *= f;
-          if (j > 0) {
-            const float of = f * step;
-            wait_pv();
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < C::DV / 2; c += 32) {
-              uint32_t o[32];
-              const uint32_t at = tmem + lanes + half * (C::DV / 2) + c;
-              tmem_ld32_nowait(at, o);
-              tmem_wait_ld();
-              reg_fence32(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * of);
-              tmem_st32(at, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        const float base = ref == -INFINITY ? 0.0f : ref;
-        const unsigned long long qs2 = two(qs, qs), base2 = two(-base, -base);
-        unsigned long long sum2 = 0ull, sum3 = 0ull;  // two zeros each
+        bool move = j == 0 || step != 1.0f;  // the reference is to move
         uint32_t w[32];
-        auto weigh = [&](bool hidden) {
+        float sum;
+        for (;;) {
+          float y[64];
+          {
+            uint32_t b0[32], b1[32];
+            tmem_ld32_nowait(s_at + half * 64, b0);
+            tmem_ld32_nowait(s_at + half * 64 + 32, b1);
+            tmem_wait_ld();
+            reg_fence32(b0);
+            reg_fence32(b1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              y[i] = __uint_as_float(b0[i]);
+              y[32 + i] = __uint_as_float(b1[i]);
+            }
+          }
+          if constexpr (E4M3) {
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sk + i);
+              split(mul2(two(y[i], y[i + 1]), f.x), y[i], y[i + 1]);
+              split(mul2(two(y[i + 2], y[i + 3]), f.y), y[i + 2], y[i + 3]);
+            }
+          }
+          if (masked) {
+            const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (!(s0 >> i & 1u)) y[i] = -INFINITY;
+              if (!(s1 >> i & 1u)) y[32 + i] = -INFINITY;
+            }
+          }
+          if (move) {
+            // The reference moves to the maximum so far, of both halves. (A row scale that is NaN makes no
+            // maximum.)
+            float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              top0 = fmaxf(top0, fmaxf(y[i], y[i + 1]));
+              top1 = fmaxf(top1, fmaxf(y[i + 2], y[i + 3]));
+            }
+            float top = fmaxf(top0, top1) * qs;
+            if (half == 1) exch[r] = top;
+            pair_sync(quarter);
+            if (half == 0) {
+              top = fmaxf(top, exch[r]);
+              exch[r] = top;
+            }
+            pair_sync(quarter);
+            top = fmaxf(ref, exch[r]);
+            const float f = exp2_approx(ref - (top == -INFINITY ? 0.0f : top));
+            ref = top;
+            l *= f;
+            if (j > 0) {
+              const float of = f * step;
+              wait_pv();
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < C::DV / 2; c += 32) {
+                uint32_t o[32];
+                const uint32_t at = tmem + lanes + half * (C::DV / 2) + c;
+                tmem_ld32_nowait(at, o);
+                tmem_wait_ld();
+                reg_fence32(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * of);
+                tmem_st32(at, o);
+              }
+              tmem_wait_st();
+            }
+            step = 1.0f;
+          }
+          // A reference of -inf (nothing but hidden keys and NaN so far) counts as 0.
+          const float base = ref == -INFINITY ? 0.0f : ref;
+          const unsigned long long qs2 = two(qs, qs), base2 = two(-base, -base);
+          unsigned long long sum2 = 0ull, sum3 = 0ull;  // two zeros each
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float e[4];
@@ -851,40 +903,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum3 = add2(sum3, two(e[2], e[3]));
             if constexpr (E4M3) {
               const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sk + KT + 2 * i);
-              float x[4];
-              split(mul2(two(e[0], e[1]), v.x), x[0], x[1]);
-              split(mul2(two(e[2], e[3]), v.y), x[2], x[3]);
-              if (hidden) {  // a hidden key's scale may be anything
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = e[k] == 0.0f ? 0.0f : x[k];
-              }
-              w[i] = pack_f16(x[0], x[1]);
-              w[i + 1] = pack_f16(x[2], x[3]);
+              split(mul2(two(e[0], e[1]), v.x), e[0], e[1]);
+              split(mul2(two(e[2], e[3]), v.y), e[2], e[3]);
+              w[i] = pack_f16(e[0], e[1]);
+              w[i + 1] = pack_f16(e[2], e[3]);
             } else {
               w[i] = pack_bf16(e[0], e[1]);
               w[i + 1] = pack_bf16(e[2], e[3]);
             }
           }
-        };
-        if (E4M3 && masked) weigh(true);
-        else weigh(false);
-        float sums[4];
-        split(sum2, sums[0], sums[1]);
-        split(sum3, sums[2], sums[3]);
-        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+          float sums[4];
+          split(sum2, sums[0], sums[1]);
+          split(sum3, sums[2], sums[3]);
+          sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+          // No weight is above the half row's sum, so a sum of at most 2^9 is all there is to check, once the
+          // row has a reference (its first tiles may have shown it nothing). One move is enough.
+          if (!pair_sync_or(quarter, !move && (sum > 512.0f || (ref == -INFINITY && seen != 0)))) break;
+          move = true;
+        }
+        l += sum;
         if constexpr (E4M3) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&scale_free[tile_no & 1]);
+          if (masked) {
+            // (A hidden key's scale may have been anything.)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t bits = static_cast<uint32_t>(seen >> (2 * i)) & 3u;
+              w[i] &= (bits & 1u ? 0xffffu : 0u) | (bits & 2u ? 0xffff0000u : 0u);
+            }
+          }
         }
         tmem_st32(s_at + half * 32, w);
         // V of this tile has arrived (what the MMA thread knows of it, it knows from here).
-        for (int st = 0; st < C::kVTile; ++st) wait(&v_full[vs + st], v_phase, kStatusWaitFull);
+        if (!v_here) wait(&v_full[vs], v_phase, kStatusWaitFull);
         if constexpr (!E4M3) {
           if (masked) {
             // V's rows that no row sees, and non-finite values that only some rows see.
             const int p1 = t.p0 + t.nt - 1;
             // A thread's vectors are the same 16 bytes of four keys, in each chunk.
-            uint4* v = reinterpret_cast<uint4*>(v_ring + vs * C::kVStage) + stid;
+            uint4* v = reinterpret_cast<uint4*>(v_ring + vs * C::kVSlot) + stid;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const int key = tile * KT + (stid >> 3) + 32 * m;
@@ -922,12 +980,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_shared();
           }
         }
-        vs += C::kVTile;
-        if (vs == NVW) {
+        if (++vs == NVW) {
           vs = 0;
           v_phase ^= 1;
         }
-        wait_pv();  // a barrier's phases are told apart by their parity: none may be passed over
+        if (!pv_done) wait_pv();  // a barrier's phases are told apart by their parity: none may be passed over
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -942,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += exch[r];
         const bool whole = i0 == 0 && n == t.count;
         float vs_f = 1.0f;
-        if constexpr (E4M3) vs_f = vref * 0.0078125f;
+        if constexpr (E4M3) vs_f = vref * 0.015625f;
         fin[(item_no & 1) * kRows + r] = whole ? (l == 0.0f ? 0.0f : vs_f / l) : vs_f;
         __syncwarp();
         if (lane == 0) mbar_arrive(&fin_full[item_no & 1]);
@@ -1197,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tile_no >= 2) wait(&scale_free[tile_no & 1], ((tile_no >> 1) - 1) & 1, kStatusWaitEmpty);
           float* to = scales + (tile_no & 1) * 2 * KT;
           to[key] = sk;
-          to[KT + key] = __fdiv_rn(sv, vref) * 128.0f;
+          to[KT + key] = __fdiv_rn(sv, vref) * 64.0f;
           if (awarp == 0 && lane == 0) {
             scale_step[tile_no & 1] = j == 0 ? 1.0f : before / vref;
             scale_ref[tile_no & 1] = vref;
@@ -1206,14 +1263,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&scale_full[tile_no & 1]);
           // V's codes to fp16, 16 at a time; rows no row sees to 0.
           wait(&full_v[vs], v_phase, kStatusWaitFull);
-          for (int c = 0; c < C::kVTile; ++c) {
-            if (tile_no * C::kVTile + c >= C::NW) wait(&empty_w[ws + c], w_phase ^ 1, kStatusWaitEmpty);
-          }
-          constexpr int kParts = C::kVBytes / 16;
-#pragma unroll 4
-          for (int i = awarp * 32 + lane; i < KT * kParts; i += kAuxWarps * 32) {
-            const int k = i / kParts, piece = i % kParts;
-            const uint4 x = *reinterpret_cast<const uint4*>(v_ring + vs * C::kVStage + i * 16);
+          if (tile_no >= C::NW) wait(&empty_w[ws], w_phase ^ 1, kStatusWaitEmpty);
+          // Four lanes take the four pieces of a chunk's row, eight lanes two rows that are 5 apart: then the
+          // swizzled places they read and write lie in different banks.
+#pragma unroll 2
+          for (int m = 0; m < KT * C::kVBytes / 16 / (kAuxWarps * 32); ++m) {
+            const int i = m * (kAuxWarps * 32) + awarp * 32 + lane, piece = i & 3, c = i / (4 * KT);
+            const int k = ((i >> 2) & (KT - 1)) ^ (i & 4 ? 4 : 0);
+            const uint32_t from = C::kVBytes == 128 ? ((c * 64 + piece * 16) ^ ((k & 7) << 4)) : piece * 16;
+            const uint4 x = *reinterpret_cast<const uint4*>(v_ring + vs * C::kVSlot + k * C::kVBytes + from);
             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
             uint32_t w[8];
 #pragma unroll
@@ -1226,8 +1284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int q = 0; q < 8; ++q) w[q] = 0;
             }
-            uint8_t* to_w = w_ring + (ws + piece / 4) * kChunk + k * 128;
-            const uint32_t byte = (piece % 4) * 32, swz = (k & 7) << 4;
+            uint8_t* to_w = w_ring + ws * C::kWSlot + c * kChunk + k * 128;
+            const uint32_t byte = piece * 32, swz = (k & 7) << 4;
             *reinterpret_cast<uint4*>(to_w + (byte ^ swz)) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(to_w + ((byte + 16) ^ swz)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
@@ -1235,14 +1293,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&empty_v[vs]);
-            for (int c = 0; c < C::kVTile; ++c) mbar_arrive(&full_w[ws + c]);
+            mbar_arrive(&full_w[ws]);
           }
           if (++vs == C::NV) {
             vs = 0;
             v_phase ^= 1;
           }
-          ws += C::kVTile;
-          if (ws == C::NW) {
+          if (++ws == C::NW) {
             ws = 0;
             w_phase ^= 1;
           }
@@ -1261,46 +1318,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ joining an item's pieces
 
-// A block for each place where a share begins (x) and each 8 rows: if that is the first cut in an item,
-// a warp joins a row of the item's pieces.
+// A block for each place where a share begins and each 8 rows: if that is the first cut in an item, a warp
+// joins a row of the item's pieces.
 template <int D>
-__global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int shares) {
+__global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a) {
   constexpr int DV = D < 256 ? D : 256, kHalves = D / DV;
   pdl_wait();
   pdl_launch_dependents();
-  const int n_tiles = *a.list.n_tiles;
-  const int parts = a.c.kv_heads * kHalves;
-  const long long total = a.list.first_unit[n_tiles] * parts;
-  constexpr int kShare = kItemCost + 1;
-  const long long ctas = min(static_cast<long long>(shares), (total + kShare - 1) / kShare);
-  const long long x = blockIdx.x + 1;
-  if (x >= ctas) return;
-  const long long cut = x * total / ctas;
-  const int entry = find_tile(a.list, n_tiles, cut, parts);
-  const KvRowTile t = a.list.tiles[entry];
-  const int units = t.count + kItemCost;
-  const long long off = cut - a.list.first_unit[entry] * parts;
-  const int part = static_cast<int>(off / units);
-  const long long item_start = cut - off % units;
-  // The pairs with the item's first and last key tiles.
-  const long long first = ((item_start + kItemCost + 1) * ctas - 1) / total;
-  const long long last = ((item_start + units) * ctas - 1) / total;
-  if (first == last || first + 1 != x) return;
+  const KvJoin j = a.list.joins[blockIdx.x + 1];
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int tok = r / a.group;
-  if (tok >= t.nt) return;
-  auto place = [&](long long c) {
-    return a.chunk_partial + (2 * c + (c > first || c * total / ctas >= item_start ? 0 : 1)) * kChunkPieceFloats;
+  if (tok >= j.nt) return;
+  auto place = [&](int c) {
+    return a.chunk_partial + (c == 0 ? j.first_place : 2 * (j.first + c)) * kChunkPieceFloats;
   };
   float top = -INFINITY;
-  for (long long c = first; c <= last; ++c) top = fmaxf(top, __ldcg(place(c) + 256 * 256 + r));
+  for (int c = lane; c < j.count; c += 32) top = fmaxf(top, __ldcg(place(c) + 256 * 256 + r));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float base = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
   float4 acc[DV / 128];
 #pragma unroll
   for (int v = 0; v < DV / 128; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (long long c = first; c <= last; ++c) {
+  for (int c = 0; c < j.count; ++c) {
     const float* from = place(c);
     const float w = exp2_approx(__ldcg(from + 256 * 256 + r) - base);
     sum = fmaf(w, __ldcg(from + 256 * 257 + r), sum);
@@ -1314,12 +1356,12 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const KvAttn a, int 
     }
   }
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const long long row = static_cast<long long>(t.row0 + tok) * a.q_heads + part / kHalves * a.group + r % a.group;
+  const long long row = static_cast<long long>(j.row0 + tok) * a.q_heads + j.part / kHalves * a.group + r % a.group;
 #pragma unroll
   for (int v = 0; v < DV / 128; ++v)
-    *reinterpret_cast<uint2*>(a.out + row * D + part % kHalves * DV + v * 128 + lane * 4) =
+    *reinterpret_cast<uint2*>(a.out + row * D + j.part % kHalves * DV + v * 128 + lane * 4) =
         make_uint2(pack_bf16(acc[v].x * f, acc[v].y * f), pack_bf16(acc[v].z * f, acc[v].w * f));
-  if (a.lse && lane == 0 && part % kHalves == 0)
+  if (a.lse && lane == 0 && j.part % kHalves == 0)
     a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147181f;
 }
 
@@ -1330,14 +1372,14 @@ cudaError_t launch(const KvAttn& a, int pairs, cudaStream_t s) {
   const uint64_t rows = (static_cast<uint64_t>(a.c.n_pages) * a.c.kv_heads) << a.c.page_log2;
   const uint32_t box = 1u << (a.c.page_log2 < 6 ? a.c.page_log2 : 6);
   if (!encode_row_chunks(&mk, a.c.k, rows, C::kRow, box, 1, 128, true) ||
-      !encode_row_chunks(&mv, a.c.v, rows, C::kRow, box, 1, C::kVBytes, !E4M3))
+      !encode_row_chunks(&mv, a.c.v, rows, C::kRow, box, 1, C::kVBytes, C::kVBytes == 128))
     return cudaErrorInvalidValue;
   const int tokens = chunk_tokens(a.group);
-  cudaError_t e = launch_pdl(kv_chunk_list_kernel, dim3(1), dim3(kListThreads), 0, s, a, tokens);
+  cudaError_t e = launch_pdl(kv_chunk_list_kernel, dim3(1), dim3(kListThreads), 0, s, a, tokens, a.c.kv_heads * C::kHalves, pairs);
   if (e == cudaSuccess)
     e = launch_pdl_pair(kv_chunk_kernel<D, E4M3>, dim3(2 * pairs), dim3(kThreads), C::kSmem, s, a, mk, mv);
   if (e == cudaSuccess && pairs > 1)
-    e = launch_pdl(kv_chunk_join_kernel<D>, dim3(pairs - 1, 256 / 8), dim3(256), 0, s, a, pairs);
+    e = launch_pdl(kv_chunk_join_kernel<D>, dim3(pairs - 1, 256 / 8), dim3(256), 0, s, a);
   return e;
 }
 
