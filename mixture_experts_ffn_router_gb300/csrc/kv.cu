@@ -50,41 +50,76 @@ __device__ __forceinline__ int2 find_place(const KvBatch& b, const KvCache& c, i
   return make_int2(kv_page(b, c, seq, pos >> c.page_log2, status), pos & ((1 << c.page_log2) - 1));
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = __uint_as_float(w[j] << 16);
-    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
+// The e4m3 codes of x / s, each quotient correctly rounded in fp32 first, of two bf16 numbers whose negated
+// values are the halves of `neg`. From the correctly rounded reciprocal of s: a quotient, its exact
+// remainder by fma, and one correction (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), two at a time; of the signs, the negated value is what keeps a -0. Far
+// from the ends of the exponent range only; a remainder that underflows belongs to a quotient that
+// rounds to the code 0 anyway. (A division per value bounded the kernel: 102 us for 317 MB.)
+__device__ __forceinline__ uint32_t quotient_codes(uint32_t neg, unsigned long long s2, unsigned long long nr2) {
+  unsigned long long nx, q, rem;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(nx) : "r"(neg << 16), "r"(neg & 0xFFFF0000u));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(nx), "l"(nr2));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rem) : "l"(q), "l"(s2), "l"(nx));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(rem), "l"(nr2), "l"(q));
+  float2 y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(q));
+  return __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ unsigned long long twice(float x) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
 }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveWarps * 32)
-    kv_write_kernel(KvBatch b, KvCache c, KvRows k, KvRows v, int parts, unsigned int* status) {
+    kv_write_kernel(KvBatch b, KvCache c, KvRows k, KvRows v, unsigned int* status) {
   constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;  // lanes of a row
   constexpr int kRowVecs = D / 8 / kLanes;         // vectors of a row per lane
   constexpr int kRows = kVecs / kRowVecs;          // rows per lane
   constexpr int kWarpRows = kRows * 32 / kLanes;
   const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  const int row = static_cast<int>(w / parts);
+  const int row = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   if (row >= b.n_tokens) return;
-  const int r0 = static_cast<int>(w % parts) * kWarpRows + lane / kLanes;
   const int sub = lane % kLanes, n_rows = 2 * c.kv_heads;
   uint4 x[kRows][kRowVecs];
+  const int r0 = blockIdx.y * kWarpRows + lane / kLanes;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = r0 + i * (32 / kLanes);
     if (r >= n_rows) continue;
-    const KvRows& src = r < c.kv_heads ? k : v;
-    const int h = r < c.kv_heads ? r : r - c.kv_heads;
-    const uint16_t* p = src.ptr + row * src.token_stride + h * src.head_stride;
+    const bool key = r < c.kv_heads;
+    const uint16_t* p = (key ? k.ptr : v.ptr) + row * (key ? k.token_stride : v.token_stride) +
+                        (key ? r : r - c.kv_heads) * (key ? k.head_stride : v.head_stride);
 #pragma unroll
     for (int j = 0; j < kRowVecs; ++j) x[i][j] = *reinterpret_cast<const uint4*>(p + (sub + j * kLanes) * 8);
   }
   const int2 at = find_place(b, c, row, lane, status);
   if (at.x < 0) return;
+  float scale = 0.0f, recip = 0.0f;  // of the lane's row lane % kRows (e4m3)
+  if constexpr (E4M3) {
+    // Each row's largest magnitude, on the bits: they order as the values do, with infinities and NaNs
+    // (which fmaxf would drop) above every finite one. Two at a time, as 16-bit numbers.
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      uint32_t top = 0;
+      if (r0 + i * (32 / kLanes) < n_rows) {
+#pragma unroll
+        for (int j = 0; j < kRowVecs; ++j)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i][j].x & 0x7fff7fffu, x[i][j].y & 0x7fff7fffu),
+                                       __vmaxu2(x[i][j].z & 0x7fff7fffu, x[i][j].w & 0x7fff7fffu)));
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (sub % kRows == i) mine = max(top << 16, top & 0xffff0000u);
+    }
+    // One division and one reciprocal per lane serve all rows.
+    scale = mine < 0x7f800000u ? __fdiv_rn(__uint_as_float(mine), 448.0f) : __uint_as_float(0x7fffffffu);
+    recip = __frcp_rn(scale);
+  }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = r0 + i * (32 / kLanes);
@@ -97,38 +132,31 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
 #pragma unroll
       for (int j = 0; j < kRowVecs; ++j) *reinterpret_cast<uint4*>(dst + (sub + j * kLanes) * 8) = x[i][j];
     } else {
-      // fmaxf drops a NaN, so the largest magnitude is taken on the bits: they order as the values
-      // do, with infinities and NaNs above every finite one.
-      uint32_t top = 0;
-      if (r < n_rows) {
-#pragma unroll
-        for (int j = 0; j < kRowVecs; ++j) {
-          const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) top = max(top, max((u[q] << 16) & 0x7fffffffu, u[q] & 0x7fff0000u));
-        }
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int from = (lane & ~(kLanes - 1)) + i;
+      const float s = __shfl_sync(0xffffffffu, scale, from), r_s = __shfl_sync(0xffffffffu, recip, from);
       if (r >= n_rows) continue;
-      const bool finite = top < 0x7f800000u;
-      const float s = finite ? __fdiv_rn(__uint_as_float(top), 448.0f) : __uint_as_float(0x7fffffffu);
       if (sub == 0) (key ? c.k_scale : c.v_scale)[to] = s;
       uint8_t* dst = (key ? c.k : c.v) + to * D;
+      const bool fast = s > 0x1p-90f && s < 0x1p90f;
+      const unsigned long long s2 = twice(s), nr2 = twice(-r_s);
 #pragma unroll
       for (int j = 0; j < kRowVecs; ++j) {
-        float f[8];
-        unpack8(x[i][j], f);
-        uint32_t code[2] = {0u, 0u};
-        if (finite && s > 0.0f) {
+        const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
+        uint32_t code[4];
+        if (fast) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 y = make_float2(__fdiv_rn(f[2 * q], s), __fdiv_rn(f[2 * q + 1], s));
-            code[q >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3))
-                            << (16 * (q & 1));
-          }
+          for (int q = 0; q < 4; ++q) code[q] = quotient_codes(u[q] ^ 0x80008000u, s2, nr2);
+        } else {
+          // A row of zeros or with a value that is not finite: codes 0.
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            code[q] = s > 0.0f ? __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(__uint_as_float(u[q] << 16), s),
+                                                                      __fdiv_rn(__uint_as_float(u[q] & 0xFFFF0000u), s)),
+                                                          __NV_SATFINITE, __NV_E4M3)
+                               : 0u;
         }
-        *reinterpret_cast<uint2*>(dst + (sub + j * kLanes) * 8) = make_uint2(code[0], code[1]);
+        *reinterpret_cast<uint2*>(dst + (sub + j * kLanes) * 8) =
+            make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
       }
     }
   }
@@ -136,18 +164,17 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveWarps * 32)
-    kv_read_kernel(KvBatch b, KvCache c, uint16_t* k_out, uint16_t* v_out, int parts, unsigned int* status) {
+    kv_read_kernel(KvBatch b, KvCache c, uint16_t* k_out, uint16_t* v_out, unsigned int* status) {
   constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;
   constexpr int kRowVecs = D / 8 / kLanes;
   constexpr int kRows = kVecs / kRowVecs;
   constexpr int kWarpRows = kRows * 32 / kLanes;
   const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  const int row = static_cast<int>(w / parts);
+  const int row = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   if (row >= b.n_tokens) return;
-  const int r0 = static_cast<int>(w % parts) * kWarpRows + lane / kLanes;
   const int sub = lane % kLanes, n_rows = 2 * c.kv_heads;
   const int2 at = find_place(b, c, row, lane, status);
+  const int r0 = blockIdx.y * kWarpRows + lane / kLanes;
   uint4 x[kRows][kRowVecs];
   float s[kRows];
 #pragma unroll
@@ -201,40 +228,38 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
   }
 }
 
-int move_parts(const KvCache& c) { return (2 * c.kv_heads * c.head_dim + 1023) / 1024; }
-
-unsigned move_blocks(const KvBatch& b, const KvCache& c) {
-  return static_cast<unsigned>((static_cast<long long>(b.n_tokens) * move_parts(c) + kMoveWarps - 1) / kMoveWarps);
+// Eight tokens to a block, 2 KB of each token's rows to a warp. (All of a token's rows to a warp, so that its
+// place is found once, was slower: 97 us against 80 for 317 MB.)
+dim3 move_grid(const KvBatch& b, const KvCache& c) {
+  return dim3((b.n_tokens + kMoveWarps - 1) / kMoveWarps, (2 * c.kv_heads * c.head_dim + 1023) / 1024);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_write(const KvBatch& b, const KvCache& c, const KvRows& k, const KvRows& v, unsigned int* status,
                             cudaStream_t s) {
-  const unsigned grid = move_blocks(b, c), block = kMoveWarps * 32;
-  const int parts = move_parts(c);
+  const dim3 grid = move_grid(b, c), block(kMoveWarps * 32);
   switch (c.head_dim * 2 + c.e4m3) {
-    case 256: kv_write_kernel<128, false><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
-    case 257: kv_write_kernel<128, true><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
-    case 512: kv_write_kernel<256, false><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
-    case 513: kv_write_kernel<256, true><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
-    case 1024: kv_write_kernel<512, false><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
-    default: kv_write_kernel<512, true><<<grid, block, 0, s>>>(b, c, k, v, parts, status); break;
+    case 256: kv_write_kernel<128, false><<<grid, block, 0, s>>>(b, c, k, v, status); break;
+    case 257: kv_write_kernel<128, true><<<grid, block, 0, s>>>(b, c, k, v, status); break;
+    case 512: kv_write_kernel<256, false><<<grid, block, 0, s>>>(b, c, k, v, status); break;
+    case 513: kv_write_kernel<256, true><<<grid, block, 0, s>>>(b, c, k, v, status); break;
+    case 1024: kv_write_kernel<512, false><<<grid, block, 0, s>>>(b, c, k, v, status); break;
+    default: kv_write_kernel<512, true><<<grid, block, 0, s>>>(b, c, k, v, status); break;
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const KvBatch& b, const KvCache& c, uint16_t* k_out, uint16_t* v_out, unsigned int* status,
                            cudaStream_t s) {
-  const unsigned grid = move_blocks(b, c), block = kMoveWarps * 32;
-  const int parts = move_parts(c);
+  const dim3 grid = move_grid(b, c), block(kMoveWarps * 32);
   switch (c.head_dim * 2 + c.e4m3) {
-    case 256: kv_read_kernel<128, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
-    case 257: kv_read_kernel<128, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
-    case 512: kv_read_kernel<256, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
-    case 513: kv_read_kernel<256, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
-    case 1024: kv_read_kernel<512, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
-    default: kv_read_kernel<512, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, parts, status); break;
+    case 256: kv_read_kernel<128, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, status); break;
+    case 257: kv_read_kernel<128, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, status); break;
+    case 512: kv_read_kernel<256, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, status); break;
+    case 513: kv_read_kernel<256, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, status); break;
+    case 1024: kv_read_kernel<512, false><<<grid, block, 0, s>>>(b, c, k_out, v_out, status); break;
+    default: kv_read_kernel<512, true><<<grid, block, 0, s>>>(b, c, k_out, v_out, status); break;
   }
   return cudaGetLastError();
 }
