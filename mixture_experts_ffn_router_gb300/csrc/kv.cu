@@ -16,9 +16,8 @@ namespace {
 
 // Writing and reading back. A row is one head's key or value of one token, D bf16 values in
 // registers as 16-byte vectors, D / 8 lanes (or D / 16 with two vectors) to a row. A warp takes
-// 2 KB of one token's rows, keys and values of all heads counted together: four loads per lane in
-// flight before the first is used, and enough warps for a single decode step's tokens to spread over
-// the SMs. Both kernels only move bytes; HBM bounds them.
+// 2 KB of one token's keys, or of its values: four loads per lane in flight before the first is used,
+// and enough warps for a single decode step's tokens to spread over the SMs.
 constexpr int kMoveWarps = 8;
 constexpr int kVecs = 4;  // 16-byte bf16 vectors per lane
 
@@ -73,74 +72,93 @@ __device__ __forceinline__ unsigned long long twice(float x) {
   return r;
 }
 
+// How a warp's lanes lie over its rows: kRows rows of each group of kLanes lanes, kVecs vectors each.
+template <int D>
+struct Move {
+  static constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;  // lanes of a row
+  static constexpr int kRowVecs = D / 8 / kLanes;         // vectors of a row per lane
+  static constexpr int kRows = kVecs / kRowVecs;          // rows per lane
+  static constexpr int kGroups = 32 / kLanes;             // rows side by side
+  static constexpr int kWarpRows = kRows * kGroups;
+};
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveWarps * 32)
     kv_write_kernel(KvBatch b, KvCache c, KvRows k, KvRows v, unsigned int* status) {
-  constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;  // lanes of a row
-  constexpr int kRowVecs = D / 8 / kLanes;         // vectors of a row per lane
-  constexpr int kRows = kVecs / kRowVecs;          // rows per lane
-  constexpr int kWarpRows = kRows * 32 / kLanes;
+  using M = Move<D>;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   if (row >= b.n_tokens) return;
-  const int sub = lane % kLanes, n_rows = 2 * c.kv_heads;
-  uint4 x[kRows][kRowVecs];
-  const int r0 = blockIdx.y * kWarpRows + lane / kLanes;
+  const bool value = blockIdx.z != 0;
+  const int sub = lane % M::kLanes, h0 = blockIdx.y * M::kWarpRows + lane / M::kLanes;
+  const long long head_stride = value ? v.head_stride : k.head_stride;
+  const uint16_t* src = (value ? v.ptr : k.ptr) + row * (value ? v.token_stride : k.token_stride) + h0 * head_stride + sub * 8;
+  uint4 x[M::kRows][M::kRowVecs];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i * (32 / kLanes);
-    if (r >= n_rows) continue;
-    const bool key = r < c.kv_heads;
-    const uint16_t* p = (key ? k.ptr : v.ptr) + row * (key ? k.token_stride : v.token_stride) +
-                        (key ? r : r - c.kv_heads) * (key ? k.head_stride : v.head_stride);
+  for (int i = 0; i < M::kRows; ++i) {
+    if (h0 + i * M::kGroups >= c.kv_heads) continue;
 #pragma unroll
-    for (int j = 0; j < kRowVecs; ++j) x[i][j] = *reinterpret_cast<const uint4*>(p + (sub + j * kLanes) * 8);
+    for (int j = 0; j < M::kRowVecs; ++j)
+      x[i][j] = *reinterpret_cast<const uint4*>(src + i * M::kGroups * head_stride + j * M::kLanes * 8);
   }
   const int2 at = find_place(b, c, row, lane, status);
   if (at.x < 0) return;
-  float scale = 0.0f, recip = 0.0f;  // of the lane's row lane % kRows (e4m3)
-  if constexpr (E4M3) {
-    // Each row's largest magnitude, on the bits: they order as the values do, with infinities and NaNs
-    // (which fmaxf would drop) above every finite one. Two at a time, as 16-bit numbers.
-    uint32_t mine = 0;
+  const long long to = ((static_cast<long long>(at.x) * c.kv_heads + h0) << c.page_log2) + at.y;  // the lane's first row
+  const long long step = static_cast<long long>(M::kGroups) << c.page_log2;
+  if constexpr (!E4M3) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(value ? c.v : c.k) + to * D + sub * 8;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      uint32_t top = 0;
-      if (r0 + i * (32 / kLanes) < n_rows) {
+    for (int i = 0; i < M::kRows; ++i) {
+      if (h0 + i * M::kGroups >= c.kv_heads) continue;
 #pragma unroll
-        for (int j = 0; j < kRowVecs; ++j)
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i][j].x & 0x7fff7fffu, x[i][j].y & 0x7fff7fffu),
-                                       __vmaxu2(x[i][j].z & 0x7fff7fffu, x[i][j].w & 0x7fff7fffu)));
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (sub % kRows == i) mine = max(top << 16, top & 0xffff0000u);
+      for (int j = 0; j < M::kRowVecs; ++j)
+        *reinterpret_cast<uint4*>(dst + i * step * D + j * M::kLanes * 8) = x[i][j];
     }
-    // One division and one reciprocal per lane serve all rows.
-    scale = mine < 0x7f800000u ? __fdiv_rn(__uint_as_float(mine), 448.0f) : __uint_as_float(0x7fffffffu);
-    recip = __frcp_rn(scale);
-  }
+  } else {
+    // Each row's largest magnitude, on the bits: they order as the values do, with infinities and NaNs
+    // (which fmaxf would drop) above every finite one. Two at a time, as 16-bit numbers; in the first steps
+    // lanes trade rows, so that a lane ends with one row's.
+    uint32_t top[M::kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i * (32 / kLanes);
-    const bool key = r < c.kv_heads;
-    const int h = key ? r : r - c.kv_heads;
-    const long long to = (((static_cast<long long>(at.x) * c.kv_heads + h) << c.page_log2) + at.y);
-    if constexpr (!E4M3) {
-      if (r >= n_rows) continue;
-      uint16_t* dst = reinterpret_cast<uint16_t*>(key ? c.k : c.v) + to * D;
+    for (int i = 0; i < M::kRows; ++i) {
+      top[i] = 0;
+      if (h0 + i * M::kGroups < c.kv_heads) {
 #pragma unroll
-      for (int j = 0; j < kRowVecs; ++j) *reinterpret_cast<uint4*>(dst + (sub + j * kLanes) * 8) = x[i][j];
-    } else {
-      const int from = (lane & ~(kLanes - 1)) + i;
+        for (int j = 0; j < M::kRowVecs; ++j)
+          top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(x[i][j].x & 0x7fff7fffu, x[i][j].y & 0x7fff7fffu),
+                                             __vmaxu2(x[i][j].z & 0x7fff7fffu, x[i][j].w & 0x7fff7fffu)));
+      }
+    }
+    int d = M::kLanes / 2;
+#pragma unroll
+    for (int half = M::kRows / 2; half > 0; half >>= 1, d >>= 1) {
+      const bool up = lane & d;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? top[i] : top[i + half], d);
+        top[i] = __vmaxu2(up ? top[i + half] : top[i], got);
+      }
+    }
+#pragma unroll
+    for (; d > 0; d >>= 1) top[0] = __vmaxu2(top[0], __shfl_xor_sync(0xffffffffu, top[0], d));
+    // Row i's is in the lanes whose highest bits (within the row's lanes) are i; one division and one
+    // reciprocal per lane serve all rows.
+    const uint32_t mine = max(top[0] << 16, top[0] & 0xffff0000u);
+    const float scale = mine < 0x7f800000u ? __fdiv_rn(__uint_as_float(mine), 448.0f) : __uint_as_float(0x7fffffffu);
+    const float recip = __frcp_rn(scale);
+    const int my_row = sub / (M::kLanes / M::kRows);
+    if (sub % (M::kLanes / M::kRows) == 0 && h0 + my_row * M::kGroups < c.kv_heads)
+      (value ? c.v_scale : c.k_scale)[to + my_row * step] = scale;
+    uint8_t* dst = (value ? c.v : c.k) + to * D + sub * 8;
+#pragma unroll
+    for (int i = 0; i < M::kRows; ++i) {
+      const int from = (lane & ~(M::kLanes - 1)) + i * (M::kLanes / M::kRows);
       const float s = __shfl_sync(0xffffffffu, scale, from), r_s = __shfl_sync(0xffffffffu, recip, from);
-      if (r >= n_rows) continue;
-      if (sub == 0) (key ? c.k_scale : c.v_scale)[to] = s;
-      uint8_t* dst = (key ? c.k : c.v) + to * D;
+      if (h0 + i * M::kGroups >= c.kv_heads) continue;
       const bool fast = s > 0x1p-90f && s < 0x1p90f;
       const unsigned long long s2 = twice(s), nr2 = twice(-r_s);
 #pragma unroll
-      for (int j = 0; j < kRowVecs; ++j) {
+      for (int j = 0; j < M::kRowVecs; ++j) {
         const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
         uint32_t code[4];
         if (fast) {
@@ -155,8 +173,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
                                                           __NV_SATFINITE, __NV_E4M3)
                                : 0u;
         }
-        *reinterpret_cast<uint2*>(dst + (sub + j * kLanes) * 8) =
-            make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+        *reinterpret_cast<uint2*>(dst + i * step * D + j * M::kLanes * 8) =
+            make_uint2(__byte_perm(code[0], code[1], 0x5410), __byte_perm(code[2], code[3], 0x5410));
       }
     }
   }
@@ -165,50 +183,43 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveWarps * 32)
     kv_read_kernel(KvBatch b, KvCache c, uint16_t* k_out, uint16_t* v_out, unsigned int* status) {
-  constexpr int kLanes = D / 8 < 32 ? D / 8 : 32;
-  constexpr int kRowVecs = D / 8 / kLanes;
-  constexpr int kRows = kVecs / kRowVecs;
-  constexpr int kWarpRows = kRows * 32 / kLanes;
+  using M = Move<D>;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   if (row >= b.n_tokens) return;
-  const int sub = lane % kLanes, n_rows = 2 * c.kv_heads;
+  const bool value = blockIdx.z != 0;
+  const int sub = lane % M::kLanes, h0 = blockIdx.y * M::kWarpRows + lane / M::kLanes;
   const int2 at = find_place(b, c, row, lane, status);
-  const int r0 = blockIdx.y * kWarpRows + lane / kLanes;
-  uint4 x[kRows][kRowVecs];
-  float s[kRows];
+  const long long from = ((static_cast<long long>(max(at.x, 0)) * c.kv_heads + h0) << c.page_log2) + at.y;
+  const long long step = static_cast<long long>(M::kGroups) << c.page_log2;
+  const uint8_t* src = (value ? c.v : c.k) + (from * D + sub * 8) * (E4M3 ? 1 : 2);
+  uint4 x[M::kRows][M::kRowVecs];
+  float s[M::kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i * (32 / kLanes);
+  for (int i = 0; i < M::kRows; ++i) {
     s[i] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kRowVecs; ++j) x[i][j] = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= n_rows || at.x < 0) continue;
-    const bool key = r < c.kv_heads;
-    const int h = key ? r : r - c.kv_heads;
-    const long long from = (((static_cast<long long>(at.x) * c.kv_heads + h) << c.page_log2) + at.y);
+    for (int j = 0; j < M::kRowVecs; ++j) x[i][j] = make_uint4(0u, 0u, 0u, 0u);
+    if (h0 + i * M::kGroups >= c.kv_heads || at.x < 0) continue;
 #pragma unroll
-    for (int j = 0; j < kRowVecs; ++j) {
-      const long long e = from * D + (sub + j * kLanes) * 8;
+    for (int j = 0; j < M::kRowVecs; ++j) {
+      const uint8_t* p = src + (i * step * D + j * M::kLanes * 8) * (E4M3 ? 1 : 2);
       if constexpr (E4M3) {
-        const uint2 code = *reinterpret_cast<const uint2*>((key ? c.k : c.v) + e);
+        const uint2 code = *reinterpret_cast<const uint2*>(p);
         x[i][j].x = code.x;
         x[i][j].y = code.y;
       } else {
-        x[i][j] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(key ? c.k : c.v) + e);
+        x[i][j] = *reinterpret_cast<const uint4*>(p);
       }
     }
-    if constexpr (E4M3) s[i] = (key ? c.k_scale : c.v_scale)[from];
+    if constexpr (E4M3) s[i] = (value ? c.v_scale : c.k_scale)[from + i * step];
   }
+  uint16_t* dst = (value ? v_out : k_out) + (static_cast<long long>(row) * c.kv_heads + h0) * D + sub * 8;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i * (32 / kLanes);
-    if (r >= n_rows) continue;
-    const bool key = r < c.kv_heads;
-    const int h = key ? r : r - c.kv_heads;
-    uint16_t* dst = (key ? k_out : v_out) + (static_cast<long long>(row) * c.kv_heads + h) * D;
+  for (int i = 0; i < M::kRows; ++i) {
+    if (h0 + i * M::kGroups >= c.kv_heads) continue;
 #pragma unroll
-    for (int j = 0; j < kRowVecs; ++j) {
+    for (int j = 0; j < M::kRowVecs; ++j) {
       uint4 y = x[i][j];
       if constexpr (E4M3) {
         const uint32_t code[2] = {x[i][j].x, x[i][j].y};
@@ -223,15 +234,15 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
         }
         y = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      *reinterpret_cast<uint4*>(dst + (sub + j * kLanes) * 8) = y;
+      *reinterpret_cast<uint4*>(dst + (i * M::kGroups * D + j * M::kLanes * 8)) = y;
     }
   }
 }
 
-// Eight tokens to a block, 2 KB of each token's rows to a warp. (All of a token's rows to a warp, so that its
-// place is found once, was slower: 97 us against 80 for 317 MB.)
+// Eight tokens to a block, 2 KB of each token's keys or values to a warp. (All of a token's rows to a warp,
+// so that its place is found once, was slower: 97 us against 80 for 317 MB.)
 dim3 move_grid(const KvBatch& b, const KvCache& c) {
-  return dim3((b.n_tokens + kMoveWarps - 1) / kMoveWarps, (2 * c.kv_heads * c.head_dim + 1023) / 1024);
+  return dim3((b.n_tokens + kMoveWarps - 1) / kMoveWarps, (c.kv_heads * c.head_dim + 1023) / 1024, 2);
 }
 
 }  // namespace
