@@ -529,10 +529,12 @@ class KVBatch:
         self.device = cu_q.device
         self.struct = moe_ffn_kv_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(),
                                        pages.stride(0) if n > 1 else cols, cols, n, 0, int(max_new))
+        self._ref = ctypes.byref(self.struct)
 
-    def of(self, n_tokens: int) -> moe_ffn_kv_batch:
+    def of(self, n_tokens: int):
+        """The C structure (by reference) for tensors of n_tokens token rows."""
         self.struct.n_tokens = n_tokens
-        return self.struct
+        return self._ref
 
 
 class KVCache:
@@ -541,6 +543,7 @@ class KVCache:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.struct = moe_ffn_kv_cache(*(t.data_ptr() if t is not None else None for t in (k, v, k_scale, v_scale)))
+        self._ref = ctypes.byref(self.struct)
 
 
 class PagedKV:
@@ -569,7 +572,8 @@ class PagedKV:
         self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
         self.ctx = moe_ffn_kv_init(self.cfg, self.workspace.data_ptr(), self.nbytes, int(device))
         self._handle = _vp(self.ctx)
-        self._last = None
+        self._lib = lib()
+        self._last = self._last_raw = None
 
     def new_cache(self) -> KVCache:
         """A zeroed cache of one layer."""
@@ -603,31 +607,35 @@ class PagedKV:
         import torch
         if t.dtype != torch.bfloat16:
             raise ValueError("%s must be torch.bfloat16, got %s" % (what, t.dtype))
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
-            raise ValueError("%s must have shape [tokens, %d, %d], got %s" % (what, heads, self.head_dim,
-                                                                              tuple(t.shape)))
-        if not t.is_cuda or t.device != self.device:
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim:
+            raise ValueError("%s must have shape [tokens, %d, %d], got %s" % (what, heads, self.head_dim, tuple(shape)))
+        if t.device != self.device:
             raise ValueError("%s must be on %s" % (what, self.device))
         ts, hs, es = t.stride()
         # A dimension of one element has no stride that matters.
-        ts, hs = ts if t.shape[0] > 1 else 0, hs if heads > 1 else 0
+        if shape[0] <= 1:
+            ts = 0
+        if heads == 1:
+            hs = 0
         if es != 1 or ts % 8 or hs % 8:
             raise ValueError("%s must have a contiguous last dimension and strides that are multiples of 8" % what)
         return moe_ffn_kv_rows(t.data_ptr(), ts, hs)
 
     def _begin(self, cache, batch):
+        """The cache's structure and the stream of a call, ordered after the handle's last one."""
         import torch
         if not isinstance(cache, KVCache):
             cache = self.cache(**cache)
         if batch.device != self.device:
             raise ValueError("the batch must be on %s" % self.device)
-        stream = torch.cuda.current_stream(self.device)
-        if self._last is None or self._last.cuda_stream != stream.cuda_stream:
-            if not torch.cuda.is_current_stream_capturing():
-                if self._last is not None:
-                    stream.wait_stream(self._last)
-                self._last = stream
-        return cache.struct, _vp(stream.cuda_stream)
+        raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if raw != self._last_raw and not torch.cuda.is_current_stream_capturing():
+            stream = torch.cuda.current_stream(self.device)
+            if self._last is not None:
+                stream.wait_stream(self._last)
+            self._last, self._last_raw = stream, raw
+        return cache._ref, raw
 
     def write(self, cache, batch: KVBatch, k, v) -> None:
         """Writes the new tokens' keys and values, bf16 [tokens, kv_heads, head_dim] each, into `cache`
@@ -636,7 +644,7 @@ class PagedKV:
         if k.shape[0] != v.shape[0]:
             raise ValueError("k has %d tokens, v %d" % (k.shape[0], v.shape[0]))
         c, s = self._begin(cache, batch)
-        _check("moe_ffn_kv_write", moe_ffn_kv_write(self._handle, c, batch.of(k.shape[0]), kr, vr, s))
+        _check("moe_ffn_kv_write", self._lib.moe_ffn_kv_write(self._handle, c, batch.of(k.shape[0]), kr, vr, s))
 
     def read(self, cache, batch: KVBatch, n_tokens=None):
         """The batch's tokens read back: (k, v), bf16 [tokens, kv_heads, head_dim]. n_tokens: the token
@@ -647,7 +655,8 @@ class PagedKV:
         k, v = (torch.empty((n_tokens, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
                 for _ in range(2))
         c, s = self._begin(cache, batch)
-        _check("moe_ffn_kv_read", moe_ffn_kv_read(self._handle, c, batch.of(n_tokens), k.data_ptr(), v.data_ptr(), s))
+        _check("moe_ffn_kv_read",
+               self._lib.moe_ffn_kv_read(self._handle, c, batch.of(n_tokens), k.data_ptr(), v.data_ptr(), s))
         return k, v
 
     def attention(self, cache, batch: KVBatch, q, window: int = 0, sinks: int = 0, scale=None, out=None):
@@ -667,8 +676,9 @@ class PagedKV:
         lse = torch.empty((T, self.q_heads), dtype=torch.float32, device=self.device)
         c, s = self._begin(cache, batch)
         _check("moe_ffn_kv_attention",
-               moe_ffn_kv_attention(self._handle, c, batch.of(T), qr, self.default_scale if scale is None else scale,
-                                    window, sinks, out.data_ptr(), lse.data_ptr(), s))
+               self._lib.moe_ffn_kv_attention(self._handle, c, batch.of(T), qr,
+                                              self.default_scale if scale is None else scale, window, sinks,
+                                              out.data_ptr(), lse.data_ptr(), s))
         return out, lse
 
     def status(self, stream=None):

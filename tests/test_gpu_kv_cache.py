@@ -361,7 +361,8 @@ def test_refusals():
         kv.attention(c, batch, torch.zeros(2, 4, 257, dtype=torch.bfloat16, device="cuda")[:, :, :256])
     L = B.lib()
     rows = kv._rows("q", q, 4)
-    st = batch.of(2)
+    st = batch.struct
+    st.n_tokens = 2
     args = (rows, 0.1, 0, 0, q.data_ptr() + (1 << 20), None, None)
     assert L.moe_ffn_kv_attention(kv._handle, B.moe_ffn_kv_cache(), st, *args) == B.MOE_FFN_EINVAL
     assert L.moe_ffn_kv_attention(kv._handle, c.struct, st, rows, 0.1, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
