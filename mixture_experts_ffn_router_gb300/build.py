@@ -14,7 +14,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_ffn.so")
 SOURCES = ["moe_ffn.cu", "route.cu", "router.cu", "gemm.cu", "gemm_pair.cu", "quant.cu", "noalloc.cu",
-           "selftest.cu", "kv.cu", "kv_attn.cu", "kv_decode.cu", "kv_chunk.cu"]
+           "selftest.cu", "kv.cu", "kv_decode.cu", "kv_chunk.cu"]
 HEADERS = ["internal.h", "kv.h", "ptx.cuh"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",

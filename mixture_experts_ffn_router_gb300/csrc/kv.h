@@ -117,7 +117,6 @@ cudaError_t launch_kv_write(const KvBatch& b, const KvCache& c, const KvRows& k,
                             cudaStream_t s);
 cudaError_t launch_kv_read(const KvBatch& b, const KvCache& c, uint16_t* k_out, uint16_t* v_out, unsigned int* status,
                            cudaStream_t s);
-cudaError_t launch_kv_attention(const KvAttn& a, cudaStream_t s);
 cudaError_t kv_decode_setup();
 cudaError_t launch_kv_decode(const KvAttn& a, int ctas, cudaStream_t s);
 cudaError_t kv_chunk_setup(int* pairs);

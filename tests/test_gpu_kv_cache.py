@@ -254,6 +254,79 @@ def test_long_caches(fmt, hq, hkv, d, page, new, kv, window, sinks):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 2)])
+def test_hidden_values_do_not_matter_to_single_tokens(fmt, d, window, sinks):
+    case = U.Case(fmt, 3, 1, d, 16, [1, 1, 1], [150, 200, 33], seed=16)
+    case.v[0][149, 0, 5] = math.nan        # seen
+    case.v[0][100, 0, d - 1] = math.nan    # hidden by the window
+    case.k[1][50, 0, 3] = math.nan
+    case.v[1][1, 0, 7] = math.inf          # a sink
+    U.check_attention(case, window, sinks)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_hidden_values_with_one_head_per_kv_head(fmt):
+    """Row tiles of 256 tokens: keys that some rows see lie up to 255 from the first."""
+    case = U.Case(fmt, 1, 1, 128, 32, [300], [420], seed=17)
+    for p in (121, 250, 374, 375, 376, 419):
+        case.v[0][p, 0, p % 128] = math.nan
+    U.check_attention(case)
+    U.check_attention(case, 130, 3)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n_seqs", [300, 1300])
+def test_many_sequences(fmt, n_seqs):
+    kv_len = [(7 * b) % 40 for b in range(n_seqs)]
+    U.check_attention(U.Case(fmt, 2, 1, 128, 16, [min(1, n) for n in kv_len], kv_len, seed=18))
+    U.check_attention(U.Case(fmt, 2, 1, 128, 16, [min(b % 3, n) for b, n in enumerate(kv_len)], kv_len, seed=19))
+
+
+@pytest.mark.parametrize("fmt,page,pages", [("bf16", 128, 20000), ("e4m3", 16, 300000)])
+def test_offsets_beyond_32_bits(fmt, page, pages):
+    """The sequence's pages are the last of a cache of over 2^32 bytes."""
+    case = U.Case(fmt, 4, 2, 512, page, [1, 40], [300, 200], seed=20)
+    case.pages[case.pages >= 0] += pages - case.n_pages
+    case.n_pages = pages
+    assert 2 * pages * page * 512 * (2 if fmt == "bf16" else 1) > 1 << 32
+    case.garbage = "zero"
+    kv = case.handle()
+    c = case.filled(kv)
+    U.check_attention(case, kv=kv, cache=c)
+    one = U.Case(fmt, 4, 2, 512, page, [1, 1], [300, 200], seed=20)
+    one.pages, one.n_pages = case.pages, pages
+    U.check_attention(one, kv=kv, cache=c)
+    k, _ = kv.read(c, case.batch([300, 200]), n_tokens=500)
+    want = torch.cat([case.stored("k", b) for b in range(2)])
+    U.check_close(k, want, (U.BF + U.F32) * want.abs(), "k")
+
+
+def test_expanded_inputs():
+    """Queries and keys that are one row seen many times (strides of 0)."""
+    case = U.Case("bf16", 4, 2, 128, 16, [20], [20], seed=21)
+    case.q[:] = case.q[:1, :1]
+    case.k[0][:] = case.k[0][:1]
+    kv = case.handle()
+    c = case.empty_cache(kv)
+    kv.write(c, case.batch(), case.k[0][:1].cuda().expand(20, -1, -1), case.v[0].cuda())
+    U.check_attention(case, kv=kv, cache=c, q=case.q[:1, :1].cuda().expand(20, 4, -1))
+
+
+@pytest.mark.parametrize("layer,fmt", [("sliding", "e4m3"), ("global", "bf16")])
+def test_example_serves_a_layer(layer, fmt):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_layer.py")
+    spec = importlib.util.spec_from_file_location("serve_layer", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    off, status = m.main(["--layer", layer, "--format", fmt, "--users", "4", "--steps", "3"])
+    # Two ways of cutting the same sums: bf16 outputs of each stage, a few roundings apart (a token near a
+    # tie of the router may change an expert, which the norm over all tokens bounds).
+    assert status == 0 and off < 2e-2
+
+
 def test_captured_step_replays_with_new_lengths():
     """Write and attention of a decode step in a graph; the batch's tensors change between replays."""
     case = U.Case("e4m3", 4, 2, 256, 16, [1, 1], [30, 51], seed=11)
