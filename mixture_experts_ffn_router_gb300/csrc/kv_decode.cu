@@ -137,8 +137,9 @@ __device__ __forceinline__ bool compute_sync_or(bool c) {
 }
 
 // What an item costs beside its tiles (its queries, its end), in tiles: shares are equal in units, an
-// item being kItemCost units and one for each tile. XXITEM
-constexpr int kItemCost = 2;
+// item being kItemCost units and one for each tile. (Equal in tiles, a batch of 64 ragged sequences took
+// 95 us instead of 85: the CTAs with its short ones came last.) And what joining pieces costs.
+constexpr int kItemCost = 2, kJoinCost = 4;
 
 constexpr int kJoin = 24;  // pieces joined at once, at most 32
 
@@ -167,6 +168,29 @@ __device__ __forceinline__ SeqTiles seq_tiles(const KvAttn& a, int seq) {
   return t;
 }
 
+// Where CTA x's share begins, and the CTA whose share holds a unit. (64-bit divisions are long; few batches
+// need them.)
+__device__ __forceinline__ long long decode_share(int x, long long total, int ctas) {
+  if (total < (1 << 22)) return static_cast<unsigned>(x) * static_cast<unsigned>(total) / static_cast<unsigned>(ctas);
+  return x * total / ctas;
+}
+__device__ __forceinline__ int decode_owner(long long unit, long long total, int ctas) {
+  if (total < (1 << 22))
+    return (static_cast<unsigned>(unit + 1) * static_cast<unsigned>(ctas) - 1) / static_cast<unsigned>(total);
+  return static_cast<int>(((unit + 1) * ctas - 1) / total);
+}
+
+// Writes rows of zeros (and -infinity) for `rows` rows of one head from `first` on, of which the caller
+// takes number `id` of every `of`.
+template <int D>
+__device__ __forceinline__ void clear_rows(const KvAttn& a, long long first, long long rows, long long id, long long of) {
+  for (long long i = id; i < rows; i += of) {
+    const long long to = first + i;
+    for (int j = 0; j < D; j += 8) *reinterpret_cast<uint4*>(a.out + to * D + j) = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse) a.lse[to] = -INFINITY;
+  }
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 2)
     kv_decode_kernel(const KvAttn a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -183,8 +207,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ int s_last;
   __shared__ float s_top[kComputeWarps][kDecodeHeads], s_vtop[kComputeWarps][kDecodeHeads];
   __shared__ float s_weight[kDecodeHeads][32], s_join[kDecodeHeads][2];
-  __shared__ long long s_sum[kThreads / 32], s_total, s_before;
-  __shared__ int s_seq;
+  __shared__ long long s_units[2][kThreads / 32], s_total, s_begin;
+  __shared__ int s_items[2][kThreads / 32], s_most[2][kThreads / 32];
+  __shared__ struct {
+    SeqTiles t;
+    int seq, head, u0;
+  } s_first;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -199,84 +227,106 @@ __global__ void __launch_bounds__(kThreads, 2)
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
   }
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
 
-  // The units of all sequences, and the sequence this CTA's share begins in.
+  // The units of all sequences, and the sequence this CTA's share begins in. A thread looks at a sequence
+  // at a time, kThreads of them in a round; most batches take one round, whose counts then stay at hand.
   const int heads = a.c.kv_heads, n_seqs = a.b.n_seqs;
-  auto block_sum = [&](long long v) {  // inclusive sum over the threads; s_total: over the block
+  const int rounds = (n_seqs + kThreads - 1) / kThreads;
+  SeqTiles t = {};
+  long long all = 0, some = 0;  // units and items of every head, before this round
+  int most = 0;
+  long long units_to = 0, items_to = 0;  // of the round's sequences up to this thread's
+  auto look = [&](int round, bool clear) {
+    const int b = round * kThreads + tid;
+    t.count = 0;
+    if (b < n_seqs) {
+      t = seq_tiles<KT>(a, b);
+      if (clear && t.span.p < 0 && b % gridDim.x == blockIdx.x && t.row < a.b.n_tokens && a.b.cu_q[b + 1] > t.row)
+        clear_rows<D>(a, static_cast<long long>(t.row) * a.q_heads, a.q_heads, 0, 1);  // a token that sees nothing
+    }
+    units_to = t.count > 0 ? t.count + kItemCost : 0;
+    items_to = t.count > 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += up;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = v;
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    if (tid == kThreads - 1) s_total = before + v;
-    __syncthreads();
-    return before + v;
-  };
-  auto units_of = [](int tiles) { return tiles > 0 ? tiles + kItemCost : 0; };
-  int own = 0;  // units of sequence tid's items, each
-  long long mine = 0;
-  for (int b = tid; b < n_seqs; b += kThreads) {
-    const SeqTiles t = seq_tiles<KT>(a, b);
-    if (b == tid) own = units_of(t.count);
-    mine += units_of(t.count);
-    if (t.span.p < 0 && b % gridDim.x == blockIdx.x && t.row < a.b.n_tokens && a.b.cu_q[b + 1] > t.row) {
-      // A token that sees nothing.
-      for (int h = 0; h < a.q_heads; ++h) {
-        const long long to = static_cast<long long>(t.row) * a.q_heads + h;
-        for (int i = 0; i < D; i += 8) *reinterpret_cast<uint4*>(a.out + to * D + i) = make_uint4(0u, 0u, 0u, 0u);
-        if (a.lse) a.lse[to] = -INFINITY;
+      const long long u = __shfl_up_sync(0xffffffffu, units_to, o), i = __shfl_up_sync(0xffffffffu, items_to, o);
+      if (lane >= o) {
+        units_to += u;
+        items_to += i;
       }
     }
-  }
+    const int top = __reduce_max_sync(0xffffffffu, t.count);
+    const int at = round & 1;  // (a round's sums are read before the round after the next writes them)
+    if (lane == 31) {
+      s_units[at][warp] = units_to;
+      s_items[at][warp] = static_cast<int>(items_to);
+      s_most[at][warp] = top;
+    }
+    __syncthreads();
+    long long units = 0, items = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) {
+        units_to += units;
+        items_to += items;
+      }
+      units += s_units[at][w];
+      items += s_items[at][w];
+      most = max(most, s_most[at][w]);
+    }
+    units_to += all;
+    items_to += some;
+    all += units;
+    some += items;
+  };
+  for (int r = 0; r < max(rounds, 1); ++r) look(r, true);
   {  // Rows of no sequence.
     const int used = n_seqs > 0 ? min(max(a.b.cu_q[n_seqs], 0), a.b.n_tokens) : 0;
-    const long long n = static_cast<long long>(a.b.n_tokens - used) * a.q_heads;
-    for (long long i = static_cast<long long>(blockIdx.x) * kThreads + tid; i < n; i += static_cast<long long>(gridDim.x) * kThreads) {
-      const long long to = static_cast<long long>(used) * a.q_heads + i;
-      for (int j = 0; j < D; j += 8) *reinterpret_cast<uint4*>(a.out + to * D + j) = make_uint4(0u, 0u, 0u, 0u);
-      if (a.lse) a.lse[to] = -INFINITY;
-    }
+    clear_rows<D>(a, static_cast<long long>(used) * a.q_heads, static_cast<long long>(a.b.n_tokens - used) * a.q_heads,
+                  static_cast<long long>(blockIdx.x) * kThreads + tid, static_cast<long long>(gridDim.x) * kThreads);
   }
-  long long upto = block_sum(mine);
-  const long long total = s_total * heads;
-  // A share is at least one item of one tile: below that pieces cost more than they save.
-  constexpr int kShare = kItemCost + 1;
-  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kShare - 1) / kShare);
+  // A share is at least one item of one tile: below that pieces cost more than they save. And where items
+  // one by one end no later than equal shares and their joins would, nothing is cut and items are counted.
+  const bool whole =
+      (some * heads + gridDim.x - 1) / gridDim.x * (most + kItemCost) <= all * heads / gridDim.x + kJoinCost;
+  const long long total = (whole ? some : all) * heads;
+  const int least = whole ? 1 : kItemCost + 1;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + least - 1) / least));
   if (blockIdx.x >= ctas) return;
-  const long long begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
-  for (int base = 0;; base += kThreads) {
-    // One block of sequences after the other; the first block's counts are at hand.
-    long long before = 0;
-    if (base == 0 && n_seqs <= kThreads) {
-      before = 0;
-    } else {
-      if (base > 0) own = base + tid < n_seqs ? units_of(seq_tiles<KT>(a, base + tid).count) : 0;
-      if (tid == 0 && base == 0) s_before = 0;
-      upto = block_sum(own);
-      before = s_before;
-    }
-    const long long lo = (before + upto - own) * heads, hi = (before + upto) * heads;
-    if (begin >= lo && begin < hi) {
-      s_seq = base + tid;
-      s_sum[0] = lo;
-    }
-    const bool here = __syncthreads_or(begin >= lo && begin < hi);
-    if (here || base + kThreads >= n_seqs) break;
-    if (tid == 0) s_before = before + s_total;
+  const long long begin = decode_share(blockIdx.x, total, ctas);
+  if (rounds > 1) {
+    all = some = 0;
     __syncthreads();
   }
-  int seq = s_seq;
-  const long long seq_start = s_sum[0];
-  SeqTiles t = seq_tiles<KT>(a, seq);
-  int head = static_cast<int>((begin - seq_start) / units_of(t.count));
-  int u0 = static_cast<int>((begin - seq_start) % units_of(t.count));  // where the item goes on, in units
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) look(r, false);
+    const int own = t.count > 0 ? (whole ? 1 : t.count + kItemCost) : 0;
+    const long long hi = (whole ? items_to : units_to) * heads, lo = hi - static_cast<long long>(own) * heads;
+    if (begin >= lo && begin < hi) {
+      s_first.t = t;
+      s_first.seq = r * kThreads + tid;
+      s_first.head = static_cast<int>((begin - lo) / own);
+      s_first.u0 = static_cast<int>((begin - lo) % own);
+    }
+  }
+  if (tid == 0) {
+    s_total = total;
+    s_begin = begin;
+  }
+  __syncthreads();
+  t = s_first.t;
+  int seq = s_first.seq, head = s_first.head, u0 = s_first.u0;  // u0: where the item goes on, in units
+  int left = static_cast<int>(decode_share(blockIdx.x + 1, total, ctas) - begin);  // units of the share
+  const int cost = whole ? 0 : kItemCost;
+  // Units of the item in hand, tiles of it in the share, and the first of these.
+  int un, i0, n;
+  auto take = [&] {
+    un = min((whole ? 1 : t.count + cost) - u0, left);
+    i0 = whole ? 0 : max(u0 - cost, 0);
+    n = whole ? t.count : max(u0 + un - cost, 0) - i0;
+  };
 
   const int rows_log2 = min(a.c.page_log2, KT == 128 ? 7 : KT == 64 ? 6 : 5);
   const int R = 1 << rows_log2;  // rows of a box
@@ -302,9 +352,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t policy = policy_evict_first();
     bool alive = true;
     int issued = 0;
-    for (long long pos = begin; pos < end && alive;) {
-      const int un = static_cast<int>(min(static_cast<long long>(units_of(t.count) - u0), end - pos));
-      const int i0 = max(u0 - kItemCost, 0), n = max(u0 + un - kItemCost, 0) - i0;
+    while (left > 0 && alive) {
+      take();
       for (int i = i0; i < i0 + n && alive; ++i) {
         const int tile = i < t.front ? i : i + t.skip;
         const int p0 = tile * KT + (lane << rows_log2);  // the first position of this lane's page part
@@ -346,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           next_unit();
         }
       }
-      pos += un;
-      if (pos < end) next_item();
+      left -= un;
+      if (left > 0) next_item();
     }
     if (!alive && lane == 0) {
       // Given up: the copies on their way land before the CTA's shared memory goes.
@@ -385,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int piece = E4M3 ? (C::VT > 1 ? lane & 16 : 0) : (lane & 8) << 1;
     voff[v] = ((byte >> 7) << (7 + rows_log2)) + key * 128 + (((byte & 127) + piece) ^ ((lane & 7) << 4));
   }
-  for (long long pos = begin; pos < end;) {
-    const int un = static_cast<int>(min(static_cast<long long>(units_of(t.count) - u0), end - pos));
-    const int i0 = max(u0 - kItemCost, 0), n = max(u0 + un - kItemCost, 0) - i0;
+  int taken = 0;  // units of the share before the item
+  while (left > 0) {
+    take();
     if (n == 0) break;  // the share ends in front of the item's first tile
     // The queries as the second operand of S^T = K Q^T: lane holds head r8.
     uint32_t q[C::kQRegs];
@@ -680,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     compute_sync();
-    const long long item_start = pos - u0;
     const long long to = static_cast<long long>(t.row) * a.q_heads + head * a.group;  // the first head's output row
     const int h0 = 2 * c4, h1 = h0 + 1;
     // The dimension of o[v][0]; o[v][2] is `apart` further.
@@ -704,9 +752,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
       // A piece. Its place is this CTA's first if the item began before the CTA's share or with it, as
       // it did for all of the item's CTAs but its first.
-      const int first = static_cast<int>(((item_start + kItemCost + 1) * ctas - 1) / total);
-      const int count = static_cast<int>(((item_start + kItemCost + t.count) * ctas - 1) / total) - first + 1;
-      const int first_place = 2 * first + (first * total / ctas >= item_start ? 0 : 1);
+      const long long all_units = s_total, item_start = s_begin + taken - u0;
+      const int first = decode_owner(item_start + cost, all_units, ctas);
+      const int count = decode_owner(item_start + cost + t.count - 1, all_units, ctas) - first + 1;
+      const int first_place = 2 * first + (decode_share(first, all_units, ctas) >= item_start ? 0 : 1);
       auto place = [&](int x) { return x == 0 ? first_place : 2 * (first + x); };  // of the item's piece x
       constexpr long long piece_floats = decode_piece_floats(D);
       const int me = static_cast<int>(blockIdx.x) - first;
@@ -813,8 +862,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         apart_in = span;
       }
     }
-    pos += un;
-    if (pos < end) next_item();
+    taken += un;
+    left -= un;
+    if (left > 0) next_item();
   }
 }
 
