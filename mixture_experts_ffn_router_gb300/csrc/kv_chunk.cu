@@ -5,8 +5,7 @@
 // heads of a token lie next to each other, so a tile of keys and values read once serves all of them.
 // A cluster of two CTAs works on it as an SM pair (cta_group::2), 128 rows each; a key tile, 128
 // positions, is loaded by halves: each CTA holds 64 keys of K and half of the width of V, so the pair
-// reads it once. (One CTA for 128 rows, with whole tiles, was bound by its loads and by the shared
-// memory that its products read: XXPAIR.) For each key tile:
+// reads it once, and a ring of the same shared memory holds twice the tiles. For each key tile:
 //   S = Q K^T    256 x 128 x D, operands in shared memory, fp32 accumulator in TMEM (two of them);
 //   P = exp2(scaled S - M) by eight warps of each CTA, written over S in TMEM with 16 bits;
 //   O += P V     256 x (width) x 128, P from TMEM, V as it lies in the cache (its width is the
@@ -15,9 +14,10 @@
 // O takes 256 TMEM columns beside the two S, so a head of width 512 is two items that each take
 // half of V's width and form S for themselves (1.5 times the products of one pass).
 //
-// Softmax: one pass in base 2, against a reference M per row that moves (with O and the sum rescaled)
-// only when a score passes it by more than 8, so O is almost never read back: P is at most 2^8, summed
-// in fp32 and rounded to bf16 (2^-8 of each weight) for the product with V.
+// Softmax: one pass in base 2, against a reference M per row. M moves, with O and the sum rescaled, only
+// when half a row's weights in a tile sum to more than 2^9, so O is almost never read back and no maximum
+// is taken: weights are at most 2^9, summed in fp32 and rounded to bf16 (half a step is 2^-8 of each) for
+// the product with V.
 //
 // Work. An item is a row tile, a kv head and a half of V's width where it has two. The key tiles of all
 // items, one after the other with item_cost more for each item, are shared out evenly over the pairs
@@ -26,9 +26,19 @@
 // adds in the order of the tiles.
 //
 // Warps: 0 loads K and V by TMA (boxes of one page's rows, 128-byte swizzle), 1 issues the MMAs (in the
-// pair's first CTA), 4..11 are the softmax (two warps per 32 rows, each half the columns) and write the
-// output, 12..15 bring the queries into shared memory, gathered by row. What the MMA thread waits for
-// is counted on barriers of the first CTA, which the other's warps and copies reach over the cluster.
+// pair's first CTA), 4..11 are the softmax (two warps per 32 rows, each half the columns), 12..15 bring
+// the queries into shared memory, gathered by row, and write an item's output while the next one is under
+// way. What the MMA thread waits for is counted on barriers of the first CTA, which the other's warps and
+// copies reach over the cluster.
+//
+// What bounds it. Prompts of 4096 tokens, 16 heads on 8: width 256 1.44 PFLOP/s, width 512 1.05 (1.57 with
+// the second S), of 1.95 measured for a burst and 1.73 sustained; at these the power limit holds the
+// clock. A key tile takes 2500 cycles where its products are 2048 (width 256): the softmax's chain, from
+// S to P, is 2400. Width 128 (products 1024) and e4m3, whose softmax multiplies by two scales per key
+// and shares its SM's issue slots with the widening, are bound by that chain: 2300 and 4000 cycles. Measured
+// and not kept: the softmax warps in two groups that take turns at whole tiles (width 256 430 us against
+// 376, with two S to work from a group's turn waits for the other's products), V looked through by warps
+// 12..15 (385).
 //
 // Hidden values. P is 0 for a key a row does not see, but 0 times a NaN or an infinity is not 0, so in
 // key tiles with hidden keys the softmax warps clear V's rows that no row of the tile sees, and
@@ -39,8 +49,9 @@
 // two numbers lose lies 2^-18 below the row's largest magnitude), which needs no widened copy of K.
 // The keys' scales multiply S. V's codes are widened to fp16, exactly, by warps 12..15 on the way to
 // the tensor cores. The values' scales multiply P before it is rounded to fp16, relative to the
-// largest scale so far and 2^7 up: P is then at most 2^15, and what is lost under fp16's smallest
-// number is 2^-32 of a weight of 1 per key.
+// largest scale so far and 2^6 up: P is then at most 2^15, and what is lost under fp16's smallest
+// number is 2^-31 of a weight of 1 per key. (A NaN among the codes, which moe_ffn_kv_write does not make,
+// may reach rows that do not see it; a NaN scale does not.)
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
