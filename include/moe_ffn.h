@@ -327,7 +327,8 @@ int moe_ffn_selftest_wait_expiry(uint32_t* status_word, unsigned long long* reco
  *     gets MOE_FFN_STATUS_BAD_INDEX (moe_ffn_kv_device_status) and the results of the sequences
  *     concerned are unspecified.
  * The cache holds keys and values as [n_pages, kv_heads, page_size, head_dim], as bf16, or as e4m3
- * with one fp32 scale per token and head in [n_pages, kv_heads, page_size]; a value is code * scale.
+ * with one fp32 scale per token and head in [n_pages, kv_heads, page_size]; a value is code * scale
+ * (scales not negative, and no NaN among the codes, as moe_ffn_kv_write makes them).
  * Calls on one handle share its workspace: they must not overlap in time (one stream, or ordered).
  */
 #define MOE_FFN_KV_BF16 0
