@@ -32,7 +32,7 @@
 // copies reach over the cluster.
 //
 // What bounds it. Prompts of 4096 tokens, 16 heads on 8: width 256 1.44 PFLOP/s, width 512 1.05 (1.57 with
-// the second S), of 1.95 measured for a burst and 1.73 sustained; at these the power limit holds the
+// the second S), of 1.91 measured for a burst and 1.72 sustained; at these the power limit holds the
 // clock. A key tile takes 2500 cycles where its products are 2048 (width 256): the softmax's chain, from
 // S to P, is 2400. Width 128 (products 1024) and e4m3, whose softmax multiplies by two scales per key
 // and shares its SM's issue slots with the widening, are bound by that chain: 2300 and 4000 cycles. Measured

@@ -31,7 +31,7 @@
 // the largest per key. (mma.sync on e4m3 itself, with queries split in two e4m3 parts, was slower: 883 us
 // against 772 for 64 sequences of 16384 tokens, 8 heads of width 256.)
 //
-// Measured: 64 sequences of 16384 tokens, of the 6.78 TB/s of a copy: bf16 7.1 TB/s (8 heads of width 128)
+// Measured: 64 sequences of 16384 tokens, of the 6.70 TB/s of a copy: bf16 7.1 TB/s (8 heads of width 128)
 // and 6.9 (2 of 512); e4m3 6.3, 6.3 and 5.9 (width 128, 256, 512), where the widening of the codes, some
 // 600 instructions per warp and tile, fills the issue slots. A call takes about 6 us beside its loads: 3 to
 // find its work and load its queries, the rest to join pieces.
