@@ -32,8 +32,8 @@
 // against 772 for 64 sequences of 16384 tokens, 8 heads of width 256.)
 //
 // Measured: 64 sequences of 16384 tokens, of the 6.70 TB/s of a copy: bf16 7.1 TB/s (8 heads of width 128)
-// and 6.9 (2 of 512); e4m3 6.3, 6.3 and 5.9 (width 128, 256, 512), where the widening of the codes, some
-// 600 instructions per warp and tile, fills the issue slots. A call takes about 6 us beside its loads: 3 to
+// and 6.9 (2 of 512); e4m3 6.8, 6.9 and 6.5 (width 128, 256, 512; there the widening of the codes, some 600
+// instructions per warp and tile, is as long as the loads). A call takes about 6 us beside its loads: 3 to
 // find its work and load its queries, the rest to join pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -62,6 +62,10 @@ struct Dec {
   static constexpr int kSteps = kRow / 32 / DS;                      // 32-byte steps of a key row per warp
   static constexpr int kQRegs = D / DS / 8;
   static constexpr int VT = D / (16 * kComputeWarps);                // 16-wide blocks of V per warp
+  // Of the steps of 32 keys through V, those unrolled. A CTA's two warps per scheduler execute the tile
+  // in step and wait for its instructions: 64 sequences of 16384 e4m3 tokens take 333 us with 1 and 419 with
+  // 2 at width 512, 637 and 640 at 256; at 128, whose steps are short, 337 with 1 and 324 with all 4.
+  static constexpr int kVUnroll = D == 128 ? 4 : 1;
   static constexpr int SP = KT + 4;                                  // row pitch of S, in floats
   static constexpr int PP = KT + 8;                                  // row pitch of P, in 16-bit values
   static constexpr int kSBytes = DS > 1 ? DS * kDecodeHeads * SP * 4 : 0;
@@ -647,65 +651,69 @@ __global__ void __launch_bounds__(kThreads, 2)
       if constexpr (!E4M3) mbar_wait_bounded(&full[unit], phase, &abort_flag, a.status, kStatusWaitFull);
       const uint32_t vbase = smem_u32(ring + unit * C::kUnit);
       const uint32_t paddr = smem_u32(pb) + ((lane & 7) * C::PP + (lane >> 3) * 8) * 2;
+      auto products = [&](bool hide) {  // inlined with either value
+#pragma unroll(C::kVUnroll)
+        for (int k2 = 0; k2 < KT / 32; ++k2) {
+          uint32_t pr[4];
+          ldsm4(paddr + k2 * 64, pr);
 #pragma unroll
-      for (int k2 = 0; k2 < KT / 32; ++k2) {
-        uint32_t pr[4];
-        ldsm4(paddr + k2 * 64, pr);
+          for (int kk = 0; kk < 2; ++kk) {
+            const int k = 2 * k2 + kk;
+            const uint32_t b0 = pr[2 * kk], b1 = pr[2 * kk + 1];
+            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+            if (hide) {
+              // Hidden values may be anything, NaN included: they become 0.
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const int k = 2 * k2 + kk;
-          const uint32_t b0 = pr[2 * kk], b1 = pr[2 * kk + 1];
-          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-          if (masked) {
-            // Hidden values may be anything, NaN included: they become 0.
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int at = tile * KT + 16 * k + 2 * c4 + (y & 1) + 8 * (y >> 1);
-              const uint32_t gone = at > t.span.p || (at < t.span.lo && at >= t.span.sinks) ? 0xffffu << (16 * (y & 1)) : 0u;
-              if (y < 2) keep0 &= ~gone;
-              else keep1 &= ~gone;
+              for (int y = 0; y < 4; ++y) {
+                const int at = tile * KT + 16 * k + 2 * c4 + (y & 1) + 8 * (y >> 1);
+                const uint32_t gone = at > t.span.p || (at < t.span.lo && at >= t.span.sinks) ? 0xffffu << (16 * (y & 1)) : 0u;
+                if (y < 2) keep0 &= ~gone;
+                else keep1 &= ~gone;
+              }
             }
-          }
-          const uint32_t vk = vbase + block(k);
-          if constexpr (E4M3) {
-            // A 16-byte piece is 16 dimensions; as 16-bit pairs the transposed load gives a lane the
-            // dimensions 2 r8 and 2 r8 + 1, which become the rows r8 and r8 + 8 of the block.
+            const uint32_t vk = vbase + block(k);
+            if constexpr (E4M3) {
+              // A 16-byte piece is 16 dimensions; as 16-bit pairs the transposed load gives a lane the
+              // dimensions 2 r8 and 2 r8 + 1, which become the rows r8 and r8 + 8 of the block.
 #pragma unroll
-            for (int v = 0; v < C::VT; v += 2) {
-              uint32_t w[4];
-              if constexpr (C::VT > 1) ldsm4_trans(vk + voff[v / 2], w);
-              else ldsm2_trans(vk + voff[0], w[0], w[1]);
+              for (int v = 0; v < C::VT; v += 2) {
+                uint32_t w[4];
+                if constexpr (C::VT > 1) ldsm4_trans(vk + voff[v / 2], w);
+                else ldsm2_trans(vk + voff[0], w[0], w[1]);
 #pragma unroll
-              for (int y = 0; y < (C::VT > 1 ? 2 : 1); ++y) {
-                uint32_t fr[4];
-                // Bytes: d and d + 1 of one key, then of the next.
-                widen_e4m3(__byte_perm(w[2 * y], 0, 0x3120), fr[0], fr[1]);
-                widen_e4m3(__byte_perm(w[2 * y + 1], 0, 0x3120), fr[2], fr[3]);
-                if (masked) {
-                  fr[0] &= keep0;
-                  fr[1] &= keep0;
-                  fr[2] &= keep1;
-                  fr[3] &= keep1;
+                for (int y = 0; y < (C::VT > 1 ? 2 : 1); ++y) {
+                  uint32_t fr[4];
+                  // Bytes: d and d + 1 of one key, then of the next.
+                  widen_e4m3(__byte_perm(w[2 * y], 0, 0x3120), fr[0], fr[1]);
+                  widen_e4m3(__byte_perm(w[2 * y + 1], 0, 0x3120), fr[2], fr[3]);
+                  if (hide) {
+                    fr[0] &= keep0;
+                    fr[1] &= keep0;
+                    fr[2] &= keep1;
+                    fr[3] &= keep1;
+                  }
+                  mma_f16(o[v + y], fr, b0, b1);
                 }
-                mma_f16(o[v + y], fr, b0, b1);
               }
-            }
-          } else {
+            } else {
 #pragma unroll
-            for (int v = 0; v < C::VT; ++v) {
-              uint32_t w[4];
-              ldsm4_trans(vk + voff[v], w);
-              if (masked) {
-                w[0] &= keep0;
-                w[1] &= keep0;
-                w[2] &= keep1;
-                w[3] &= keep1;
+              for (int v = 0; v < C::VT; ++v) {
+                uint32_t w[4];
+                ldsm4_trans(vk + voff[v], w);
+                if (hide) {
+                  w[0] &= keep0;
+                  w[1] &= keep0;
+                  w[2] &= keep1;
+                  w[3] &= keep1;
+                }
+                mma_bf16(o[v], w, b0, b1);
               }
-              mma_bf16(o[v], w, b0, b1);
             }
           }
         }
-      }
+      };
+      if (masked) products(true);
+      else products(false);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[unit]);
       next_unit();
