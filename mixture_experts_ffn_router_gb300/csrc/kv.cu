@@ -517,10 +517,10 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   a.counters_in = kv->counters_in;
   a.partial = kv->partial;
   a.list = kv->list;
-  // Of costs of 2 to 7 tiles the best: prompts of 1500 to 4100 tokens take 201 us in bf16 with 3 (208 with
-  // 2, 212 with 5); in e4m3, where the queries are split on the way, 318 with 7 against 399 with 3 at width
-  // 256, but at width 128 a mixed batch takes 154 with 4 against 167 with 7.
-  a.item_cost = !a.c.e4m3 ? 3 : a.c.head_dim == 128 ? 4 : 8;
+  // Of costs of 2 to 8 tiles the best: prompts of 1500 to 4100 tokens of width 256 take 196 us in bf16 with 3
+  // (207 with 2, 201 with 4, 206 with 5); in e4m3, where the queries are split on the way, 281 with 4 (303
+  // with 3, 289 with 6). At width 512 a mixed e4m3 batch would take 186 with 5 against 194.
+  a.item_cost = a.c.e4m3 ? 4 : 3;
   a.chunk_partial = kv->chunk_partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

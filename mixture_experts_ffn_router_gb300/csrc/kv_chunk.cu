@@ -1173,51 +1173,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           tok >= t.nt ? 0ull
                       : reinterpret_cast<unsigned long long>(a.q.ptr + static_cast<long long>(t.row0 + tok) * a.q.token_stride +
                                                              (head * a.group + rr % a.group) * a.q.head_stride);
-      if constexpr (!E4M3) {
+      // Where 16 bytes of a row lie.
+      auto place = [&](int r, int v) {
+        const uint32_t byte = (lane % kLanes + v * 32) * 16;
+        return (byte >> 7) * kChunk + r * 128 + ((byte & 127) ^ ((r & 7) << 4));
+      };
 #pragma unroll 8
-        for (int g = 0; g < 32; g += kRowsAtOnce) {
-          const unsigned long long from = __shfl_sync(0xffffffffu, own_row, g + lane / kLanes);
-          const int r = awarp * 32 + g + lane / kLanes;
+      for (int g = 0; g < 32; g += kRowsAtOnce) {
+        const unsigned long long from = __shfl_sync(0xffffffffu, own_row, g + lane / kLanes);
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) {
-            const uint32_t byte = (lane % kLanes + v * 32) * 16;
-            // (A row that is none reads nothing and leaves zeros; any address will do.)
-            const unsigned long long at = from ? from + byte : reinterpret_cast<unsigned long long>(a.q.ptr);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             smem_u32(sq) + (byte >> 7) * kChunk + r * 128 + ((byte & 127) ^ ((r & 7) << 4))),
-                         "l"(at), "r"(from ? 16 : 0)
-                         : "memory");
-          }
+        for (int v = 0; v < kVecs; ++v) {
+          // (A row that is none reads nothing and leaves zeros; any address will do.)
+          const unsigned long long at =
+              from ? from + (lane % kLanes + v * 32) * 16 : reinterpret_cast<unsigned long long>(a.q.ptr);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_u32(sq) + place(awarp * 32 + g + lane / kLanes, v)),
+                       "l"(at), "r"(from ? 16 : 0)
+                       : "memory");
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-      } else {
-        constexpr int kBatch = 8 / kVecs;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (E4M3) {
+        // A row's two parts take the place of its values: the warp that brought it reads it, then writes them.
+        // (Through registers, eight rows at a time, each with a wait of its own for L2, an item cost 6 key
+        // tiles instead of 4.)
+        __syncwarp();
+        constexpr int kBatch = 2 / kVecs;
 #pragma unroll 1
         for (int g = 0; g < 32; g += kBatch * kRowsAtOnce) {
           uint4 x[kBatch][kVecs];
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const unsigned long long from = __shfl_sync(0xffffffffu, own_row, g + b * kRowsAtOnce + lane / kLanes);
+          for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v) {
-              x[b][v] = make_uint4(0u, 0u, 0u, 0u);
-              if (from) x[b][v] = *reinterpret_cast<const uint4*>(from + (lane % kLanes + v * 32) * 16);
-            }
-          }
+            for (int v = 0; v < kVecs; ++v)
+              x[b][v] = *reinterpret_cast<const uint4*>(sq + place(awarp * 32 + g + b * kRowsAtOnce + lane / kLanes, v));
+          __syncwarp();
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {
             const int r = awarp * 32 + g + b * kRowsAtOnce + lane / kLanes;
             const uint32_t swz = (r & 7) << 4;
             // A power of two that brings the row's largest magnitude into [128, 256).
-            uint32_t top = 0;
+            uint32_t two_tops = 0;
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
               const uint32_t u[4] = {x[b][v].x, x[b][v].y, x[b][v].z, x[b][v].w};
 #pragma unroll
-              for (int q = 0; q < 4; ++q) top = max(top, max((u[q] << 16) & 0x7fffffffu, u[q] & 0x7fffffffu));
+              for (int q = 0; q < 4; ++q) two_tops = __vmaxu2(two_tops, u[q] & 0x7fff7fffu);
             }
+            uint32_t top = max(two_tops << 16, two_tops & 0xffff0000u);
+            if constexpr (kLanes == 32) {
+              top = __reduce_max_sync(0xffffffffu, top);
+            } else {
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
             const int e = static_cast<int>(top >> 23), up_exp = e == 255 ? 255 : min(261 - e, 254);
             const float up = e == 255 ? 1.0f : __uint_as_float(static_cast<uint32_t>(up_exp) << 23);
             if (lane % kLanes == 0) q_exp[(item_no & 1) * kRows + r] = static_cast<uint8_t>(up_exp);
