@@ -1283,12 +1283,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float want = __uint_as_float(min((most >> 23) + 1u, 254u) << 23);
           const float before = vref;
           if (most > 0) vref = fmaxf(vref, want);
+          // 1 / vref, another power of two (of 2^127 a subnormal one): a product with it is the quotient.
+          const uint32_t vexp = __float_as_uint(vref) >> 23;
+          const float inv = __uint_as_float(vexp == 254 ? 0x00400000u : (254u - vexp) << 23);
           if (tile_no >= 2) wait(&scale_free[tile_no & 1], ((tile_no >> 1) - 1) & 1, kStatusWaitEmpty);
           float* to = scales + (tile_no & 1) * 2 * KT;
           to[key] = sk;
-          to[KT + key] = __fdiv_rn(sv, vref) * 64.0f;
+          to[KT + key] = sv * inv * 64.0f;
           if (awarp == 0 && lane == 0) {
-            scale_step[tile_no & 1] = j == 0 ? 1.0f : before / vref;
+            scale_step[tile_no & 1] = j == 0 ? 1.0f : before * inv;
             scale_ref[tile_no & 1] = vref;
           }
           __syncwarp();
