@@ -527,8 +527,8 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   const int ctas = 2 * kv->num_sms < kDecodeMaxCtas ? 2 * kv->num_sms : kDecodeMaxCtas;
   // A single token of up to kDecodeHeads heads per kv head fills an item of the decode kernel; the chunk
   // kernel computes tiles of 256 rows of which it would fill `group`. Single tokens through the one and the other:
-  // one short sequence 14 and 20 us, 64 e4m3 sequences (width 512) 88 and 331, 256 windows 217 and 376,
-  // one long bf16 sequence 96 and 144.
+  // one short sequence 14 and 20 us, 64 e4m3 sequences (width 512) 78 and 226, 256 windows 217 and 360,
+  // one long bf16 sequence 96 and 124.
   const cudaError_t e = a.b.max_new <= 1 && a.group <= kDecodeHeads ? launch_kv_decode(a, ctas, s)
                                                                     : launch_kv_chunk(a, kv->chunk_pairs, s);
   return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;

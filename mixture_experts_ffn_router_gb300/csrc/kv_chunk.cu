@@ -31,14 +31,16 @@
 // way. What the MMA thread waits for is counted on barriers of the first CTA, which the other's warps and
 // copies reach over the cluster.
 //
-// What bounds it. Prompts of 4096 tokens, 16 heads on 8: width 256 1.44 PFLOP/s, width 512 1.05 (1.57 with
+// What bounds it. Prompts of 4096 tokens, 16 heads on 8: width 256 1.54 PFLOP/s, width 512 1.14 (1.71 with
 // the second S), of 1.91 measured for a burst and 1.72 sustained; at these the power limit holds the
-// clock. A key tile takes 2500 cycles where its products are 2048 (width 256): the softmax's chain, from
-// S to P, is 2400. Width 128 (products 1024) and e4m3, whose softmax multiplies by two scales per key
-// and shares its SM's issue slots with the widening, are bound by that chain: 2300 and 4000 cycles. Measured
-// and not kept: the softmax warps in two groups that take turns at whole tiles (width 256 430 us against
-// 376, with two S to work from a group's turn waits for the other's products), V looked through by warps
-// 12..15 (385).
+// clock. A key tile takes about 2400 cycles where its products are 2048 (width 256): the softmax's chain,
+// from S to P, is nearly as long. Width 128 (products 1024) and e4m3, whose softmax multiplies by two
+// scales per key and shares its SM's issue slots with the widening, are bound by that chain: about 1800, and
+// 2400 and 3200 (e4m3, widths 128 and 256). Much of the chain is instructions on their way: see wait_slow.
+// Measured and not kept: the softmax warps in two groups that take turns at whole tiles (width 256 430 us
+// against 376, with two S to work from a group's turn waits for the other's products), V looked through by
+// warps 12..15 (385), S loaded before what else there is to know of the tile (width 128 293 against 283), more
+// registers for the softmax by setmaxnreg (width 256 1% less, width 512 5% more, e4m3 3% more).
 //
 // Hidden values. P is 0 for a key a row does not see, but 0 times a NaN or an infinity is not 0, so in
 // key tiles with hidden keys the softmax warps clear V's rows that no row of the tile sees, and
