@@ -82,6 +82,20 @@ struct Move {
   static constexpr int kWarpRows = kRows * kGroups;
 };
 
+// The same of eight numbers by divisions, out of line; of a row of zeros or with a value that is not finite
+// codes 0.
+__device__ __noinline__ uint2 divided_codes(uint4 x, float s) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  uint32_t code[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    code[q] = s > 0.0f ? __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(__uint_as_float(u[q] << 16), s),
+                                                              __fdiv_rn(__uint_as_float(u[q] & 0xFFFF0000u), s)),
+                                                  __NV_SATFINITE, __NV_E4M3)
+                       : 0u;
+  return make_uint2(__byte_perm(code[0], code[1], 0x5410), __byte_perm(code[2], code[3], 0x5410));
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kMoveWarps * 32)
     kv_write_kernel(KvBatch b, KvCache c, KvRows k, KvRows v, unsigned int* status) {
@@ -159,22 +173,17 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
       const unsigned long long s2 = twice(s), nr2 = twice(-r_s);
 #pragma unroll
       for (int j = 0; j < M::kRowVecs; ++j) {
-        const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
-        uint32_t code[4];
-        if (fast) {
+        uint2 codes;
+        if (__builtin_expect(fast, 1)) {
+          const uint32_t u[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
+          uint32_t code[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) code[q] = quotient_codes(u[q] ^ 0x80008000u, s2, nr2);
+          codes = make_uint2(__byte_perm(code[0], code[1], 0x5410), __byte_perm(code[2], code[3], 0x5410));
         } else {
-          // A row of zeros or with a value that is not finite: codes 0.
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            code[q] = s > 0.0f ? __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(__uint_as_float(u[q] << 16), s),
-                                                                      __fdiv_rn(__uint_as_float(u[q] & 0xFFFF0000u), s)),
-                                                          __NV_SATFINITE, __NV_E4M3)
-                               : 0u;
+          codes = divided_codes(x[i][j], s);
         }
-        *reinterpret_cast<uint2*>(dst + i * step * D + j * M::kLanes * 8) =
-            make_uint2(__byte_perm(code[0], code[1], 0x5410), __byte_perm(code[2], code[3], 0x5410));
+        *reinterpret_cast<uint2*>(dst + i * step * D + j * M::kLanes * 8) = codes;
       }
     }
   }
