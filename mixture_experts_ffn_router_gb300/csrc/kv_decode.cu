@@ -32,9 +32,9 @@
 // against 772 for 64 sequences of 16384 tokens, 8 heads of width 256.)
 //
 // Measured: 64 sequences of 16384 tokens, of the 6.70 TB/s of a copy: bf16 7.1 TB/s (8 heads of width 128)
-// and 6.9 (2 of 512); e4m3 6.8, 6.9 and 6.5 (width 128, 256, 512; there the widening of the codes, some 600
-// instructions per warp and tile, is as long as the loads). A call takes about 6 us beside its loads: 3 to
-// find its work and load its queries, the rest to join pieces.
+// and 6.9 (2 of 512); e4m3 6.8, 6.9 and 6.5 (width 128, 256, 512; there a tile's chain of widened products,
+// weights and barriers is as long as its loads, with 42% of the issue slots busy). A call takes about 6 us
+// beside its loads: 3 to find its work and load its queries, the rest to join pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
