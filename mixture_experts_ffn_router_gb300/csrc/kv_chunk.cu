@@ -92,9 +92,9 @@ struct Chk {
   static constexpr int kWSlot = kVTile * kChunk;
   static constexpr int NV = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : (D == 512 ? 1 : D == 256 ? 2 : 6);
   static constexpr int NW = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : 0;
-  // Of a thread's pieces of V to widen, those unrolled: at width 128 4 prompts of 4096 tokens take 393 us
-  // with 1 and 402 with 2 (fewer instructions to fetch), at 256 575 and 552.
-  static constexpr int kWUnroll = D == 128 ? 1 : 2;
+  // Of a thread's pieces of V to widen, those unrolled: prompts of 1500 to 4100 tokens take 206 us with 1
+  // and 219 with 4 at width 128 (fewer instructions to fetch), but 284 and 272 at width 256.
+  static constexpr int kWUnroll = D == 128 ? 1 : 4;
   static constexpr int kScaleBytes = E4M3 ? 2 * 2 * KT * 4 : 0;
   static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 18) + 24 + (E4M3 ? 32 : 96) + 15) / 16 * 16;
   static constexpr int kSmem =
