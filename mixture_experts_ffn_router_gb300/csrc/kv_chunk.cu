@@ -98,7 +98,7 @@ struct Chk {
   static constexpr int kScaleBytes = E4M3 ? 2 * 2 * KT * 4 : 0;
   static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 18) + 24 + (E4M3 ? 32 : 96) + 15) / 16 * 16;
   static constexpr int kSmem =
-      kQBytes + NK * kKStage + NV * kVSlot + NW * kWSlot + kScaleBytes + 3 * kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
+      kQBytes + NK * kKStage + NV * kVSlot + NW * kWSlot + kScaleBytes + 4 * kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* v_ring = k_ring + C::NK * C::kKStage;
   uint8_t* w_ring = v_ring + C::NV * C::kVSlot;
   float* scales = reinterpret_cast<float*>(w_ring + C::NW * C::kWSlot);  // [2][2][KT]
-  float* exch = scales + C::kScaleBytes / 4;                          // [kRows]
-  float* fin = exch + kRows;  // [2][kRows] what an item's O is multiplied by, of alternate items
+  float* exch = scales + C::kScaleBytes / 4;                          // [kRows] maxima of a tile
+  float* row_sums = exch + kRows;  // [kRows] an item's sums
+  float* fin = row_sums + kRows;  // [2][kRows] what an item's O is multiplied by, of alternate items
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(fin + 2 * kRows);          // [2][kRows] (e4m3), of alternate items
   uint64_t* full_k = reinterpret_cast<uint64_t*>(q_exp + (E4M3 ? 2 * kRows : 0));  // first CTA's: both CTAs' keys
   uint64_t* empty_k = full_k + C::NK;
@@ -1017,11 +1018,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // The rows' sums, and what the output is multiplied by; warps 12..15 write it.
-      pair_sync(quarter);  // (exch may still be read for the last tile's reference)
-      if (half == 1) exch[r] = l;
+      // One half's sum goes to the other through words of its own: in exch the next item's first maximum could
+      // follow it before it is read. (It has been read before the next sum comes: each of an item's tiles
+      // has a barrier.)
+      if (half == 1) row_sums[r] = l;
       pair_sync(quarter);
       if (half == 0) {
-        l += exch[r];
+        l += row_sums[r];
         const bool whole = i0 == 0 && n == t.count;
         float vs_f = 1.0f;
         if constexpr (E4M3) vs_f = vref * 0.015625f;

@@ -283,6 +283,20 @@ def test_many_sequences(fmt, n_seqs):
     U.check_attention(U.Case(fmt, 2, 1, 128, 16, [min(b % 3, n) for b, n in enumerate(kv_len)], kv_len, seed=19))
 
 
+@pytest.mark.parametrize("fmt,d", SHAPES)
+def test_items_that_follow_each_other_keep_their_sums(fmt, d):
+    """Ten and more short items to a pair of SMs, one straight after the other: each row's weights are summed from
+    two halves, whose exchange the next item's must not overtake."""
+    new = [1 + b % 5 for b in range(400)]
+    case = U.Case(fmt, 4, 2, d, 16, new, [n + (3 * b) % 7 for b, n in enumerate(new)], seed=30)
+    kv = case.handle()
+    c, batch, q = case.filled(kv), case.batch(), case.q.cuda()
+    out, lse = U.check_attention(case, kv=kv, cache=c, q=q)
+    for _ in range(30):
+        out2, lse2 = kv.attention(c, batch, q)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("fmt,page,pages", [("bf16", 128, 20000), ("e4m3", 16, 300000)])
 def test_offsets_beyond_32_bits(fmt, page, pages):
     """The sequence's pages are the last of a cache of over 2^32 bytes."""
