@@ -52,8 +52,15 @@
 // The keys' scales multiply S. V's codes are widened to fp16, exactly, by warps 12..15 on the way to
 // the tensor cores. The values' scales multiply P before it is rounded to fp16, relative to the
 // largest scale so far and 2^6 up: P is then at most 2^15, and what is lost under fp16's smallest
-// number is 2^-31 of a weight of 1 per key. (A NaN among the codes, which moe_ffn_kv_write does not make,
+// number is 2^-31 of a weight of 1 per key of that scale. (A NaN among the codes, which moe_ffn_kv_write does not make,
 // may reach rows that do not see it; a NaN scale does not.)
+//
+// Scales far apart. A reference that all rows of an item share would take the values of a row that does not
+// see the largest scale (or hardly weighs it) out of fp16. So where an item's scales span more than kFarScales,
+// zeros among them, its further tiles go through far_weights: P = exp2(s + log2(scale) - R) with a reference R
+// per row, over the keys that the row sees, rounded to bf16 (as over a bf16 cache, half a step is 2^-8), which
+// holds 2^-133 of the largest term; V's codes are widened to bf16 there, exactly too. Up to there a shared
+// reference loses at most 2^-19 per key of the row's largest term.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -96,15 +103,22 @@ struct Chk {
   // and 219 with 4 at width 128 (fewer instructions to fetch), but 284 and 272 at width 256.
   static constexpr int kWUnroll = D == 128 ? 1 : 4;
   static constexpr int kScaleBytes = E4M3 ? 2 * 2 * KT * 4 : 0;
-  static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 18) + 24 + (E4M3 ? 32 : 96) + 15) / 16 * 16;
+  static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 18) + 32 + (E4M3 ? 48 : 96) + 15) / 16 * 16;
   static constexpr int kSmem =
-      kQBytes + NK * kKStage + NV * kVSlot + NW * kWSlot + kScaleBytes + 4 * kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
+      kQBytes + NK * kKStage + NV * kVSlot + NW * kWSlot + kScaleBytes + (E4M3 ? 5 : 4) * kRows * 4 + (E4M3 ? 2 * kRows : 0) + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// To 2^-22 of the result, or outside (1/2, 2) of its size: 2^-15 of a weight at the ends of the range.
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -273,7 +287,17 @@ __device__ __forceinline__ void or_shared(uint32_t addr, uint32_t bits) {
   asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(bits) : "memory");
 }
 
+// Warps 12..15: the same two.
 __device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 6, 128;" ::: "memory"); }
+__device__ __forceinline__ bool aux_sync_or(bool c) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, 6, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(c ? 1 : 0)
+      : "memory");
+  return r != 0;
+}
 
 // ------------------------------------------------------------------ the list of row tiles
 
@@ -412,6 +436,103 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
   return mbar_wait_bounded(bar, parity, abort, status, why);
 }
 
+// The weights of a tile whose values' scales are far from others of the item (e4m3): as the kernel's own code
+// for a tile's weights, with a reference of the row's own for P, in base 2 like the scores, that moves when a
+// term passes it by more than 2^15 and then leaves the largest term at 2^7. The maximum moves in every such tile.
+// Few caches have such tiles: what is theirs lies out of line and takes its time (one prompt of 4096 tokens,
+// 16 heads on 8 of width 256: 281 us with a large scale at its start, 147 without; to find out costs the others
+// 0 to 2.5%).
+constexpr float kFarScales = 4096.0f;
+
+struct FarRow {
+  float ref, l;  // maximum of the scores, and this half row's sum
+  float vref;    // reference of P
+};
+
+// s_at, o_at: TMEM of the row's S (and P) and of this half of its O; sk: this half's key scales, the values'
+// scales' logarithms KT further.
+template <int kCols>
+__device__ __noinline__ FarRow far_weights(FarRow row, uint32_t s_at, uint32_t o_at, const float* sk, unsigned long long seen,
+                                           float qs, float* top_at, float* vtop_at, int half, int quarter, bool first) {
+  float y[64];
+  {
+    uint32_t b0[32], b1[32];
+    tmem_ld32_nowait(s_at + half * 64, b0);
+    tmem_ld32_nowait(s_at + half * 64 + 32, b1);
+    tmem_wait_ld();
+    reg_fence32(b0);
+    reg_fence32(b1);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      y[i] = __uint_as_float(b0[i]);
+      y[32 + i] = __uint_as_float(b1[i]);
+    }
+  }
+  // (The scales of hidden keys may be anything; what becomes of -inf and a logarithm of infinity or NaN makes no
+  // maximum.)
+  float top = -INFINITY, vtop = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    y[i] = seen >> i & 1ull ? y[i] * sk[i] * qs : -INFINITY;
+    top = fmaxf(top, y[i]);
+    vtop = fmaxf(vtop, y[i] + sk[KT + i]);
+  }
+  if (half == 1) {
+    *top_at = top;
+    *vtop_at = vtop;
+  }
+  pair_sync(quarter);
+  if (half == 0) {
+    *top_at = fmaxf(top, *top_at);
+    *vtop_at = fmaxf(vtop, *vtop_at);
+  }
+  pair_sync(quarter);
+  top = fmaxf(row.ref, *top_at);
+  vtop = *vtop_at;
+  pair_sync(quarter);  // (the next tile's may follow)
+  const float base = top == -INFINITY ? 0.0f : top;
+  row.l *= exp2_approx(row.ref - base);
+  row.ref = top;
+  const bool move = vtop > row.vref + 15.0f;
+  const float vref = move ? vtop - 7.0f : row.vref;
+  const float vbase = vref == -INFINITY ? 0.0f : vref;
+  if (!first && __any_sync(0xffffffffu, move)) {
+    const float f = move ? exp2_approx(row.vref - vbase) : 1.0f;
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+      uint32_t o[32];
+      tmem_ld32_nowait(o_at + c, o);
+      tmem_wait_ld();
+      reg_fence32(o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      tmem_st32(o_at + c, o);
+    }
+  }
+  row.vref = vref;
+  float sum = 0.0f;
+  uint32_t w[32];
+#pragma unroll
+  for (int i = 0; i < 64; i += 2) {
+    sum += exp2_approx(y[i] - base) + exp2_approx(y[i + 1] - base);
+    w[i / 2] = pack_bf16(exp2_approx(y[i] + sk[KT + i] - vbase), exp2_approx(y[i + 1] + sk[KT + i + 1] - vbase));
+    const uint32_t bits = static_cast<uint32_t>(seen >> i) & 3u;
+    w[i / 2] &= (bits & 1u ? 0xffffu : 0u) | (bits & 2u ? 0xffff0000u : 0u);
+  }
+  row.l += sum;
+  tmem_st32(s_at + half * 32, w);
+  return row;
+}
+
+// A widened tile's values from fp16 to bf16, by warps 12..15.
+__device__ __noinline__ void far_values(uint32_t* w, int pairs) {
+  aux_sync();
+  for (int i = threadIdx.x - kAuxWarp0 * 32; i < pairs; i += kAuxWarps * 32) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w + i));
+    w[i] = pack_bf16(f.x, f.y);
+  }
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_chunk_kernel(const KvAttn a, const __grid_constant__ CUtensorMap map_k,
@@ -425,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* scales = reinterpret_cast<float*>(w_ring + C::NW * C::kWSlot);  // [2][2][KT]
   float* exch = scales + C::kScaleBytes / 4;                          // [kRows] maxima of a tile
   float* row_sums = exch + kRows;  // [kRows] an item's sums
-  float* fin = row_sums + kRows;  // [2][kRows] what an item's O is multiplied by, of alternate items
+  float* vexch = row_sums + kRows;  // [kRows] (e4m3) as exch, with the values' scales
+  float* fin = vexch + (E4M3 ? kRows : 0);  // [2][kRows] what an item's O is multiplied by, of alternate items
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(fin + 2 * kRows);          // [2][kRows] (e4m3), of alternate items
   uint64_t* full_k = reinterpret_cast<uint64_t*>(q_exp + (E4M3 ? 2 * kRows : 0));  // first CTA's: both CTAs' keys
   uint64_t* empty_k = full_k + C::NK;
@@ -448,8 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* scale_step = reinterpret_cast<float*>(tmem_slot + 2);  // [2] what O is multiplied by before a tile
-  float* scale_ref = scale_step + 2;  // [2] what the values' scales of a tile are relative to
-  uint32_t* aux_top = tmem_slot + 6;  // [2][4], the tile's largest scale by warps
+  float* scale_ref = scale_step + 2;  // [2] what the values' scales of a tile are relative to; 0: far apart
+  uint32_t* aux_top = tmem_slot + 8;  // [2][4] (at a multiple of 16 bytes), the tile's largest scale by warps
+  uint32_t* w_far = aux_top + 8;      // [NW] whether a widened tile is bf16
   uint32_t* odd = aux_top;            // [3][8] (bf16) keys with values that either CTA cleared, of items in turn
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -720,6 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       constexpr uint32_t kIdescS = idesc_of(E4M3 ? 0u : 1u, false, 256, KT);
       constexpr uint32_t kIdescV = idesc_of(E4M3 ? 0u : 1u, true, 256, C::DV);
+      constexpr uint32_t kIdescFar = idesc_of(1u, true, 256, C::DV);
       constexpr int NVW = E4M3 ? C::NW : C::NV;
       uint8_t* const v_chunks = E4M3 ? w_ring : v_ring;
       uint64_t* const v_empty = E4M3 ? empty_w : empty_v;
@@ -775,9 +899,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int u = uniform(vs);
           const uint64_t vb = smem_desc_v(smem_u32(v_chunks) + u * (E4M3 ? C::kWSlot : C::kVSlot));
           const uint32_t add = uniform(j > 0 ? 1 : 0);
+          uint32_t idesc = kIdescV;
+          if constexpr (E4M3) {
+            if (__builtin_expect(__any_sync(0xffffffffu, w_far[vs] != 0), 0)) idesc = kIdescFar;
+          }
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            umma_ta_pair_elect(tm, p + 8 * k, vb + k * (2048 >> 4), kIdescV, k > 0 ? 1u : add);
+            umma_ta_pair_elect(tm, p + 8 * k, vb + k * (2048 >> 4), idesc, k > 0 ? 1u : add);
           commit_pair_elect(&v_empty[u]);
           if (++vs == NVW) vs = 0;
           commit_pair_elect(o_done);
@@ -814,12 +942,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = q_exp[(item_no & 1) * kRows + r];
         if (p >= 0) qs = e == 255 ? __uint_as_float(0x7fffffffu) : qs / __uint_as_float(static_cast<uint32_t>(e) << 23);
       }
-      float ref = -INFINITY, l = 0.0f, vref = 0.0f;
+      float ref = -INFINITY, l = 0.0f;
+      float vref = 0.0f;  // what the values' scales are relative to
+      bool far = false;
       // P V of the tile before is complete.
       auto wait_pv = [&] {
         if (tile_no > 0) wait(o_done, (tile_no - 1) & 1, kStatusWaitAccFull);
       };
-      for (int j = 0; j < n; ++j, ++tile_no) {
+      int j = 0;
+      for (; j < n; ++j, ++tile_no) {
         const int tile = tile_at(i0 + j);
         const bool masked = is_masked(tile);
         const float* sk = scales + (tile_no & 1) * 2 * KT + half * 64;
@@ -829,7 +960,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (E4M3) {
           wait(&scale_full[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitFull);
           step = scale_step[tile_no & 1];
-          vref = scale_ref[tile_no & 1];
+          const float now = scale_ref[tile_no & 1];
+          if (__builtin_expect(now == 0.0f, 0)) {
+            far = true;
+            break;
+          }
+          vref = now;
         }
         // What the end of the tile waits for has mostly happened by now.
         const bool v_here = mbar_test(&v_full[vs], v_phase), pv_done = tile_no == 0 || mbar_test(o_done, (tile_no - 1) & 1);
@@ -1016,6 +1152,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) arrive_first(&p_ready[tile_no & 1]);
       }
+      if constexpr (E4M3) {
+        if (__builtin_expect(far, 0)) {
+          // The tiles from the first whose scales are far from others on. The reference of P is the same number
+          // until it moves.
+          FarRow row = {ref, l, j == 0 || ref == -INFINITY ? -INFINITY : ref + log2f(vref) - 6.0f};
+#pragma unroll 1
+          for (; j < n; ++j, ++tile_no) {
+            wait(&s_full[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitAccFull);
+            wait(&scale_full[tile_no & 1], (tile_no >> 1) & 1, kStatusWaitFull);
+            wait_pv();
+            tc_fence_after();
+            const int k0 = tile_at(i0 + j) * KT + half * 64;
+            const unsigned long long seen = low_bits(p + 1 - k0) & ~(low_bits(lo - k0) & ~low_bits(a.sinks - k0));
+            row = far_weights<C::DV / 2>(row, tmem + lanes + 256 + (tile_no & 1) * KT, tmem + lanes + half * (C::DV / 2),
+                                         scales + (tile_no & 1) * 2 * KT + half * 64, seen, qs, &exch[r], &vexch[r], half,
+                                         quarter, j == 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&scale_free[tile_no & 1]);
+            wait(&v_full[vs], v_phase, kStatusWaitFull);
+            if (++vs == NVW) {
+              vs = 0;
+              v_phase ^= 1;
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_first(&p_ready[tile_no & 1]);
+          }
+          ref = row.ref;
+          l = row.l;
+          vref = row.vref == -INFINITY || ref == -INFINITY ? 64.0f : 64.0f * exp2f(row.vref - ref);
+        }
+      }
 
       // The rows' sums, and what the output is multiplied by; warps 12..15 write it.
       // One half's sum goes to the other through words of its own: in exch the next item's first maximum could
@@ -1163,10 +1332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int next_page = -1;
       float2 next_scales = make_float2(0.0f, 0.0f);
+      bool next_seen = false;
       if constexpr (E4M3) {
         const int page = page_of(0);
         next_page = page_of(1);
         next_scales = scales_of(0, page);
+        next_seen = page >= 0;
       }
       if (item_no > 0) wait(q_free, (item_no - 1) & 1, kStatusWaitEmpty);
       // A warp brings 32 rows; each lane knows where one of them is, or that there is none.
@@ -1271,20 +1442,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!E4M3) output_last();
       if constexpr (E4M3) {
         float vref = __uint_as_float(0x00800000u);  // at least the values' largest scale so far, a power of two
+        // The scales so far of keys that some row sees: the largest, and the smallest of this thread's.
+        uint32_t largest = 0, smallest = 0x7f7fffffu;
         for (int j = 0; j < n; ++j, ++tile_no) {
           const int tile = tile_at(i0 + j);
           const bool masked = is_masked(tile);
           // The scales of this thread's key: for the keys as they are, for the values relative to vref.
           const float sk = next_scales.x, sv = next_scales.y;
+          const bool counts = next_seen && __float_as_uint(sv) < 0x7f800000u;
           next_scales = scales_of(j + 1, next_page);
+          next_seen = next_page >= 0;
           next_page = page_of(j + 2);
-          const uint32_t bits = __float_as_uint(sv);
-          const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, counts ? __float_as_uint(sv) : 0u);
+          if (counts) smallest = min(smallest, __float_as_uint(sv));
           if (lane == 0) aux_top[(tile_no & 1) * 4 + awarp] = top;
           aux_sync();
-          uint32_t most = 0;
-#pragma unroll
-          for (int w = 0; w < kAuxWarps; ++w) most = max(most, aux_top[(tile_no & 1) * 4 + w]);
+          const uint4 tops = *reinterpret_cast<const uint4*>(aux_top + (tile_no & 1) * 4);
+          const uint32_t most = max(max(tops.x, tops.y), max(tops.z, tops.w));
+          largest = max(largest, most);
+          const bool far = aux_sync_or(__uint_as_float(smallest) * kFarScales < __uint_as_float(largest));
           const float want = __uint_as_float(min((most >> 23) + 1u, 254u) << 23);
           const float before = vref;
           if (most > 0) vref = fmaxf(vref, want);
@@ -1294,10 +1470,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tile_no >= 2) wait(&scale_free[tile_no & 1], ((tile_no >> 1) - 1) & 1, kStatusWaitEmpty);
           float* to = scales + (tile_no & 1) * 2 * KT;
           to[key] = sk;
-          to[KT + key] = sv * inv * 64.0f;
+          to[KT + key] = far ? log2_approx(sv) : sv * inv * 64.0f;
           if (awarp == 0 && lane == 0) {
             scale_step[tile_no & 1] = j == 0 ? 1.0f : before * inv;
-            scale_ref[tile_no & 1] = vref;
+            scale_ref[tile_no & 1] = far ? 0.0f : vref;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&scale_full[tile_no & 1]);
@@ -1329,6 +1505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(to_w + (byte ^ swz)) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(to_w + ((byte + 16) ^ swz)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
+          if (awarp == 0 && lane == 0) w_far[ws] = far ? 1 : 0;
+          if (__builtin_expect(far, 0)) far_values(reinterpret_cast<uint32_t*>(w_ring + ws * C::kWSlot), C::kWSlot / 4);
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {

@@ -297,6 +297,46 @@ def test_items_that_follow_each_other_keep_their_sums(fmt, d):
         assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 2)])
+@pytest.mark.parametrize("at", [0, 64, 200, 290])
+def test_values_of_far_apart_sizes(fmt, d, window, sinks, at):
+    """A value 2^40 above the others counts for the rows that see it alone, in whichever key tile it is."""
+    case = U.Case(fmt, 4, 2, d, 32, [300, 40, 1], [300, 291, 291], seed=31)
+    for v in case.v:
+        v[:] *= 2.0 ** -30
+        if at < len(v):
+            v[at] *= 2.0 ** 40
+    U.check_attention(case, window, sinks)
+
+
+@pytest.mark.parametrize("d", [128, 256, 512])
+def test_values_of_far_apart_sizes_in_whole_items(d):
+    """The same in more items than there are pairs of SMs, which are then not cut: one after the other, with
+    their large value in another tile, or in none."""
+    case = U.Case("e4m3", 2, 2, d, 16, [140] * 60, [140 + 9 * (b % 7) for b in range(60)], seed=32)
+    for b, v in enumerate(case.v):
+        if b % 5:
+            v[(37 * b) % 140] *= 2.0 ** (40 if b % 2 else -40)
+    U.check_attention(case)
+
+
+@pytest.mark.parametrize("d", [128, 256, 512])
+@pytest.mark.parametrize("new", [1, 160])
+@pytest.mark.parametrize("big,score", [(2.0 ** 40, -45.0), (0.0, 30.0), (2.0 ** -40, 25.0)])
+def test_values_far_from_their_weights(d, new, big, score):
+    """A large value of hardly any weight, and zeros or small ones of nearly all: the other keys' share of the
+    output is as exact as their own sizes ask for."""
+    for at in (3, 150, 299 - new // 2):
+        case = U.Case("e4m3", 2, 1, d, 64, [new], [300], seed=33)
+        u = torch.randn(d, generator=torch.Generator().manual_seed(d)).to(torch.bfloat16)
+        case.q[:] = u
+        case.k[0][:] *= 0.25
+        case.k[0][at, 0] = (u.double() * score * d ** 0.5 / (u.double() ** 2).sum()).to(torch.bfloat16)
+        case.v[0][at] *= big
+        U.check_attention(case)
+
+
 @pytest.mark.parametrize("fmt,page,pages", [("bf16", 128, 20000), ("e4m3", 16, 300000)])
 def test_offsets_beyond_32_bits(fmt, page, pages):
     """The sequence's pages are the last of a cache of over 2^32 bytes."""
