@@ -319,7 +319,7 @@ int moe_ffn_selftest_wait_expiry(uint32_t* status_word, unsigned long long* reco
  * included and last: new token i is at position kv_len[b] - n_b + i. Position p of sequence b is
  * kept in slot p % page_size of page pages[b * pages_stride + p / page_size].
  *   - New tokens at a negative position (kv_len[b] < n_b) and token rows at or after
- *     cu_q[n_seqs] (padding) belong to no position: they are not written, read back as 0 and attend
+ *     cu_q[n_seqs] (padding), or before cu_q[0], belong to no position: they are not written, read back as 0 and attend
  *     to nothing.
  *   - cu_q must start at 0 and not decrease, n_b <= max_new, and kv_len[b] <= pages_cols *
  *     page_size; entries of the page table past a sequence's last token are not read. The kernels

@@ -137,8 +137,18 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvBatch& b, const KvCache& c,
   s.n = min(max(r1 - s.row0, 0), min(b.n_tokens - s.row0, b.max_new));
   const long long room = static_cast<long long>(b.pages_cols) << c.page_log2;
   s.len = static_cast<int>(min(static_cast<long long>(max(len, 0)), min(room, 0x7fffff00LL)));
-  if (s.row0 != r0 || s.row0 + s.n != r1 || s.len != len) atomicOr(status, 0x10u);
+  if (s.row0 != r0 || s.row0 + s.n != r1 || s.len != len || (seq == 0 && r0 != 0)) atomicOr(status, 0x10u);
   return s;
+}
+
+// Rows of no sequence: those before the first one's and those from the last one's end on.
+struct KvNoRows {
+  int before, after;
+};
+
+__device__ __forceinline__ KvNoRows kv_no_rows(const KvBatch& b) {
+  if (b.n_seqs == 0) return {0, 0};
+  return {min(max(b.cu_q[0], 0), b.n_tokens), min(max(b.cu_q[b.n_seqs], 0), b.n_tokens)};
 }
 
 // The positions one token sees: [0, sinks) and [lo, p], p < 0 for none.

@@ -642,14 +642,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_tiles = *a.list.n_tiles;
   const int parts = a.c.kv_heads * C::kHalves;
   {  // Rows of no sequence, and of tokens that see nothing.
-    const int used = a.b.n_seqs > 0 ? min(max(a.b.cu_q[a.b.n_seqs], 0), a.b.n_tokens) : 0;
+    const KvNoRows none = kv_no_rows(a.b);
     auto clear = [&](long long to) {
       for (int j = 0; j < D; j += 8) *reinterpret_cast<uint4*>(a.out + to * D + j) = make_uint4(0u, 0u, 0u, 0u);
       if (a.lse) a.lse[to] = -INFINITY;
     };
-    const long long n = static_cast<long long>(a.b.n_tokens - used) * a.q_heads;
+    const long long before = static_cast<long long>(none.before) * a.q_heads;
+    const long long n = before + static_cast<long long>(a.b.n_tokens - none.after) * a.q_heads;
     for (long long i = static_cast<long long>(blockIdx.x) * kThreads + tid; i < n; i += static_cast<long long>(gridDim.x) * kThreads)
-      clear(static_cast<long long>(used) * a.q_heads + i);
+      clear(i < before ? i : static_cast<long long>(none.after) * a.q_heads + i - before);
     for (int e = blockIdx.x; e < n_tiles; e += gridDim.x) {
       const KvRowTile t = a.list.tiles[e];
       if (t.count > 0) continue;

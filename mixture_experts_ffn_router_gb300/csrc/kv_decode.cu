@@ -292,9 +292,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   for (int r = 0; r < max(rounds, 1); ++r) look(r, true);
   {  // Rows of no sequence.
-    const int used = n_seqs > 0 ? min(max(a.b.cu_q[n_seqs], 0), a.b.n_tokens) : 0;
-    clear_rows<D>(a, static_cast<long long>(used) * a.q_heads, static_cast<long long>(a.b.n_tokens - used) * a.q_heads,
-                  static_cast<long long>(blockIdx.x) * kThreads + tid, static_cast<long long>(gridDim.x) * kThreads);
+    const KvNoRows none = kv_no_rows(a.b);
+    const long long id = static_cast<long long>(blockIdx.x) * kThreads + tid, of = static_cast<long long>(gridDim.x) * kThreads;
+    clear_rows<D>(a, static_cast<long long>(none.after) * a.q_heads,
+                  static_cast<long long>(a.b.n_tokens - none.after) * a.q_heads, id, of);
+    if (none.before > 0) clear_rows<D>(a, 0, static_cast<long long>(none.before) * a.q_heads, id, of);
   }
   // A share is at least one item of one tile: below that pieces cost more than they save. And where items
   // one by one end no later than equal shares and their joins would, nothing is cut and items are counted.

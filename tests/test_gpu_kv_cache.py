@@ -451,6 +451,28 @@ def test_bad_tables_set_the_status_word():
     want, _ = U.check_attention(case, kv=kv, cache=c)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 1], [3, 20]])
+def test_rows_before_the_first_sequence(fmt, new):
+    """cu_q must start at 0: the status word says so, and the rows before it are rows of no sequence."""
+    case = U.Case(fmt, 4, 2, 256, 16, new, [40, 33], seed=34, pad_rows=4)
+    kv = case.handle()
+    c = case.filled(kv)
+    batch = case.batch()
+    batch.tensors[0].add_(3)
+    q = case.q.cuda()
+    out, lse = kv.attention(c, batch, q, out=torch.ones_like(q))
+    torch.cuda.synchronize()
+    assert kv.status() == (B.MOE_FFN_EDEVICE, B.STATUS_BITS["BAD_INDEX"])
+    for rows in (slice(0, 3), slice(case.T - 1, case.T)):
+        assert not out[rows].any() and (lse[rows] == -math.inf).all()
+    for call in (lambda: kv.read(c, batch, n_tokens=case.T),
+                 lambda: kv.write(kv.new_cache(), batch, q[:, :2], q[:, 2:])):
+        call()
+        torch.cuda.synchronize()
+        assert kv.status() == (B.MOE_FFN_EDEVICE, B.STATUS_BITS["BAD_INDEX"])
+
+
 def test_empty_batches_do_nothing():
     case = U.Case("bf16", 4, 2, 256, 16, [], [], seed=14)
     kv = case.handle()
