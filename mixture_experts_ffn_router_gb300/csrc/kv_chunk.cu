@@ -755,16 +755,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (bool more = start(); more && alive; more = next()) {
       const int head = part / C::kHalves, half = part % C::kHalves;
-      // The position a box begins at, and the page table's entry of it (or a refusal).
+      // The position a box begins at, -1 if no row sees any of it, and the page table's entry of it.
       auto fetch = [&](int j, int& first) {
         first = j < n ? tile_at(i0 + j) * KT + (box << rows_log2) : 0x7fffffff;
         const bool need = first <= t.p0 + t.nt - 1 &&
                           (a.window == 0 || first + (1 << rows_log2) - 1 > max(t.p0, 0) - a.window || first < a.sinks);
-        return need ? a.b.pages[t.seq * a.b.pages_stride + (first >> a.c.page_log2)] : -2;
+        if (!need) first = -1;
+        return need ? a.b.pages[t.seq * a.b.pages_stride + (first >> a.c.page_log2)] : -1;
       };
       auto boxes_of = [&](int page, int first) {
         const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
-        if (page != -2 && !ok) atomicOr(a.status, kStatusBadIndex);
+        if (first >= 0 && !ok) atomicOr(a.status, kStatusBadIndex);
         Boxes o;
         o.who = __ballot_sync(0xffffffffu, ok) & ((1u << boxes) - 1);
         o.row = ok ? ((page * a.c.kv_heads + head) << a.c.page_log2) + (first & (R - 1)) : 0;

@@ -473,6 +473,35 @@ def test_rows_before_the_first_sequence(fmt, new):
         assert kv.status() == (B.MOE_FFN_EDEVICE, B.STATUS_BITS["BAD_INDEX"])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 30, 20]])
+@pytest.mark.parametrize("bad", [-1, -2, -7, -2 ** 31, "n_pages", 2 ** 31 - 1])
+def test_every_bad_page_id_is_reported(fmt, new, bad):
+    """By each operator that needs it; the other sequences do not notice."""
+    case = U.Case(fmt, 4, 2, 256, 16, new, [40, 50, 33], seed=35)
+    kv = case.handle()
+    c = case.filled(kv)
+    q = case.q.cuda()
+    want, _ = kv.attention(c, case.batch(), q)
+    batch = case.batch()
+    batch.tensors[2][1, 3] = case.n_pages if bad == "n_pages" else bad  # of positions 48 and 49
+    out, _ = kv.attention(c, batch, q)
+    torch.cuda.synchronize()
+    assert kv.status() == (B.MOE_FFN_EDEVICE, B.STATUS_BITS["BAD_INDEX"])
+    a, b = case.cu[1], case.cu[2]
+    assert torch.equal(out[:a], want[:a]) and torch.equal(out[b:], want[b:])
+    for call in (lambda: kv.read(c, batch, n_tokens=case.T),
+                 lambda: kv.write(c, batch, q[:, :2], q[:, 2:])):
+        call()
+        torch.cuda.synchronize()
+        assert kv.status() == (B.MOE_FFN_EDEVICE, B.STATUS_BITS["BAD_INDEX"])
+    # An entry that no token sees may hold anything.
+    batch.tensors[2][1, 3] = case.pages[1, 3]
+    batch.tensors[2][2, 3] = -2 if bad == "n_pages" else bad
+    kv.attention(c, batch, q)
+    _ok(kv)
+
+
 def test_empty_batches_do_nothing():
     case = U.Case("bf16", 4, 2, 256, 16, [], [], seed=14)
     kv = case.handle()
