@@ -538,10 +538,12 @@ class KVBatch:
 
 
 class KVCache:
-    """One layer's cache tensors, checked once (PagedKV.cache and PagedKV.new_cache make it)."""
+    """One layer's cache tensors, checked once (PagedKV.cache and PagedKV.new_cache make it). kind: the
+    shape, type and device they were checked for; handles of another kind check them again and refuse."""
 
-    def __init__(self, k, v, k_scale=None, v_scale=None):
+    def __init__(self, k, v, k_scale=None, v_scale=None, kind=None):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.kind = kind
         self.struct = moe_ffn_kv_cache(*(t.data_ptr() if t is not None else None for t in (k, v, k_scale, v_scale)))
         self._ref = ctypes.byref(self.struct)
 
@@ -569,6 +571,7 @@ class PagedKV:
         self.dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
         self.default_scale = self.head_dim ** -0.5
         self.device = torch.device("cuda", int(device))
+        self._kind = (self.shape, self.dtype, self.device)
         self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
         self.ctx = moe_ffn_kv_init(self.cfg, self.workspace.data_ptr(), self.nbytes, int(device))
         self._handle = _vp(self.ctx)
@@ -580,8 +583,8 @@ class PagedKV:
         import torch
         k, v = (torch.zeros(self.shape, dtype=self.dtype, device=self.device) for _ in range(2))
         if self.fmt == "bf16":
-            return KVCache(k, v)
-        return KVCache(k, v, *(torch.zeros(self.shape[:3], device=self.device) for _ in range(2)))
+            return KVCache(k, v, kind=self._kind)
+        return KVCache(k, v, *(torch.zeros(self.shape[:3], device=self.device) for _ in range(2)), kind=self._kind)
 
     def cache(self, k, v, k_scale=None, v_scale=None) -> KVCache:
         """A cache over existing tensors, checked against this shape."""
@@ -601,7 +604,7 @@ class PagedKV:
             _check_placement(name, t)
             if t.device != self.device:
                 raise ValueError("%s must be on %s" % (name, self.device))
-        return KVCache(k, v, k_scale, v_scale)
+        return KVCache(k, v, k_scale, v_scale, self._kind)
 
     def _rows(self, what, t, heads):
         import torch
@@ -627,6 +630,8 @@ class PagedKV:
         import torch
         if not isinstance(cache, KVCache):
             cache = self.cache(**cache)
+        elif cache.kind != self._kind:
+            cache = self.cache(cache.k, cache.v, cache.k_scale, cache.v_scale)
         if batch.device != self.device:
             raise ValueError("the batch must be on %s" % self.device)
         raw = torch._C._cuda_getCurrentRawStream(self.device.index)

@@ -516,6 +516,27 @@ def test_empty_batches_do_nothing():
     assert not out.any() and torch.isinf(lse).all()
 
 
+def test_caches_of_another_kind_of_layer_are_refused():
+    sliding, glob = B.PagedKV(16, 8, 256, 64, 6), B.PagedKV(16, 2, 512, 64, 6)
+    e4m3, same = B.PagedKV(16, 8, 256, 64, 6, "e4m3"), B.PagedKV(32, 8, 256, 64, 6, max_seqs=3)
+    c = sliding.new_cache()
+    cu, kv_len = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([0, 3], [3]))
+    batch = B.KVBatch(cu, kv_len, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), max_new=3)
+    x = {h: torch.ones(3, h.kv_heads, h.head_dim, dtype=torch.bfloat16, device="cuda") for h in (sliding, glob, e4m3, same)}
+    for h, other in ((glob, c), (e4m3, c), (sliding, glob.new_cache()), (sliding, e4m3.new_cache()),
+                     (glob, B.KVCache(c.k, c.v))):
+        for call in (lambda: h.write(other, batch, x[h], x[h]), lambda: h.read(other, batch, 3),
+                     lambda: h.attention(other, batch, x[h].repeat_interleave(h.q_heads // h.kv_heads, 1))):
+            with pytest.raises(ValueError):
+                call()
+    assert not c.k.any() and not c.v.any()
+    # Another handle of the same shape may use it, and tensors put together by hand are checked per call.
+    same.write(c, batch, x[same], x[same])
+    k, v = sliding.read(B.KVCache(c.k, c.v), batch, 3)
+    _ok(sliding)
+    assert torch.equal(k, x[same]) and torch.equal(v, x[same])
+
+
 def test_refusals():
     case = U.Case("bf16", 4, 2, 256, 16, [2], [5], seed=15)
     kv = case.handle()

@@ -117,6 +117,30 @@ def test_caches_are_checked(fmt, change, match):
         _stub(fmt).cache(**given)
 
 
+def _meta_cache(shape, dtype, scales, kind=None):
+    c = B.KVCache(*(torch.empty(shape, dtype=dtype, device="meta") for _ in range(2)),
+                  *(torch.empty(shape[:3], device="meta") for _ in range(2 if scales else 0)))
+    c.kind = kind
+    return c
+
+
+@pytest.mark.parametrize("shape,dtype,scales", [
+    ((10, 2, 64, 512), torch.bfloat16, False), ((9, 8, 64, 256), torch.bfloat16, False),
+    ((10, 8, 32, 256), torch.bfloat16, False), ((10, 8, 64, 256), torch.float8_e4m3fn, True),
+    ((10, 8, 64, 256), torch.float16, False)])
+def test_caches_of_another_handle_are_checked(shape, dtype, scales):
+    """A cache made for another shape, format or device is refused before anything is launched."""
+    kv = _stub()
+    kv._kind = ((10, 8, 64, 256), torch.bfloat16, kv.device)
+    for kind in (None, (shape, dtype, kv.device)):
+        c = _meta_cache(shape, dtype, scales, kind)
+        with pytest.raises(ValueError, match="must be|has no scales"):
+            kv._begin(c, None)
+    other = _meta_cache((10, 8, 64, 256), torch.bfloat16, False, ((10, 8, 64, 256), torch.bfloat16, torch.device("cuda", 1)))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        kv._begin(other, None)
+
+
 @pytest.mark.parametrize("cu,kv,pages,new,match", [
     ((4,), (4,), (4, 2), 1, "sequences"), ((5,), (4,), (3, 2), 1, "sequences"), ((5,), (4, 1), (4, 2), 1, "dimension"),
     ((5,), (4,), (4,), 1, "dimension"), ((5,), (4,), (4, 2), -1, "max_new"), ((5,), (4,), (4, 2), 1, "CUDA tensor")])
