@@ -695,6 +695,7 @@ class PagedKV:
         if self.ctx:
             moe_ffn_kv_destroy(self.ctx)
             self.ctx = 0
+            self._handle = None  # calls are refused from here on
 
     def __del__(self):
         try:

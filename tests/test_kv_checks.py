@@ -141,6 +141,29 @@ def test_caches_of_another_handle_are_checked(shape, dtype, scales):
         kv._begin(other, None)
 
 
+def test_calls_after_close_are_refused(monkeypatch):
+    monkeypatch.setattr(B, "moe_ffn_kv_destroy", lambda kv: None)
+    kv = _stub()
+    kv.ctx, kv._handle, kv._lib, kv.default_scale = 4096, ctypes.c_void_p(4096), B.lib(), 0.1
+    kv._begin = lambda cache, batch: (B.moe_ffn_kv_cache(), 0)
+    kv._rows = lambda what, t, heads: B.moe_ffn_kv_rows()
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: torch.zeros(1))
+
+    class Batch:
+        def of(self, n):
+            return B.moe_ffn_kv_batch()
+
+    kv.close()
+    assert not kv.ctx and not kv._handle  # before any call: the C side cannot tell a handle that is gone
+    x = torch.zeros(1, 1, 1)
+    for call in (lambda: kv.write(None, Batch(), x, x), lambda: kv.read(None, Batch(), 1),
+                 lambda: kv.attention(None, Batch(), x)):
+        with pytest.raises(B.MoeFFNError) as e:
+            call()
+        assert e.value.status == B.MOE_FFN_EINVAL
+    kv.close()
+
+
 @pytest.mark.parametrize("cu,kv,pages,new,match", [
     ((4,), (4,), (4, 2), 1, "sequences"), ((5,), (4,), (3, 2), 1, "sequences"), ((5,), (4, 1), (4, 2), 1, "dimension"),
     ((5,), (4,), (4,), 1, "dimension"), ((5,), (4,), (4, 2), -1, "max_new"), ((5,), (4,), (4, 2), 1, "CUDA tensor")])
