@@ -553,7 +553,7 @@ class PagedKV:
 
     fmt "bf16", or "e4m3" with an fp32 scale per token and head. Calls go to the current stream; a call
     on another stream than the last one's first waits for that one (not while a graph is captured:
-    order the replays yourself)."""
+    order the replays yourself, and keep the handle as long as the graph)."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, n_pages: int, fmt: str = "bf16",
                  max_tokens: int = 8192, max_seqs: int = 256, device: int = 0):
@@ -639,6 +639,7 @@ class PagedKV:
             stream = torch.cuda.current_stream(self.device)
             if self._last is not None:
                 stream.wait_stream(self._last)
+            self.workspace.record_stream(stream)  # dropped early, it stays until the stream is done with it
             self._last, self._last_raw = stream, raw
         return cache._ref, raw
 

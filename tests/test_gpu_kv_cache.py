@@ -427,6 +427,26 @@ def test_calls_on_two_streams_are_ordered():
         assert torch.equal(got, want)
 
 
+def test_a_dropped_handle_leaves_its_workspace_to_the_stream_that_uses_it():
+    case = U.Case("bf16", 4, 2, 256, 16, [200], [3000], seed=36)
+    kv = case.handle()
+    c, batch, q = case.filled(kv), case.batch(), case.q.cuda()
+    want, _ = kv.attention(c, batch, q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    at, nbytes = kv.workspace.data_ptr(), kv.nbytes
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        out, _ = kv.attention(c, batch, q)
+    del kv
+    other = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert all(t.data_ptr() != at for t in other)
+    for t in other:
+        t.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_bad_tables_set_the_status_word():
     """Page ids and lengths out of range: nothing out of the cache is touched, and the status says so."""
     case = U.Case("bf16", 4, 2, 256, 16, [1, 1, 20], [40, 20, 33], seed=13)

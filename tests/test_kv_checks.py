@@ -164,6 +164,34 @@ def test_calls_after_close_are_refused(monkeypatch):
     kv.close()
 
 
+def test_the_workspace_is_held_for_each_stream_it_is_used_on(monkeypatch):
+    """The allocator must not hand the workspace on while another stream than the one it was made on uses it."""
+    class Stream:
+        def __init__(self, raw):
+            self.raw, self.waited = raw, []
+
+        def wait_stream(self, other):
+            self.waited.append(other)
+
+    now = {"stream": None, "capturing": False}
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: now["stream"].raw, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now["stream"])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
+    kv = _stub()
+    kv._kind = (kv.shape, kv.dtype, kv.device)
+    kv._last = kv._last_raw = None
+    held = []
+    kv.workspace = type("Workspace", (), {"record_stream": lambda self, stream: held.append(stream)})()
+    cache = _meta_cache(kv.shape, kv.dtype, False, kv._kind)
+    batch = type("Batch", (), {"device": kv.device})()
+    a, b = Stream(7), Stream(9)
+    for stream, capturing in ((a, False), (a, False), (b, False), (b, True), (a, True), (a, False)):
+        now.update(stream=stream, capturing=capturing)
+        assert kv._begin(cache, batch)[1] == stream.raw
+    assert held == [a, b, a]
+    assert b.waited == [a] and a.waited == [b]
+
+
 @pytest.mark.parametrize("cu,kv,pages,new,match", [
     ((4,), (4,), (4, 2), 1, "sequences"), ((5,), (4,), (3, 2), 1, "sequences"), ((5,), (4, 1), (4, 2), 1, "dimension"),
     ((5,), (4,), (4,), 1, "dimension"), ((5,), (4,), (4, 2), -1, "max_new"), ((5,), (4,), (4, 2), 1, "CUDA tensor")])
