@@ -457,7 +457,11 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   kv->list.joins = reinterpret_cast<KvJoin*>(kv->ws + l.joins);
   kv->list.max_tiles = static_cast<int>(max_row_tiles(*cfg));
   kv->chunk_partial = reinterpret_cast<float*>(kv->ws + l.chunk_partial);
-  if (kv_decode_setup() != cudaSuccess || kv_chunk_setup(&kv->chunk_pairs) != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  // The workspace may be memory that work still queued on some stream writes: that ends before the control words
+  // are cleared, and the clearing before any call.
+  if (kv_decode_setup() != cudaSuccess || kv_chunk_setup(&kv->chunk_pairs) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
     delete kv;
     return MOE_FFN_ECUDA;
   }

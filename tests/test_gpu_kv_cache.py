@@ -447,6 +447,29 @@ def test_a_dropped_handle_leaves_its_workspace_to_the_stream_that_uses_it():
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("new", [1, 200])
+def test_a_workspace_of_memory_still_being_written(new):
+    """Made on a side stream, from a block that work queued there before still writes."""
+    case = U.Case("bf16", 4, 2, 256, 16, [new], [3000], seed=37)
+    kv = case.handle()
+    c, batch, q = case.filled(kv), case.batch(), case.q.cuda()
+    want, _ = kv.attention(c, batch, q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        block = torch.empty(kv.nbytes, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        block.fill_(255)
+        at = block.data_ptr()
+        del block
+        late = case.handle()
+        assert late.workspace.data_ptr() == at
+        out, _ = late.attention(c, batch, q)
+    torch.cuda.synchronize()
+    assert late.status() == (B.MOE_FFN_OK, 0)
+    assert torch.equal(out, want)
+
+
 def test_bad_tables_set_the_status_word():
     """Page ids and lengths out of range: nothing out of the cache is touched, and the status says so."""
     case = U.Case("bf16", 4, 2, 256, 16, [1, 1, 20], [40, 20, 33], seed=13)
