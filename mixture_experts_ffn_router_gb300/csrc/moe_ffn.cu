@@ -318,8 +318,9 @@ int moe_ffn_init(moe_ffn_ctx** out, const moe_ffn_config* cfg, void* workspace, 
       c->map_hd[k] = c->map_h[k];
     }
   }
-  // The small control words start at zero; the kernels keep them consistent afterwards.
-  if (!ok || cudaMemset(w + L.hist, 0, L.exp_tiles - L.hist) != cudaSuccess ||
+  // The small control words start at zero; the kernels keep them consistent afterwards. (The workspace may be
+  // memory that work still queued on some stream writes: that ends first.)
+  if (!ok || cudaDeviceSynchronize() != cudaSuccess || cudaMemset(w + L.hist, 0, L.exp_tiles - L.hist) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     delete c;
     return MOE_FFN_ECUDA;
