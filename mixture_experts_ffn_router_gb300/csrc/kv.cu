@@ -550,10 +550,13 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
 int moe_ffn_kv_device_status(moe_ffn_kv* kv, void* stream, uint32_t* word) {
   if (!kv) return MOE_FFN_EINVAL;
   if (cudaSetDevice(kv->device) != cudaSuccess) return MOE_FFN_ECUDA;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOE_FFN_ECUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_FFN_ECUDA;
   uint32_t v = 0;
   if (cudaMemcpy(&v, kv->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_FFN_ECUDA;
-  if (v != 0 && cudaMemset(kv->status, 0, 4) != cudaSuccess) return MOE_FFN_ECUDA;
+  // (Done before this returns: a clearing that lands later could take the next call's report with it.)
+  if (v != 0 && (cudaMemsetAsync(kv->status, 0, 4, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
+    return MOE_FFN_ECUDA;
   if (word) *word = v;
   return v ? MOE_FFN_EDEVICE : MOE_FFN_OK;
 }

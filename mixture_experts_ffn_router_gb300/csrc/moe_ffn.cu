@@ -677,7 +677,9 @@ int moe_ffn_device_status(moe_ffn_ctx* c, void* stream, uint32_t* word) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_FFN_ECUDA;
   uint32_t v = 0;
   if (cudaMemcpy(&v, c->buf.status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_FFN_ECUDA;
-  if (v != 0 && cudaMemset(c->buf.status, 0, 4) != cudaSuccess) return MOE_FFN_ECUDA;
+  // (Done before this returns: a clearing that lands later could take the next call's report with it.)
+  if (v != 0 && (cudaMemsetAsync(c->buf.status, 0, 4, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
+    return MOE_FFN_ECUDA;
   if (word) *word = v;
   return v ? MOE_FFN_EDEVICE : MOE_FFN_OK;
 }

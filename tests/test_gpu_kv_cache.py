@@ -545,6 +545,20 @@ def test_every_bad_page_id_is_reported(fmt, new, bad):
     _ok(kv)
 
 
+def test_no_report_is_lost_between_calls():
+    """On a stream that does not wait for the legacy one: each bad call is reported, right after the last report."""
+    case = U.Case("bf16", 2, 2, 128, 16, [1], [20], seed=38)
+    kv = case.handle()
+    c, batch, q = case.filled(kv), case.batch(), case.q.cuda()
+    batch.tensors[2][0, 1] = -1
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(200):
+            kv.attention(c, batch, q)
+            assert kv.status() == (B.MOE_FFN_EDEVICE, B.STATUS_BITS["BAD_INDEX"])
+        assert kv.status() == (B.MOE_FFN_OK, 0)
+
+
 def test_empty_batches_do_nothing():
     case = U.Case("bf16", 4, 2, 256, 16, [], [], seed=14)
     kv = case.handle()
