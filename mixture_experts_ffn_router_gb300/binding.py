@@ -529,12 +529,17 @@ class KVBatch:
         self.device = cu_q.device
         self.struct = moe_ffn_kv_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(),
                                        pages.stride(0) if n > 1 else cols, cols, n, 0, int(max_new))
-        self._ref = ctypes.byref(self.struct)
+        self._last = (-1, None)
 
     def of(self, n_tokens: int):
-        """The C structure (by reference) for tensors of n_tokens token rows."""
-        self.struct.n_tokens = n_tokens
-        return self._ref
+        """The C structure (by reference) for tensors of n_tokens token rows. One that was given out is not
+        changed again: another thread's call may still be reading it."""
+        last = self._last
+        if last[0] != n_tokens:
+            s = moe_ffn_kv_batch.from_buffer_copy(self.struct)
+            s.n_tokens = n_tokens
+            last = self._last = (n_tokens, ctypes.byref(s))
+        return last[1]
 
 
 class KVCache:

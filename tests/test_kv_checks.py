@@ -141,6 +141,35 @@ def test_caches_of_another_handle_are_checked(shape, dtype, scales):
         kv._begin(other, None)
 
 
+class _OnDevice:
+    """What KVBatch's checks read of a CUDA tensor."""
+    is_cuda, dtype, device = True, torch.int32, torch.device("cuda", 0)
+
+    def __init__(self, *shape):
+        self.shape = shape
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i):
+        return (self.shape[1], 1)[i] if len(self.shape) == 2 else 1
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_a_batch_given_to_one_call_is_not_changed_by_the_next():
+    """Threads with a handle each may share a batch, for tensors of different token counts."""
+    batch = B.KVBatch(_OnDevice(5), _OnDevice(4), _OnDevice(4, 2), max_new=3)
+    given = [batch.of(n) for n in (3, 5, 5, 3)]
+    structs = [ctypes.cast(g, ctypes.POINTER(B.moe_ffn_kv_batch)).contents for g in given]
+    assert [s.n_tokens for s in structs] == [3, 5, 5, 3]
+    assert all((s.n_seqs, s.pages_cols, s.pages_stride, s.max_new, s.cu_q) == (4, 2, 2, 3, 4096) for s in structs)
+
+
 def test_calls_after_close_are_refused(monkeypatch):
     monkeypatch.setattr(B, "moe_ffn_kv_destroy", lambda kv: None)
     kv = _stub()
