@@ -580,7 +580,6 @@ class PagedKV:
         self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
         self.ctx = moe_ffn_kv_init(self.cfg, self.workspace.data_ptr(), self.nbytes, int(device))
         self._handle = _vp(self.ctx)
-        self._lib = lib()
         self._last = self._last_raw = None
 
     def new_cache(self) -> KVCache:
@@ -655,7 +654,7 @@ class PagedKV:
         if k.shape[0] != v.shape[0]:
             raise ValueError("k has %d tokens, v %d" % (k.shape[0], v.shape[0]))
         c, s = self._begin(cache, batch)
-        _check("moe_ffn_kv_write", self._lib.moe_ffn_kv_write(self._handle, c, batch.of(k.shape[0]), kr, vr, s))
+        _check("moe_ffn_kv_write", moe_ffn_kv_write(self._handle, c, batch.of(k.shape[0]), kr, vr, s))
 
     def read(self, cache, batch: KVBatch, n_tokens=None):
         """The batch's tokens read back: (k, v), bf16 [tokens, kv_heads, head_dim]. n_tokens: the token
@@ -667,7 +666,7 @@ class PagedKV:
                 for _ in range(2))
         c, s = self._begin(cache, batch)
         _check("moe_ffn_kv_read",
-               self._lib.moe_ffn_kv_read(self._handle, c, batch.of(n_tokens), k.data_ptr(), v.data_ptr(), s))
+               moe_ffn_kv_read(self._handle, c, batch.of(n_tokens), k.data_ptr(), v.data_ptr(), s))
         return k, v
 
     def attention(self, cache, batch: KVBatch, q, window: int = 0, sinks: int = 0, scale=None, out=None):
@@ -687,9 +686,9 @@ class PagedKV:
         lse = torch.empty((T, self.q_heads), dtype=torch.float32, device=self.device)
         c, s = self._begin(cache, batch)
         _check("moe_ffn_kv_attention",
-               self._lib.moe_ffn_kv_attention(self._handle, c, batch.of(T), qr,
-                                              self.default_scale if scale is None else scale, window, sinks,
-                                              out.data_ptr(), lse.data_ptr(), s))
+               moe_ffn_kv_attention(self._handle, c, batch.of(T), qr,
+                                    self.default_scale if scale is None else scale, window, sinks,
+                                    out.data_ptr(), lse.data_ptr(), s))
         return out, lse
 
     def status(self, stream=None):

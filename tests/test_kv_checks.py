@@ -170,6 +170,24 @@ def test_a_batch_given_to_one_call_is_not_changed_by_the_next():
     assert all((s.n_seqs, s.pages_cols, s.pages_stride, s.max_new, s.cu_q) == (4, 2, 2, 3, 4096) for s in structs)
 
 
+def test_operators_go_through_the_c_entry_points(monkeypatch):
+    seen = []
+    for name in ("moe_ffn_kv_write", "moe_ffn_kv_read", "moe_ffn_kv_attention"):
+        monkeypatch.setattr(B, name, lambda *a, name=name: seen.append((name, a[0], a[2], a[-1])) or B.MOE_FFN_OK)
+    kv = _stub()
+    kv._handle, kv.default_scale = 11, 0.1
+    kv._begin = lambda cache, batch: ("cache", 7)
+    kv._rows = lambda what, t, heads: what
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: torch.zeros(1))
+    batch = type("Batch", (), {"of": lambda self, n: ("batch", n)})()
+    x = torch.zeros(3, 1, 1)
+    kv.write(None, batch, x, x)
+    kv.read(None, batch, 2)
+    kv.attention(None, batch, x)
+    assert seen == [("moe_ffn_kv_write", 11, ("batch", 3), 7), ("moe_ffn_kv_read", 11, ("batch", 2), 7),
+                    ("moe_ffn_kv_attention", 11, ("batch", 3), 7)]
+
+
 def test_calls_after_close_are_refused(monkeypatch):
     monkeypatch.setattr(B, "moe_ffn_kv_destroy", lambda kv: None)
     kv = _stub()
