@@ -398,7 +398,7 @@ int moe_ffn_kv_write(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ff
                      const moe_ffn_kv_rows* k, const moe_ffn_kv_rows* v, void* stream);
 
 /* Reads the batch's "new" tokens back out of the cache: k_out and v_out, device pointers,
- * [n_tokens, kv_heads, head_dim] bf16 contiguous, code * scale rounded once. With n_b = kv_len[b] that
+ * [n_tokens, kv_heads, head_dim] bf16 contiguous, not overlapping the cache, code * scale rounded once. With n_b = kv_len[b] that
  * is the whole of each sequence. Asynchronous on `stream`. */
 int moe_ffn_kv_read(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch, void* k_out,
                     void* v_out, void* stream);
@@ -408,9 +408,10 @@ int moe_ffn_kv_read(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn
  *   out = sum_j softmax_j(scale * q . K_j) V_j over the visible positions j <= p,
  * and with window > 0 only those with j > p - window or j < sinks. Nothing visible: out = 0.
  *   q      [n_tokens, q_heads, head_dim] bf16;
- *   out    device pointer, [n_tokens, q_heads, head_dim] bf16 contiguous, not overlapping q;
+ *   out    device pointer, [n_tokens, q_heads, head_dim] bf16 contiguous, not overlapping q or the cache;
  *   lse    device pointer or NULL, [n_tokens, q_heads] fp32: log sum_j exp(scale * q . K_j)
- *          (-infinity where nothing is visible), for joining with attention over other keys;
+ *          (-infinity where nothing is visible), for joining with attention over other keys; not
+ *          overlapping out, q or the cache;
  *   scale  finite, > 0 (head_dim^-1/2 as a rule); window >= 0 (0: none); sinks >= 0.
  * What is in slots no token sees (NaN included) does not change the result. Deterministic: the same
  * inputs give bitwise-equal outputs. Asynchronous on `stream`; nothing is allocated or read back. */

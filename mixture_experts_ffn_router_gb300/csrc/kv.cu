@@ -374,6 +374,13 @@ size_t kv_rows_bytes(const KvRows& r, int tokens, int heads, int d) {
   return static_cast<size_t>((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + d) * 2;
 }
 
+// Whether an output would meet the cache that the call reads.
+bool meets_cache(const void* p, size_t bytes, const KvCache& c) {
+  const size_t rows = (static_cast<size_t>(c.n_pages) * c.kv_heads) << c.page_log2, values = rows * c.head_dim * (c.e4m3 ? 1 : 2);
+  return meet(p, bytes, c.k, values) || meet(p, bytes, c.v, values) ||
+         (c.e4m3 && (meet(p, bytes, c.k_scale, rows * 4) || meet(p, bytes, c.v_scale, rows * 4)));
+}
+
 // The workspace: control words (zeroed when the handle is made), then the kernels' pieces.
 struct KvLayout {
   size_t status, counters, counters_in, n_tiles, partial, first_tile, tiles, first_unit, shares, joins, chunk_partial,
@@ -492,7 +499,7 @@ int moe_ffn_kv_read(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn
   if (off16(k_out) || off16(v_out)) return MOE_FFN_EALIGN;
   const size_t bytes = static_cast<size_t>(b.n_tokens) * c.kv_heads * c.head_dim * 2;
   if (meet(k_out, bytes, v_out, bytes) || meet(k_out, bytes, kv->ws, kv->ws_bytes) ||
-      meet(v_out, bytes, kv->ws, kv->ws_bytes))
+      meet(v_out, bytes, kv->ws, kv->ws_bytes) || meets_cache(k_out, bytes, c) || meets_cache(v_out, bytes, c))
     return MOE_FFN_EINVAL;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
   return launch_kv_read(b, c, static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out), kv->status,
@@ -514,9 +521,10 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   if (off16(out) || off4(lse)) return MOE_FFN_EALIGN;
   const moe_ffn_kv_config& f = kv->cfg;
   const size_t rows = static_cast<size_t>(a.b.n_tokens) * f.q_heads, bytes = rows * f.head_dim * 2;
-  if (meet(out, bytes, a.q.ptr, kv_rows_bytes(a.q, a.b.n_tokens, f.q_heads, f.head_dim)) ||
-      meet(out, bytes, kv->ws, kv->ws_bytes) ||
-      (lse && (meet(lse, rows * 4, out, bytes) || meet(lse, rows * 4, kv->ws, kv->ws_bytes))))
+  const size_t q_bytes = kv_rows_bytes(a.q, a.b.n_tokens, f.q_heads, f.head_dim);
+  if (meet(out, bytes, a.q.ptr, q_bytes) || meet(out, bytes, kv->ws, kv->ws_bytes) || meets_cache(out, bytes, a.c) ||
+      (lse && (meet(lse, rows * 4, out, bytes) || meet(lse, rows * 4, kv->ws, kv->ws_bytes) ||
+               meet(lse, rows * 4, a.q.ptr, q_bytes) || meets_cache(lse, rows * 4, a.c))))
     return MOE_FFN_EINVAL;
   a.group = f.q_heads / f.kv_heads;
   a.q_heads = f.q_heads;

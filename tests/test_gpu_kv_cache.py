@@ -594,6 +594,32 @@ def test_caches_of_another_kind_of_layer_are_refused():
     assert torch.equal(k, x[same]) and torch.equal(v, x[same])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_outputs_that_overlap_what_is_read_are_refused(fmt):
+    case = U.Case(fmt, 4, 2, 256, 16, [2], [40], seed=39)
+    kv = case.handle()
+    c, batch = case.filled(kv), case.batch()
+    q = torch.zeros(64, 4, 256, dtype=torch.bfloat16, device="cuda")[:2]
+    out, lse = torch.empty(2, 4, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 4, device="cuda")
+    kept = [t.clone() for t in (c.k, c.v, c.k_scale, c.v_scale) if t is not None]
+    rows, struct = kv._rows("q", q, 4), batch.of(2)
+    inside = [t.data_ptr() + 64 for t in (c.k, c.v, c.k_scale, c.v_scale) if t is not None]
+
+    def attention(o, l):
+        return B.moe_ffn_kv_attention(kv.ctx, c.struct, struct, rows, 0.1, 0, 0, o, l, 0)
+
+    assert attention(out.data_ptr(), q.data_ptr()) == B.MOE_FFN_EINVAL
+    for at in inside:
+        assert attention(at, lse.data_ptr()) == B.MOE_FFN_EINVAL
+        assert attention(out.data_ptr(), at) == B.MOE_FFN_EINVAL
+        assert B.moe_ffn_kv_read(kv.ctx, c.struct, struct, at, out.data_ptr(), 0) == B.MOE_FFN_EINVAL
+        assert B.moe_ffn_kv_read(kv.ctx, c.struct, struct, out.data_ptr(), at, 0) == B.MOE_FFN_EINVAL
+    assert attention(out.data_ptr(), lse.data_ptr()) == B.MOE_FFN_OK
+    _ok(kv)
+    for t, was in zip((c.k, c.v, c.k_scale, c.v_scale), kept):
+        assert torch.equal(t.view(torch.uint8), was.view(torch.uint8))
+
+
 def test_refusals():
     case = U.Case("bf16", 4, 2, 256, 16, [2], [5], seed=15)
     kv = case.handle()
