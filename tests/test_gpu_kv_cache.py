@@ -337,6 +337,55 @@ def test_values_far_from_their_weights(d, new, big, score):
         U.check_attention(case)
 
 
+@pytest.mark.parametrize("fmt,hq,hkv,d", [("bf16", 18, 2, 128), ("e4m3", 16, 1, 256), ("bf16", 33, 1, 256),
+                                          ("e4m3", 64, 1, 128), ("bf16", 64, 1, 512), ("e4m3", 66, 2, 512)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [4, 1, 9]])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1024, 4)])
+def test_many_heads_per_kv_head_over_long_caches(fmt, hq, hkv, d, new, window, sinks):
+    case, h, c, want = _large(fmt, hq, hkv, d, 32, new, [6001, 700, 2048], seed=22)
+    out, lse = h.attention(c, case.batch(), case.q.cuda(), window=window, sinks=sinks)
+    _ok(h)
+    w, wl = want(window, sinks)
+    # As for other long caches: a rounding of the weights, one of the result, and what is held in fp32.
+    U.check_close(lse, wl, torch.full_like(wl, 2.0 ** -10), "lse")
+    U.check_close(out, w, 2 * U.BF * w.abs() + U.BF + 2.0 ** -10, "out")
+
+
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("new,max_new", [([1, 1, 1], 50), ([1, 0, 1], 2), ([30, 1, 3], 1000)])
+def test_a_bound_above_the_longest_sequence(fmt, d, new, max_new):
+    case = U.Case(fmt, 4, 2, d, 32, new, [300, 40, 131], seed=23)
+    kv = case.handle()
+    c, b = case.filled(kv), case.batch()
+    out, lse = kv.attention(c, B.KVBatch(*b.tensors, max_new=max_new), case.q.cuda())
+    _ok(kv)
+    want, wl, tol, ltol = U.attention(case)
+    U.check_close(lse, wl, ltol, "lse")
+    U.check_close(out, want, tol, "out")
+
+
+def test_shares_past_32_bits():
+    """More key tiles than 32-bit arithmetic divides among the CTAs: 520 single tokens on 131072, whose tables
+    name the same 64 pages over and over, so that each sees the same 1024 keys 128 times."""
+    n, hq, d, times = 520, 8, 128, 128
+    kv = B.PagedKV(hq, hq, d, 16, 64, "bf16", max_tokens=1024, max_seqs=n)
+    c = kv.new_cache()
+    g = torch.Generator(device="cuda").manual_seed(24)
+    c.k.normal_(generator=g)
+    c.v.normal_(generator=g)
+    q = torch.randn(n, hq, d, generator=g, device="cuda").bfloat16()
+    pages = torch.arange(64, dtype=torch.int32, device="cuda").repeat(n, times)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    out, lse = kv.attention(c, B.KVBatch(cu, torch.full_like(cu[:-1], 1024 * times), pages, max_new=1), q)
+    _ok(kv)
+    k, v = (t.transpose(1, 2).reshape(1024, hq, d).double() for t in (c.k, c.v))
+    s = torch.einsum("thd,jhd->thj", q.double(), k) * d ** -0.5
+    want = torch.einsum("thj,jhd->thd", torch.softmax(s, -1), v)
+    # Sums of 2^17 terms in fp32, in pieces of at most 2^17: 2^-7 at worst, of the weights and of the values.
+    U.check_close(lse, (torch.logsumexp(s, -1) + math.log(times)).cpu(), torch.full((n, hq), 2.0 ** -7 + 2.0 ** -10).double(), "lse")
+    U.check_close(out, want.cpu(), (2 * U.BF * want.abs() + U.BF + 2.0 ** -6).cpu(), "out")
+
+
 @pytest.mark.parametrize("fmt,page,pages", [("bf16", 128, 20000), ("e4m3", 16, 300000)])
 def test_offsets_beyond_32_bits(fmt, page, pages):
     """The sequence's pages are the last of a cache of over 2^32 bytes."""
@@ -425,6 +474,28 @@ def test_calls_on_two_streams_are_ordered():
             got, _ = kv.attention(c2, batch, q)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("new", [1, 150])
+def test_calls_of_one_handle_on_two_streams_follow_each_other(new):
+    """The handle's workspace holds pieces of cut items: with nothing ordered by hand, a call on one stream starts
+    after the other stream's, long and short ones in turn."""
+    cases = [U.Case("bf16", 16, 2, 512, 64, [new], [n], seed=n) for n in (60000, 3000, 20000)]
+    for case in cases:
+        case.n_pages = max(x.n_pages for x in cases)
+    kv = cases[0].handle()
+    calls = [(case.filled(kv), case.batch(), case.q.cuda()) for case in cases]
+    want = [kv.attention(*call) for call in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i in range(24):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(kv.attention(*calls[i % 3]))
+    torch.cuda.synchronize()
+    _ok(kv)
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 3][0]) and torch.equal(lse, want[i % 3][1]), i
 
 
 def test_a_dropped_handle_leaves_its_workspace_to_the_stream_that_uses_it():
