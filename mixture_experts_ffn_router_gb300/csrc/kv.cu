@@ -538,9 +538,10 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
   a.counters_in = kv->counters_in;
   a.partial = kv->partial;
   a.list = kv->list;
-  // Of costs of 2 to 8 tiles the best: prompts of 1500 to 4100 tokens of width 256 take 196 us in bf16 with 3
-  // (207 with 2, 201 with 4, 206 with 5); in e4m3, where the queries are split on the way, 281 with 4 (303
-  // with 3, 289 with 6). At width 512 a mixed e4m3 batch would take 186 with 5 against 194.
+  // One cost per format, of 2 to 6 tiles. Prompts of 1500 to 4100 tokens of width 256 take 196 us in bf16 with 3
+  // (206 with 2, 202 with 4, 206 with 5); in e4m3, where the queries are split on the way, 279 with 4 (302
+  // with 3, 275 with 5, 280 with 6). Of the other widths in e4m3, 128 takes 210 with 4 and 216 with 5, 512 672 and
+  // 651, and a mixed batch 130 and 135 (width 128), 196 and 186 (512).
   a.item_cost = a.c.e4m3 ? 4 : 3;
   a.chunk_partial = kv->chunk_partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;

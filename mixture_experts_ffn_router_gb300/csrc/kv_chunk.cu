@@ -14,7 +14,8 @@
 // O takes 256 TMEM columns beside the two S, so a head of width 512 is two items that each take
 // half of V's width and form S for themselves (1.5 times the products of one pass).
 //
-// Softmax: one pass in base 2, against a reference M per row. M moves, with O and the sum rescaled, only
+// Softmax: one pass in base 2 (M. Milakov and N. Gimelshein, "Online normalizer calculation for softmax", 2018),
+// against a reference M per row instead of the running maximum. M moves, with O and the sum rescaled, only
 // when half a row's weights in a tile sum to more than 2^9, so O is almost never read back and no maximum
 // is taken: weights are at most 2^9, summed in fp32 and rounded to bf16 (half a step is 2^-8 of each) for
 // the product with V.
@@ -99,8 +100,8 @@ struct Chk {
   static constexpr int kWSlot = kVTile * kChunk;
   static constexpr int NV = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : (D == 512 ? 1 : D == 256 ? 2 : 6);
   static constexpr int NW = E4M3 ? (D == 128 ? 4 : D == 256 ? 2 : 1) : 0;
-  // Of a thread's pieces of V to widen, those unrolled: prompts of 1500 to 4100 tokens take 206 us with 1
-  // and 219 with 4 at width 128 (fewer instructions to fetch), but 284 and 272 at width 256.
+  // Of a thread's pieces of V to widen, those unrolled: prompts of 1500 to 4100 tokens take 210 us with 1
+  // and 213 with 4 at width 128 (fewer instructions to fetch), but 291 and 279 at width 256, 687 and 672 at 512.
   static constexpr int kWUnroll = D == 128 ? 1 : 4;
   static constexpr int kScaleBytes = E4M3 ? 2 * 2 * KT * 4 : 0;
   static constexpr int kBarBytes = (8 * (2 * NK + 2 * NV + 2 * NW + 18) + 32 + (E4M3 ? 48 : 96) + 15) / 16 * 16;

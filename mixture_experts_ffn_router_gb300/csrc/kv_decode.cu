@@ -18,7 +18,8 @@
 // through shared memory to all warps, each of which multiplies its own eighth of V's width: no output
 // is joined between warps.
 //
-// Softmax: one pass in base 2. The weights are exp2(s - M) with a reference M that all warps share and
+// Softmax: one pass in base 2 (M. Milakov and N. Gimelshein, "Online normalizer calculation for softmax", 2018).
+// The weights are exp2(s - M) with a reference M that all warps share and
 // that moves (to the maximum so far, with the outputs and sums rescaled) only when a score passes it
 // by more than 8: a tile then costs one barrier, which also tells every warp whether a score did.
 // Weights are so at most 2^8, kept in fp32 for the sum l, and rounded to 16 bits for the product with V.
@@ -31,9 +32,9 @@
 // the largest per key. (mma.sync on e4m3 itself, with queries split in two e4m3 parts, was slower: 883 us
 // against 772 for 64 sequences of 16384 tokens, 8 heads of width 256.)
 //
-// Measured: 64 sequences of 16384 tokens, of the 6.70 TB/s of a copy: bf16 7.1 TB/s (8 heads of width 128)
-// and 6.9 (2 of 512); e4m3 6.8, 6.9 and 6.5 (width 128, 256, 512; there a tile's chain of widened products,
-// weights and barriers is as long as its loads, with 42% of the issue slots busy). A call takes about 6 us
+// Measured: 64 sequences of 16384 tokens, beside the 6.70 TB/s of a copy: bf16 7.1, 7.2 and 7.0 TB/s (8 heads of
+// width 128, 8 of 256, 2 of 512); e4m3 6.7, 6.8 and 6.5 (there a tile's chain of widened products, weights and
+// barriers is as long as its loads, with 42% of the issue slots busy). A call takes about 6 us
 // beside its loads: 3 to find its work and load its queries, the rest to join pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
