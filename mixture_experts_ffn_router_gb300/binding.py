@@ -499,6 +499,12 @@ class MoeFFN:
             pass
 
 
+def _as_c_int(n: int) -> int:
+    """The nearest window or number of sinks that a C int holds: no position lies further (ctypes would keep the
+    lowest 32 bits), and a negative one is refused by the library."""
+    return min(max(n, -1), 0x7fffffff)
+
+
 class KVBatch:
     """The new tokens of a step, for PagedKV: device int32 tensors cu_q [n_seqs + 1] (first token row
     of each sequence), kv_len [n_seqs] (cached tokens, the new ones included) and pages [n_seqs, cols]
@@ -518,6 +524,7 @@ class KVBatch:
                 raise ValueError("%s must be torch.int32, got %s" % (name, t.dtype))
         if max_new < 0:
             raise ValueError("max_new must not be negative")
+        max_new = _as_c_int(max_new)
         for name, t in (("cu_q", cu_q), ("kv_len", kv_len)):
             _check_placement(name, t)
         cols = pages.shape[1]
@@ -687,7 +694,7 @@ class PagedKV:
         c, s = self._begin(cache, batch)
         _check("moe_ffn_kv_attention",
                moe_ffn_kv_attention(self._handle, c, batch.of(T), qr,
-                                    self.default_scale if scale is None else scale, window, sinks,
+                                    self.default_scale if scale is None else scale, _as_c_int(window), _as_c_int(sinks),
                                     out.data_ptr(), lse.data_ptr(), s))
         return out, lse
 

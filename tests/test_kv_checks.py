@@ -188,6 +188,22 @@ def test_operators_go_through_the_c_entry_points(monkeypatch):
                     ("moe_ffn_kv_attention", 11, ("batch", 3), 7)]
 
 
+@pytest.mark.parametrize("given,passed", [(0, 0), (1024, 1024), (-1, -1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                          (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 63 - 1, 2 ** 31 - 1), (-2 ** 32, -1)])
+def test_windows_and_sinks_of_any_size_keep_their_meaning(monkeypatch, given, passed):
+    """A C int would keep their lowest 32 bits."""
+    seen = []
+    monkeypatch.setattr(B, "moe_ffn_kv_attention", lambda *a: seen.append(a[5:7]) or B.MOE_FFN_OK)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: torch.zeros(1))
+    kv = _stub()
+    kv._handle, kv.default_scale = 11, 0.1
+    kv._begin = lambda cache, batch: ("cache", 7)
+    kv._rows = lambda what, t, heads: what
+    batch = type("Batch", (), {"of": lambda self, n: ("batch", n)})()
+    kv.attention(None, batch, torch.zeros(3, 1, 1), window=given, sinks=given)
+    assert seen == [(passed, passed)]
+
+
 def test_calls_after_close_are_refused(monkeypatch):
     monkeypatch.setattr(B, "moe_ffn_kv_destroy", lambda kv: None)
     kv = _stub()
