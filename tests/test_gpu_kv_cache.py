@@ -321,6 +321,36 @@ def test_values_of_far_apart_sizes_in_whole_items(d):
     U.check_attention(case)
 
 
+@pytest.mark.parametrize("fmt,d", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 2)])
+def test_hidden_values_and_far_apart_sizes(fmt, d, window, sinks):
+    """NaN and infinities among values of far apart sizes change only the rows that see them."""
+    case = U.Case(fmt, 2, 1, d, 16, [90, 1], [150, 200], seed=40)
+    case.v[0][20] *= 2.0 ** 40
+    case.v[0][140] *= 2.0 ** 50
+    case.v[0][130, 0, 5] = math.nan
+    case.v[0][100, 0, d - 1] = math.inf
+    case.k[0][145, 0, 3] = math.nan
+    case.v[0][30, 0, 40] = math.nan
+    case.k[1][20, 0, 3] = math.nan
+    case.v[1][60] = 0
+    U.check_attention(case, window, sinks)
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 128), ("e4m3", 256)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 1, 9]])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 40, 2 ** 40), (5, 2 ** 31 - 1)])
+def test_windows_and_sinks_as_long_as_numbers_go(fmt, d, new, window, sinks):
+    case = U.Case(fmt, 4, 2, d, 32, new, [300, 40, 5], seed=41)  # (four rows before the first position)
+    kv = case.handle()
+    c, q = case.filled(kv), case.q.cuda()
+    out, lse = kv.attention(c, case.batch(), q, window=window, sinks=sinks)
+    _ok(kv)
+    want, wl, tol, ltol = U.attention(case)
+    U.check_close(lse, wl, ltol, "lse")
+    U.check_close(out, want, tol, "out")
+
+
 @pytest.mark.parametrize("d", [128, 256, 512])
 @pytest.mark.parametrize("new", [1, 160])
 @pytest.mark.parametrize("big,score", [(2.0 ** 40, -45.0), (0.0, 30.0), (2.0 ** -40, 25.0)])
