@@ -422,8 +422,172 @@ int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const mo
 /* As moe_ffn_device_status, for a handle of the paged cache. */
 int moe_ffn_kv_device_status(moe_ffn_kv* kv, void* stream, uint32_t* word);
 
+/* A tree of drafted tokens per sequence. The batch's "new" tokens of a sequence are the nodes of its tree, in
+ * the slots after its context (kv_len[b] counts them): node i, of n_b <= MOE_FFN_KV_TREE_NODES, has the parent
+ * parents[cu_q[b] + i], a node before it (-1 <= parent < i; -1: it follows the context itself). It sees the
+ * context, its ancestors and itself, and it stands at position kv_len[b] - n_b + depth, depth being the number of
+ * its ancestors. */
+#define MOE_FFN_KV_TREE_NODES 256
+
+/* The trees of a batch in the form that the attention reads, made once for all layers.
+ *   parents  device pointer, [n_tokens] int32;
+ *   masks    device pointer, [n_tokens, 8] uint32, 16-byte aligned: bit j of a row says that the node sees node j
+ *            of its sequence (rows of no sequence: 0);
+ *   depth    device pointer, [n_tokens] int32 (rows of no sequence: 0): with the context's length, the
+ *            positions that rotary embeddings of the drafted tokens take.
+ * The three do not overlap. max_new above MOE_FFN_KV_TREE_NODES: MOE_FFN_EINVAL. A parent out of its range counts as
+ * -1 and sets MOE_FFN_STATUS_BAD_INDEX. Asynchronous on `stream`. */
+int moe_ffn_kv_tree(moe_ffn_kv* kv, const moe_ffn_kv_batch* batch, const int32_t* parents, uint32_t* masks,
+                    int32_t* depth, void* stream);
+
+/* Attention of the trees' nodes over the cache (which holds them already). As moe_ffn_kv_attention, but what a node
+ * sees is the context, its ancestors and itself; the window and the sinks go by positions: with window > 0 what lies
+ * at a position at or below its own less `window` is hidden unless it lies below `sinks`.
+ *   masks  what moe_ffn_kv_tree made of this batch (a bit of a node after the row's own is ignored); it does not
+ *          overlap out or lse.
+ * The nodes of a sequence with kv_len[b] < n_b see nothing (out 0, lse -infinity), and set
+ * MOE_FFN_STATUS_BAD_INDEX. */
+int moe_ffn_kv_tree_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch,
+                              const uint32_t* masks, const moe_ffn_kv_rows* q, float scale, int window, int sinks,
+                              void* out, float* lse, void* stream);
+
+/* Keeps one path of each tree: the keys and values of the nodes nodes[b * nodes_stride + i], i < counts[b], move to
+ * the slots after the context, in that order, in each of the n_layers caches. What lies behind them is left
+ * as it is.
+ *   caches   host array of n_layers caches of the handle's shape, none of which overlaps another;
+ *   batch    the trees' batch; n_tokens: at least the last value of cu_q;
+ *   nodes    device pointer, [n_seqs, nodes_cols] int32, rows nodes_stride >= nodes_cols entries apart, each
+ *            ascending: i <= nodes[b][i] < n_b;
+ *   counts   device pointer, [n_seqs] int32, 0 <= counts[b] <= nodes_cols;
+ *   new_len  device pointer or NULL, [n_seqs] int32: kv_len[b] - n_b + counts[b], the cached tokens that remain; it
+ *            overlaps none of the inputs.
+ * A path stops before a node out of its range or out of order, a count out of its range is brought into it, and of a
+ * sequence with kv_len[b] < n_b nothing moves (new_len: kv_len[b]); each sets MOE_FFN_STATUS_BAD_INDEX.
+ * Asynchronous on `stream`. */
+int moe_ffn_kv_keep(moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n_layers, const moe_ffn_kv_batch* batch,
+                    const int32_t* nodes, long long nodes_stride, int nodes_cols, const int32_t* counts,
+                    int32_t* new_len, void* stream);
+
+/* The states of beams follow the beams' parents. User u's beams are the rows u * beams .. u * beams + beams - 1 of
+ * the page table, all with lengths[u] cached tokens, whose full pages any of them may share; the pages from the one
+ * that is under way (number lengths[u] / page_size) on are each beam's own. After the call, beam k continues what
+ * beam parents[u * beams + k] held before:
+ *   - the table's entries of full pages are the parent's (the pages themselves are not copied);
+ *   - of the page under way, the lengths[u] % page_size first slots are copied from the parent's into its own, in
+ *     each of the n_layers caches.
+ *   caches   host array of n_layers (>= 0) caches of the handle's shape, none of which overlaps another;
+ *   pages    device pointer, [users * beams, pages_cols] int32, rows pages_stride >= pages_cols entries apart;
+ *   lengths  device pointer, [users] int32; parents: device pointer, [users, beams] int32; neither overlaps pages;
+ *   users    0..max_seqs / beams; beams: 1..MOE_FFN_BEAM_MAX.
+ * A parent out of 0..beams-1 counts as the beam itself, a length out of 0..pages_cols * page_size is brought into
+ * it, and a page id that is none is not touched; each sets MOE_FFN_STATUS_BAD_INDEX. Asynchronous on `stream`. */
+#define MOE_FFN_BEAM_MAX 64
+int moe_ffn_kv_reorder(moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n_layers, int32_t* pages,
+                       long long pages_stride, int pages_cols, const int32_t* lengths, const int32_t* parents,
+                       int users, int beams, void* stream);
+
 /* Releases the handle's host state. Safe on NULL. */
 void moe_ffn_kv_destroy(moe_ffn_kv* kv);
+
+/* ------------------------------------------------------------------------------------------------
+ * What a serving step needs around the cache and the block: the norms with the residual between two blocks, rotary
+ * positions, and the selection of a beam search. These calls have no handle: they run on the calling thread's
+ * current device, whose memory the pointers are.
+ */
+
+/* The norm after one block and the one before the next, with the gated residual between them:
+ *   y = scale * (x + gate * N(block; post)),  n = N(y; pre),  N(v; w) = v / sqrt(mean(v^2) + eps) * (1 + w)
+ * (the Gemma form of the weights, as in the block's own norms), row by row, in fp32, n from y before that is
+ * rounded; y and n are rounded to bf16 once. Sums of squares above fp32's range make a row's norm 0. */
+typedef struct moe_ffn_norm {
+  const void* x;           /* [tokens, hidden] bf16, rows x_stride elements apart: the residual */
+  const void* block;       /* the same, or NULL: nothing is added */
+  const void* gate;        /* the same, or NULL: 1. A stride of 0 gives every row the same gate */
+  const float* post;       /* [hidden] fp32, or NULL: block is added without a norm */
+  const float* pre;        /* [hidden] fp32; NULL if and only if n is */
+  void* y;                 /* [tokens, hidden] bf16, or NULL */
+  void* n;                 /* the same, or NULL; not both */
+  long long x_stride, block_stride, gate_stride;  /* >= 0 */
+  long long y_stride, n_stride;                   /* >= hidden */
+  float scale;             /* finite */
+  float eps;               /* > 0 */
+  int tokens;              /* >= 0 */
+  int hidden;              /* a multiple of 8, 8..MOE_FFN_NORM_MAX_HIDDEN */
+} moe_ffn_norm;
+#define MOE_FFN_NORM_MAX_HIDDEN 16384
+
+/* Pointers are 16-byte aligned and strides multiples of 8. Each of y and n may be x or block itself (the same pointer
+ * and stride); apart from that the outputs overlap nothing. Without a block there is neither gate nor post.
+ * Asynchronous on `stream`. */
+int moe_ffn_block_norm(const moe_ffn_norm* a, void* stream);
+
+/* Rotary positions with one or several axes (text, or time, height and width of images and video). Pair i of
+ * a head, the elements (i, pairs + i), or (2i, 2i + 1) where `interleaved`, turns by the angle
+ * positions[axis[i], token] * freq[i]; elements from 2 * pairs on are left as they are:
+ *   out = s * (a cos - b sin, b cos + a sin),  in fp32, rounded to bf16 once; s applies to turned elements only.
+ * `inverse` turns back: the transposed map, which is the gradient of the forward one. */
+#define MOE_FFN_ROTARY_MAX_AXES 8
+#define MOE_FFN_ROTARY_MAX_PAIRS 512
+
+typedef struct moe_ffn_rotary_pair {
+  uint64_t turn;  /* freq / 2 pi modulo 1, times 2^64: a product with a position wraps at whole turns, so that angles
+                     are exact to about 2^-30 turns at any position */
+  uint64_t axis;
+} moe_ffn_rotary_pair;
+
+/* Host only: the table of `pairs` pairs from their frequencies (radians per position, finite) and axes. */
+int moe_ffn_rotary_table(const double* freq, const int* axis, int pairs, moe_ffn_rotary_pair* table);
+
+typedef struct moe_ffn_rotary {
+  const moe_ffn_rotary_pair* table;  /* device pointer, [pairs], its axes below `axes` (others count as axis 0) */
+  const int32_t* positions;          /* device pointer, [axes, tokens], any values, rows positions_stride apart */
+  long long positions_stride;        /* >= 0 */
+  float scale;                       /* finite */
+  int pairs;                         /* a multiple of 4; 4..MOE_FFN_ROTARY_MAX_PAIRS, 2 * pairs <= head_dim */
+  int axes;                          /* 1..MOE_FFN_ROTARY_MAX_AXES */
+  int interleaved;
+  int inverse;
+  int tokens;                        /* >= 0 */
+  int head_dim;                      /* a multiple of 8, at most 1024 */
+  int q_heads, k_heads;              /* 0..1024; 0: none */
+} moe_ffn_rotary;
+
+/* Turns q and k: bf16, [tokens, heads, head_dim], as moe_ffn_kv_rows describes them. An output is its input itself
+ * (the same pointer and strides), or overlaps nothing; its rows do not overlap each other. q or k with 0 heads is not
+ * looked at. Asynchronous on `stream`. */
+int moe_ffn_rotary_apply(const moe_ffn_rotary* a, const moe_ffn_kv_rows* q, const moe_ffn_kv_rows* k,
+                         const moe_ffn_kv_rows* q_out, const moe_ffn_kv_rows* k_out, void* stream);
+
+/* The selection of a beam search: of each user's beams * vocab continuations, the `count` with the largest
+ *   scores[u, k] + logits[u, k, t] - log sum_t exp(logits[u, k, t]),
+ * best first, ties by the lower beam, then the lower token. A finished beam has one continuation, the end token, with
+ * its score unchanged, and its logits are not read. A continuation of -infinity or NaN is none (a NaN or +infinity
+ * among a beam's logits leaves it without any); where there are fewer than `count`, the rest have score
+ * -infinity, beam -1 and token -1. The sums are formed to about 1e-8, the comparisons made in fp64. */
+typedef struct moe_ffn_beam {
+  const void* logits;      /* device pointer, [users * beams, vocab], rows logits_stride elements apart */
+  long long logits_stride; /* >= 0 */
+  const float* scores;     /* device pointer, [users, beams] fp32 */
+  const uint8_t* finished; /* device pointer, [users, beams], nonzero: finished; or NULL */
+  float* out_scores;       /* device pointer, [users, count] fp32 */
+  int32_t* out_beams;      /* device pointer, [users, count] */
+  int32_t* out_tokens;     /* device pointer, [users, count] */
+  int logits_fp32;         /* 0: bf16, 1: fp32 */
+  int end_token;           /* 0..vocab-1 (looked at where finished is not NULL) */
+  int users;               /* 0..MOE_FFN_BEAM_MAX_USERS */
+  int beams;               /* 1..MOE_FFN_BEAM_MAX */
+  int vocab;               /* 1..MOE_FFN_BEAM_MAX_VOCAB */
+  int count;               /* 1..MOE_FFN_BEAM_MAX */
+} moe_ffn_beam;
+#define MOE_FFN_BEAM_MAX_USERS 4096
+#define MOE_FFN_BEAM_MAX_VOCAB 16777216
+
+/* Bytes of device workspace that a selection of these sizes needs (0 if they are out of range). */
+size_t moe_ffn_beam_workspace_bytes(int users, int beams, int vocab, int count);
+
+/* Pointers are aligned to their elements; outputs overlap nothing. `workspace`: device pointer, 256-byte aligned,
+ * whose contents do not matter; calls that share one must not overlap in time. Asynchronous on `stream`. */
+int moe_ffn_beam_select(const moe_ffn_beam* a, void* workspace, size_t workspace_bytes, void* stream);
 
 /* A static string naming a status code. */
 const char* moe_ffn_status_string(int status);

@@ -97,6 +97,31 @@ class moe_ffn_kv_rows(ctypes.Structure):
     _fields_ = [("ptr", _vp), ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
 
 
+KV_TREE_NODES, BEAM_MAX, ROTARY_MAX_PAIRS, ROTARY_MAX_AXES = 256, 64, 512, 8  # as include/moe_ffn.h has them
+
+
+class moe_ffn_norm(ctypes.Structure):
+    _fields_ = ([(f, _vp) for f in ("x", "block", "gate", "post", "pre", "y", "n")]
+                + [(f, ctypes.c_longlong) for f in ("x_stride", "block_stride", "gate_stride", "y_stride", "n_stride")]
+                + [("scale", ctypes.c_float), ("eps", ctypes.c_float), ("tokens", ctypes.c_int), ("hidden", ctypes.c_int)])
+
+
+class moe_ffn_rotary_pair(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_uint64), ("axis", ctypes.c_uint64)]
+
+
+class moe_ffn_rotary(ctypes.Structure):
+    _fields_ = ([("table", _vp), ("positions", _vp), ("positions_stride", ctypes.c_longlong), ("scale", ctypes.c_float)]
+                + [(f, ctypes.c_int) for f in ("pairs", "axes", "interleaved", "inverse", "tokens", "head_dim", "q_heads",
+                                               "k_heads")])
+
+
+class moe_ffn_beam(ctypes.Structure):
+    _fields_ = ([("logits", _vp), ("logits_stride", ctypes.c_longlong)]
+                + [(f, _vp) for f in ("scores", "finished", "out_scores", "out_beams", "out_tokens")]
+                + [(f, ctypes.c_int) for f in ("logits_fp32", "end_token", "users", "beams", "vocab", "count")])
+
+
 _LIB = None
 
 
@@ -159,6 +184,28 @@ def lib():
         L.moe_ffn_kv_device_status.argtypes = [_vp, _vp, ctypes.POINTER(ctypes.c_uint32)]
         L.moe_ffn_kv_destroy.restype = None
         L.moe_ffn_kv_destroy.argtypes = [_vp]
+        L.moe_ffn_kv_tree.restype = ctypes.c_int
+        L.moe_ffn_kv_tree.argtypes = [_vp, batch_p, _vp, _vp, _vp, _vp]
+        L.moe_ffn_kv_tree_attention.restype = ctypes.c_int
+        L.moe_ffn_kv_tree_attention.argtypes = [_vp, cache_p, batch_p, _vp, rows_p, ctypes.c_float, ctypes.c_int,
+                                                ctypes.c_int, _vp, _vp, _vp]
+        L.moe_ffn_kv_keep.restype = ctypes.c_int
+        L.moe_ffn_kv_keep.argtypes = [_vp, cache_p, ctypes.c_int, batch_p, _vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp,
+                                      _vp]
+        L.moe_ffn_kv_reorder.restype = ctypes.c_int
+        L.moe_ffn_kv_reorder.argtypes = [_vp, cache_p, ctypes.c_int, _vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp,
+                                         ctypes.c_int, ctypes.c_int, _vp]
+        L.moe_ffn_block_norm.restype = ctypes.c_int
+        L.moe_ffn_block_norm.argtypes = [ctypes.POINTER(moe_ffn_norm), _vp]
+        L.moe_ffn_rotary_table.restype = ctypes.c_int
+        L.moe_ffn_rotary_table.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int), ctypes.c_int,
+                                           ctypes.POINTER(moe_ffn_rotary_pair)]
+        L.moe_ffn_rotary_apply.restype = ctypes.c_int
+        L.moe_ffn_rotary_apply.argtypes = [ctypes.POINTER(moe_ffn_rotary), rows_p, rows_p, rows_p, rows_p, _vp]
+        L.moe_ffn_beam_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_ffn_beam_workspace_bytes.argtypes = [ctypes.c_int] * 4
+        L.moe_ffn_beam_select.restype = ctypes.c_int
+        L.moe_ffn_beam_select.argtypes = [ctypes.POINTER(moe_ffn_beam), _vp, ctypes.c_size_t, _vp]
         L.moe_ffn_destroy.restype = None
         L.moe_ffn_destroy.argtypes = [_vp]
         _LIB = L
@@ -352,6 +399,54 @@ def moe_ffn_kv_device_status(kv: int, stream: int):
 
 def moe_ffn_kv_destroy(kv: int) -> None:
     lib().moe_ffn_kv_destroy(_vp(kv))
+
+
+def moe_ffn_kv_tree(kv: int, batch: moe_ffn_kv_batch, parents: int, masks: int, depth: int, stream: int) -> int:
+    return lib().moe_ffn_kv_tree(kv, batch, parents, masks, depth, stream)
+
+
+def moe_ffn_kv_tree_attention(kv: int, cache: moe_ffn_kv_cache, batch: moe_ffn_kv_batch, masks: int, q: moe_ffn_kv_rows,
+                              scale: float, window: int, sinks: int, out: int, lse: int, stream: int) -> int:
+    return lib().moe_ffn_kv_tree_attention(kv, cache, batch, masks, q, scale, window, sinks, out, lse, stream)
+
+
+def moe_ffn_kv_keep(kv: int, caches, n_layers: int, batch: moe_ffn_kv_batch, nodes: int, nodes_stride: int,
+                    nodes_cols: int, counts: int, new_len: int, stream: int) -> int:
+    return lib().moe_ffn_kv_keep(kv, caches, n_layers, batch, nodes, nodes_stride, nodes_cols, counts, new_len, stream)
+
+
+def moe_ffn_kv_reorder(kv: int, caches, n_layers: int, pages: int, pages_stride: int, pages_cols: int, lengths: int,
+                       parents: int, users: int, beams: int, stream: int) -> int:
+    return lib().moe_ffn_kv_reorder(kv, caches, n_layers, pages, pages_stride, pages_cols, lengths, parents, users, beams,
+                                    stream)
+
+
+def moe_ffn_block_norm(args: moe_ffn_norm, stream: int) -> int:
+    return lib().moe_ffn_block_norm(args, stream)
+
+
+def moe_ffn_rotary_table(freq, axis) -> list:
+    """The pairs (turn, axis) of frequencies (radians per position) and axes."""
+    n = len(freq)
+    if len(axis) != n:
+        raise ValueError("%d frequencies, %d axes" % (n, len(axis)))
+    table = (moe_ffn_rotary_pair * max(n, 1))()
+    _check("moe_ffn_rotary_table", lib().moe_ffn_rotary_table((ctypes.c_double * max(n, 1))(*freq),
+                                                               (ctypes.c_int * max(n, 1))(*axis), n, table))
+    return [(e.turn, e.axis) for e in table]
+
+
+def moe_ffn_rotary_apply(args: moe_ffn_rotary, q: moe_ffn_kv_rows, k: moe_ffn_kv_rows, q_out: moe_ffn_kv_rows,
+                         k_out: moe_ffn_kv_rows, stream: int) -> int:
+    return lib().moe_ffn_rotary_apply(args, q, k, q_out, k_out, stream)
+
+
+def moe_ffn_beam_workspace_bytes(users: int, beams: int, vocab: int, count: int) -> int:
+    return lib().moe_ffn_beam_workspace_bytes(int(users), int(beams), int(vocab), int(count))
+
+
+def moe_ffn_beam_select(args: moe_ffn_beam, workspace: int, workspace_bytes: int, stream: int) -> int:
+    return lib().moe_ffn_beam_select(args, workspace, workspace_bytes, stream)
 
 
 # ------------------------------------------------------------------ torch convenience layer
@@ -549,6 +644,17 @@ class KVBatch:
         return last[1]
 
 
+class KVTree:
+    """The trees of a batch as PagedKV.tree_attention reads them (PagedKV.tree makes it): masks, int32
+    [tokens, 8], and depth, int32 [tokens], each node's number of ancestors: its position is the context's length
+    plus that."""
+
+    def __init__(self, masks, depth):
+        self.masks, self.depth = masks, depth
+        self.device = masks.device
+        self.n_tokens = masks.shape[0]
+
+
 class KVCache:
     """One layer's cache tensors, checked once (PagedKV.cache and PagedKV.new_cache make it). kind: the
     shape, type and device they were checked for; handles of another kind check them again and refuse."""
@@ -638,12 +744,15 @@ class PagedKV:
 
     def _begin(self, cache, batch):
         """The cache's structure and the stream of a call, ordered after the handle's last one."""
-        import torch
         if not isinstance(cache, KVCache):
             cache = self.cache(**cache)
         elif cache.kind != self._kind:
             cache = self.cache(cache.k, cache.v, cache.k_scale, cache.v_scale)
-        if batch.device != self.device:
+        return cache._ref, self._stream(batch)
+
+    def _stream(self, batch=None):
+        import torch
+        if batch is not None and batch.device != self.device:
             raise ValueError("the batch must be on %s" % self.device)
         raw = torch._C._cuda_getCurrentRawStream(self.device.index)
         if raw != self._last_raw and not torch.cuda.is_current_stream_capturing():
@@ -652,7 +761,7 @@ class PagedKV:
                 stream.wait_stream(self._last)
             self.workspace.record_stream(stream)  # dropped early, it stays until the stream is done with it
             self._last, self._last_raw = stream, raw
-        return cache._ref, raw
+        return raw
 
     def write(self, cache, batch: KVBatch, k, v) -> None:
         """Writes the new tokens' keys and values, bf16 [tokens, kv_heads, head_dim] each, into `cache`
@@ -680,6 +789,9 @@ class PagedKV:
         """Attention of the new tokens' queries, bf16 [tokens, q_heads, head_dim], over the cache, causal,
         with an optional sliding window and first positions that stay visible: (out, lse), bf16 like q
         (contiguous) and fp32 [tokens, q_heads]. scale: head_dim ** -0.5 if not given."""
+        return self._attend(cache, batch, None, q, window, sinks, scale, out)
+
+    def _attend(self, cache, batch, tree, q, window, sinks, scale, out):
         import torch
         qr = self._rows("q", q, self.q_heads)
         T = q.shape[0]
@@ -692,11 +804,103 @@ class PagedKV:
             _check_placement("out", out)
         lse = torch.empty((T, self.q_heads), dtype=torch.float32, device=self.device)
         c, s = self._begin(cache, batch)
-        _check("moe_ffn_kv_attention",
-               moe_ffn_kv_attention(self._handle, c, batch.of(T), qr,
-                                    self.default_scale if scale is None else scale, _as_c_int(window), _as_c_int(sinks),
-                                    out.data_ptr(), lse.data_ptr(), s))
+        scale = self.default_scale if scale is None else scale
+        window, sinks = _as_c_int(window), _as_c_int(sinks)
+        if tree is None:
+            _check("moe_ffn_kv_attention", moe_ffn_kv_attention(self._handle, c, batch.of(T), qr, scale, window, sinks,
+                                                                out.data_ptr(), lse.data_ptr(), s))
+        else:
+            _check("moe_ffn_kv_tree_attention",
+                   moe_ffn_kv_tree_attention(self._handle, c, batch.of(T), tree.masks.data_ptr(), qr, scale, window, sinks,
+                                             out.data_ptr(), lse.data_ptr(), s))
         return out, lse
+
+    def _ids(self, what, t, *shape):
+        import torch
+        if t.dtype != torch.int32 or tuple(t.shape) != shape:
+            raise ValueError("%s must be torch.int32 of shape %s, got %s of shape %s" % (what, list(shape), t.dtype,
+                                                                                         list(t.shape)))
+        if t.device != self.device or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous tensor on %s" % (what, self.device))
+
+    def _layers(self, caches):
+        """Several layers' caches as an array of structures."""
+        if isinstance(caches, (KVCache, dict)):
+            caches = [caches]
+        made = []
+        for c in caches:
+            if not isinstance(c, KVCache):
+                c = self.cache(**c)
+            elif c.kind != self._kind:
+                c = self.cache(c.k, c.v, c.k_scale, c.v_scale)
+            made.append(c)
+        return (moe_ffn_kv_cache * max(len(made), 1))(*(c.struct for c in made)), len(made)
+
+    def tree(self, batch: KVBatch, parents) -> KVTree:
+        """The trees of a batch whose new tokens are drafted ones: parents, int32 [tokens], gives each node's parent
+        among its sequence's nodes (an earlier one), or -1 where it follows the context. At most 256 nodes to a
+        sequence. One serves all layers."""
+        import torch
+        if parents.dim() != 1:
+            raise ValueError("parents must have one dimension, got shape %s" % (list(parents.shape),))
+        T = parents.shape[0]
+        self._ids("parents", parents, T)
+        masks = torch.empty((T, 8), dtype=torch.int32, device=self.device)
+        depth = torch.empty((T,), dtype=torch.int32, device=self.device)
+        s = self._stream(batch)
+        _check("moe_ffn_kv_tree", moe_ffn_kv_tree(self._handle, batch.of(T), parents.data_ptr(), masks.data_ptr(),
+                                                  depth.data_ptr(), s))
+        return KVTree(masks, depth)
+
+    def tree_attention(self, cache, batch: KVBatch, tree: KVTree, q, window: int = 0, sinks: int = 0, scale=None, out=None):
+        """Attention of drafted tokens' queries, bf16 [tokens, q_heads, head_dim], over the cache, which holds their
+        keys and values: a node sees the context, its ancestors and itself (window and sinks by positions).
+        Returns (out, lse) as attention does."""
+        if tree.device != self.device or tree.n_tokens != q.shape[0]:
+            raise ValueError("the tree has %d tokens on %s, q %d on %s" % (tree.n_tokens, tree.device, q.shape[0], self.device))
+        return self._attend(cache, batch, tree, q, window, sinks, scale, out)
+
+    def keep(self, caches, batch: KVBatch, nodes, counts):
+        """Keeps one path of each tree of `batch` in all layers' `caches` (a list, or one): the nodes
+        nodes[b, i], i < counts[b], ascending, move to the slots after the context. nodes: int32
+        [sequences, any], counts: int32 [sequences]. Returns the cached tokens that remain, int32 [sequences]."""
+        import torch
+        n = batch.tensors[1].shape[0]
+        if nodes.dim() != 2:
+            raise ValueError("nodes must have two dimensions, got shape %s" % (list(nodes.shape),))
+        self._ids("nodes", nodes, n, nodes.shape[1])
+        self._ids("counts", counts, n)
+        layers, n_layers = self._layers(caches)
+        new_len = torch.empty((n,), dtype=torch.int32, device=self.device)
+        s = self._stream(batch)
+        _check("moe_ffn_kv_keep",
+               moe_ffn_kv_keep(self._handle, layers, n_layers, batch.of(self.cfg.max_tokens), nodes.data_ptr(), nodes.shape[1],
+                               nodes.shape[1], counts.data_ptr(), new_len.data_ptr(), s))
+        return new_len
+
+    def reorder(self, caches, pages, lengths, parents) -> None:
+        """The states of beams follow their parents, int32 [users, beams], in all layers' `caches` (a list, or one).
+        pages: the page table, int32 [users * beams, cols] with contiguous rows, changed in place; lengths: int32
+        [users], the cached tokens of each of a user's beams. Full pages are shared through the table; of
+        the page under way, which with those after it is each beam's own, the tokens so far are copied."""
+        import torch
+        if parents.dim() != 2:
+            raise ValueError("parents must have two dimensions, got shape %s" % (list(parents.shape),))
+        users, beams = parents.shape
+        self._ids("parents", parents, users, beams)
+        self._ids("lengths", lengths, users)
+        if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != users * beams:
+            raise ValueError("pages must be torch.int32 of shape [%d, columns], got %s of shape %s" % (
+                users * beams, pages.dtype, list(pages.shape)))
+        cols = pages.shape[1]
+        stride = pages.stride(0) if pages.shape[0] > 1 else cols
+        if pages.device != self.device or (cols > 1 and pages.stride(1) != 1) or stride < cols:
+            raise ValueError("pages must be a tensor with contiguous rows on %s" % self.device)
+        layers, n_layers = self._layers(caches)
+        s = self._stream()
+        _check("moe_ffn_kv_reorder",
+               moe_ffn_kv_reorder(self._handle, layers, n_layers, pages.data_ptr(), stride, cols, lengths.data_ptr(),
+                                  parents.data_ptr(), users, beams, s))
 
     def status(self, stream=None):
         import torch
@@ -714,6 +918,194 @@ class PagedKV:
             self.close()
         except Exception:
             pass
+
+
+def _launch(call, device, *args):
+    """A call without a handle, on the current stream of its tensors' device."""
+    import torch
+    raw = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        return call(*args, raw)
+    with torch.cuda.device(device):
+        return call(*args, raw)
+
+
+def _norm_rows(what, t, T, H, device):
+    """Address and row stride of bf16 [T, H] rows."""
+    import torch
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, H):
+        raise ValueError("%s must be torch.bfloat16 of shape [%d, %d], got %s of shape %s" % (what, T, H, t.dtype,
+                                                                                              list(t.shape)))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (what, device))
+    stride = t.stride(0) if T > 1 else H
+    if t.stride(1) != 1 or stride % 8:
+        raise ValueError("%s must have contiguous rows, a multiple of 8 elements apart" % what)
+    return t.data_ptr(), stride
+
+
+def block_norm(x, block=None, post=None, gate=None, scale: float = 1.0, pre=None, eps: float = 1e-6, out=None, normed=None):
+    """The norm after one block and the one before the next, with the gated residual between them:
+
+        y = scale * (x + gate * N(block; post)),  n = N(y; pre),  N(v; w) = v / rms(v) * (1 + w)
+
+    x, block and gate: bf16 [tokens, hidden] (rows may be strided, a gate for all rows expanded); post and pre: fp32
+    [hidden]. Without a block y is scale * x; without post the block is added without a norm. Returns (y, n), bf16; n
+    is None without pre, and y is None where it would be x itself (no block, scale 1, no out). out and normed: where y
+    and n go, x or block themselves if wished."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions, got shape %s" % (list(x.shape),))
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    T, H = x.shape
+    device = x.device
+    if block is None and (post is not None or gate is not None):
+        raise ValueError("post and gate need a block")
+    if pre is None and normed is not None:
+        raise ValueError("normed needs pre")
+    a = moe_ffn_norm()
+    a.x, a.x_stride = _norm_rows("x", x, T, H, device)
+    if block is not None:
+        a.block, a.block_stride = _norm_rows("block", block, T, H, device)
+    if gate is not None:
+        a.gate, a.gate_stride = _norm_rows("gate", gate, T, H, device)
+    for name, w in (("post", post), ("pre", pre)):
+        if w is None:
+            continue
+        _check_type_size(name, w, torch.float32, H)
+        if w.device != device or not w.is_contiguous():
+            raise ValueError("%s must be a contiguous tensor on %s" % (name, device))
+        setattr(a, name, w.data_ptr())
+    if out is None and (block is not None or scale != 1.0 or pre is None):
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+    if normed is None and pre is not None:
+        normed = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+    if out is not None:
+        a.y, a.y_stride = _norm_rows("out", out, T, H, device)
+    if normed is not None:
+        a.n, a.n_stride = _norm_rows("normed", normed, T, H, device)
+    a.scale, a.eps, a.tokens, a.hidden = scale, eps, T, H
+    _check("moe_ffn_block_norm", _launch(moe_ffn_block_norm, device, a))
+    return out, normed
+
+
+class Rotary:
+    """Rotary positions with one or several axes. freqs: each pair's radians per position; axes: the axis whose
+    position turns it (all 0 if not given). Pair i of a head is (i, pairs + i), or (2i, 2i + 1) where interleaved;
+    elements after the pairs stay as they are. scale multiplies the turned elements."""
+
+    def __init__(self, freqs, axes=None, interleaved: bool = False, scale: float = 1.0, device: int = 0):
+        import torch
+        freqs = [float(f) for f in freqs]
+        axes = [0] * len(freqs) if axes is None else [int(i) for i in axes]
+        if not freqs or len(freqs) % 4 or len(freqs) > ROTARY_MAX_PAIRS:
+            raise ValueError("the number of pairs must be a multiple of 4 up to %d, got %d" % (ROTARY_MAX_PAIRS, len(freqs)))
+        rows = moe_ffn_rotary_table(freqs, axes)
+        signed = [[v - (1 << 64) if v >= 1 << 63 else v for v in row] for row in rows]
+        self.device = torch.device("cuda", int(device))
+        self.pairs, self.axes = len(freqs), max(axes) + 1
+        self.interleaved, self.scale = bool(interleaved), float(scale)
+        self.table = torch.tensor(signed, dtype=torch.int64).to(self.device)
+
+    def apply(self, q, k, positions, inverse: bool = False, inplace: bool = False):
+        """Turns q and k, bf16 [tokens, heads, width] each (any strides of 8 elements; k may be None), by positions, int32
+        [axes, tokens] (or [tokens] for one axis). Returns (q, k), new tensors or, inplace, the given ones. inverse turns
+        back, which is also the gradient's way."""
+        import torch
+        if positions.dim() == 1:
+            positions = positions.unsqueeze(0)
+        T = q.shape[0]
+        if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[0] < self.axes or positions.shape[1] != T:
+            raise ValueError("positions must be torch.int32 of shape [%d, %d], got %s of shape %s" % (
+                self.axes, T, positions.dtype, list(positions.shape)))
+        if positions.device != self.device or (T > 1 and positions.stride(1) != 1) or positions.stride(0) < 0:
+            raise ValueError("positions must have contiguous rows on %s" % self.device)
+        a = moe_ffn_rotary(self.table.data_ptr(), positions.data_ptr(), positions.stride(0) if self.axes > 1 else 0, self.scale,
+                           self.pairs, self.axes, self.interleaved, inverse, T, q.shape[-1], 0, 0)
+        rows, outs = [None, None], [None, None]
+        given = [q, k]
+        for i, (name, t) in enumerate((("q", q), ("k", k))):
+            if t is None:
+                continue
+            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != q.shape[2]:
+                raise ValueError("%s must be torch.bfloat16 of shape [%d, heads, %d], got %s of shape %s" % (
+                    name, T, q.shape[-1], t.dtype, list(t.shape)))
+            if t.device != self.device:
+                raise ValueError("%s must be on %s" % (name, self.device))
+            heads = t.shape[1]
+            given[i] = t if inplace else torch.empty(t.shape, dtype=torch.bfloat16, device=self.device)
+            for to, x in ((rows, t), (outs, given[i])):
+                ts, hs, es = x.stride()
+                if es != 1 or (T > 1 and ts % 8) or (heads > 1 and hs % 8):
+                    raise ValueError("%s must have a contiguous last dimension and strides that are multiples of 8" % name)
+                to[i] = moe_ffn_kv_rows(x.data_ptr(), ts if T > 1 else 0, hs if heads > 1 else 0)
+            if i == 0:
+                a.q_heads = heads
+            else:
+                a.k_heads = heads
+        _check("moe_ffn_rotary_apply",
+               _launch(moe_ffn_rotary_apply, self.device, a, rows[0], rows[1], outs[0], outs[1]))
+        return given[0], given[1]
+
+
+class BeamSearch:
+    """The selection of a beam search, with its workspace: of each user's beams * vocab continuations the `count` best.
+    Calls share the workspace: on another stream than the last one's, a call first waits for that one (not while
+    a graph is captured: order the replays yourself, and keep the object as long as the graph)."""
+
+    def __init__(self, users: int, beams: int, vocab: int, count: int, device: int = 0):
+        import torch
+        self.users, self.beams, self.vocab, self.count = int(users), int(beams), int(vocab), int(count)
+        self.nbytes = moe_ffn_beam_workspace_bytes(self.users, self.beams, self.vocab, self.count)
+        if self.nbytes == 0:
+            raise ValueError("invalid configuration")
+        self.device = torch.device("cuda", int(device))
+        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+        self._last = self._last_raw = None
+
+    def select(self, logits, scores, finished=None, end_token: int = 0):
+        """logits: bf16 or fp32 [users * beams, vocab] (or [users, beams, vocab]), rows may be strided; scores: fp32
+        [users, beams], the beams' sums so far (-infinity: no such beam); finished: bool [users, beams], whose only
+        continuation is end_token with the same score. Returns (scores, beams, tokens), each [users, count], best first;
+        beam and token are -1 where there is no further continuation."""
+        import torch
+        U, K, V, C = self.users, self.beams, self.vocab, self.count
+        if logits.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("logits must be torch.bfloat16 or torch.float32, got %s" % logits.dtype)
+        if tuple(logits.shape) == (U, K, V):
+            if U > 1 and K > 1 and logits.stride(0) != K * logits.stride(1):
+                raise ValueError("logits' rows must lie at one stride")
+            stride = logits.stride(1) if K > 1 else logits.stride(0)
+        elif tuple(logits.shape) == (U * K, V):
+            stride = logits.stride(0)
+        else:
+            raise ValueError("logits must have shape [%d, %d], got %s" % (U * K, V, list(logits.shape)))
+        if V > 1 and logits.stride(-1) != 1:
+            raise ValueError("logits must have contiguous rows")
+        for name, t, dtype in (("scores", scores, torch.float32), ("finished", finished, torch.bool)):
+            if t is None and name == "finished":
+                continue
+            if t.dtype != dtype or tuple(t.shape) != (U, K) or not t.is_contiguous():
+                raise ValueError("%s must be contiguous, %s of shape [%d, %d], got %s of shape %s" % (name, dtype, U, K, t.dtype,
+                                                                                                      list(t.shape)))
+        for name, t in (("logits", logits), ("scores", scores), ("finished", finished)):
+            if t is not None and t.device != self.device:
+                raise ValueError("%s must be on %s" % (name, self.device))
+        out = torch.empty((U, C), dtype=torch.float32, device=self.device)
+        ids = torch.empty((2, U, C), dtype=torch.int32, device=self.device)
+        a = moe_ffn_beam(logits.data_ptr(), stride if U * K > 1 else V, scores.data_ptr(),
+                         finished.data_ptr() if finished is not None else None, out.data_ptr(), ids[0].data_ptr(),
+                         ids[1].data_ptr(), logits.dtype == torch.float32, int(end_token), U, K, V, C)
+        raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if raw != self._last_raw and not torch.cuda.is_current_stream_capturing():
+            stream = torch.cuda.current_stream(self.device)
+            if self._last is not None:
+                stream.wait_stream(self._last)
+            self.workspace.record_stream(stream)  # dropped early, it stays until the stream is done with it
+            self._last, self._last_raw = stream, raw
+        _check("moe_ffn_beam_select", _launch(moe_ffn_beam_select, self.device, a, self.workspace.data_ptr(), self.nbytes))
+        return out, ids[0], ids[1]
 
 
 def view_tensor(ptr: int, shape, dtype, device: int = 0):

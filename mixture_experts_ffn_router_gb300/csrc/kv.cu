@@ -303,6 +303,7 @@ struct moe_ffn_kv {
   KvChunkList list;
   float* chunk_partial;
   int chunk_pairs;  // SM pairs of the kernel for chunks
+  int tree_pairs;   // and of the one for trees
 };
 
 namespace {
@@ -324,23 +325,24 @@ bool meet(const void* a, size_t an, const void* b, size_t bn) {
   return x < y + bn && y < x + an;
 }
 
-// Checks a call's cache and batch and gives them in the kernels' form. Returns MOE_FFN_OK, an error,
-// or 1 if there is nothing to do.
-int kv_arguments(const moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch, KvBatch* b,
-                 KvCache* c) {
-  if (!kv || !cache || !batch) return MOE_FFN_EINVAL;
+// The shape of a handle's caches.
+KvCache kv_shape(const moe_ffn_kv* kv) {
+  KvCache c = {};
+  c.n_pages = kv->cfg.n_pages;
+  c.kv_heads = kv->cfg.kv_heads;
+  c.page_log2 = kv->cfg.page_size == 16 ? 4 : kv->cfg.page_size == 32 ? 5 : kv->cfg.page_size == 64 ? 6 : 7;
+  c.head_dim = kv->cfg.head_dim;
+  c.e4m3 = kv->cfg.format == MOE_FFN_KV_E4M3 ? 1 : 0;
+  return c;
+}
+
+// Checks a call's batch and gives it in the kernels' form. Returns MOE_FFN_OK, an error, or 1 if it has no tokens.
+int kv_batch_arguments(const moe_ffn_kv* kv, const moe_ffn_kv_batch* batch, KvBatch* b) {
+  if (!kv || !batch) return MOE_FFN_EINVAL;
   if (batch->n_tokens < 0 || batch->n_seqs < 0 || batch->pages_cols < 0 || batch->max_new < 0 ||
       batch->pages_stride < batch->pages_cols)
     return MOE_FFN_EINVAL;
   if (batch->n_tokens > kv->cfg.max_tokens || batch->n_seqs > kv->cfg.max_seqs) return MOE_FFN_ETOOBIG;
-  if (batch->n_tokens == 0) return 1;
-  const bool q8 = kv->cfg.format == MOE_FFN_KV_E4M3;
-  if (!cache->k || !cache->v || (q8 && (!cache->k_scale || !cache->v_scale))) return MOE_FFN_EINVAL;
-  if (batch->n_seqs > 0 && (!batch->cu_q || !batch->kv_len || (batch->pages_cols > 0 && !batch->pages)))
-    return MOE_FFN_EINVAL;
-  if (off16(cache->k) || off16(cache->v) || (q8 && (off16(cache->k_scale) || off16(cache->v_scale))) ||
-      off4(batch->cu_q) || off4(batch->kv_len) || off4(batch->pages))
-    return MOE_FFN_EALIGN;
   b->cu_q = batch->cu_q;
   b->kv_len = batch->kv_len;
   b->pages = batch->pages;
@@ -349,16 +351,48 @@ int kv_arguments(const moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_
   b->n_seqs = batch->n_seqs;
   b->n_tokens = batch->n_tokens;
   b->max_new = batch->max_new;
+  if (batch->n_seqs > 0 && batch->n_tokens > 0 && (!batch->cu_q || !batch->kv_len || (batch->pages_cols > 0 && !batch->pages)))
+    return MOE_FFN_EINVAL;
+  if (batch->n_tokens > 0 && (off4(batch->cu_q) || off4(batch->kv_len) || off4(batch->pages))) return MOE_FFN_EALIGN;
+  return batch->n_tokens == 0 ? 1 : MOE_FFN_OK;
+}
+
+// Checks a call's cache and batch and gives them in the kernels' form. Returns MOE_FFN_OK, an error,
+// or 1 if there is nothing to do.
+int kv_arguments(const moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch, KvBatch* b,
+                 KvCache* c) {
+  if (!cache) return MOE_FFN_EINVAL;
+  const int rc = kv_batch_arguments(kv, batch, b);
+  if (rc != MOE_FFN_OK) return rc;
+  *c = kv_shape(kv);
+  if (!cache->k || !cache->v || (c->e4m3 && (!cache->k_scale || !cache->v_scale))) return MOE_FFN_EINVAL;
+  if (off16(cache->k) || off16(cache->v) || (c->e4m3 && (off16(cache->k_scale) || off16(cache->v_scale)))) return MOE_FFN_EALIGN;
   c->k = static_cast<uint8_t*>(cache->k);
   c->v = static_cast<uint8_t*>(cache->v);
   c->k_scale = cache->k_scale;
   c->v_scale = cache->v_scale;
-  c->n_pages = kv->cfg.n_pages;
-  c->kv_heads = kv->cfg.kv_heads;
-  c->page_log2 = kv->cfg.page_size == 16 ? 4 : kv->cfg.page_size == 32 ? 5 : kv->cfg.page_size == 64 ? 6 : 7;
-  c->head_dim = kv->cfg.head_dim;
-  c->e4m3 = q8 ? 1 : 0;
   return MOE_FFN_OK;
+}
+
+// Several layers' caches.
+int kv_layers_ok(const moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n) {
+  if (!caches) return MOE_FFN_EINVAL;
+  const bool q8 = kv->cfg.format == MOE_FFN_KV_E4M3;
+  for (int i = 0; i < n; ++i) {
+    const moe_ffn_kv_cache& c = caches[i];
+    if (!c.k || !c.v || (q8 && (!c.k_scale || !c.v_scale))) return MOE_FFN_EINVAL;
+    if (off16(c.k) || off16(c.v) || (q8 && (off16(c.k_scale) || off16(c.v_scale)))) return MOE_FFN_EALIGN;
+  }
+  return MOE_FFN_OK;
+}
+
+KvLayers kv_layers(const moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n) {
+  KvLayers l = {};
+  const bool q8 = kv->cfg.format == MOE_FFN_KV_E4M3;
+  for (int i = 0; i < n; ++i)
+    l.layer[i] = {static_cast<uint8_t*>(caches[i].k), static_cast<uint8_t*>(caches[i].v), q8 ? caches[i].k_scale : nullptr,
+                  q8 ? caches[i].v_scale : nullptr};
+  return l;
 }
 
 int kv_rows(const moe_ffn_kv_rows* r, KvRows* o) {
@@ -372,6 +406,14 @@ int kv_rows(const moe_ffn_kv_rows* r, KvRows* o) {
 
 size_t kv_rows_bytes(const KvRows& r, int tokens, int heads, int d) {
   return static_cast<size_t>((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + d) * 2;
+}
+
+// Whether an output would meet the batch's own arrays.
+bool meets_batch(const void* p, size_t bytes, const KvBatch& b) {
+  const size_t n = static_cast<size_t>(b.n_seqs);
+  if (n == 0) return false;
+  return meet(p, bytes, b.cu_q, (n + 1) * 4) || meet(p, bytes, b.kv_len, n * 4) ||
+         meet(p, bytes, b.pages, ((n - 1) * static_cast<size_t>(b.pages_stride) + b.pages_cols) * 4);
 }
 
 // Whether an output would meet the cache that the call reads.
@@ -421,6 +463,61 @@ int on_device(const moe_ffn_kv* kv) {
   return cur == kv->device || cudaSetDevice(kv->device) == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
 }
 
+// Both forms of attention: masks NULL is the causal one.
+int kv_attend(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch, const uint32_t* masks,
+              const moe_ffn_kv_rows* q, float scale, int window, int sinks, void* out, float* lse, void* stream) {
+  KvAttn a;
+  int rc = kv_arguments(kv, cache, batch, &a.b, &a.c);
+  if (rc < 0) return rc;
+  if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0 || sinks < 0) return MOE_FFN_EINVAL;
+  if (rc > 0) return MOE_FFN_OK;
+  if ((rc = kv_rows(q, &a.q)) != MOE_FFN_OK) return rc;
+  if (!out) return MOE_FFN_EINVAL;
+  if (off16(out) || off4(lse)) return MOE_FFN_EALIGN;
+  const moe_ffn_kv_config& f = kv->cfg;
+  const size_t rows = static_cast<size_t>(a.b.n_tokens) * f.q_heads, bytes = rows * f.head_dim * 2;
+  const size_t q_bytes = kv_rows_bytes(a.q, a.b.n_tokens, f.q_heads, f.head_dim);
+  if (meet(out, bytes, a.q.ptr, q_bytes) || meet(out, bytes, kv->ws, kv->ws_bytes) || meets_cache(out, bytes, a.c) ||
+      (lse && (meet(lse, rows * 4, out, bytes) || meet(lse, rows * 4, kv->ws, kv->ws_bytes) ||
+               meet(lse, rows * 4, a.q.ptr, q_bytes) || meets_cache(lse, rows * 4, a.c))))
+    return MOE_FFN_EINVAL;
+  if (masks && (meet(masks, static_cast<size_t>(a.b.n_tokens) * 32, out, bytes) ||
+                (lse && meet(masks, static_cast<size_t>(a.b.n_tokens) * 32, lse, rows * 4))))
+    return MOE_FFN_EINVAL;
+  a.group = f.q_heads / f.kv_heads;
+  a.q_heads = f.q_heads;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.status = kv->status;
+  a.counters = kv->counters;
+  a.counters_in = kv->counters_in;
+  a.partial = kv->partial;
+  a.list = kv->list;
+  a.tree = masks;
+  // One cost per format, of 2 to 6 tiles. Prompts of 1500 to 4100 tokens of width 256 take 196 us in bf16 with 3
+  // (206 with 2, 202 with 4, 206 with 5); in e4m3, where the queries are split on the way, 279 with 4 (302
+  // with 3, 275 with 5, 280 with 6). Of the other widths in e4m3, 128 takes 210 with 4 and 216 with 5, 512 672 and
+  // 651, and a mixed batch 130 and 135 (width 128), 196 and 186 (512).
+  a.item_cost = a.c.e4m3 ? 4 : 3;
+  a.chunk_partial = kv->chunk_partial;
+  if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int ctas = 2 * kv->num_sms < kDecodeMaxCtas ? 2 * kv->num_sms : kDecodeMaxCtas;
+  // A single token of up to kDecodeHeads heads per kv head fills an item of the decode kernel; the chunk
+  // kernel computes tiles of 256 rows of which it would fill `group`. Single tokens through the one and the other:
+  // one short sequence 14 and 20 us, 64 e4m3 sequences (width 512) 78 and 226, 256 windows 217 and 360,
+  // one long bf16 sequence 96 and 124.
+  // (A tree of one node is a single token.)
+  cudaError_t e;
+  if (a.b.max_new <= 1 && a.group <= kDecodeHeads) e = launch_kv_decode(a, ctas, s);
+  else if (masks) e = launch_kv_tree_chunk(a, kv->tree_pairs, s);
+  else e = launch_kv_chunk(a, kv->chunk_pairs, s);
+  return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -467,6 +564,7 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   // The workspace may be memory that work still queued on some stream writes: that ends before the control words
   // are cleared, and the clearing before any call.
   if (kv_decode_setup() != cudaSuccess || kv_chunk_setup(&kv->chunk_pairs) != cudaSuccess ||
+      kv_tree_chunk_setup(&kv->tree_pairs) != cudaSuccess || kv_moves_setup() != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     delete kv;
@@ -511,49 +609,90 @@ int moe_ffn_kv_read(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn
 int moe_ffn_kv_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch,
                          const moe_ffn_kv_rows* q, float scale, int window, int sinks, void* out, float* lse,
                          void* stream) {
-  KvAttn a;
-  int rc = kv_arguments(kv, cache, batch, &a.b, &a.c);
+  return kv_attend(kv, cache, batch, nullptr, q, scale, window, sinks, out, lse, stream);
+}
+
+int moe_ffn_kv_tree(moe_ffn_kv* kv, const moe_ffn_kv_batch* batch, const int32_t* parents, uint32_t* masks,
+                    int32_t* depth, void* stream) {
+  KvBatch b;
+  int rc = kv_batch_arguments(kv, batch, &b);
   if (rc < 0) return rc;
-  if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0 || sinks < 0) return MOE_FFN_EINVAL;
+  if (b.max_new > MOE_FFN_KV_TREE_NODES) return MOE_FFN_EINVAL;
   if (rc > 0) return MOE_FFN_OK;
-  if ((rc = kv_rows(q, &a.q)) != MOE_FFN_OK) return rc;
-  if (!out) return MOE_FFN_EINVAL;
-  if (off16(out) || off4(lse)) return MOE_FFN_EALIGN;
-  const moe_ffn_kv_config& f = kv->cfg;
-  const size_t rows = static_cast<size_t>(a.b.n_tokens) * f.q_heads, bytes = rows * f.head_dim * 2;
-  const size_t q_bytes = kv_rows_bytes(a.q, a.b.n_tokens, f.q_heads, f.head_dim);
-  if (meet(out, bytes, a.q.ptr, q_bytes) || meet(out, bytes, kv->ws, kv->ws_bytes) || meets_cache(out, bytes, a.c) ||
-      (lse && (meet(lse, rows * 4, out, bytes) || meet(lse, rows * 4, kv->ws, kv->ws_bytes) ||
-               meet(lse, rows * 4, a.q.ptr, q_bytes) || meets_cache(lse, rows * 4, a.c))))
+  if (!parents || !masks || !depth) return MOE_FFN_EINVAL;
+  if (off16(masks) || off4(parents) || off4(depth)) return MOE_FFN_EALIGN;
+  const size_t n = static_cast<size_t>(b.n_tokens);
+  if (meet(parents, 4 * n, masks, 32 * n) || meet(parents, 4 * n, depth, 4 * n) || meet(depth, 4 * n, masks, 32 * n) ||
+      meet(masks, 32 * n, kv->ws, kv->ws_bytes) || meet(depth, 4 * n, kv->ws, kv->ws_bytes) ||
+      meets_batch(masks, 32 * n, b) || meets_batch(depth, 4 * n, b))
     return MOE_FFN_EINVAL;
-  a.group = f.q_heads / f.kv_heads;
-  a.q_heads = f.q_heads;
-  a.scale = scale;
-  a.window = window;
-  a.sinks = sinks;
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.status = kv->status;
-  a.counters = kv->counters;
-  a.counters_in = kv->counters_in;
-  a.partial = kv->partial;
-  a.list = kv->list;
-  // One cost per format, of 2 to 6 tiles. Prompts of 1500 to 4100 tokens of width 256 take 196 us in bf16 with 3
-  // (206 with 2, 202 with 4, 206 with 5); in e4m3, where the queries are split on the way, 279 with 4 (302
-  // with 3, 275 with 5, 280 with 6). Of the other widths in e4m3, 128 takes 210 with 4 and 216 with 5, 512 672 and
-  // 651, and a mixed batch 130 and 135 (width 128), 196 and 186 (512).
-  a.item_cost = a.c.e4m3 ? 4 : 3;
-  a.chunk_partial = kv->chunk_partial;
   if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int ctas = 2 * kv->num_sms < kDecodeMaxCtas ? 2 * kv->num_sms : kDecodeMaxCtas;
-  // A single token of up to kDecodeHeads heads per kv head fills an item of the decode kernel; the chunk
-  // kernel computes tiles of 256 rows of which it would fill `group`. Single tokens through the one and the other:
-  // one short sequence 14 and 20 us, 64 e4m3 sequences (width 512) 78 and 226, 256 windows 217 and 360,
-  // one long bf16 sequence 96 and 124.
-  const cudaError_t e = a.b.max_new <= 1 && a.group <= kDecodeHeads ? launch_kv_decode(a, ctas, s)
-                                                                    : launch_kv_chunk(a, kv->chunk_pairs, s);
-  return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
+  return launch_kv_tree(b, kv_shape(kv), parents, masks, depth, kv->status, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_FFN_OK
+             : MOE_FFN_ECUDA;
+}
+
+int moe_ffn_kv_tree_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_batch* batch,
+                              const uint32_t* masks, const moe_ffn_kv_rows* q, float scale, int window, int sinks,
+                              void* out, float* lse, void* stream) {
+  if (!batch || (!masks && batch->n_tokens > 0)) return MOE_FFN_EINVAL;
+  if (off16(masks)) return MOE_FFN_EALIGN;
+  if (batch->max_new > MOE_FFN_KV_TREE_NODES) return MOE_FFN_EINVAL;
+  return kv_attend(kv, cache, batch, masks, q, scale, window, sinks, out, lse, stream);
+}
+
+int moe_ffn_kv_keep(moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n_layers, const moe_ffn_kv_batch* batch,
+                    const int32_t* nodes, long long nodes_stride, int nodes_cols, const int32_t* counts,
+                    int32_t* new_len, void* stream) {
+  KvBatch b;
+  int rc = kv_batch_arguments(kv, batch, &b);
+  if (rc < 0) return rc;
+  if (b.max_new > MOE_FFN_KV_TREE_NODES || n_layers < 1 || nodes_cols < 0 || nodes_stride < nodes_cols) return MOE_FFN_EINVAL;
+  if ((rc = kv_layers_ok(kv, caches, n_layers)) != MOE_FFN_OK) return rc;
+  if (b.n_seqs == 0) return MOE_FFN_OK;
+  if (!b.cu_q || !b.kv_len || (b.pages_cols > 0 && !b.pages) || !counts || (nodes_cols > 0 && !nodes)) return MOE_FFN_EINVAL;
+  if (off4(b.cu_q) || off4(b.kv_len) || off4(b.pages) || off4(nodes) || off4(counts) || off4(new_len)) return MOE_FFN_EALIGN;
+  const size_t n = static_cast<size_t>(b.n_seqs);
+  if (new_len && (meets_batch(new_len, 4 * n, b) || meet(new_len, 4 * n, counts, 4 * n) || meet(new_len, 4 * n, kv->ws, kv->ws_bytes) ||
+                  meet(new_len, 4 * n, nodes, (static_cast<size_t>(n - 1) * nodes_stride + nodes_cols) * 4)))
+    return MOE_FFN_EINVAL;
+  if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
+  if (b.n_tokens == 0) b.n_tokens = 1;  // (a bound of cu_q; no rows are read)
+  for (int first = 0; first < n_layers; first += kMaxLayers) {
+    const int m = n_layers - first < kMaxLayers ? n_layers - first : kMaxLayers;
+    if (launch_kv_keep(b, kv_shape(kv), kv_layers(kv, caches + first, m), m, nodes, nodes_stride, nodes_cols, counts,
+                       first == 0 ? new_len : nullptr, kv->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return MOE_FFN_ECUDA;
+  }
+  return MOE_FFN_OK;
+}
+
+int moe_ffn_kv_reorder(moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n_layers, int32_t* pages,
+                       long long pages_stride, int pages_cols, const int32_t* lengths, const int32_t* parents,
+                       int users, int beams, void* stream) {
+  if (!kv || n_layers < 0 || pages_cols < 0 || pages_stride < pages_cols || users < 0 || beams < 1 ||
+      beams > MOE_FFN_BEAM_MAX)
+    return MOE_FFN_EINVAL;
+  if (static_cast<long long>(users) * beams > kv->cfg.max_seqs) return MOE_FFN_ETOOBIG;
+  int rc = n_layers > 0 ? kv_layers_ok(kv, caches, n_layers) : MOE_FFN_OK;
+  if (rc != MOE_FFN_OK) return rc;
+  if (users == 0 || pages_cols == 0) return MOE_FFN_OK;
+  if (!pages || !lengths || !parents) return MOE_FFN_EINVAL;
+  if (off4(pages) || off4(lengths) || off4(parents)) return MOE_FFN_EALIGN;
+  const size_t rows = static_cast<size_t>(users) * beams, table = ((rows - 1) * static_cast<size_t>(pages_stride) + pages_cols) * 4;
+  if (meet(pages, table, lengths, static_cast<size_t>(users) * 4) || meet(pages, table, parents, rows * 4) ||
+      meet(pages, table, kv->ws, kv->ws_bytes))
+    return MOE_FFN_EINVAL;
+  if ((rc = on_device(kv)) != MOE_FFN_OK) return rc;
+  int first = 0;
+  do {
+    const int m = n_layers - first < kMaxLayers ? n_layers - first : kMaxLayers;
+    if (launch_kv_reorder(kv_shape(kv), kv_layers(kv, caches + first, m), m, pages, pages_stride, pages_cols, lengths, parents,
+                          users, beams, first == 0, kv->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return MOE_FFN_ECUDA;
+    first += m;
+  } while (first < n_layers);
+  return MOE_FFN_OK;
 }
 
 int moe_ffn_kv_device_status(moe_ffn_kv* kv, void* stream, uint32_t* word) {

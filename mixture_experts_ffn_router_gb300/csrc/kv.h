@@ -31,6 +31,18 @@ struct KvCache {
   int e4m3;
 };
 
+// The tensors of several layers' caches, for one launch.
+struct KvLayer {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;  // NULL in bf16
+  float* v_scale;
+};
+constexpr int kMaxLayers = 32;
+struct KvLayers {
+  KvLayer layer[kMaxLayers];
+};
+
 struct KvRows {
   const uint16_t* ptr;
   long long token_stride;
@@ -46,7 +58,7 @@ struct KvRowTile {
   int front;  // tiles of the sinks, before the window's
   int skip;   // tiles between the two
   int count;  // tiles in all
-  int unused;
+  int node0;  // trees: the first row's node; p0 is then the context's last position
 };
 
 // A pair's share of the work: units [begin, end), and the item it begins in.
@@ -92,6 +104,7 @@ struct KvAttn {
   int* counters_in; // [2 * kDecodeMaxCtas] the same, of groups of an item's pieces
   float* partial;   // pieces of items that several CTAs share
   KvChunkList list;      // the same for chunks of tokens
+  const uint32_t* tree;  // [n_tokens][8] the nodes that each row sees, or NULL: causal
   int item_cost;         // what an item costs beside its key tiles, in key tiles (chunks of tokens)
   float* chunk_partial;
 };
@@ -121,6 +134,17 @@ cudaError_t kv_decode_setup();
 cudaError_t launch_kv_decode(const KvAttn& a, int ctas, cudaStream_t s);
 cudaError_t kv_chunk_setup(int* pairs);
 cudaError_t launch_kv_chunk(const KvAttn& a, int pairs, cudaStream_t s);
+cudaError_t kv_tree_chunk_setup(int* pairs);
+cudaError_t launch_kv_tree_chunk(const KvAttn& a, int pairs, cudaStream_t s);
+cudaError_t kv_moves_setup();
+cudaError_t launch_kv_tree(const KvBatch& b, const KvCache& c, const int32_t* parents, uint32_t* masks, int32_t* depth,
+                           unsigned int* status, cudaStream_t s);
+cudaError_t launch_kv_keep(const KvBatch& b, const KvCache& c, const KvLayers& l, int n_layers, const int32_t* nodes,
+                           long long nodes_stride, int nodes_cols, const int32_t* counts, int32_t* new_len,
+                           unsigned int* status, cudaStream_t s);
+cudaError_t launch_kv_reorder(const KvCache& c, const KvLayers& l, int n_layers, int32_t* pages, long long pages_stride,
+                              int pages_cols, const int32_t* lengths, const int32_t* parents, int users, int beams,
+                              bool first_group, unsigned int* status, cudaStream_t s);
 
 #ifdef __CUDACC__
 // What a batch says of one sequence, with every value brought into range.

@@ -62,6 +62,13 @@
 // per row, over the keys that the row sees, rounded to bf16 (as over a bf16 cache, half a step is 2^-8), which
 // holds 2^-133 of the largest term; V's codes are widened to bf16 there, exactly too. Up to there a shared
 // reference loses at most 2^-19 per key of the row's largest term.
+//
+// Trees of drafted tokens (kv_tree.cu compiles this file a second time, with KV_TREE set). The new tokens are nodes in
+// the slots after the context; a node sees the context, through its window, and of the other nodes those in its mask.
+// So only what a row sees is another: in the tiles that hold nodes, or where windows begin, its bits come from
+// the node's mask (tree_seen); that is a tile or two of an item. Keys that no row of a tile sees, and those that
+// all see, are bounded by indexes alone, as for causal rows: a node comes after its ancestors and stands no deeper
+// than its number.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -69,9 +76,15 @@
 #include "kv.h"
 #include "ptx.cuh"
 
+#ifndef KV_TREE
+#define KV_TREE 0
+#endif
+
 namespace moe {
 
 namespace {
+
+constexpr bool kTree = KV_TREE != 0;
 
 constexpr int kThreads = 512;
 constexpr int kRows = 128;   // rows of a row tile in a CTA
@@ -302,17 +315,63 @@ __device__ __forceinline__ bool aux_sync_or(bool c) {
 
 // ------------------------------------------------------------------ the list of row tiles
 
+// The last key that a row tile's rows see, and the least position that one of them stands at.
+__device__ __forceinline__ int last_key(const KvRowTile& t) { return kTree ? t.p0 + t.node0 + t.nt : t.p0 + t.nt - 1; }
+__device__ __forceinline__ int least_position(const KvRowTile& t) { return kTree ? t.p0 + 1 : max(t.p0, 0); }
+
+// Which of the keys k0 .. k0 + 63 the node of a row tile's token `tok` sees, by bits.
+__device__ __noinline__ unsigned long long tree_seen(const KvAttn& a, const KvRowTile& t, int tok, int k0) {
+  if (tok >= t.nt) return 0ull;
+  const int first = t.p0 + 1, node = t.node0 + tok;  // key of node 0
+  const uint4* m = reinterpret_cast<const uint4*>(a.tree) + 2LL * (t.row0 + tok);
+  const uint4 lo4 = m[0], hi4 = m[1];
+  const unsigned long long words[4] = {lo4.x | static_cast<unsigned long long>(lo4.y) << 32,
+                                       lo4.z | static_cast<unsigned long long>(lo4.w) << 32,
+                                       hi4.x | static_cast<unsigned long long>(hi4.y) << 32,
+                                       hi4.z | static_cast<unsigned long long>(hi4.w) << 32};
+  // Ancestors in the order of their numbers stand at depths 0, 1, ...: those whose rank is within the window of the
+  // node's, or whose position is a sink's, are seen.
+  const int own = first - k0;  // bit of node 0
+  int depth = -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) depth += __popcll(words[i] & low_bits(node + 1 - 64 * i));
+  const int least = a.window > 0 ? depth - a.window + 1 : 0;  // rank
+  unsigned long long seen = 0ull;
+  int rank = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    unsigned long long w = words[i] & low_bits(node + 1 - 64 * i);
+    const int here = __popcll(w);
+    if (rank < least) {
+      // Its lowest bits, of ranks below `least` that are no sinks', go.
+      int r = rank;
+      for (unsigned long long rest = w; rest != 0ull && r < least; rest &= rest - 1ull, ++r)
+        if (first + r >= a.sinks) w &= ~(rest & (0ull - rest));
+    }
+    rank += here;
+    const int shift = own + 64 * i;
+    if (shift > -64 && shift < 64) seen |= shift >= 0 ? w << shift : w >> -shift;
+  }
+  const int lo = a.window > 0 ? first + depth - a.window + 1 : 0;
+  return seen | (low_bits(first - k0) & ~(low_bits(lo - k0) & ~low_bits(a.sinks - k0)));
+}
+
 // What the tokens [i0, i0 + nt) of a sequence see together.
 __device__ __forceinline__ KvRowTile row_tile(const KvAttn& a, int seq, const KvSeq& s, int i0, int tokens) {
   KvRowTile t;
   t.seq = seq;
   t.row0 = s.row0 + i0;
   t.nt = min(tokens, s.n - i0);
-  t.p0 = s.len - s.n + i0;
+  t.node0 = i0;
+  t.p0 = kTree ? s.len - s.n - 1 : s.len - s.n + i0;
   t.front = t.skip = t.count = 0;
-  const int p1 = t.p0 + t.nt - 1;
+  if (kTree && s.len < s.n) {
+    atomicOr(a.status, kStatusBadIndex);
+    return t;
+  }
+  const int p1 = last_key(t);
   if (p1 < 0) return t;
-  const KvSpan span = kv_span(max(t.p0, 0), a.window, a.sinks);
+  const KvSpan span = kv_span(least_position(t), a.window, a.sinks);
   const int first = span.lo / KT;
   t.front = min((span.sinks + KT - 1) / KT, first);
   t.skip = first - t.front;
@@ -702,24 +761,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Whether every row of the item sees every key of the tile.
   auto tile_at = [&](int i) { return i < t.front ? i : i + t.skip; };
   auto is_masked = [&](int tile) {
-    const int k0 = tile * KT, k1 = k0 + KT - 1, p1 = t.p0 + t.nt - 1;
+    const int k0 = tile * KT, k1 = k0 + KT - 1, p1 = last_key(t);
     return !(k1 <= t.p0 && (a.window == 0 || k0 > p1 - a.window || k1 < a.sinks));
   };
   // The keys that some row of the item sees.
   auto any_sees = [&](int j) {
-    const int p1 = t.p0 + t.nt - 1;
-    return j <= p1 && (a.window == 0 || j > max(t.p0, 0) - a.window || j < a.sinks);
+    const int p1 = last_key(t);
+    return j <= p1 && (a.window == 0 || j > least_position(t) - a.window || j < a.sinks);
   };
 
-  // Adds the values that were cleared of V (bf16) back to 32 columns of the row of the token at p.
-  auto put_back = [&](const KvRowTile& it, int head, int col, int p, int no, uint32_t (&o)[32]) {
-    const int p1 = it.p0 + it.nt - 1, lo = a.window > 0 ? p - a.window + 1 : 0;
+  // Adds the values that were cleared of V (bf16) back to 32 columns of the row of a token.
+  auto put_back = [&](const KvRowTile& it, int head, int col, int tok, int no, uint32_t (&o)[32]) {
+    const int p1 = last_key(it), p = it.p0 + tok, lo = a.window > 0 ? p - a.window + 1 : 0;
     // Each set bit stands for up to two keys; a key that every row of the tile sees was not cleared.
     for (int b = 0; b < 512; ++b) {
       if (!(odd[no % 3 * 8 + ((b & 255) >> 5)] >> (b & 31) & 1)) continue;
-      const int key = b < 256 ? it.p0 + 1 + b : max(it.p0, 0) - a.window + 1 + b - 256;
+      const int key = b < 256 ? it.p0 + 1 + b : least_position(it) - a.window + 1 + b - 256;
       if (b >= 256 && (a.window == 0 || key > it.p0)) continue;
-      if (key < 0 || key > p || (key < lo && key >= a.sinks)) continue;
+      if constexpr (kTree) {
+        if (key < 0 || key > p1 || !(tree_seen(a, it, tok, key) & 1ull)) continue;
+      } else {
+        if (key < 0 || key > p || (key < lo && key >= a.sinks)) continue;
+      }
       if (key <= it.p0 && (a.window == 0 || key > p1 - a.window || key < a.sinks)) continue;
       const int page = kv_page(a.b, a.c, it.seq, key >> a.c.page_log2, a.status);
       if (page < 0) continue;
@@ -759,8 +822,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The position a box begins at, -1 if no row sees any of it, and the page table's entry of it.
       auto fetch = [&](int j, int& first) {
         first = j < n ? tile_at(i0 + j) * KT + (box << rows_log2) : 0x7fffffff;
-        const bool need = first <= t.p0 + t.nt - 1 &&
-                          (a.window == 0 || first + (1 << rows_log2) - 1 > max(t.p0, 0) - a.window || first < a.sinks);
+        const bool need = first <= last_key(t) &&
+                          (a.window == 0 || first + (1 << rows_log2) - 1 > least_position(t) - a.window || first < a.sinks);
         if (!need) first = -1;
         return need ? a.b.pages[t.seq * a.b.pages_stride + (first >> a.c.page_log2)] : -1;
       };
@@ -936,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = part / C::kHalves, vhalf = part % C::kHalves;
       const int tok = rr / a.group;
       const bool live = tok < t.nt;
-      const int p = live ? t.p0 + tok : -1;
+      const int p = live ? (kTree ? 0 : t.p0 + tok) : -1;  // (a node is somewhere; tree_seen knows where)
       const int lo = a.window > 0 ? p - a.window + 1 : 0;  // first position in the window
       float qs = a.scale * 1.44269504f;
       if constexpr (E4M3) {
@@ -977,7 +1040,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned long long seen = ~0ull;
         if (__builtin_expect(masked, 0)) {
           const int k0 = tile * KT + half * 64;
-          seen = low_bits(p + 1 - k0) & ~(low_bits(lo - k0) & ~low_bits(a.sinks - k0));
+          if constexpr (kTree) seen = tree_seen(a, t, tok, k0);
+          else seen = low_bits(p + 1 - k0) & ~(low_bits(lo - k0) & ~low_bits(a.sinks - k0));
         }
         bool move = j == 0 || step != 1.0f;  // the reference is to move
         uint32_t w[32];
@@ -1105,7 +1169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!E4M3) {
           if (__builtin_expect(masked, 0)) {
             // V's rows that no row sees, and non-finite values that only some rows see.
-            const int p1 = t.p0 + t.nt - 1;
+            const int p1 = last_key(t);
             // A thread's vectors are the same 16 bytes of four keys, in each chunk.
             uint4* v = reinterpret_cast<uint4*>(v_ring + vs * C::kVSlot) + stid;
 #pragma unroll
@@ -1135,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *at = make_uint4(xs[0], xs[1], xs[2], xs[3]);
                 // The pair's row tile has up to 256 tokens; keys only some of them see lie after the first
                 // token, or leave the first tokens' windows: 256 bits by the distance, of either kind.
-                const int bit = (key > t.p0 ? key - t.p0 - 1 : key - (max(t.p0, 0) - a.window + 1)) & 255;
+                const int bit = (key > t.p0 ? key - t.p0 - 1 : key - (least_position(t) - a.window + 1)) & 255;
                 const uint32_t to = smem_u32(&odd[item_no % 3 * 8 + (bit >> 5)]), mark = 1u << (bit & 31);
                 or_shared(mapa_shared(to, 0), mark);
                 or_shared(mapa_shared(to, 1), mark);
@@ -1167,7 +1231,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_pv();
             tc_fence_after();
             const int k0 = tile_at(i0 + j) * KT + half * 64;
-            const unsigned long long seen = low_bits(p + 1 - k0) & ~(low_bits(lo - k0) & ~low_bits(a.sinks - k0));
+            unsigned long long seen;
+            if constexpr (kTree) seen = is_masked(tile_at(i0 + j)) ? tree_seen(a, t, tok, k0) : ~0ull;
+            else seen = low_bits(p + 1 - k0) & ~(low_bits(lo - k0) & ~low_bits(a.sinks - k0));
             row = far_weights<C::DV / 2>(row, tmem + lanes + 256 + (tile_no & 1) * KT, tmem + lanes + half * (C::DV / 2),
                                          scales + (tile_no & 1) * 2 * KT + half * 64, seen, qs, &exch[r], &vexch[r], half,
                                          quarter, j == 0);
@@ -1282,7 +1348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_first(o_free);
         }
         if constexpr (!E4M3) {
-          if (cleared && live) put_back(it, head, vhalf * C::DV + col, it.p0 + tok, no, o);
+          if (cleared && live) put_back(it, head, vhalf * C::DV + col, tok, no, o);
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
@@ -1629,7 +1695,15 @@ cudaError_t setup(int* pairs) {
 
 }  // namespace
 
-cudaError_t kv_chunk_setup(int* pairs) {
+#if KV_TREE
+#define KV_CHUNK_SETUP kv_tree_chunk_setup
+#define KV_CHUNK_LAUNCH launch_kv_tree_chunk
+#else
+#define KV_CHUNK_SETUP kv_chunk_setup
+#define KV_CHUNK_LAUNCH launch_kv_chunk
+#endif
+
+cudaError_t KV_CHUNK_SETUP(int* pairs) {
   *pairs = kChunkMaxPairs;
   cudaError_t e = setup<128, false>(pairs);
   if (e == cudaSuccess) e = setup<256, false>(pairs);
@@ -1640,7 +1714,7 @@ cudaError_t kv_chunk_setup(int* pairs) {
   return e;
 }
 
-cudaError_t launch_kv_chunk(const KvAttn& a, int pairs, cudaStream_t s) {
+cudaError_t KV_CHUNK_LAUNCH(const KvAttn& a, int pairs, cudaStream_t s) {
   switch (a.c.head_dim * 2 + a.c.e4m3) {
     case 256: return launch<128, false>(a, pairs, s);
     case 257: return launch<128, true>(a, pairs, s);

@@ -1,0 +1,303 @@
+// rotary.cu — rotary positions with one or several axes, on queries and keys in one launch.
+//
+// Pair i of a head turns by the angle positions[axis[i], token] * freq[i]. Each value is read and written once (4 bytes
+// meet 3 operations), so HBM bounds it, or the launch where tokens are few. A CTA takes a token: its threads first
+// load the pairs of all heads that are theirs, then form the token's cosines and sines, each once, in shared
+// memory, while the loads are under way, and turn the pairs.
+//
+// Angles. In fp32 a position of a million leaves a tenth of a radian unknown, and in fp64 an angle would cost more
+// than the rest. Here a frequency is a fraction of a turn in 64-bit fixed point: its product with the position, modulo
+// 2^64, is the angle modulo a turn, and its upper 32 bits, as a signed number, the angle in (-1/2, 1/2] turns to
+// 2^-33, which sincospif takes.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "internal.h"
+#include "moe_ffn.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kAtOnce = 4;  // items of a thread whose loads are under way together
+
+struct Rows {
+  const uint16_t* in;
+  uint16_t* out;
+  long long in_token, in_head, out_token, out_head;
+};
+
+struct RotaryParams {
+  Rows q, k;
+  const moe_ffn_rotary_pair* table;
+  const int32_t* positions;
+  long long positions_stride;
+  float scale;
+  float sign;
+  int pairs, axes, head_dim, q_heads, k_heads;
+  int copy;  // elements after the pairs are to be copied
+};
+
+template <int VEC>
+struct Vec;
+template <>
+struct Vec<8> {
+  using T = uint4;
+};
+template <>
+struct Vec<4> {
+  using T = uint2;
+};
+
+template <int VEC>
+__device__ __forceinline__ void unpack(const typename Vec<VEC>::T& v, float (&f)[VEC]) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ typename Vec<VEC>::T pack(const float (&f)[VEC]) {
+  typename Vec<VEC>::T v;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return v;
+}
+
+// VEC: bf16 values of a vector. An item is a head's vector of first elements and the one of second elements, or,
+// interleaved, two neighbouring vectors' worth of pairs; after the pairs' items come those of the rest of a head,
+// two vectors each where they go.
+template <int VEC, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
+  using V = typename Vec<VEC>::T;
+  __shared__ float2 cs[MOE_FFN_ROTARY_MAX_PAIRS];
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long token = blockIdx.x;
+  const int turned = p.pairs / VEC;                                             // items of a head's pairs
+  const int rest = p.copy ? (p.head_dim - 2 * p.pairs) / VEC : 0;               // and vectors after them
+  const int per = turned + (rest + 1) / 2;
+  const int items = (p.q_heads + p.k_heads) * per;
+  bool ready = false;
+  for (int base = threadIdx.x;; base += kAtOnce * kThreads) {
+    V a[kAtOnce], b[kAtOnce];
+    uint16_t *to_a[kAtOnce], *to_b[kAtOnce];
+    int at[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int item = base + j * kThreads;
+      at[j] = -1;
+      to_a[j] = to_b[j] = nullptr;
+      if (item >= items) continue;
+      int head = item / per;
+      const int i = item - head * per;
+      const bool key = head >= p.q_heads;
+      if (key) head -= p.q_heads;
+      const Rows& r = key ? p.k : p.q;
+      int x, y;  // elements where the two vectors begin
+      if (i < turned) {
+        at[j] = i * VEC;
+        x = INTERLEAVED ? 2 * i * VEC : i * VEC;
+        y = INTERLEAVED ? x + VEC : x + p.pairs;
+      } else {
+        x = 2 * p.pairs + 2 * (i - turned) * VEC;
+        y = x + VEC;
+      }
+      const bool two = y + VEC <= p.head_dim;
+      const uint16_t* from = r.in + token * r.in_token + head * r.in_head;
+      uint16_t* to = r.out + token * r.out_token + head * r.out_head;
+      a[j] = *reinterpret_cast<const V*>(from + x);
+      to_a[j] = to + x;
+      if (two) {
+        b[j] = *reinterpret_cast<const V*>(from + y);
+        to_b[j] = to + y;
+      }
+    }
+    if (!ready) {
+      for (int i = threadIdx.x; i < p.pairs; i += kThreads) {
+        const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(p.table + i);
+        const int axis = e.y < static_cast<unsigned long long>(p.axes) ? static_cast<int>(e.y) : 0;
+        const long long pos = p.positions[axis * p.positions_stride + token];
+        const unsigned long long turns = e.x * static_cast<unsigned long long>(pos);
+        // The nearest number of 2^-32 turns; two of them to a half.
+        const int near = static_cast<int>((turns + 0x80000000ull) >> 32);
+        float s, c;
+        sincospif(static_cast<float>(near) * 0x1p-31f, &s, &c);
+        cs[i] = make_float2(c * p.scale, s * p.scale * p.sign);
+      }
+      __syncthreads();
+      ready = true;
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (!to_a[j]) continue;
+      if (at[j] >= 0) {
+        float f[VEC], g[VEC];
+        unpack<VEC>(a[j], f);
+        unpack<VEC>(b[j], g);
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int i = 0; i < VEC / 2; ++i) {
+            const float2 u = cs[at[j] + i], w = cs[at[j] + VEC / 2 + i];
+            const float f0 = f[2 * i], g0 = g[2 * i];
+            f[2 * i] = f0 * u.x - f[2 * i + 1] * u.y;
+            f[2 * i + 1] = f[2 * i + 1] * u.x + f0 * u.y;
+            g[2 * i] = g0 * w.x - g[2 * i + 1] * w.y;
+            g[2 * i + 1] = g[2 * i + 1] * w.x + g0 * w.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float2 u = cs[at[j] + i];
+            const float f0 = f[i];
+            f[i] = f0 * u.x - g[i] * u.y;
+            g[i] = g[i] * u.x + f0 * u.y;
+          }
+        }
+        a[j] = pack<VEC>(f);
+        b[j] = pack<VEC>(g);
+      }
+      *reinterpret_cast<V*>(to_a[j]) = a[j];
+      if (to_b[j]) *reinterpret_cast<V*>(to_b[j]) = b[j];
+    }
+    if (base - static_cast<int>(threadIdx.x) + kAtOnce * kThreads >= items) break;
+  }
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// [tokens, heads, dim] bf16 values, in bytes.
+struct Extent {
+  uintptr_t at;
+  long long token, head;
+};
+
+Extent extent(const moe_ffn_kv_rows& r, int tokens, int heads) {
+  return {reinterpret_cast<uintptr_t>(r.ptr), tokens > 1 ? 2 * r.token_stride : 0, heads > 1 ? 2 * r.head_stride : 0};
+}
+
+bool apart_modulo(uintptr_t a, long long an, uintptr_t b, long long bn, long long s) {
+  if (s < an + bn) return false;
+  const long long d = a <= b ? static_cast<long long>((b - a) % s) : (s - static_cast<long long>((a - b) % s)) % s;
+  return d >= an && s - d >= bn;
+}
+
+// Whether two tensors certainly have no byte in common: one lies before the other, or their tokens (or heads) lie
+// between each other's, at one stride.
+bool apart(const Extent& a, int a_heads, const Extent& b, int b_heads, int tokens, int dim) {
+  const long long row = 2LL * dim;
+  const long long an = (a_heads - 1) * a.head + row, bn = (b_heads - 1) * b.head + row;  // a token's
+  const long long at = (tokens - 1) * a.token, bt = (tokens - 1) * b.token;
+  if (a.at + at + an <= b.at || b.at + bt + bn <= a.at) return true;
+  if (tokens > 1 && a.token == b.token && a.token > 0 && apart_modulo(a.at, an, b.at, bn, a.token)) return true;
+  return a_heads > 1 && b_heads > 1 && a.head == b.head && a.head > 0 && apart_modulo(a.at, at + row, b.at, bt + row, a.head);
+}
+
+bool own_rows_apart(const Extent& e, int tokens, int heads, int dim) {
+  const long long row = 2LL * dim;
+  if (heads > 1 && e.head < row) return false;
+  if (tokens > 1 && e.token < row) return false;
+  return heads <= 1 || tokens <= 1 || e.token >= (heads - 1) * e.head + row || e.head >= (tokens - 1) * e.token + row;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+extern "C" int moe_ffn_rotary_table(const double* freq, const int* axis, int pairs, moe_ffn_rotary_pair* table) {
+  if (!freq || !axis || !table || pairs < 1 || pairs > MOE_FFN_ROTARY_MAX_PAIRS) return MOE_FFN_EINVAL;
+  for (int i = 0; i < pairs; ++i)
+    if (!std::isfinite(freq[i]) || axis[i] < 0 || axis[i] >= MOE_FFN_ROTARY_MAX_AXES) return MOE_FFN_EINVAL;
+  for (int i = 0; i < pairs; ++i) {
+    const double turns = std::fmod(std::fabs(freq[i]) / 6.283185307179586476925, 1.0);  // in [0, 1)
+    const uint64_t t = static_cast<uint64_t>(std::ldexp(turns, 64));
+    table[i].turn = freq[i] < 0.0 ? 0 - t : t;
+    table[i].axis = static_cast<uint64_t>(axis[i]);
+  }
+  return MOE_FFN_OK;
+}
+
+extern "C" int moe_ffn_rotary_apply(const moe_ffn_rotary* a, const moe_ffn_kv_rows* q, const moe_ffn_kv_rows* k,
+                                    const moe_ffn_kv_rows* q_out, const moe_ffn_kv_rows* k_out, void* stream) {
+  using namespace moe;
+  if (!a || a->tokens < 0 || a->pairs < 4 || a->pairs > MOE_FFN_ROTARY_MAX_PAIRS || a->pairs % 4 != 0 ||
+      a->head_dim < 8 || a->head_dim > 1024 || a->head_dim % 8 != 0 || 2 * a->pairs > a->head_dim || a->axes < 1 ||
+      a->axes > MOE_FFN_ROTARY_MAX_AXES || a->q_heads < 0 || a->q_heads > 1024 || a->k_heads < 0 || a->k_heads > 1024 ||
+      !std::isfinite(a->scale) || a->positions_stride < 0)
+    return MOE_FFN_EINVAL;
+  if (a->tokens == 0 || a->q_heads + a->k_heads == 0) return MOE_FFN_OK;
+  if (!a->table || !a->positions) return MOE_FFN_EINVAL;
+  if (off16(a->table) || (reinterpret_cast<uintptr_t>(a->positions) & 3u) != 0) return MOE_FFN_EALIGN;
+  const moe_ffn_kv_rows* given[2][2] = {{q, q_out}, {k, k_out}};
+  const int heads[2] = {a->q_heads, a->k_heads};
+  Extent ins[2], outs[2];
+  bool in_place[2] = {false, false};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    for (const moe_ffn_kv_rows* r : given[i]) {
+      if (!r || !r->ptr || r->token_stride < 0 || r->head_stride < 0) return MOE_FFN_EINVAL;
+      if (off16(r->ptr) || r->token_stride % 8 != 0 || r->head_stride % 8 != 0) return MOE_FFN_EALIGN;
+    }
+    ins[i] = extent(*given[i][0], a->tokens, heads[i]);
+    outs[i] = extent(*given[i][1], a->tokens, heads[i]);
+    in_place[i] = ins[i].at == outs[i].at && ins[i].token == outs[i].token && ins[i].head == outs[i].head;
+    if (!own_rows_apart(outs[i], a->tokens, heads[i], a->head_dim)) return MOE_FFN_EINVAL;
+  }
+  const size_t table_bytes = a->pairs * sizeof(moe_ffn_rotary_pair);
+  const size_t positions_bytes = ((a->axes - 1) * a->positions_stride + a->tokens) * sizeof(int32_t);
+  for (int o = 0; o < 2; ++o) {
+    if (heads[o] == 0) continue;
+    for (int i = 0; i < 2; ++i) {
+      if (heads[i] == 0) continue;
+      if (!(i == o && in_place[i]) && !apart(outs[o], heads[o], ins[i], heads[i], a->tokens, a->head_dim))
+        return MOE_FFN_EINVAL;
+      if (i != o && !apart(outs[o], heads[o], outs[i], heads[i], a->tokens, a->head_dim)) return MOE_FFN_EINVAL;
+    }
+    const uintptr_t end = outs[o].at + (a->tokens - 1) * outs[o].token + (heads[o] - 1) * outs[o].head + 2 * a->head_dim;
+    const uintptr_t t = reinterpret_cast<uintptr_t>(a->table), x = reinterpret_cast<uintptr_t>(a->positions);
+    if ((t < end && outs[o].at < t + table_bytes) || (x < end && outs[o].at < x + positions_bytes)) return MOE_FFN_EINVAL;
+  }
+  RotaryParams p = {};
+  Rows* rows[2] = {&p.q, &p.k};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    rows[i]->in = static_cast<const uint16_t*>(given[i][0]->ptr);
+    rows[i]->out = static_cast<uint16_t*>(const_cast<void*>(given[i][1]->ptr));
+    rows[i]->in_token = given[i][0]->token_stride;
+    rows[i]->in_head = given[i][0]->head_stride;
+    rows[i]->out_token = given[i][1]->token_stride;
+    rows[i]->out_head = given[i][1]->head_stride;
+    if (!in_place[i]) p.copy = 1;
+  }
+  p.table = a->table;
+  p.positions = a->positions;
+  p.positions_stride = a->positions_stride;
+  p.scale = a->scale;
+  p.sign = a->inverse ? -1.0f : 1.0f;
+  p.pairs = a->pairs;
+  p.axes = a->axes;
+  p.head_dim = a->head_dim;
+  p.q_heads = a->q_heads;
+  p.k_heads = a->k_heads;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(a->tokens), block(kThreads);
+  // Vectors of 16 bytes where the second elements of the pairs begin at a multiple of that, of 8 else.
+  cudaError_t e;
+  if (a->pairs % 8 == 0)
+    e = a->interleaved ? launch_pdl(rotary_kernel<8, true>, grid, block, 0, s, p)
+                       : launch_pdl(rotary_kernel<8, false>, grid, block, 0, s, p);
+  else
+    e = a->interleaved ? launch_pdl(rotary_kernel<4, true>, grid, block, 0, s, p)
+                       : launch_pdl(rotary_kernel<4, false>, grid, block, 0, s, p);
+  return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
+}

@@ -1,0 +1,223 @@
+"""The beam search's selection on a GB300 against its definition in 64 bits: beams and tokens are equal, scores
+are off by half a step of fp32 (2^-24) and the 1e-7 that the sums are held to."""
+import math
+
+import pytest
+import torch
+
+from mixture_experts_ffn_router_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.lib()
+
+
+def _wanted(logits, scores, count, finished=None, end=0):
+    U, K = scores.shape
+    x = logits.reshape(U, K, -1).double()
+    V = x.shape[-1]
+    x = torch.log_softmax(x, -1)
+    if finished is not None:
+        one = torch.full((V,), -math.inf, dtype=torch.float64, device=x.device)
+        one[end] = 0.0
+        x = torch.where(finished[..., None], one, x)
+    x = (x + scores.double()[..., None]).view(U, K * V)
+    x = torch.where(x > -math.inf, x, -math.inf)  # NaN is none
+    best, at = torch.sort(x, dim=1, descending=True, stable=True)
+    best, at = best[:, :count], at[:, :count]
+    short = count - best.shape[1]
+    if short > 0:
+        best = torch.cat((best, torch.full((U, short), -math.inf, device=x.device, dtype=torch.float64)), 1)
+        at = torch.cat((at, torch.zeros(U, short, dtype=at.dtype, device=x.device)), 1)
+    none = best == -math.inf
+    return best, (at // V).masked_fill(none, -1).int(), (at % V).masked_fill(none, -1).int()
+
+
+def _check(logits, scores, count, finished=None, end=0, search=None, vocab=None):
+    U, K = scores.shape
+    search = search or B.BeamSearch(U, K, logits.shape[-1], count)
+    got = search.select(logits, scores, finished=finished, end_token=end)
+    torch.cuda.synchronize()
+    want = _wanted(logits, scores, count, finished, end)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    inf = torch.isinf(want[0])
+    assert torch.equal(torch.isinf(got[0]), inf)
+    off = (got[0].double() - want[0]).abs() - 2.0 ** -24 * want[0].abs() - 1e-7
+    assert inf.all() or off[~inf].max() <= 0
+    return got
+
+
+def _inputs(U, K, V, seed=0, dtype=torch.bfloat16, spread=3.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(U * K, V, generator=g, device="cuda") * spread
+    return x.to(dtype), -6 * torch.rand(U, K, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("U,K,V,C", [(1, 1, 1, 1), (1, 1, 5, 8), (2, 3, 7, 16), (3, 4, 1000, 8), (1, 4, 32001, 8), (5, 2, 8191, 4),
+                                     (2, 5, 8193, 10), (1, 64, 777, 64), (70, 1, 501, 3), (2, 8, 262144, 16),
+                                     (1, 1, 262144, 64), (1, 2, 1500000, 5)])
+def test_sizes(U, K, V, C, dtype):
+    logits, scores = _inputs(U, K, V, seed=U + K + V, dtype=dtype)
+    _check(logits, scores, C)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("spread", [0.0, 0.01, 1.0, 30.0, 1000.0])
+def test_spreads(dtype, spread):
+    """From rows of one value, where the lowest tokens win, to rows of which one token holds all the weight."""
+    logits, scores = _inputs(2, 3, 40000, seed=int(spread) + 9, dtype=dtype, spread=spread)
+    _check(logits, scores, 12)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("count", [1, 7, 64])
+def test_orders_that_fill_the_list(dtype, count):
+    """Logits that ascend (each tile's are above all before), descend, or are mostly equal."""
+    V = 120000
+    up = torch.linspace(-400, 500, V, device="cuda")
+    steps = torch.floor(up / 100)
+    two = torch.where(torch.arange(V, device="cuda") % 3 == 0, 1.0, 2.0)
+    logits = torch.stack((up, up.flip(0), steps, two, torch.zeros_like(up), -torch.zeros_like(up))).to(dtype)
+    scores = torch.tensor([[0.0, -0.5], [-1.0, -1.0], [-2.0, -2.0]], device="cuda")
+    _check(logits, scores, count)
+
+
+def test_ties():
+    """Equal beams: the lower beam first, then the lower token; zeros of either sign are equal."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    row = torch.randint(-8, 9, (50000,), generator=g, device="cuda").float()
+    logits = row.to(torch.bfloat16).expand(4, 50000).contiguous()
+    _check(logits, torch.full((1, 4), -1.5, device="cuda"), 64)
+    z = torch.zeros(2, 20000, device="cuda")
+    z[:, ::2] = -0.0
+    z[:, 5000:] = -1.0
+    _check(z, torch.zeros(1, 2, device="cuda"), 40)
+    _check(z.to(torch.bfloat16), torch.zeros(1, 2, device="cuda"), 40)
+
+
+def test_first_step_and_finished_beams():
+    logits, scores = _inputs(3, 4, 9000, seed=5)
+    scores[:, 1:] = -math.inf
+    _check(logits, scores, 8)
+    logits, scores = _inputs(3, 4, 9000, seed=6)
+    finished = torch.tensor([[True, False, False, True], [False] * 4, [True] * 4], device="cuda")
+    logits[0] = math.nan  # a finished beam's logits are not looked at
+    for end in (0, 8999, 17):
+        got = _check(torch.where(torch.isnan(logits), 0, logits), scores, 8, finished, end)
+        same = B.BeamSearch(3, 4, 9000, 8).select(logits, scores, finished, end)
+        assert all(torch.equal(a, b) for a, b in zip(got, same))
+        assert (got[1][2, 4:] == -1).all() and (got[2][2, :4] == end).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [300, 20000, 120001])
+def test_masked_logits(dtype, V):
+    """-infinity and the type's lowest value where a token is forbidden, up to all of them."""
+    low = torch.finfo(dtype).min
+    for value in (-math.inf, low):
+        logits, scores = _inputs(2, 3, V, seed=V, dtype=dtype)
+        g = torch.Generator(device="cuda").manual_seed(7)
+        forbidden = torch.rand(logits.shape, generator=g, device="cuda") < 0.999
+        forbidden[1] = True
+        forbidden[1, V // 2] = False
+        forbidden[2] = True
+        forbidden[3, : V - 2] = True
+        logits[forbidden] = value
+        if value == low:
+            # What 64 bits leave of low + log V is low.
+            _check(torch.cat((logits[:2], logits[3:4])).contiguous(), scores[:1].contiguous(), 2)
+            rows = logits[2:3].contiguous()
+            out = B.BeamSearch(1, 1, V, 5).select(rows, torch.zeros(1, 1, device="cuda"))
+            assert (out[2] == torch.arange(5, device="cuda")).all() and (out[0] + math.log(V)).abs().max() < 1e-5
+        else:
+            _check(logits, scores, 10)
+
+
+def test_a_beam_with_nan_or_infinity_has_no_continuations():
+    logits, scores = _inputs(1, 3, 30000, seed=8)
+    logits[0, 29999] = math.nan
+    logits[2, 5] = math.inf
+    got = _check(logits, scores, 6)
+    assert (got[1] == 1).all()
+    scores[0, 1] = math.nan
+    got = _check(logits, scores, 6)
+    assert (got[1] == -1).all() and (got[0] == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_at_any_address(dtype):
+    wide = torch.full((6, 5023), 99.0, dtype=dtype, device="cuda")
+    for shift in range(9):
+        logits, scores = _inputs(2, 3, 5003, seed=shift, dtype=dtype)
+        view = wide[:, shift:shift + 5003]
+        view.copy_(logits)
+        search = B.BeamSearch(2, 3, 5003, 7)
+        got = search.select(view, scores)
+        want = _check(logits, scores, 7)
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        wide.fill_(99.0)
+    one = _inputs(1, 1, 5003, seed=1, dtype=dtype)[0].expand(6, 5003)
+    _check(one, torch.arange(6.0, device="cuda").view(2, 3), 7)
+
+
+def test_three_dimensions_and_steps():
+    logits, scores = _inputs(4, 3, 700, seed=9)
+    search = B.BeamSearch(4, 3, 700, 6)
+    a = search.select(logits, scores)
+    b = search.select(logits.view(4, 3, 700), scores)
+    wide = torch.zeros(4, 3, 2, 700, dtype=torch.bfloat16, device="cuda")
+    wide[:, :, 1] = logits.view(4, 3, 700)
+    c = search.select(wide[:, :, 1], scores)
+    for x, y, z in zip(a, b, c):
+        assert torch.equal(x, y) and torch.equal(x, z)
+
+
+def test_captured_and_on_other_streams():
+    logits, scores = _inputs(2, 4, 50000, seed=10)
+    other, other_scores = _inputs(2, 4, 50000, seed=11)
+    search = B.BeamSearch(2, 4, 50000, 8)
+    want, later = (B.BeamSearch(2, 4, 50000, 8).select(a, b) for a, b in ((logits, scores), (other, other_scores)))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(9):
+        with torch.cuda.stream(streams[i % 3]):
+            got.append(search.select(*((logits, scores) if i % 2 == 0 else (other, other_scores))))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        held = search.select(logits, scores)
+    logits.copy_(other)
+    scores.copy_(other_scores)
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want if i % 2 == 0 else later))
+    assert all(torch.equal(x, y) for x, y in zip(held, later))
+
+
+def test_refusals():
+    for sizes in ((-1, 4, 100, 8), (4097, 4, 100, 8), (2, 0, 100, 8), (2, 65, 100, 8), (2, 4, 0, 8), (2, 4, (1 << 24) + 1, 8),
+                  (2, 4, 100, 0), (2, 4, 100, 65)):
+        with pytest.raises(ValueError, match="invalid"):
+            B.BeamSearch(*sizes)
+    search = B.BeamSearch(2, 4, 100, 8)
+    logits, scores = _inputs(2, 4, 100)
+    for args, match in (((logits.half(), scores), "bfloat16"), ((logits[:7], scores), "shape"), ((logits.T.contiguous().T, scores), "rows"),
+                        ((logits, scores.double()), "scores"), ((logits, scores.T.contiguous().T), "scores"),
+                        ((logits, scores, scores), "finished"), ((logits, scores.cpu()), "scores must be on"),
+                        ((torch.zeros(4, 2, 100, device="cuda", dtype=torch.bfloat16).transpose(0, 1), scores), "one stride")):
+        with pytest.raises(ValueError, match=match):
+            search.select(*args)
+    done = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    for end in (-1, 100):
+        with pytest.raises(B.MoeFFNError):
+            search.select(logits, scores, done, end)
+    empty = B.BeamSearch(0, 4, 100, 8).select(logits[:0], scores[:0])
+    assert all(t.shape == (0, 8) for t in empty)

@@ -1,0 +1,214 @@
+"""Refusals of the norms, rotary positions, trees, kept paths, beams and their selection, and their structures' layout,
+without a GPU: every call here fails its checks before it touches a pointer."""
+import ctypes
+import math
+import os
+import subprocess
+from fractions import Fraction
+
+import pytest
+import torch
+
+from mixture_experts_ffn_router_gb300 import binding as B
+from mixture_experts_ffn_router_gb300 import build as cuda_build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+AT = 1 << 20  # an address that is never looked at
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    cuda_build.build()
+
+
+def test_layouts_and_limits_match_the_header(tmp_path):
+    names = ("moe_ffn_norm", "moe_ffn_rotary_pair", "moe_ffn_rotary", "moe_ffn_beam")
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "moe_ffn.h"', "int main(void){"]
+    for st in names:
+        lines.append('printf("%s %%zu\\n", sizeof(%s));' % (st, st))
+        for f, _ in getattr(B, st)._fields_:
+            lines.append('printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (st, f, st, f))
+    lines.append('printf("limits %d %d %d %d\\n", MOE_FFN_KV_TREE_NODES, MOE_FFN_BEAM_MAX, MOE_FFN_ROTARY_MAX_PAIRS, '
+                 'MOE_FFN_ROTARY_MAX_AXES);return 0;}')
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines))
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    got = dict(l.split(" ", 1) for l in out.strip().split("\n"))
+    for st in names:
+        cls = getattr(B, st)
+        assert int(got[st]) == ctypes.sizeof(cls), st
+        for f, _ in cls._fields_:
+            assert int(got["%s.%s" % (st, f)]) == getattr(cls, f).offset, (st, f)
+    assert got["limits"] == "%d %d %d %d" % (B.KV_TREE_NODES, B.BEAM_MAX, B.ROTARY_MAX_PAIRS, B.ROTARY_MAX_AXES)
+
+
+# ------------------------------------------------------------------ norms
+
+def _norm(**change):
+    a = dict(x=AT, block=2 * AT, gate=None, post=3 * AT, pre=4 * AT, y=5 * AT, n=6 * AT, x_stride=64, block_stride=64,
+             gate_stride=0, y_stride=64, n_stride=64, scale=1.0, eps=1e-6, tokens=4, hidden=64)
+    a.update(change)
+    return B.moe_ffn_norm(**a)
+
+
+@pytest.mark.parametrize("change", [
+    dict(tokens=-1), dict(hidden=0), dict(hidden=12), dict(hidden=16392), dict(eps=0.0), dict(eps=-1e-6), dict(eps=math.nan),
+    dict(eps=math.inf), dict(scale=math.nan), dict(scale=math.inf), dict(x=None), dict(y=None, n=None, pre=None), dict(pre=None),
+    dict(n=None), dict(block=None), dict(block=None, post=None, gate=AT), dict(x_stride=-8), dict(block_stride=-8),
+    dict(gate_stride=-8), dict(y_stride=56), dict(n_stride=0),
+    dict(y=AT + 16), dict(y=AT, x_stride=72), dict(n=5 * AT), dict(n=5 * AT + 64 * 3), dict(y=3 * AT + 128), dict(n=4 * AT),
+    dict(gate=5 * AT, gate_stride=64), dict(gate=6 * AT + 16), dict(y=AT + 64, y_stride=64, x_stride=128)])
+def test_norm_refusals(change):
+    assert B.moe_ffn_block_norm(_norm(**change), None) == B.MOE_FFN_EINVAL
+
+
+@pytest.mark.parametrize("change", [dict(x=AT + 8), dict(block=AT + 2), dict(post=AT + 4), dict(pre=AT + 4), dict(y=AT + 8), dict(n=AT + 8),
+                                    dict(gate=AT + 8), dict(x_stride=68), dict(y_stride=68), dict(gate=7 * AT, gate_stride=4)])
+def test_norm_alignment(change):
+    assert B.moe_ffn_block_norm(_norm(**change), None) == B.MOE_FFN_EALIGN
+
+
+def test_norm_of_nothing():
+    assert B.lib().moe_ffn_block_norm(None, None) == B.MOE_FFN_EINVAL
+    assert B.moe_ffn_block_norm(_norm(tokens=0, x=None, y=None), None) == B.MOE_FFN_OK
+    with pytest.raises(ValueError, match="CUDA"):
+        B.block_norm(torch.zeros(2, 64, dtype=torch.bfloat16))
+
+
+# ------------------------------------------------------------------ rotary positions
+
+def test_turns_are_exact_fractions():
+    """The table's turns against the frequency over 2 pi in exact arithmetic (pi to 60 digits): the quotient is a double's, good
+    to 2^-51 of itself, then truncated to 2^-64."""
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494")
+    freqs = [1.0, 1e4 ** -0.5, 1e-6, -0.3, 6.283185307179586, 12345.678, 0.0, 1e300, 5e-324, -1e-9]
+    for (turn, axis), f, a in zip(B.moe_ffn_rotary_table(freqs, [i % 8 for i in range(10)]), freqs, range(10)):
+        assert axis == a % 8
+        if abs(f) > 1e20:
+            continue  # no digit of the fraction is left
+        exact = Fraction(f) / two_pi
+        off = (Fraction(turn, 1 << 64) - exact) % 1
+        off = min(off, 1 - off)
+        assert off <= abs(exact) / (1 << 51) + Fraction(1, 1 << 64)
+
+
+def test_tables_are_checked():
+    for freqs, axes in (([math.nan] * 4, [0] * 4), ([math.inf], [0]), ([1.0], [8]), ([1.0], [-1]), ([], []), ([1.0] * 513, [0] * 513)):
+        with pytest.raises(B.MoeFFNError):
+            B.moe_ffn_rotary_table(freqs, axes)
+    with pytest.raises(ValueError):
+        B.moe_ffn_rotary_table([1.0, 2.0], [0])
+    for n in (0, 6, 516):
+        with pytest.raises(ValueError, match="pairs"):
+            B.Rotary([1.0] * n)
+
+
+def _rotary(rows=None, **change):
+    a = dict(table=AT, positions=2 * AT, positions_stride=4, scale=1.0, pairs=32, axes=1, interleaved=0, inverse=0, tokens=4,
+             head_dim=64, q_heads=2, k_heads=1)
+    a.update(change)
+    r = {n: B.moe_ffn_kv_rows(AT * (3 + i), 64 * (2 - i % 2), 64) for i, n in enumerate(("q", "k", "q_out", "k_out"))}
+    for n, v in (rows or {}).items():
+        r[n] = None if v is None else B.moe_ffn_kv_rows(*v)
+    return B.moe_ffn_rotary_apply(B.moe_ffn_rotary(**a), r["q"], r["k"], r["q_out"], r["k_out"], None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(tokens=-1), dict(pairs=0), dict(pairs=6), dict(pairs=36), dict(pairs=516, head_dim=1032), dict(head_dim=60), dict(head_dim=1032),
+    dict(axes=0), dict(axes=9), dict(q_heads=-1), dict(k_heads=1025), dict(scale=math.nan), dict(positions_stride=-1), dict(table=None),
+    dict(positions=None), dict(rows=dict(q=None)), dict(rows=dict(k_out=None)), dict(rows=dict(q=(None, 128, 64))),
+    dict(rows=dict(q=(3 * AT, -128, 64))),
+    dict(rows=dict(q_out=(3 * AT + 128, 128, 64))),            # over the input, shifted
+    dict(rows=dict(q_out=(3 * AT, 256, 64))),                  # the same place, other strides
+    dict(rows=dict(q_out=(5 * AT, 64, 64))),                   # its own tokens overlap
+    dict(rows=dict(q_out=(5 * AT, 128, 0))),
+    dict(rows=dict(k_out=(5 * AT + 128, 64, 64))),             # over the other output
+    dict(rows=dict(q_out=(4 * AT, 128, 64))),                  # over the other input
+    dict(rows=dict(q_out=(AT, 128, 64))),                      # over the table
+    dict(rows=dict(k_out=(2 * AT - 16, 64, 64)))])             # over the positions
+def test_rotary_refusals(change):
+    assert _rotary(**change) == B.MOE_FFN_EINVAL
+
+
+@pytest.mark.parametrize("change", [dict(table=AT + 8), dict(positions=AT * 2 + 2), dict(rows=dict(q=(3 * AT + 8, 128, 64))),
+                                    dict(rows=dict(k_out=(6 * AT, 68, 64))), dict(rows=dict(k=(4 * AT, 64, 4)))])
+def test_rotary_alignment(change):
+    assert _rotary(**change) == B.MOE_FFN_EALIGN
+
+
+def test_rotary_of_nothing():
+    assert _rotary(tokens=0, table=None, rows=dict(q=None)) == B.MOE_FFN_OK
+    assert _rotary(q_heads=0, k_heads=0, table=None) == B.MOE_FFN_OK
+
+
+# ------------------------------------------------------------------ selection
+
+def _beam(workspace=10 * AT, nbytes=1 << 30, **change):
+    a = dict(logits=AT, logits_stride=100, scores=20 * AT, finished=None, out_scores=30 * AT, out_beams=31 * AT, out_tokens=32 * AT,
+             logits_fp32=0, end_token=0, users=2, beams=4, vocab=100, count=8)
+    a.update(change)
+    return B.moe_ffn_beam_select(B.moe_ffn_beam(**a), workspace, nbytes, None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(users=-1), dict(users=4097), dict(beams=0), dict(beams=65), dict(vocab=0), dict(vocab=(1 << 24) + 1), dict(count=0),
+    dict(count=65), dict(logits_stride=-1), dict(logits=None), dict(scores=None), dict(out_scores=None), dict(out_beams=None),
+    dict(out_tokens=None), dict(workspace=None), dict(finished=AT * 40, end_token=-1), dict(finished=AT * 40, end_token=100),
+    dict(out_beams=30 * AT + 60), dict(out_scores=20 * AT), dict(out_tokens=AT + 4), dict(out_tokens=10 * AT),
+    dict(finished=32 * AT + 1), dict(workspace=AT)])
+def test_selection_refusals(change):
+    assert _beam(**change) == B.MOE_FFN_EINVAL
+
+
+def test_selection_alignment_and_room():
+    for change in (dict(logits=AT + 1), dict(logits=AT + 2, logits_fp32=1), dict(scores=20 * AT + 2), dict(out_beams=31 * AT + 1),
+                   dict(workspace=10 * AT + 64)):
+        assert _beam(**change) == B.MOE_FFN_EALIGN
+    need = B.moe_ffn_beam_workspace_bytes(2, 4, 100, 8)
+    assert need > 0 and _beam(nbytes=need - 1) == B.MOE_FFN_ETOOBIG
+    assert _beam(users=0, logits=None) == B.MOE_FFN_OK
+    assert B.lib().moe_ffn_beam_select(None, None, 0, None) == B.MOE_FFN_EINVAL
+    for sizes in ((-1, 4, 100, 8), (4097, 1, 100, 8), (2, 65, 100, 8), (2, 4, 0, 8), (2, 4, 100, 0), (2, 4, 100, 65)):
+        assert B.moe_ffn_beam_workspace_bytes(*sizes) == 0
+        with pytest.raises(ValueError, match="invalid"):
+            B.BeamSearch(*sizes)
+    # The largest of each, and all of them together, have a size.
+    assert B.moe_ffn_beam_workspace_bytes(4096, 64, 1 << 24, 64) > 4096 * 64 * 64 * 8
+
+
+# ------------------------------------------------------------------ the cache's calls
+
+def test_calls_without_a_handle():
+    L = B.lib()
+    c, b, r = B.moe_ffn_kv_cache(), B.moe_ffn_kv_batch(), B.moe_ffn_kv_rows()
+    assert L.moe_ffn_kv_tree(None, b, None, None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_tree_attention(None, c, b, None, r, 1.0, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_tree_attention(None, c, None, None, r, 1.0, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_keep(None, c, 1, b, None, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_reorder(None, c, 1, None, 0, 0, None, None, 0, 1, None) == B.MOE_FFN_EINVAL
+
+
+def _stub():
+    """A PagedKV without a device: what its argument checks read."""
+    kv = B.PagedKV.__new__(B.PagedKV)
+    kv.ctx, kv.fmt, kv.device = 0, "bf16", torch.device("cuda", 0)
+    kv.q_heads, kv.kv_heads, kv.head_dim, kv.shape = 16, 8, 256, (10, 8, 64, 256)
+    kv.dtype, kv._kind = torch.bfloat16, None
+    return kv
+
+
+def test_arguments_of_the_cache_are_checked():
+    kv = _stub()
+    ids = lambda *shape: torch.zeros(shape, dtype=torch.int32)  # noqa: E731
+    batch = B.KVBatch.__new__(B.KVBatch)
+    batch.tensors, batch.device = (ids(3), ids(2), ids(2, 4)), kv.device
+    for call, match in ((lambda: kv.tree(batch, ids(5, 1)), "one dimension"), (lambda: kv.tree(batch, ids(5).long()), "int32"),
+                        (lambda: kv.tree(batch, ids(5)), "contiguous tensor on cuda"),
+                        (lambda: kv.keep([], batch, ids(2), ids(2)), "two dimensions"),
+                        (lambda: kv.keep([], batch, ids(3, 4), ids(2)), "nodes must be"),
+                        (lambda: kv.reorder([], ids(4, 2), ids(2), ids(4)), "two dimensions"),
+                        (lambda: kv.reorder([], ids(4, 2), ids(2), ids(2, 2).float()), "parents must be"),
+                        (lambda: kv.tree_attention(None, batch, B.KVTree(ids(5, 8), ids(5)), torch.zeros(4, 16, 256)), "tokens")):
+        with pytest.raises(ValueError, match=match):
+            call()
