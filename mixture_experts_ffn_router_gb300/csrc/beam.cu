@@ -3,20 +3,24 @@
 // A continuation's value is score + x - log sum exp(x) over its beam's logits x, so within a beam the order is the
 // logits' own: one pass over a beam's logits yields both its sum of exponentials and its `count` largest, and a
 // second kernel compares the beams' best. The logits are read once, two or four bytes for one exponential and
-// three operations; HBM bounds it where there are many beams, the launches and the last steps where there are few.
+// half a dozen operations; HBM bounds it where there are many beams, the launches and the last steps where there are few.
 //
 // The pass. A row's logits are cut into equal parts, a CTA each, so that few beams fill the GPU too. A CTA takes
-// tiles of 256 x 32 logits, the next one's loads under way. The first tile gives a threshold: at least `count` of
-// the 256 threads' maxima are not below it, so nothing below it counts, and what passes it later must be above it
-// (of equal logits the lower token wins). What passes is put into a list in shared memory, a few times `count` as a
-// rule; a list that grows long (logits that ascend, or many equal ones) is cut to the `count` best, which raise
-// the threshold, and tiles that could overfill it go through in four steps.
+// tiles of 256 x 4 vectors, the next one's loads under way. The first tile gives a threshold that at least `count` of
+// the 256 threads' maxima are above: nothing below it counts. A vector with something above it is noted, about `count`
+// of each tile as a rule, without a barrier; at the end these are looked through, and what is above the threshold is
+// ranked. Where that is more than the lists hold (logits that ascend, or many equal ones), the part is gone through again
+// in steps that the list has room for: when it is long, it is cut to the `count` best, which raise the threshold.
 //
-// Sums. exp(x - R) = 2^((x - R) log2 e) with the first tile's maximum as R, and log2 e in two parts. Sums of eight
-// go into a pair of fp32 numbers that keeps the rounding (D. E. Knuth, "The Art of Computer Programming" 2, 4.2.2,
-// Theorem B). The hardware's exponential is off by up to 2^-22 of a term: that averages out over many, but not where
-// one token holds most of the weight, so the selected logits' terms are exchanged for ones in fp64. log sum exp is
-// then good to about 1e-8, below which values of different beams seldom lie.
+// Sums. What is at most the threshold is added as exp(x - R) with R the first tile's maximum, by the hardware's
+// 2^x: that is off by up to 2^-22 of a term, which averages out over many small ones, and sums of 16 go into a pair of
+// fp32 numbers that keeps the rounding (D. E. Knuth, "The Art of Computer Programming" 2, 4.2.2, Theorem B). What is above
+// it may outweigh all else: the selected logits' terms are formed in such pairs, by the exponential's series, the
+// others' are added as integers, whose sum does not depend on the order in which they were noted. log sum exp is then
+// good to about 1e-8, below which values of different beams seldom lie, and equal rows have equal sums wherever they lie.
+//
+// fp64 is slow here (an operation takes a warp 16 cycles or more, and its result some 60): only the last comparisons
+// are made in it.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -31,14 +35,16 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerThread = 32;               // logits of a tile
-constexpr int kTile = kThreads * kPerThread;
-constexpr int kSteps = 4;                    // of a tile that could overfill the list
+constexpr int kVecs = 4;                     // 16-byte vectors of a thread in a tile
+constexpr int kNoted = 1024;                 // vectors
 constexpr int kList = 4096;
-constexpr int kListLong = kList - kTile / kSteps;
+constexpr int kListLong = kList - kThreads * 8 - 32;  // what still has room for a vector of each thread, and the ends
 constexpr int kMaxSplits = 64;
 constexpr int kMaxCount = MOE_FFN_BEAM_MAX;
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinHeld = 2048;  // candidates
+constexpr int kJoinList = 512;
 
 struct BeamParams {
   const void* logits;
@@ -48,12 +54,12 @@ struct BeamParams {
   float* out_scores;
   int32_t* out_beams;
   int32_t* out_tokens;
-  double* part_sum;       // [rows, splits] sums, in units of exp(part_ref)
+  float2* part_sum;       // [rows, splits] sums in two numbers, in units of exp(part_ref)
   float* part_ref;
   float* part_x;          // [rows, splits, count] the part's largest logits, best first
   int32_t* part_token;    // and their tokens, -1 for none
   int end_token, beams, vocab, count, splits;
-  int part;               // logits of a part, a multiple of 8
+  int part;               // vectors of a part
 };
 
 // fp32 numbers in an order of unsigned integers.
@@ -63,6 +69,11 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float from_ordered(uint32_t o) {
   return __uint_as_float(o ^ (o & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x));
+  return u ^ (u >> 63 ? ~0ull : 1ull << 63);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -80,7 +91,70 @@ __device__ __forceinline__ float term(float x, float ref) {
   return exp2_approx(fmaf(d, kLog2eLow, __fmul_rn(d, kLog2eHigh)));
 }
 
-// A sum in two fp32 numbers.
+__device__ __forceinline__ unsigned long long two(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The same of eight numbers, two at a time.
+__device__ __forceinline__ void terms(const float (&x)[8], float ref, float (&e)[8]) {
+  const unsigned long long r2 = two(-ref, -ref), high = two(kLog2eHigh, kLog2eHigh), low = two(kLog2eLow, kLog2eLow);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const unsigned long long d = add2(two(x[i], x[i + 1]), r2);
+    unsigned long long t;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(d), "l"(high));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(d), "l"(low), "l"(t));
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(t));
+    e[i] = exp2_approx(a);
+    e[i + 1] = exp2_approx(b);
+  }
+}
+
+// Distances below a maximum in 256 bins, eight to a factor of two, from 2^-20 to 2^12; NaN and what is further is in the last.
+constexpr int kBins = 256;
+constexpr int kBinShift = 20, kBinFirst = (127 - 20) << 3;
+__device__ __forceinline__ int bin_of(float d) {
+  return min(max(static_cast<int>(__float_as_uint(d) >> kBinShift) - kBinFirst, 0), kBins - 1);
+}
+// What all distances in bins up to b are below; infinity for the last.
+__device__ __forceinline__ float bin_end(int b) {
+  return b == kBins - 1 ? INFINITY : __uint_as_float(static_cast<uint32_t>(b + 1 + kBinFirst) << kBinShift);
+}
+// The first bin up to which there are at least `count`, or the last; for a whole warp.
+__device__ __forceinline__ int bin_reached(const int* bins, int count) {
+  const int lane = threadIdx.x & 31;
+  const int4 a = reinterpret_cast<const int4*>(bins)[2 * lane], b = reinterpret_cast<const int4*>(bins)[2 * lane + 1];
+  const int n[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  int upto = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) upto += n[i];
+  const int mine = upto;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += up;
+  }
+  int at = upto - mine, bin = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    at += n[i];
+    bin += at < count ? 1 : 0;
+  }
+  const unsigned reached = __ballot_sync(0xffffffffu, upto >= count);
+  if (reached == 0) return kBins - 1;
+  const int which = __ffs(reached) - 1;
+  return __shfl_sync(0xffffffffu, 8 * lane + bin, which);
+}
+
+// A number in two of fp32, the second what the first leaves of it; and operations that lose about 2^-46.
 struct Sum {
   float hi = 0.0f, lo = 0.0f;
   __device__ __forceinline__ void add(float v) {
@@ -88,7 +162,79 @@ struct Sum {
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
     hi = s;
   }
+  __device__ __forceinline__ void add(const Sum& o) {
+    add(o.hi);
+    lo = __fadd_rn(lo, o.lo);
+  }
+  // By a number near it in size, so that neither part is lost; and the first part the sum of both.
+  __device__ __forceinline__ void times(const Sum& o) {
+    const float h = __fmul_rn(hi, o.hi);
+    lo = fmaf(hi, o.hi, -h) + fmaf(hi, o.lo, lo * o.hi);
+    hi = h;
+    settle();
+  }
+  __device__ __forceinline__ void settle() {
+    const float s = __fadd_rn(hi, lo);
+    lo = __fsub_rn(lo, __fsub_rn(s, hi));
+    hi = s;
+  }
 };
+
+__device__ __forceinline__ Sum difference(float a, float b) {
+  Sum s;
+  s.hi = __fsub_rn(a, b);
+  const float t = __fsub_rn(a, s.hi);  // b, but for the rounding
+  s.lo = __fadd_rn(__fsub_rn(t, b), __fsub_rn(a, __fadd_rn(s.hi, t)));
+  return s;
+}
+
+// exp(d) to about 2^-30, of d up to 1 or so; below e^-87, 0. d less a multiple k of log 2 (W. J. Cody and W. Waite, "Software
+// Manual for the Elementary Functions", 1980: the multiple of a constant of 16 bits is exact, the rest's is added),
+// then the series, its first three terms in two numbers.
+__device__ __forceinline__ Sum exp_pair(const Sum& d) {
+  constexpr float kLn2High = 0.693145752f, kLn2Low = 1.42860677e-6f;
+  if (!(d.hi > -87.0f)) return Sum{d.hi == d.hi ? 0.0f : d.hi, 0.0f};  // (NaN stays)
+  const float k = rintf(d.hi * kLog2eHigh);
+  Sum x;
+  x.hi = fmaf(-k, kLn2High, d.hi);
+  x.lo = fmaf(-k, kLn2Low, d.lo);
+  x.settle();
+  const float q = x.hi * x.hi;
+  const float q_lo = fmaf(x.hi, x.hi, -q) + 2.0f * x.hi * x.lo;
+  float r = fmaf(x.hi, 1.0f / 362880.0f, 1.0f / 40320.0f);
+  r = fmaf(x.hi, r, 1.0f / 5040.0f);
+  r = fmaf(x.hi, r, 1.0f / 720.0f);
+  r = fmaf(x.hi, r, 1.0f / 120.0f);
+  r = fmaf(x.hi, r, 1.0f / 24.0f);
+  r = fmaf(x.hi, r, 1.0f / 6.0f);
+  Sum e;
+  e.hi = 1.0f;
+  e.add(x.hi);
+  e.add(0.5f * q);
+  e.lo += fmaf(0.5f, q_lo, x.lo) + x.hi * q * r;
+  e.settle();
+  const float scale = __uint_as_float(static_cast<uint32_t>(static_cast<int>(k) + 127) << 23);
+  e.hi *= scale;
+  e.lo *= scale;
+  return e;
+}
+
+// log(s) of s from about 1 to 2^60: from its fp32 value l, s exp(-l) is 1 + t, and log(1 + t) two terms of t.
+__device__ __forceinline__ Sum log_pair(const Sum& s) {
+  const float l = logf(s.hi);
+  Sum minus;
+  minus.hi = -l;
+  Sum t = exp_pair(minus);
+  t.times(s);
+  t.add(-1.0f);
+  t.settle();
+  Sum r;
+  r.hi = l;
+  r.add(t.hi - 0.5f * t.hi * t.hi);
+  r.lo += t.lo;
+  r.settle();
+  return s.hi > 0.0f && s.hi < INFINITY ? r : Sum{l, 0.0f};
+}
 
 template <typename T>
 struct Logits;
@@ -103,6 +249,7 @@ struct Logits<uint16_t> {
       f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   }
+  __device__ static __forceinline__ float value(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
   __device__ static __forceinline__ uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
 };
 template <>
@@ -114,30 +261,56 @@ struct Logits<float> {
     f[2] = __uint_as_float(v.z);
     f[3] = __uint_as_float(v.w);
   }
+  __device__ static __forceinline__ float value(float x) { return x; }
   __device__ static __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
-// A vector of a row at virtual element v * kVec, where the row begins at virtual element `skip` (so that vectors are
-// aligned) and ends before `end`; elements that are not the part's, [lo, hi), count as -infinity.
-template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T* base, int v, int lo, int hi) {
-  constexpr int N = Logits<T>::kVec;
-  const int e = v * N;
-  if (e >= lo && e + N <= hi) return __ldcs(reinterpret_cast<const uint4*>(base + e));
-  uint4 x = Logits<T>::none();
-  if (e + N <= lo || e >= hi) return x;
-  uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (e + i < lo || e + i >= hi) continue;
-    if constexpr (N == 8) {
-      const uint32_t s = base[e + i];
-      u[i / 2] = i & 1 ? (u[i / 2] & 0xffffu) | (s << 16) : (u[i / 2] & 0xffff0000u) | s;
+// A row's vectors begin at its first element, wherever that lies, so that equal rows have equal sums. Where that is no
+// multiple of 16 bytes (SHIFTED: of some row), a vector is cut out of two aligned blocks. A row's first vector and its
+// last one to two, whose blocks hold other bytes too, are taken element by element.
+template <bool SHIFTED>
+struct Raw;
+template <>
+struct Raw<false> {
+  uint4 a;
+};
+template <>
+struct Raw<true> {
+  uint4 a, b;
+};
+
+// Vector v of the row whose first block is `blocks`, if it is one of [lo, hi); else -infinity.
+template <typename T, bool SHIFTED>
+__device__ __forceinline__ Raw<SHIFTED> load_vec(const uint4* blocks, int v, int lo, int hi) {
+  Raw<SHIFTED> r;
+  r.a = Logits<T>::none();
+  if constexpr (SHIFTED) r.b = r.a;
+  if (v >= lo && v < hi) {
+    if constexpr (SHIFTED) {
+      r.a = __ldg(blocks + v);
+      r.b = __ldg(blocks + v + 1);
     } else {
-      u[i] = __float_as_uint(base[e + i]);
+      r.a = __ldcs(blocks + v);
     }
   }
-  return make_uint4(u[0], u[1], u[2], u[3]);
+  return r;
+}
+
+// The vector that begins `shift` bytes after its first block.
+template <bool SHIFTED>
+__device__ __forceinline__ uint4 cut(const Raw<SHIFTED>& r, int shift) {
+  if constexpr (SHIFTED) {
+    uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+    const int bits = (shift & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+  } else {
+    return r.a;
+  }
 }
 
 // A list entry: by logit (-0 is 0), of equal ones by the lower token.
@@ -151,11 +324,24 @@ struct Shared {
   unsigned long long list[kList];
   unsigned long long best[kMaxCount];
   unsigned long long warp_best[2][kWarps];
-  double warp_sum[kWarps];
+  int noted[kNoted];
+  alignas(16) int bins[kBins];
+  Sum warp_sum[kWarps];
+  long long warp_fixed[kWarps];
   float warp_max[kWarps];
+  int n_noted;
   int n;
-  int unused;
 };
+
+__device__ __forceinline__ float cta_max(Shared& s, float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if ((threadIdx.x & 31) == 0) s.warp_max[threadIdx.x >> 5] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v = fmaxf(v, s.warp_max[w]);
+  return v;
+}
 
 // The `count` best of the first n entries of the list (fewer if there are fewer), best first, in s.best; their
 // number. All entries differ. Few entries are ranked by comparing each with all; of many, the best is taken `count`
@@ -165,7 +351,8 @@ __device__ int select_best(Shared& s, int n, int count) {
   if (n <= kThreads) {
     const unsigned long long mine = tid < n ? s.list[tid] : 0ull;
     int rank = 0;
-    for (int i = 0; i < n; ++i) rank += s.list[i] > mine ? 1 : 0;
+    if ((tid & ~31) < n)
+      for (int i = 0; i < n; ++i) rank += s.list[i] > mine ? 1 : 0;
     if (tid < n && rank < count) s.best[rank] = mine;
     __syncthreads();
     return found;
@@ -199,10 +386,10 @@ __device__ int select_best(Shared& s, int n, int count) {
   return found;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) beam_part_kernel(const BeamParams p) {
+template <typename T, bool SHIFTED>
+__global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(const BeamParams p) {
   using L = Logits<T>;
-  constexpr int N = L::kVec, kVecs = kPerThread / N;
+  constexpr int N = L::kVec;
   __shared__ Shared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -210,151 +397,190 @@ __global__ void __launch_bounds__(kThreads, 2) beam_part_kernel(const BeamParams
   const int row = blockIdx.x / p.splits, split = blockIdx.x - row * p.splits;
   if (p.finished && p.finished[row]) return;
   const T* logits = static_cast<const T*>(p.logits) + row * p.stride;
-  const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(logits) & 15u) / sizeof(T));
-  const T* base = logits - skip;
-  // The part, in elements from the aligned base.
-  const int lo = max(skip, split * p.part);
-  const int hi = static_cast<int>(min(static_cast<long long>(skip) + p.vocab, static_cast<long long>(split + 1) * p.part));
-  const int first = split * p.part / N;
-  const int tiles = hi > lo ? (hi - split * p.part + kTile - 1) / kTile : 0;
-  if (tid == 0) s.n = 0;
+  const int shift = SHIFTED ? static_cast<int>(reinterpret_cast<uintptr_t>(logits) & 15u) : 0;
+  const uint4* blocks = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(logits) - shift);
+  // The part's vectors, of the row's whole ones but the first and the last; the first part has the row's ends too, an
+  // element to a thread.
+  const int end = p.vocab / N - 1;
+  const int lo = 1 + split * p.part, hi = max(lo, min(end, lo + p.part));
+  const int tiles = (hi - lo + kThreads * kVecs - 1) / (kThreads * kVecs);
+  const int head = end > 1 ? N : p.vocab;
+  int side = -1;
+  if (split == 0) side = tid < head ? tid : end > 1 && end * N + tid - head < p.vocab ? end * N + tid - head : -1;
+  const float x_side = side < 0 ? -INFINITY : L::value(logits[side]);
+  if (tid == 0) s.n = s.n_noted = 0;
+  s.bins[tid] = 0;
 
-  uint4 v[kVecs];
+  Raw<SHIFTED> v[kVecs];
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) v[u] = load_vec(base, first + u * kThreads + tid, lo, hi);
-  float f[kPerThread];
-  float ref = -INFINITY;
-  uint32_t bar = 0;        // what passes is above it, in the order of ordered()
-  Sum sum;
-  if (tiles > 0) {
-    // The first tile's maximum, and a value that at least `count` of the threads' maxima reach: the upper 16 bits of
-    // the largest such.
-    float m = -INFINITY;
+  for (int u = 0; u < kVecs; ++u) v[u] = load_vec<T, SHIFTED>(blocks, lo + u * kThreads + tid, lo, hi);
+  // The first tile's maximum (with the row's ends), and a value that at least `count` of the threads' maxima are above: from
+  // the number of them at each distance from the maximum.
+  float m = x_side;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      L::unpack(v[u], f + u * N);
+  for (int u = 0; u < kVecs; ++u) {
+    float f[N];
+    L::unpack(cut<SHIFTED>(v[u], shift), f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) m = fmaxf(m, f[u * N + i]);
-    }
-    float top = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) s.warp_max[warp] = top;
-    const uint32_t mine = ordered(m + 0.0f) >> 16;
-    uint32_t at = 0;
-#pragma unroll
-    for (int b = 15; b >= 0; --b) {
-      const uint32_t probe = at | 1u << b;
-      if (__syncthreads_count(mine >= probe) >= p.count) at = probe;
-    }
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.warp_max[w]);
-    // (A maximum of infinity makes terms of NaN, which is what the sum is to be.)
-    ref = top;
-    bar = max(at << 16, ordered(-INFINITY) + 1u) - 1u;
-    if (bar == ordered(-0.0f)) --bar;  // (0 and -0 both are above it)
+    for (int i = 0; i < N; ++i) m = fmaxf(m, f[i]);
   }
-  float above = from_ordered(bar);
+  float ref = cta_max(s, m);
+  atomicAdd(&s.bins[bin_of(ref - m)], 1);
+  __syncthreads();
+  // (Rounded down, and by more than the distances' rounding: what is in the bins is above it.)
+  float above = -INFINITY;
+  const float d = bin_end(bin_reached(s.bins, p.count));
+  if (ref < INFINITY && d < INFINITY) above = __fsub_rd(ref, d * 1.000001f);
+  float unit = ref == -INFINITY ? 0.0f : ref;
+
+  Sum sum;
+  if (side >= 0) {
+    if (x_side > above) s.list[atomicAdd(&s.n, 1)] = entry(x_side, side);
+    else sum.add(term(x_side, unit));
+  }
   for (int t = 0; t < tiles; ++t) {
-    const int at = first + t * (kTile / N) + tid;  // this thread's first vector
+    const int at = lo + t * (kThreads * kVecs) + tid;  // this thread's first vector
+    unsigned long long sum2 = 0ull;                    // of 16 numbers, two zeros
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) L::unpack(v[u], f + u * N);
-    if (t + 1 < tiles) {
+    for (int g = 0; g < kVecs * N / 8; ++g) {
+      float f[8];
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) v[u] = load_vec(base, at + kTile / N + u * kThreads, lo, hi);
-    }
-    float m[kVecs];
-    float top = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      m[u] = f[u * N];
-#pragma unroll
-      for (int i = 1; i < N; ++i) m[u] = fmaxf(m[u], f[u * N + i]);
-      top = fmaxf(top, m[u]);
-    }
-    if (__builtin_expect(top > ref + 30.0f, 0)) {  // far above the reference, or the first that is finite: it moves
-      const float by = term(ref, top);
-      sum.hi *= by;
-      sum.lo *= by;
-      ref = top;
-    }
-    const float unit = ref == -INFINITY ? 0.0f : ref;
-#pragma unroll
-    for (int g = 0; g < kPerThread / 8; ++g) {
+      for (int k = 0; k < 8 / N; ++k) {
+        const int u = g * (8 / N) + k;
+        L::unpack(cut<SHIFTED>(v[u], shift), f + k * N);
+        v[u] = load_vec<T, SHIFTED>(blocks, at + (kVecs + u) * kThreads, lo, hi);  // the next tile's (none after the last)
+      }
       float e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = term(f[g * 8 + i], unit);
+      terms(f, unit, e);
+      const float top = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
       if (__builtin_expect(top > above, 0)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum.add(e[i]);
-      } else {
-        sum.add(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])));
+        for (int i = 0; i < 8; ++i) e[i] = f[i] > above ? 0.0f : e[i];
+#pragma unroll
+        for (int k = 0; k < 8 / N; ++k) {
+          const int to = atomicAdd(&s.n_noted, 1);
+          if (to < kNoted) s.noted[to] = at + (g * (8 / N) + k) * kThreads;
+        }
+      }
+      sum2 = add2(sum2, add2(add2(two(e[0], e[1]), two(e[2], e[3])), add2(two(e[4], e[5]), two(e[6], e[7]))));
+      if (g & 1) {
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(sum2));
+        sum.add(a + b);
+        sum2 = 0ull;
       }
     }
-    // (The barrier also has everybody know the list's length before anybody adds to it.)
-    const int could = __syncthreads_count(top > above) * kPerThread;
-    const int have = s.n;
+  }
+  __syncthreads();
+  const int noted = s.n_noted;
+  for (int i = tid; i < min(noted, kNoted); i += kThreads) {
+    const int at = s.noted[i];
+    float f[N];
+    L::unpack(cut<SHIFTED>(load_vec<T, SHIFTED>(blocks, at, lo, hi), shift), f);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (!(f[k] > above)) continue;
+      const int to = atomicAdd(&s.n, 1);
+      if (to < kList) s.list[to] = entry(f[k], at * N + k);
+    }
+  }
+  __syncthreads();
+  int found = -1;
+  long long fixed = 0;
+  if (__builtin_expect(noted <= kNoted && s.n <= kList, 1)) {
+    // What is listed but not selected is added in units of 2^-36 exp(ref), as long as it is no more than e^10 of these (or
+    // there are more than `count` such: then in the other way).
+    const int n = s.n;
+    found = select_best(s, n, p.count);
+    bool large = false;
+    for (int i = tid; i < n; i += kThreads) {
+      const unsigned long long e = s.list[i];
+      if (e >= s.best[found - 1]) continue;
+      const float x = entry_x(e);
+      large |= x > ref + 10.0f;
+      fixed += __float2ll_rn(term(x, unit) * 0x1p36f);
+    }
+    if (__syncthreads_or(large)) found = -1;
+  }
+  if (found < 0) {
+    float m = x_side;
+    for (int i = lo + tid; i < hi; i += kThreads) {
+      float f[N];
+      L::unpack(cut<SHIFTED>(load_vec<T, SHIFTED>(blocks, i, lo, hi), shift), f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) m = fmaxf(m, f[k]);
+    }
     __syncthreads();
-    if (have + could <= kList) {
-      if (top > above) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-          if (!(m[u] > above)) continue;
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (f[u * N + i] > above) s.list[atomicAdd(&s.n, 1)] = entry(f[u * N + i], (at + u * kThreads) * N + i - skip);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int u0 = 0; u0 < kSteps; ++u0) {
-        __syncthreads();
-        const int n = s.n;
-        if (n > kListLong) {
-          const int found = select_best(s, n, p.count);
-          if (tid < found) s.list[tid] = s.best[tid];
-          if (tid == 0) s.n = found;
-          if (found == p.count) {
-            bar = max(bar, static_cast<uint32_t>(s.best[found - 1] >> 32));
-            above = from_ordered(bar);
-          }
-          __syncthreads();
-        } else {
-          __syncthreads();
-        }
-#pragma unroll
-        for (int u = u0 * kVecs / kSteps; u < (u0 + 1) * kVecs / kSteps; ++u) {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (f[u * N + i] > above) s.list[atomicAdd(&s.n, 1)] = entry(f[u * N + i], (at + u * kThreads) * N + i - skip);
-        }
-      }
+    ref = cta_max(s, m);
+    unit = ref == -INFINITY ? 0.0f : ref;
+    above = -INFINITY;
+    fixed = 0;
+    sum = Sum();
+    if (side >= 0) sum.add(term(x_side, unit));
+    if (tid == 0) s.n = 0;
+    for (int at = lo; at < hi; at += kThreads) {
       __syncthreads();
+      const int n = s.n;
+      __syncthreads();
+      if (at == lo && side < head && x_side > above) s.list[atomicAdd(&s.n, 1)] = entry(x_side, side);
+      if (n > kListLong) {
+        const int best = select_best(s, n, p.count);
+        if (tid < best) s.list[tid] = s.best[tid];
+        if (tid == 0) s.n = best;
+        above = fmaxf(above, entry_x(s.best[best - 1]));  // (as many as are asked for: of equal ones the earlier win)
+        __syncthreads();
+      }
+      if (at + tid >= hi) continue;
+      float f[N];
+      L::unpack(cut<SHIFTED>(load_vec<T, SHIFTED>(blocks, at + tid, lo, hi), shift), f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        sum.add(term(f[k], unit));
+        if (f[k] > above) s.list[atomicAdd(&s.n, 1)] = entry(f[k], (at + tid) * N + k);
+      }
     }
+    if (side >= head && x_side > above) s.list[atomicAdd(&s.n, 1)] = entry(x_side, side);
+    __syncthreads();
+    found = select_best(s, s.n, p.count);
+    // (These terms were added by the hardware's exponential.)
+    if (tid < found) sum.add(-term(entry_x(s.best[tid]), unit));
   }
-  __syncthreads();
-  const int found = select_best(s, s.n, p.count);
-  // The CTA's largest reference, and the sum in its units.
-  float most = ref;
+  // The sum in units of the largest logit's exponential: the selected ones' terms in the order of their ranks.
+  const float most = found > 0 ? entry_x(s.best[0]) : ref;
+  sum.settle();
+  const Sum by = exp_pair(difference(ref, most));
+  if (ref != most) sum.times(by);
+  if (tid < found) sum.add(exp_pair(difference(entry_x(s.best[tid]), most)));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0) s.warp_max[warp] = most;
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w) most = fmaxf(most, s.warp_max[w]);
-  double all = static_cast<double>(sum.hi) + static_cast<double>(sum.lo);
-  if (ref != most) all *= exp(static_cast<double>(ref) - static_cast<double>(most));
-  if (tid < found) {
-    // (Where a thread's reference has moved, its term of x was a little different from this one.)
-    const float x = entry_x(s.best[tid]);
-    all += exp(static_cast<double>(x) - static_cast<double>(most)) - static_cast<double>(term(x, most));
+  for (int o = 16; o > 0; o >>= 1) {
+    Sum other;
+    other.hi = __shfl_xor_sync(0xffffffffu, sum.hi, o);
+    other.lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
+    fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+    sum.add(other);
+    sum.settle();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  if (lane == 0) s.warp_sum[warp] = all;
+  if (lane == 0) {
+    s.warp_sum[warp] = sum;
+    s.warp_fixed[warp] = fixed;
+  }
   __syncthreads();
   const long long out = static_cast<long long>(row) * p.splits + split;
   if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) all += s.warp_sum[w];
-    p.part_sum[out] = all;
+    for (int w = 1; w < kWarps; ++w) {
+      sum.add(s.warp_sum[w]);
+      fixed += s.warp_fixed[w];
+    }
+    // The integer, in two numbers.
+    Sum whole;
+    whole.hi = __ll2float_rn(fixed);
+    whole.lo = __ll2float_rn(fixed - __float2ll_rn(whole.hi));
+    whole.hi *= 0x1p-36f;
+    whole.lo *= 0x1p-36f;
+    if (ref != most) whole.times(by);
+    sum.add(whole);
+    sum.settle();
+    p.part_sum[out] = make_float2(sum.hi, sum.lo);
     p.part_ref[out] = most;
   }
   if (tid < p.count) {
@@ -363,107 +589,216 @@ __global__ void __launch_bounds__(kThreads, 2) beam_part_kernel(const BeamParams
   }
 }
 
-// Whether (a, i) comes before (b, j): the larger value, of equal ones the lower place.
-__device__ __forceinline__ bool before(double a, long long i, double b, long long j) { return a > b || (a == b && i < j); }
+// A candidate in the order of unsigned integers: its value in fp64, of equal ones (-0 is 0) the lower beam, then the
+// lower token.
+struct Candidate {
+  unsigned long long value;  // 0: none
+  uint32_t place;            // beam << 24 | token
+};
+static_assert(MOE_FFN_BEAM_MAX_VOCAB <= 1 << 24 && MOE_FFN_BEAM_MAX <= 1 << 8, "places");
+__device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
+  return a.value > b.value || (a.value == b.value && a.place < b.place);
+}
 
-// A CTA per user: the beams' log sum exp, then the best of all parts' candidates, taken `count` times. A thread holds
-// the best of its own candidates, which are those of some parts' ranks in turn.
+__device__ __forceinline__ double value_of(unsigned long long o) {
+  return __longlong_as_double(static_cast<long long>(o ^ (o >> 63 ? 1ull << 63 : ~0ull)));
+}
+
+// A CTA per user: the beams' log sum exp, then the best of all parts' candidates, found as in a part: a distance from the
+// largest value within which there are `count`, a list of these, and the order by comparing each with all. Candidates
+// have their values formed in fp32 first, with a bound of what that loses.
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParams p) {
-  constexpr int kJoinWarps = kJoinThreads / 32;
   // A continuation's value is (x - ref) + shift: the sum of exp(x - ref) is what has been formed. NaN: none.
-  __shared__ double shift[MOE_FFN_BEAM_MAX], beam_ref[MOE_FFN_BEAM_MAX];
-  __shared__ double warp_value[2][kJoinWarps];
-  __shared__ long long warp_place[2][kJoinWarps];
+  __shared__ double shift[MOE_FFN_BEAM_MAX];
+  __shared__ float rough_shift[MOE_FFN_BEAM_MAX], beam_ref[MOE_FFN_BEAM_MAX];
+  __shared__ bool ended[MOE_FFN_BEAM_MAX];
+  __shared__ float held[kJoinHeld];
+  __shared__ Candidate list[kJoinList];
+  __shared__ float warp_top[kJoinWarps], warp_off[kJoinWarps];
+  __shared__ alignas(16) int bins[kBins];
+  __shared__ int found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, user = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
   const long long row0 = static_cast<long long>(user) * p.beams;
+  const int per_beam = p.splits * p.count, n = p.beams * per_beam;
+  const float* xs = p.part_x + row0 * per_beam;
+  const int32_t* tokens = p.part_token + row0 * per_beam;
+  static_assert(kJoinThreads == kBins && kThreads == kBins, "a bin to a thread");
+  bins[tid] = 0;
+  if (tid == 0) found = 0;
   for (int k = warp; k < p.beams; k += kJoinWarps) {
     const long long row = row0 + k;
-    if (p.finished && p.finished[row]) continue;
-    float top = -INFINITY;
-    for (int i = lane; i < p.splits; i += 32) top = fmaxf(top, p.part_ref[row * p.splits + i]);
+    static_assert(kMaxSplits == 64, "two parts of a row to a lane");
+    const bool end = p.finished && p.finished[row];
+    const float score = p.scores[row];
+    float r[2] = {-INFINITY, -INFINITY};
+    float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = lane + 32 * j;
+      if (end || i >= p.splits) continue;
+      r[j] = p.part_ref[row * p.splits + i];
+      part[j] = p.part_sum[row * p.splits + i];
+    }
+    float top = fmaxf(r[0], r[1]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    double sum = 0.0;
-    for (int i = lane; i < p.splits; i += 32)
-      sum += p.part_sum[row * p.splits + i] * exp(static_cast<double>(p.part_ref[row * p.splits + i]) - static_cast<double>(top));
+    Sum sum;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int j = 0; j < 2; ++j) {
+      if (j > 0 && p.splits <= 32) break;
+      Sum a;
+      a.hi = part[j].x;
+      a.lo = part[j].y;
+      if (r[j] != top) a.times(exp_pair(difference(r[j], top)));
+      sum.add(a);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Sum other;
+      other.hi = __shfl_xor_sync(0xffffffffu, sum.hi, o);
+      other.lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
+      sum.add(other);
+      sum.settle();
+    }
+    const Sum l = log_pair(sum);
     if (lane == 0) {
-      shift[k] = static_cast<double>(p.scores[row]) - log(sum);
+      ended[k] = end;
       beam_ref[k] = top;
+      const double sh = end ? static_cast<double>(score)
+                            : static_cast<double>(score) - (static_cast<double>(l.hi) + static_cast<double>(l.lo));
+      shift[k] = sh;
+      rough_shift[k] = static_cast<float>(sh);
     }
   }
   __syncthreads();
-  const int per_beam = p.splits * p.count, n = p.beams * per_beam;
-  // The best of this thread's candidates that come after (value, place).
-  double best;
-  long long place;
-  auto look = [&](double after, long long after_place) {
-    best = -INFINITY;
-    place = 0x7fffffffffffffffLL;
-    for (int i = tid; i < n; i += kJoinThreads) {
-      const int k = i / per_beam;
-      double v;
-      long long at;
-      if (p.finished && p.finished[row0 + k]) {
-        if (i - k * per_beam != 0) continue;
-        v = static_cast<double>(p.scores[row0 + k]);
-        at = static_cast<long long>(k) * p.vocab + p.end_token;
-      } else {
-        const int token = p.part_token[row0 * per_beam + i];
-        if (token < 0) continue;
-        v = (static_cast<double>(p.part_x[row0 * per_beam + i]) - beam_ref[k]) + shift[k];
-        at = static_cast<long long>(k) * p.vocab + token;
-      }
-      if (v > -INFINITY && before(after, after_place, v, at) && before(v, at, best, place)) {
-        best = v;
-        place = at;
-      }
+  const float per_beam_inv = 1.0f / static_cast<float>(per_beam);
+  // (n is at most 2^18: the product is off by less than the distance of i + 1/2 from a multiple.)
+  auto beam_of = [&](int i) { return static_cast<int>((static_cast<float>(i) + 0.5f) * per_beam_inv); };
+  // A candidate's value in fp32, and what it may be off by: half a step of each of two operations and of shift.
+  auto rough = [&](int i, float& off) {
+    const int k = beam_of(i);
+    const float t = rough_shift[k];
+    if (ended[k]) {
+      off = 0x1p-22f * fabsf(t);
+      return i == k * per_beam ? t : -INFINITY;
     }
+    const float d = xs[i] - beam_ref[k];
+    off = 0x1p-22f * (fabsf(d) + fabsf(t));
+    return tokens[i] >= 0 ? d + t : -INFINITY;
   };
-  look(INFINITY, -1);
+  auto exact = [&](int i) {
+    const int k = beam_of(i);
+    double v = shift[k];
+    int token = p.end_token;
+    if (!ended[k]) {
+      v += static_cast<double>(xs[i]) - static_cast<double>(beam_ref[k]);
+      token = tokens[i];
+    } else if (i != k * per_beam) {
+      token = -1;
+    }
+    Candidate c;
+    c.value = token >= 0 && v > -INFINITY ? ordered(v + 0.0) : 0ull;
+    c.place = static_cast<uint32_t>(k) << 24 | static_cast<uint32_t>(token & 0xffffff);
+    return c;
+  };
+  float top = -INFINITY, off = 0.0f;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kJoinThreads) {
+    float o;
+    const float v = rough(i, o);
+    if (i < kJoinHeld) held[i] = v;
+    top = fmaxf(top, v);
+    if (v > -INFINITY) off = fmaxf(off, o);
+  }
+  auto value = [&](int i) {
+    float o;
+    return i < kJoinHeld ? held[i] : rough(i, o);
+  };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, o));
+  }
+  if (lane == 0) {
+    warp_top[warp] = top;
+    warp_off[warp] = off;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    top = fmaxf(top, warp_top[w]);
+    off = fmaxf(off, warp_off[w]);
+  }
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float v = value(i);
+    if (v > -INFINITY) atomicAdd(&bins[bin_of(top - v)], 1);
+  }
+  __syncthreads();
+  float least = -INFINITY;
+  const float d = bin_end(bin_reached(bins, p.count));
+  if (top < INFINITY && d < INFINITY) least = __fsub_rd(top, fmaf(2.0f, off, d * 1.000001f));
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float v = value(i);
+    if (v > -INFINITY && v >= least) {
+      const int to = atomicAdd(&found, 1);
+      if (to < kJoinList) list[to].place = i;
+    }
+  }
+  __syncthreads();
+  auto answer = [&](int c, const Candidate& a) {
+    const long long o = static_cast<long long>(user) * p.count + c;
+    const unsigned long long u = a.value;
+    const bool some = u != 0ull;
+    p.out_scores[o] = some ? static_cast<float>(value_of(u)) : -INFINITY;
+    p.out_beams[o] = some ? static_cast<int>(a.place >> 24) : -1;
+    p.out_tokens[o] = some ? static_cast<int>(a.place & 0xffffff) : -1;
+  };
+  const int have = found;
+  if (have <= kJoinList) {
+    for (int i = tid; i < have; i += kJoinThreads) list[i] = exact(static_cast<int>(list[i].place));
+    __syncthreads();
+    for (int i = tid; i < have; i += kJoinThreads) {
+      const Candidate c = list[i];
+      int rank = 0;
+      for (int j = 0; j < have; ++j) rank += before(list[j], c) ? 1 : 0;
+      if (rank < p.count) answer(rank, c);
+    }
+    for (int c = have + tid; c < p.count; c += kJoinThreads) answer(c, Candidate{0ull, 0u});
+    return;
+  }
+  // More than that, where many values lie close together. The best after the last one is taken `count` times.
+  Candidate last = {~0ull, 0u};
   for (int c = 0; c < p.count; ++c) {
-    double v = best;
-    long long at = place;
+    Candidate a = {0ull, 0xffffffffu};
+    for (int i = tid; i < n; i += kJoinThreads) {
+      const float v = value(i);
+      if (!(v > -INFINITY && v >= least)) continue;
+      const Candidate b = exact(i);
+      if (b.value != 0ull && before(last, b) && before(b, a)) a = b;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const double w = __shfl_xor_sync(0xffffffffu, v, o);
-      const long long a = __shfl_xor_sync(0xffffffffu, at, o);
-      if (before(w, a, v, at)) {
-        v = w;
-        at = a;
-      }
-    }
-    if (lane == 0) {
-      warp_value[c & 1][warp] = v;
-      warp_place[c & 1][warp] = at;
+      const Candidate b = {__shfl_xor_sync(0xffffffffu, a.value, o), __shfl_xor_sync(0xffffffffu, a.place, o)};
+      if (before(b, a)) a = b;
     }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (before(warp_value[c & 1][w], warp_place[c & 1][w], v, at)) {
-        v = warp_value[c & 1][w];
-        at = warp_place[c & 1][w];
-      }
-    }
-    const bool some = v > -INFINITY;
-    if (tid == 0) {
-      const long long o = static_cast<long long>(user) * p.count + c;
-      p.out_scores[o] = static_cast<float>(v);
-      p.out_beams[o] = some ? static_cast<int>(at / p.vocab) : -1;
-      p.out_tokens[o] = some ? static_cast<int>(at % p.vocab) : -1;
-    }
-    if (some && best == v && place == at) look(v, at);
+    if (lane == 0) list[warp] = a;
+    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w)
+      if (before(list[w], a)) a = list[w];
+    if (tid == 0) answer(c, a);
+    last = a;
   }
 }
 
-// Parts of a row: enough for three CTAs on each SM, of a tile at least, and few tiles where rows are long, so that
-// the lists stay short.
+// Parts of a row: enough for four CTAs on each SM, of a tile at least, and few tiles where rows are long, so that
+// the lists stay short. (Tiles of bf16 logits, which have the larger ones: one workspace serves both types.)
 int beam_splits(int rows, int vocab) {
-  const int tiles = (vocab + 8 + kTile - 1) / kTile;
-  int splits = (3 * 152 + rows - 1) / (rows > 0 ? rows : 1);
+  constexpr int kTile = kThreads * kVecs * 8;
+  const int tiles = (vocab + kTile - 1) / kTile;
+  int splits = (4 * 152 + rows - 1) / (rows > 0 ? rows : 1);
   const int least = (tiles + 15) / 16;
   if (splits < least) splits = least;
   if (splits > tiles) splits = tiles;
@@ -545,7 +880,7 @@ extern "C" int moe_ffn_beam_select(const moe_ffn_beam* a, void* workspace, size_
   p.out_beams = a->out_beams;
   p.out_tokens = a->out_tokens;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part_sum = reinterpret_cast<double*>(ws + l.sum);
+  p.part_sum = reinterpret_cast<float2*>(ws + l.sum);
   p.part_ref = reinterpret_cast<float*>(ws + l.ref);
   p.part_x = reinterpret_cast<float*>(ws + l.x);
   p.part_token = reinterpret_cast<int32_t*>(ws + l.token);
@@ -554,10 +889,17 @@ extern "C" int moe_ffn_beam_select(const moe_ffn_beam* a, void* workspace, size_
   p.vocab = a->vocab;
   p.count = a->count;
   p.splits = beam_splits(rows, a->vocab);
-  p.part = ((a->vocab + 8 + p.splits - 1) / p.splits + 7) / 8 * 8;
+  p.part = (a->vocab / static_cast<int>(16 / element) + p.splits - 1) / p.splits;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = a->logits_fp32 ? launch_pdl(beam_part_kernel<float>, dim3(p.splits * rows), dim3(kThreads), 0, s, p)
-                                 : launch_pdl(beam_part_kernel<uint16_t>, dim3(p.splits * rows), dim3(kThreads), 0, s, p);
+  const bool shifted = reinterpret_cast<uintptr_t>(a->logits) % 16 != 0 || (rows > 1 && a->logits_stride * element % 16 != 0);
+  const dim3 grid(p.splits * rows), block(kThreads);
+  cudaError_t e;
+  if (a->logits_fp32)
+    e = shifted ? launch_pdl(beam_part_kernel<float, true>, grid, block, 0, s, p)
+                : launch_pdl(beam_part_kernel<float, false>, grid, block, 0, s, p);
+  else
+    e = shifted ? launch_pdl(beam_part_kernel<uint16_t, true>, grid, block, 0, s, p)
+                : launch_pdl(beam_part_kernel<uint16_t, false>, grid, block, 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(beam_join_kernel, dim3(a->users), dim3(kJoinThreads), 0, s, p);
   return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
 }

@@ -94,6 +94,10 @@ def test_ties():
     row = torch.randint(-8, 9, (50000,), generator=g, device="cuda").float()
     logits = row.to(torch.bfloat16).expand(4, 50000).contiguous()
     _check(logits, torch.full((1, 4), -1.5, device="cuda"), 64)
+    # Rows of odd lengths begin at any address, and equal ones are equal all the same.
+    for dtype in (torch.bfloat16, torch.float32):
+        odd = (row[:49999] / 3).to(dtype).expand(7, 49999).contiguous()
+        _check(odd, torch.full((1, 7), -1.5, device="cuda"), 64)
     z = torch.zeros(2, 20000, device="cuda")
     z[:, ::2] = -0.0
     z[:, 5000:] = -1.0
