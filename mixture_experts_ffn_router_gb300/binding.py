@@ -7,6 +7,7 @@ library has not been built: there is no fallback.
 """
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe_ffn.so")
@@ -122,6 +123,18 @@ class moe_ffn_beam(ctypes.Structure):
                 + [(f, ctypes.c_int) for f in ("logits_fp32", "end_token", "users", "beams", "vocab", "count")])
 
 
+# Some calls' structures are packed into bytes: a ctypes structure of a dozen fields takes longer than the call.
+_PACK_NORM = struct.Struct("@7P5q2f2i").pack
+_PACK_ROTARY = struct.Struct("@2Pqf8i4x").pack
+_PACK_ROWS = struct.Struct("@Pqq").pack
+_PACK_BEAM = struct.Struct("@Pq5P6i").pack
+
+
+def _by_ref(s):
+    """A structure, or one that is packed or absent already, as an argument."""
+    return ctypes.byref(s) if isinstance(s, ctypes.Structure) else s
+
+
 _LIB = None
 
 
@@ -190,22 +203,22 @@ def lib():
         L.moe_ffn_kv_tree_attention.argtypes = [_vp, cache_p, batch_p, _vp, rows_p, ctypes.c_float, ctypes.c_int,
                                                 ctypes.c_int, _vp, _vp, _vp]
         L.moe_ffn_kv_keep.restype = ctypes.c_int
-        L.moe_ffn_kv_keep.argtypes = [_vp, cache_p, ctypes.c_int, batch_p, _vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp,
+        L.moe_ffn_kv_keep.argtypes = [_vp, _vp, ctypes.c_int, batch_p, _vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp,
                                       _vp]
         L.moe_ffn_kv_reorder.restype = ctypes.c_int
-        L.moe_ffn_kv_reorder.argtypes = [_vp, cache_p, ctypes.c_int, _vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp,
+        L.moe_ffn_kv_reorder.argtypes = [_vp, _vp, ctypes.c_int, _vp, ctypes.c_longlong, ctypes.c_int, _vp, _vp,
                                          ctypes.c_int, ctypes.c_int, _vp]
         L.moe_ffn_block_norm.restype = ctypes.c_int
-        L.moe_ffn_block_norm.argtypes = [ctypes.POINTER(moe_ffn_norm), _vp]
+        L.moe_ffn_block_norm.argtypes = [_vp, _vp]
         L.moe_ffn_rotary_table.restype = ctypes.c_int
         L.moe_ffn_rotary_table.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int), ctypes.c_int,
                                            ctypes.POINTER(moe_ffn_rotary_pair)]
         L.moe_ffn_rotary_apply.restype = ctypes.c_int
-        L.moe_ffn_rotary_apply.argtypes = [ctypes.POINTER(moe_ffn_rotary), rows_p, rows_p, rows_p, rows_p, _vp]
+        L.moe_ffn_rotary_apply.argtypes = [_vp] * 6
         L.moe_ffn_beam_workspace_bytes.restype = ctypes.c_size_t
         L.moe_ffn_beam_workspace_bytes.argtypes = [ctypes.c_int] * 4
         L.moe_ffn_beam_select.restype = ctypes.c_int
-        L.moe_ffn_beam_select.argtypes = [ctypes.POINTER(moe_ffn_beam), _vp, ctypes.c_size_t, _vp]
+        L.moe_ffn_beam_select.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
         L.moe_ffn_destroy.restype = None
         L.moe_ffn_destroy.argtypes = [_vp]
         _LIB = L
@@ -412,17 +425,17 @@ def moe_ffn_kv_tree_attention(kv: int, cache: moe_ffn_kv_cache, batch: moe_ffn_k
 
 def moe_ffn_kv_keep(kv: int, caches, n_layers: int, batch: moe_ffn_kv_batch, nodes: int, nodes_stride: int,
                     nodes_cols: int, counts: int, new_len: int, stream: int) -> int:
-    return lib().moe_ffn_kv_keep(kv, caches, n_layers, batch, nodes, nodes_stride, nodes_cols, counts, new_len, stream)
+    return lib().moe_ffn_kv_keep(kv, _by_ref(caches), n_layers, batch, nodes, nodes_stride, nodes_cols, counts, new_len, stream)
 
 
 def moe_ffn_kv_reorder(kv: int, caches, n_layers: int, pages: int, pages_stride: int, pages_cols: int, lengths: int,
                        parents: int, users: int, beams: int, stream: int) -> int:
-    return lib().moe_ffn_kv_reorder(kv, caches, n_layers, pages, pages_stride, pages_cols, lengths, parents, users, beams,
+    return lib().moe_ffn_kv_reorder(kv, _by_ref(caches), n_layers, pages, pages_stride, pages_cols, lengths, parents, users, beams,
                                     stream)
 
 
 def moe_ffn_block_norm(args: moe_ffn_norm, stream: int) -> int:
-    return lib().moe_ffn_block_norm(args, stream)
+    return lib().moe_ffn_block_norm(_by_ref(args), stream)
 
 
 def moe_ffn_rotary_table(freq, axis) -> list:
@@ -438,7 +451,7 @@ def moe_ffn_rotary_table(freq, axis) -> list:
 
 def moe_ffn_rotary_apply(args: moe_ffn_rotary, q: moe_ffn_kv_rows, k: moe_ffn_kv_rows, q_out: moe_ffn_kv_rows,
                          k_out: moe_ffn_kv_rows, stream: int) -> int:
-    return lib().moe_ffn_rotary_apply(args, q, k, q_out, k_out, stream)
+    return lib().moe_ffn_rotary_apply(*(_by_ref(s) for s in (args, q, k, q_out, k_out)), stream)
 
 
 def moe_ffn_beam_workspace_bytes(users: int, beams: int, vocab: int, count: int) -> int:
@@ -446,7 +459,7 @@ def moe_ffn_beam_workspace_bytes(users: int, beams: int, vocab: int, count: int)
 
 
 def moe_ffn_beam_select(args: moe_ffn_beam, workspace: int, workspace_bytes: int, stream: int) -> int:
-    return lib().moe_ffn_beam_select(args, workspace, workspace_bytes, stream)
+    return lib().moe_ffn_beam_select(_by_ref(args), workspace, workspace_bytes, stream)
 
 
 # ------------------------------------------------------------------ torch convenience layer
@@ -664,6 +677,7 @@ class KVCache:
         self.kind = kind
         self.struct = moe_ffn_kv_cache(*(t.data_ptr() if t is not None else None for t in (k, v, k_scale, v_scale)))
         self._ref = ctypes.byref(self.struct)
+        self.packed = bytes(self.struct)
 
 
 class PagedKV:
@@ -817,24 +831,24 @@ class PagedKV:
 
     def _ids(self, what, t, *shape):
         import torch
-        if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        if t.dtype != torch.int32 or t.shape != shape:
             raise ValueError("%s must be torch.int32 of shape %s, got %s of shape %s" % (what, list(shape), t.dtype,
                                                                                          list(t.shape)))
         if t.device != self.device or not t.is_contiguous():
             raise ValueError("%s must be a contiguous tensor on %s" % (what, self.device))
 
     def _layers(self, caches):
-        """Several layers' caches as an array of structures."""
+        """Several layers' caches as an array of structures, packed."""
         if isinstance(caches, (KVCache, dict)):
             caches = [caches]
-        made = []
+        packed = []
         for c in caches:
             if not isinstance(c, KVCache):
                 c = self.cache(**c)
             elif c.kind != self._kind:
                 c = self.cache(c.k, c.v, c.k_scale, c.v_scale)
-            made.append(c)
-        return (moe_ffn_kv_cache * max(len(made), 1))(*(c.struct for c in made)), len(made)
+            packed.append(c.packed)
+        return b"".join(packed), len(packed)
 
     def tree(self, batch: KVBatch, parents) -> KVTree:
         """The trees of a batch whose new tokens are drafted ones: parents, int32 [tokens], gives each node's parent
@@ -924,24 +938,33 @@ def _launch(call, device, *args):
     """A call without a handle, on the current stream of its tensors' device."""
     import torch
     raw = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         return call(*args, raw)
     with torch.cuda.device(device):
         return call(*args, raw)
 
 
-def _norm_rows(what, t, T, H, device):
-    """Address and row stride of bf16 [T, H] rows."""
-    import torch
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, H):
-        raise ValueError("%s must be torch.bfloat16 of shape [%d, %d], got %s of shape %s" % (what, T, H, t.dtype,
-                                                                                              list(t.shape)))
+def _norm_rows(what, t, shape, device, bf16):
+    """Address and row stride of bf16 rows."""
+    if t.dtype != bf16 or t.shape != shape:
+        raise ValueError("%s must be torch.bfloat16 of shape %s, got %s of shape %s" % (what, list(shape), t.dtype,
+                                                                                        list(t.shape)))
     if t.device != device:
         raise ValueError("%s must be on %s" % (what, device))
-    stride = t.stride(0) if T > 1 else H
-    if t.stride(1) != 1 or stride % 8:
+    step, one = t.stride()
+    if shape[0] <= 1:
+        step = shape[1]
+    if one != 1 or step % 8:
         raise ValueError("%s must have contiguous rows, a multiple of 8 elements apart" % what)
-    return t.data_ptr(), stride
+    return t.data_ptr(), step
+
+
+def _norm_weight(what, w, H, device, f32):
+    if w.dtype != f32 or w.numel() != H:
+        _check_type_size(what, w, f32, H)
+    if w.device != device or not w.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor on %s" % (what, device))
+    return w.data_ptr()
 
 
 def block_norm(x, block=None, post=None, gate=None, scale: float = 1.0, pre=None, eps: float = 1e-6, out=None, normed=None):
@@ -954,39 +977,37 @@ def block_norm(x, block=None, post=None, gate=None, scale: float = 1.0, pre=None
     is None without pre, and y is None where it would be x itself (no block, scale 1, no out). out and normed: where y
     and n go, x or block themselves if wished."""
     import torch
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions, got shape %s" % (list(x.shape),))
+    bf16, f32, shape = torch.bfloat16, torch.float32, x.shape
+    if len(shape) != 2:
+        raise ValueError("x must have two dimensions, got shape %s" % (list(shape),))
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    T, H = x.shape
+    T, H = shape
     device = x.device
     if block is None and (post is not None or gate is not None):
         raise ValueError("post and gate need a block")
     if pre is None and normed is not None:
         raise ValueError("normed needs pre")
-    a = moe_ffn_norm()
-    a.x, a.x_stride = _norm_rows("x", x, T, H, device)
-    if block is not None:
-        a.block, a.block_stride = _norm_rows("block", block, T, H, device)
-    if gate is not None:
-        a.gate, a.gate_stride = _norm_rows("gate", gate, T, H, device)
-    for name, w in (("post", post), ("pre", pre)):
-        if w is None:
-            continue
-        _check_type_size(name, w, torch.float32, H)
-        if w.device != device or not w.is_contiguous():
-            raise ValueError("%s must be a contiguous tensor on %s" % (name, device))
-        setattr(a, name, w.data_ptr())
-    if out is None and (block is not None or scale != 1.0 or pre is None):
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
-    if normed is None and pre is not None:
-        normed = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+    xp, xs = _norm_rows("x", x, shape, device, bf16)
+    bp, bs = (0, 0) if block is None else _norm_rows("block", block, shape, device, bf16)
+    gp, gs = (0, 0) if gate is None else _norm_rows("gate", gate, shape, device, bf16)
+    post_p = 0 if post is None else _norm_weight("post", post, H, device, f32)
+    pre_p = 0 if pre is None else _norm_weight("pre", pre, H, device, f32)
+    yp, ys = 0, 0
     if out is not None:
-        a.y, a.y_stride = _norm_rows("out", out, T, H, device)
+        yp, ys = _norm_rows("out", out, shape, device, bf16)
+    elif block is not None or scale != 1.0 or pre is None:
+        out = torch.empty(shape, dtype=bf16, device=device)
+        yp, ys = out.data_ptr(), H
+    np_, ns = 0, 0
     if normed is not None:
-        a.n, a.n_stride = _norm_rows("normed", normed, T, H, device)
-    a.scale, a.eps, a.tokens, a.hidden = scale, eps, T, H
-    _check("moe_ffn_block_norm", _launch(moe_ffn_block_norm, device, a))
+        np_, ns = _norm_rows("normed", normed, shape, device, bf16)
+    elif pre is not None:
+        normed = torch.empty(shape, dtype=bf16, device=device)
+        np_, ns = normed.data_ptr(), H
+    _check("moe_ffn_block_norm",
+           _launch(lib().moe_ffn_block_norm, device,
+                   _PACK_NORM(xp, bp, gp, post_p, pre_p, yp, np_, xs, bs, gs, ys, ns, scale, eps, T, H)))
     return out, normed
 
 
@@ -1007,46 +1028,57 @@ class Rotary:
         self.pairs, self.axes = len(freqs), max(axes) + 1
         self.interleaved, self.scale = bool(interleaved), float(scale)
         self.table = torch.tensor(signed, dtype=torch.int64).to(self.device)
+        self._table = self.table.data_ptr()
+
+    def _rows(self, what, t, T, D, bf16):
+        """A tensor's address and strides, packed, and its heads."""
+        shape = t.shape
+        if t.dtype != bf16 or len(shape) != 3 or shape[0] != T or shape[2] != D:
+            raise ValueError("%s must be torch.bfloat16 of shape [%d, heads, %d], got %s of shape %s" % (what, T, D, t.dtype,
+                                                                                                         list(shape)))
+        if t.device != self.device:
+            raise ValueError("%s must be on %s" % (what, self.device))
+        heads = shape[1]
+        ts, hs, es = t.stride()
+        # A dimension of one element has no stride that matters.
+        if T <= 1:
+            ts = 0
+        if heads <= 1:
+            hs = 0
+        if es != 1 or ts % 8 or hs % 8:
+            raise ValueError("%s must have a contiguous last dimension and strides that are multiples of 8" % what)
+        return _PACK_ROWS(t.data_ptr(), ts, hs), heads
 
     def apply(self, q, k, positions, inverse: bool = False, inplace: bool = False):
         """Turns q and k, bf16 [tokens, heads, width] each (any strides of 8 elements; k may be None), by positions, int32
         [axes, tokens] (or [tokens] for one axis). Returns (q, k), new tensors or, inplace, the given ones. inverse turns
         back, which is also the gradient's way."""
         import torch
-        if positions.dim() == 1:
-            positions = positions.unsqueeze(0)
-        T = q.shape[0]
-        if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[0] < self.axes or positions.shape[1] != T:
+        bf16, device = torch.bfloat16, self.device
+        if q.dim() != 3:
+            raise ValueError("q must have three dimensions, got shape %s" % (list(q.shape),))
+        T, _, D = q.shape
+        at = positions.shape
+        axes, n = at if len(at) == 2 else (1, at[0]) if len(at) == 1 else (0, 0)
+        if positions.dtype != torch.int32 or axes < self.axes or n != T:
             raise ValueError("positions must be torch.int32 of shape [%d, %d], got %s of shape %s" % (
-                self.axes, T, positions.dtype, list(positions.shape)))
-        if positions.device != self.device or (T > 1 and positions.stride(1) != 1) or positions.stride(0) < 0:
-            raise ValueError("positions must have contiguous rows on %s" % self.device)
-        a = moe_ffn_rotary(self.table.data_ptr(), positions.data_ptr(), positions.stride(0) if self.axes > 1 else 0, self.scale,
-                           self.pairs, self.axes, self.interleaved, inverse, T, q.shape[-1], 0, 0)
-        rows, outs = [None, None], [None, None]
-        given = [q, k]
-        for i, (name, t) in enumerate((("q", q), ("k", k))):
-            if t is None:
-                continue
-            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != q.shape[2]:
-                raise ValueError("%s must be torch.bfloat16 of shape [%d, heads, %d], got %s of shape %s" % (
-                    name, T, q.shape[-1], t.dtype, list(t.shape)))
-            if t.device != self.device:
-                raise ValueError("%s must be on %s" % (name, self.device))
-            heads = t.shape[1]
-            given[i] = t if inplace else torch.empty(t.shape, dtype=torch.bfloat16, device=self.device)
-            for to, x in ((rows, t), (outs, given[i])):
-                ts, hs, es = x.stride()
-                if es != 1 or (T > 1 and ts % 8) or (heads > 1 and hs % 8):
-                    raise ValueError("%s must have a contiguous last dimension and strides that are multiples of 8" % name)
-                to[i] = moe_ffn_kv_rows(x.data_ptr(), ts if T > 1 else 0, hs if heads > 1 else 0)
-            if i == 0:
-                a.q_heads = heads
-            else:
-                a.k_heads = heads
-        _check("moe_ffn_rotary_apply",
-               _launch(moe_ffn_rotary_apply, self.device, a, rows[0], rows[1], outs[0], outs[1]))
-        return given[0], given[1]
+                self.axes, T, positions.dtype, list(at)))
+        steps = positions.stride()
+        if positions.device != device or (T > 1 and steps[-1] != 1):
+            raise ValueError("positions must have contiguous rows on %s" % device)
+        q_rows, q_heads = self._rows("q", q, T, D, bf16)
+        k_rows, k_heads = (None, 0) if k is None else self._rows("k", k, T, D, bf16)
+        q_to, k_to = q_rows, k_rows
+        if not inplace:
+            q = torch.empty((T, q_heads, D), dtype=bf16, device=device)
+            q_to = _PACK_ROWS(q.data_ptr(), q_heads * D if T > 1 else 0, D if q_heads > 1 else 0)
+            if k is not None:
+                k = torch.empty((T, k_heads, D), dtype=bf16, device=device)
+                k_to = _PACK_ROWS(k.data_ptr(), k_heads * D if T > 1 else 0, D if k_heads > 1 else 0)
+        a = _PACK_ROTARY(self._table, positions.data_ptr(), steps[0] if self.axes > 1 else 0, self.scale, self.pairs, self.axes,
+                         self.interleaved, inverse, T, D, q_heads, k_heads)
+        _check("moe_ffn_rotary_apply", _launch(lib().moe_ffn_rotary_apply, device, a, q_rows, k_rows, q_to, k_to))
+        return q, k
 
 
 class BeamSearch:
@@ -1062,6 +1094,9 @@ class BeamSearch:
             raise ValueError("invalid configuration")
         self.device = torch.device("cuda", int(device))
         self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+        self._workspace = self.workspace.data_ptr()
+        self._shapes = tuple(torch.Size(t) for t in ((self.users * self.beams, self.vocab), (self.users, self.beams, self.vocab),
+                                                     (self.users, self.beams)))
         self._last = self._last_raw = None
 
     def select(self, logits, scores, finished=None, end_token: int = 0):
@@ -1071,41 +1106,46 @@ class BeamSearch:
         beam and token are -1 where there is no further continuation."""
         import torch
         U, K, V, C = self.users, self.beams, self.vocab, self.count
-        if logits.dtype not in (torch.bfloat16, torch.float32):
+        device, shape, steps = self.device, logits.shape, logits.stride()
+        wide = logits.dtype == torch.float32
+        if not wide and logits.dtype != torch.bfloat16:
             raise ValueError("logits must be torch.bfloat16 or torch.float32, got %s" % logits.dtype)
-        if tuple(logits.shape) == (U, K, V):
-            if U > 1 and K > 1 and logits.stride(0) != K * logits.stride(1):
+        if shape == self._shapes[0]:
+            stride = steps[0]
+        elif shape == self._shapes[1]:
+            if U > 1 and K > 1 and steps[0] != K * steps[1]:
                 raise ValueError("logits' rows must lie at one stride")
-            stride = logits.stride(1) if K > 1 else logits.stride(0)
-        elif tuple(logits.shape) == (U * K, V):
-            stride = logits.stride(0)
+            stride = steps[1] if K > 1 else steps[0]
         else:
-            raise ValueError("logits must have shape [%d, %d], got %s" % (U * K, V, list(logits.shape)))
-        if V > 1 and logits.stride(-1) != 1:
+            raise ValueError("logits must have shape [%d, %d], got %s" % (U * K, V, list(shape)))
+        if V > 1 and steps[-1] != 1:
             raise ValueError("logits must have contiguous rows")
         for name, t, dtype in (("scores", scores, torch.float32), ("finished", finished, torch.bool)):
             if t is None and name == "finished":
                 continue
-            if t.dtype != dtype or tuple(t.shape) != (U, K) or not t.is_contiguous():
+            if t.dtype != dtype or t.shape != self._shapes[2] or not t.is_contiguous():
                 raise ValueError("%s must be contiguous, %s of shape [%d, %d], got %s of shape %s" % (name, dtype, U, K, t.dtype,
                                                                                                       list(t.shape)))
-        for name, t in (("logits", logits), ("scores", scores), ("finished", finished)):
-            if t is not None and t.device != self.device:
-                raise ValueError("%s must be on %s" % (name, self.device))
-        out = torch.empty((U, C), dtype=torch.float32, device=self.device)
-        ids = torch.empty((2, U, C), dtype=torch.int32, device=self.device)
-        a = moe_ffn_beam(logits.data_ptr(), stride if U * K > 1 else V, scores.data_ptr(),
-                         finished.data_ptr() if finished is not None else None, out.data_ptr(), ids[0].data_ptr(),
-                         ids[1].data_ptr(), logits.dtype == torch.float32, int(end_token), U, K, V, C)
-        raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+            if t.device != device:
+                raise ValueError("%s must be on %s" % (name, device))
+        if logits.device != device:
+            raise ValueError("logits must be on %s" % device)
+        out = torch.empty((U, C), dtype=torch.float32, device=device)
+        ids = torch.empty((2, U, C), dtype=torch.int32, device=device)
+        at = ids.data_ptr()
+        a = _PACK_BEAM(logits.data_ptr(), stride if U * K > 1 else V, scores.data_ptr(),
+                       0 if finished is None else finished.data_ptr(), out.data_ptr(), at, at + 4 * U * C, wide, end_token, U, K, V,
+                       C)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
         if raw != self._last_raw and not torch.cuda.is_current_stream_capturing():
-            stream = torch.cuda.current_stream(self.device)
+            stream = torch.cuda.current_stream(device)
             if self._last is not None:
                 stream.wait_stream(self._last)
             self.workspace.record_stream(stream)  # dropped early, it stays until the stream is done with it
             self._last, self._last_raw = stream, raw
-        _check("moe_ffn_beam_select", _launch(moe_ffn_beam_select, self.device, a, self.workspace.data_ptr(), self.nbytes))
-        return out, ids[0], ids[1]
+        _check("moe_ffn_beam_select", _launch(lib().moe_ffn_beam_select, device, a, self._workspace, self.nbytes))
+        beams, tokens = ids.unbind(0)
+        return out, beams, tokens
 
 
 def view_tensor(ptr: int, shape, dtype, device: int = 0):

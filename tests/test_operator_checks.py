@@ -185,8 +185,8 @@ def test_calls_without_a_handle():
     assert L.moe_ffn_kv_tree(None, b, None, None, None, None) == B.MOE_FFN_EINVAL
     assert L.moe_ffn_kv_tree_attention(None, c, b, None, r, 1.0, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
     assert L.moe_ffn_kv_tree_attention(None, c, None, None, r, 1.0, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
-    assert L.moe_ffn_kv_keep(None, c, 1, b, None, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
-    assert L.moe_ffn_kv_reorder(None, c, 1, None, 0, 0, None, None, 0, 1, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_keep(None, ctypes.byref(c), 1, b, None, 0, 0, None, None, None) == B.MOE_FFN_EINVAL
+    assert L.moe_ffn_kv_reorder(None, ctypes.byref(c), 1, None, 0, 0, None, None, 0, 1, None) == B.MOE_FFN_EINVAL
 
 
 def _stub():
