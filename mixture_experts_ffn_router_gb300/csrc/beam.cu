@@ -36,7 +36,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;                     // 16-byte vectors of a thread in a tile
-constexpr int kNoted = 1024;                 // vectors
+constexpr int kNoted = 512;                  // vectors
 constexpr int kList = 4096;
 constexpr int kListLong = kList - kThreads * 8 - 32;  // what still has room for a vector of each thread, and the ends
 constexpr int kMaxSplits = 64;
@@ -324,7 +324,8 @@ struct Shared {
   unsigned long long list[kList];
   unsigned long long best[kMaxCount];
   unsigned long long warp_best[2][kWarps];
-  int noted[kNoted];
+  uint4 noted[kNoted];
+  int noted_at[kNoted];
   alignas(16) int bins[kBins];
   Sum warp_sum[kWarps];
   long long warp_fixed[kWarps];
@@ -444,10 +445,12 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
 #pragma unroll
     for (int g = 0; g < kVecs * N / 8; ++g) {
       float f[8];
+      uint4 now[8 / N];
 #pragma unroll
       for (int k = 0; k < 8 / N; ++k) {
         const int u = g * (8 / N) + k;
-        L::unpack(cut<SHIFTED>(v[u], shift), f + k * N);
+        now[k] = cut<SHIFTED>(v[u], shift);
+        L::unpack(now[k], f + k * N);
         v[u] = load_vec<T, SHIFTED>(blocks, at + (kVecs + u) * kThreads, lo, hi);  // the next tile's (none after the last)
       }
       float e[8];
@@ -459,7 +462,9 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
 #pragma unroll
         for (int k = 0; k < 8 / N; ++k) {
           const int to = atomicAdd(&s.n_noted, 1);
-          if (to < kNoted) s.noted[to] = at + (g * (8 / N) + k) * kThreads;
+          if (to >= kNoted) continue;
+          s.noted[to] = now[k];
+          s.noted_at[to] = at + (g * (8 / N) + k) * kThreads;
         }
       }
       sum2 = add2(sum2, add2(add2(two(e[0], e[1]), two(e[2], e[3])), add2(two(e[4], e[5]), two(e[6], e[7]))));
@@ -474,9 +479,9 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
   __syncthreads();
   const int noted = s.n_noted;
   for (int i = tid; i < min(noted, kNoted); i += kThreads) {
-    const int at = s.noted[i];
+    const int at = s.noted_at[i];
     float f[N];
-    L::unpack(cut<SHIFTED>(load_vec<T, SHIFTED>(blocks, at, lo, hi), shift), f);
+    L::unpack(s.noted[i], f);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       if (!(f[k] > above)) continue;
@@ -612,7 +617,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   __shared__ double shift[MOE_FFN_BEAM_MAX];
   __shared__ float rough_shift[MOE_FFN_BEAM_MAX], beam_ref[MOE_FFN_BEAM_MAX];
   __shared__ bool ended[MOE_FFN_BEAM_MAX];
-  __shared__ float held[kJoinHeld];
+  __shared__ float held[kJoinHeld], held_x[kJoinHeld];
+  __shared__ int held_token[kJoinHeld];
   __shared__ Candidate list[kJoinList];
   __shared__ float warp_top[kJoinWarps], warp_off[kJoinWarps];
   __shared__ alignas(16) int bins[kBins];
@@ -627,6 +633,14 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   static_assert(kJoinThreads == kBins && kThreads == kBins, "a bin to a thread");
   bins[tid] = 0;
   if (tid == 0) found = 0;
+  // The candidates are on their way while the sums are formed.
+#pragma unroll
+  for (int j = 0; j < kJoinHeld / kJoinThreads; ++j) {
+    const int i = tid + j * kJoinThreads;
+    if (i >= n) break;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&held_x[i])), "l"(xs + i) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&held_token[i])), "l"(tokens + i) : "memory");
+  }
   for (int k = warp; k < p.beams; k += kJoinWarps) {
     const long long row = row0 + k;
     static_assert(kMaxSplits == 64, "two parts of a row to a lane");
@@ -672,7 +686,10 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
       rough_shift[k] = static_cast<float>(sh);
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  auto x_of = [&](int i) { return i < kJoinHeld ? held_x[i] : xs[i]; };
+  auto token_of = [&](int i) { return i < kJoinHeld ? held_token[i] : tokens[i]; };
   const float per_beam_inv = 1.0f / static_cast<float>(per_beam);
   // (n is at most 2^18: the product is off by less than the distance of i + 1/2 from a multiple.)
   auto beam_of = [&](int i) { return static_cast<int>((static_cast<float>(i) + 0.5f) * per_beam_inv); };
@@ -684,17 +701,17 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
       off = 0x1p-22f * fabsf(t);
       return i == k * per_beam ? t : -INFINITY;
     }
-    const float d = xs[i] - beam_ref[k];
+    const float d = x_of(i) - beam_ref[k];
     off = 0x1p-22f * (fabsf(d) + fabsf(t));
-    return tokens[i] >= 0 ? d + t : -INFINITY;
+    return token_of(i) >= 0 ? d + t : -INFINITY;
   };
   auto exact = [&](int i) {
     const int k = beam_of(i);
     double v = shift[k];
     int token = p.end_token;
     if (!ended[k]) {
-      v += static_cast<double>(xs[i]) - static_cast<double>(beam_ref[k]);
-      token = tokens[i];
+      v += static_cast<double>(x_of(i)) - static_cast<double>(beam_ref[k]);
+      token = token_of(i);
     } else if (i != k * per_beam) {
       token = -1;
     }
@@ -793,13 +810,13 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   }
 }
 
-// Parts of a row: enough for four CTAs on each SM, of a tile at least, and few tiles where rows are long, so that
-// the lists stay short. (Tiles of bf16 logits, which have the larger ones: one workspace serves both types.)
-int beam_splits(int rows, int vocab) {
+// Parts of a row: enough for four CTAs on each SM, of a tile at least. (Tiles of bf16 logits, which have the larger ones: one workspace serves both types.)
+int beam_splits(int rows, int vocab, int count) {
   constexpr int kTile = kThreads * kVecs * 8;
   const int tiles = (vocab + kTile - 1) / kTile;
   int splits = (4 * 152 + rows - 1) / (rows > 0 ? rows : 1);
-  const int least = (tiles + 15) / 16;
+  // (Few tiles: those that note as many vectors, a few more than `count` each, as there is room for.)
+  const int least = count > 20 ? (tiles * count + 319) / 320 : (tiles + 15) / 16;
   if (splits < least) splits = least;
   if (splits > tiles) splits = tiles;
   if (splits > kMaxSplits) splits = kMaxSplits;
@@ -816,7 +833,7 @@ struct BeamLayout {
 };
 
 BeamLayout beam_layout(int users, int beams, int vocab, int count) {
-  const size_t parts = static_cast<size_t>(users) * beams * beam_splits(users * beams, vocab);
+  const size_t parts = static_cast<size_t>(users) * beams * beam_splits(users * beams, vocab, count);
   BeamLayout l;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -888,7 +905,7 @@ extern "C" int moe_ffn_beam_select(const moe_ffn_beam* a, void* workspace, size_
   p.beams = a->beams;
   p.vocab = a->vocab;
   p.count = a->count;
-  p.splits = beam_splits(rows, a->vocab);
+  p.splits = beam_splits(rows, a->vocab, a->count);
   p.part = (a->vocab / static_cast<int>(16 / element) + p.splits - 1) / p.splits;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool shifted = reinterpret_cast<uintptr_t>(a->logits) % 16 != 0 || (rows > 1 && a->logits_stride * element % 16 != 0);
