@@ -1,9 +1,10 @@
 // rotary.cu — rotary positions with one or several axes, on queries and keys in one launch.
 //
 // Pair i of a head turns by the angle positions[axis[i], token] * freq[i]. Each value is read and written once (4 bytes
-// meet 3 operations), so HBM bounds it, or the launch where tokens are few. A CTA takes a token: its threads first
-// load the pairs of all heads that are theirs, then form the token's cosines and sines, each once, in shared
-// memory, while the loads are under way, and turn the pairs.
+// meet 3 operations), so HBM bounds it, or the launch where tokens are few. A CTA takes a token. A thread has the same
+// two vectors of pairs in several heads: it loads those of its first heads, the CTA forms the token's cosines and
+// sines, each once, while these are under way, and the thread keeps its own in registers for all its heads. (Read
+// from shared memory for each head they bounded the kernel: 79 us for 9001 tokens of 18 heads of width 512.)
 //
 // Angles. In fp32 a position of a million leaves a tenth of a radian unknown, and in fp64 an angle would cost more
 // than the rest. Here a frequency is a fraction of a turn in 64-bit fixed point: its product with the position, modulo
@@ -21,8 +22,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kAtOnce = 4;  // items of a thread whose loads are under way together
+constexpr int kThreads = 128;   // at least, where heads are narrow
+constexpr int kMaxThreads = 160;
+constexpr int kAtOnce = 4;      // heads of a thread whose loads are under way together
 
 struct Rows {
   const uint16_t* in;
@@ -38,7 +40,7 @@ struct RotaryParams {
   float scale;
   float sign;
   int pairs, axes, head_dim, q_heads, k_heads;
-  int copy;  // elements after the pairs are to be copied
+  int copy;  // whether elements after the pairs are to be copied
 };
 
 template <int VEC>
@@ -74,104 +76,114 @@ __device__ __forceinline__ typename Vec<VEC>::T pack(const float (&f)[VEC]) {
   return v;
 }
 
-// VEC: bf16 values of a vector. An item is a head's vector of first elements and the one of second elements, or,
-// interleaved, two neighbouring vectors' worth of pairs; after the pairs' items come those of the rest of a head,
-// two vectors each where they go.
+// VEC: bf16 values of a vector. Of a head, `turned` threads have the vector of first elements and the one of second
+// elements (interleaved: two neighbouring vectors' worth of pairs) of VEC pairs each, the `per - turned` next ones two
+// vectors of the elements after them each, where these go elsewhere. `across` heads are taken side by side.
 template <int VEC, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const RotaryParams p, int turned, int per, int across) {
   using V = typename Vec<VEC>::T;
-  __shared__ float2 cs[MOE_FFN_ROTARY_MAX_PAIRS];
+  __shared__ alignas(16) float2 cs[MOE_FFN_ROTARY_MAX_PAIRS];
   pdl_wait();
   pdl_launch_dependents();
   const long long token = blockIdx.x;
-  const int turned = p.pairs / VEC;                                             // items of a head's pairs
-  const int rest = p.copy ? (p.head_dim - 2 * p.pairs) / VEC : 0;               // and vectors after them
-  const int per = turned + (rest + 1) / 2;
-  const int items = (p.q_heads + p.k_heads) * per;
-  bool ready = false;
-  for (int base = threadIdx.x;; base += kAtOnce * kThreads) {
-    V a[kAtOnce], b[kAtOnce];
-    uint16_t *to_a[kAtOnce], *to_b[kAtOnce];
-    int at[kAtOnce];
+  const int first = threadIdx.x / per, i = threadIdx.x - first * per;
+  const bool turns = i < turned, live = first < across;
+  // Elements where the two vectors begin.
+  int x, y;
+  if (turns) {
+    x = INTERLEAVED ? 2 * i * VEC : i * VEC;
+    y = INTERLEAVED ? x + VEC : x + p.pairs;
+  } else {
+    x = 2 * p.pairs + 2 * (i - turned) * VEC;
+    y = x + VEC;
+  }
+  const bool two = y + VEC <= p.head_dim;
+  const int heads = live ? p.q_heads + p.k_heads : 0;
+  const uint16_t* q_in = p.q.in + token * p.q.in_token;
+  const uint16_t* k_in = p.k.in + token * p.k.in_token;
+  uint16_t* q_out = p.q.out + token * p.q.out_token;
+  uint16_t* k_out = p.k.out + token * p.k.out_token;
+  V a[kAtOnce], b[kAtOnce];
+  auto load = [&](int head0) {
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
-      const int item = base + j * kThreads;
-      at[j] = -1;
-      to_a[j] = to_b[j] = nullptr;
-      if (item >= items) continue;
-      int head = item / per;
-      const int i = item - head * per;
-      const bool key = head >= p.q_heads;
-      if (key) head -= p.q_heads;
-      const Rows& r = key ? p.k : p.q;
-      int x, y;  // elements where the two vectors begin
-      if (i < turned) {
-        at[j] = i * VEC;
-        x = INTERLEAVED ? 2 * i * VEC : i * VEC;
-        y = INTERLEAVED ? x + VEC : x + p.pairs;
-      } else {
-        x = 2 * p.pairs + 2 * (i - turned) * VEC;
-        y = x + VEC;
-      }
-      const bool two = y + VEC <= p.head_dim;
-      const uint16_t* from = r.in + token * r.in_token + head * r.in_head;
-      uint16_t* to = r.out + token * r.out_token + head * r.out_head;
+      const int head = head0 + j * across;
+      if (head >= heads) continue;
+      const uint16_t* from = head < p.q_heads ? q_in + head * p.q.in_head : k_in + (head - p.q_heads) * p.k.in_head;
       a[j] = *reinterpret_cast<const V*>(from + x);
-      to_a[j] = to + x;
-      if (two) {
-        b[j] = *reinterpret_cast<const V*>(from + y);
-        to_b[j] = to + y;
-      }
+      if (two) b[j] = *reinterpret_cast<const V*>(from + y);
     }
-    if (!ready) {
-      for (int i = threadIdx.x; i < p.pairs; i += kThreads) {
-        const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(p.table + i);
-        const int axis = e.y < static_cast<unsigned long long>(p.axes) ? static_cast<int>(e.y) : 0;
-        const long long pos = p.positions[axis * p.positions_stride + token];
-        const unsigned long long turns = e.x * static_cast<unsigned long long>(pos);
-        // The nearest number of 2^-32 turns; two of them to a half.
-        const int near = static_cast<int>((turns + 0x80000000ull) >> 32);
-        float s, c;
-        sincospif(static_cast<float>(near) * 0x1p-31f, &s, &c);
-        cs[i] = make_float2(c * p.scale, s * p.scale * p.sign);
-      }
-      __syncthreads();
-      ready = true;
+  };
+  load(first);
+  for (int k = threadIdx.x; k < p.pairs; k += blockDim.x) {
+    const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(p.table + k);
+    const int axis = e.y < static_cast<unsigned long long>(p.axes) ? static_cast<int>(e.y) : 0;
+    const long long pos = p.positions[axis * p.positions_stride + token];
+    const unsigned long long turn = e.x * static_cast<unsigned long long>(pos);
+    // The nearest number of 2^-32 turns; two of them to a half.
+    const int near = static_cast<int>((turn + 0x80000000ull) >> 32);
+    float s, c;
+    sincospif(static_cast<float>(near) * 0x1p-31f, &s, &c);
+    cs[k] = make_float2(c * p.scale, s * p.scale * p.sign);
+  }
+  __syncthreads();
+  float2 u[VEC];
+  if (live && turns) {
+#pragma unroll
+    for (int k = 0; k < VEC; k += 2) {
+      const float4 w = *reinterpret_cast<const float4*>(&cs[i * VEC + k]);
+      u[k] = make_float2(w.x, w.y);
+      u[k + 1] = make_float2(w.z, w.w);
     }
+  }
+  for (int head0 = first; head0 < heads; head0 += kAtOnce * across) {
+    if (head0 != first) load(head0);
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
-      if (!to_a[j]) continue;
-      if (at[j] >= 0) {
+      const int head = head0 + j * across;
+      if (head >= heads) continue;
+      if (turns) {
         float f[VEC], g[VEC];
         unpack<VEC>(a[j], f);
         unpack<VEC>(b[j], g);
         if constexpr (INTERLEAVED) {
 #pragma unroll
-          for (int i = 0; i < VEC / 2; ++i) {
-            const float2 u = cs[at[j] + i], w = cs[at[j] + VEC / 2 + i];
-            const float f0 = f[2 * i], g0 = g[2 * i];
-            f[2 * i] = f0 * u.x - f[2 * i + 1] * u.y;
-            f[2 * i + 1] = f[2 * i + 1] * u.x + f0 * u.y;
-            g[2 * i] = g0 * w.x - g[2 * i + 1] * w.y;
-            g[2 * i + 1] = g[2 * i + 1] * w.x + g0 * w.y;
+          for (int k = 0; k < VEC / 2; ++k) {
+            const float2 v = u[k], w = u[VEC / 2 + k];
+            const float f0 = f[2 * k], g0 = g[2 * k];
+            f[2 * k] = f0 * v.x - f[2 * k + 1] * v.y;
+            f[2 * k + 1] = f[2 * k + 1] * v.x + f0 * v.y;
+            g[2 * k] = g0 * w.x - g[2 * k + 1] * w.y;
+            g[2 * k + 1] = g[2 * k + 1] * w.x + g0 * w.y;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float2 u = cs[at[j] + i];
-            const float f0 = f[i];
-            f[i] = f0 * u.x - g[i] * u.y;
-            g[i] = g[i] * u.x + f0 * u.y;
+          for (int k = 0; k < VEC; ++k) {
+            const float f0 = f[k];
+            f[k] = f0 * u[k].x - g[k] * u[k].y;
+            g[k] = g[k] * u[k].x + f0 * u[k].y;
           }
         }
         a[j] = pack<VEC>(f);
         b[j] = pack<VEC>(g);
       }
-      *reinterpret_cast<V*>(to_a[j]) = a[j];
-      if (to_b[j]) *reinterpret_cast<V*>(to_b[j]) = b[j];
+      uint16_t* to = head < p.q_heads ? q_out + head * p.q.out_head : k_out + (head - p.q_heads) * p.k.out_head;
+      *reinterpret_cast<V*>(to + x) = a[j];
+      if (two) *reinterpret_cast<V*>(to + y) = b[j];
     }
-    if (base - static_cast<int>(threadIdx.x) + kAtOnce * kThreads >= items) break;
   }
+}
+
+template <int VEC, bool INTERLEAVED>
+cudaError_t launch(const RotaryParams& p, int tokens, cudaStream_t s) {
+  const int turned = p.pairs / VEC, rest = p.copy ? (p.head_dim - 2 * p.pairs) / VEC : 0;
+  const int per = turned + (rest + 1) / 2;
+  // As many heads side by side as a CTA of about kThreads threads has room for, and there are.
+  const int heads = p.q_heads + p.k_heads;
+  int across = per >= kThreads ? 1 : kThreads / per;
+  if (across > heads) across = heads;
+  const int threads = (per * across + 31) / 32 * 32;
+  return launch_pdl(rotary_kernel<VEC, INTERLEAVED>, dim3(tokens), dim3(threads), 0, s, p, turned, per, across);
 }
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -290,14 +302,9 @@ extern "C" int moe_ffn_rotary_apply(const moe_ffn_rotary* a, const moe_ffn_kv_ro
   p.q_heads = a->q_heads;
   p.k_heads = a->k_heads;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(a->tokens), block(kThreads);
   // Vectors of 16 bytes where the second elements of the pairs begin at a multiple of that, of 8 else.
   cudaError_t e;
-  if (a->pairs % 8 == 0)
-    e = a->interleaved ? launch_pdl(rotary_kernel<8, true>, grid, block, 0, s, p)
-                       : launch_pdl(rotary_kernel<8, false>, grid, block, 0, s, p);
-  else
-    e = a->interleaved ? launch_pdl(rotary_kernel<4, true>, grid, block, 0, s, p)
-                       : launch_pdl(rotary_kernel<4, false>, grid, block, 0, s, p);
+  if (a->pairs % 8 == 0) e = a->interleaved ? launch<8, true>(p, a->tokens, s) : launch<8, false>(p, a->tokens, s);
+  else e = a->interleaved ? launch<4, true>(p, a->tokens, s) : launch<4, false>(p, a->tokens, s);
   return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
 }
