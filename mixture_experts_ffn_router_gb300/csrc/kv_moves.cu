@@ -18,7 +18,7 @@ constexpr int kNodes = 256;
 constexpr int kWords = kNodes / 32;
 
 // A sequence's tree per CTA, a thread per node, which walks up to the root over parents in shared memory.
-__global__ void __launch_bounds__(kNodes) kv_tree_kernel(const KvBatch b, const KvCache c, const int32_t* parents, uint32_t* masks,
+__global__ void __launch_bounds__(kNodes) kv_tree_masks_kernel(const KvBatch b, const KvCache c, const int32_t* parents, uint32_t* masks,
                                                          int32_t* depth, unsigned int* status) {
   __shared__ int parent[kNodes];
   pdl_wait();
@@ -252,7 +252,7 @@ cudaError_t kv_moves_setup() {
 
 cudaError_t launch_kv_tree(const KvBatch& b, const KvCache& c, const int32_t* parents, uint32_t* masks, int32_t* depth,
                            unsigned int* status, cudaStream_t s) {
-  return launch_pdl(kv_tree_kernel, dim3(b.n_seqs + 1), dim3(kNodes), 0, s, b, c, parents, masks, depth, status);
+  return launch_pdl(kv_tree_masks_kernel, dim3(b.n_seqs + 1), dim3(kNodes), 0, s, b, c, parents, masks, depth, status);
 }
 
 cudaError_t launch_kv_keep(const KvBatch& b, const KvCache& c, const KvLayers& l, int n_layers, const int32_t* nodes,

@@ -3,9 +3,14 @@
 //   y = scale * (x + gate * N(block; post)),  n = N(y; pre),  N(v; w) = v / sqrt(mean(v^2) + eps) * (1 + w)
 //
 // 8 to 10 bytes per value meet a dozen operations, so HBM bounds it, or the launch where tokens are few. A CTA takes
-// one row, whose values stay in its registers from the only load to the stores: a thread holds up to kMaxVecs vectors
-// of eight of x, block and gate, all loaded before the first is used. The two sums of squares are a reduction over
-// the CTA each. The row's statistics and y are fp32; y and n are rounded once.
+// a row at a time, whose values stay in its registers from the only load to the stores: a thread holds up to kMaxVecs
+// vectors of eight of x, block and gate. The two sums of squares are a reduction over the CTA each. The row's statistics
+// and y are fp32; y and n are rounded once.
+//
+// Narrow rows: a warp for each, whose sums need no barrier. Others, where they are few or very wide: a CTA for each, all its
+// loads before the first use. Many rows: CTAs that stay, each with every gridDim-th row, the weights in registers and the
+// next kAhead rows on their way into shared memory (a thread copies what it will read itself, so no barrier is needed for
+// that).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -20,6 +25,7 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 constexpr int kMaxVecs = 4;
+constexpr int kRowWarps = 8;    // of a CTA, where a row is a warp's
 
 struct NormParams {
   const uint16_t* x;
@@ -53,17 +59,19 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// The sum over the CTA, in every thread. `sums` holds a float per warp and is not used again before the next barrier.
-__device__ __forceinline__ float cta_sum(float v, float* sums) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  v = lane < warps ? sums[lane] : 0.0f;
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// The sum over the CTA, in every thread. `sums` holds a float per warp and is not used again before the next barrier.
+__device__ __forceinline__ float cta_sum(float v, float* sums) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  return warp_sum(lane < warps ? sums[lane] : 0.0f);
 }
 
 // Multiplies by (1 + w) of eight features.
@@ -74,17 +82,21 @@ __device__ __forceinline__ void weighted(float (&f)[8], const float* w, float r)
   for (int i = 0; i < 8; ++i) f[i] = f[i] * r * (1.0f + g[i]);
 }
 
-template <int VECS>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormParams p) {
+// WARP: a row to a warp, else to a CTA.
+template <int VECS, bool WARP>
+__global__ void __launch_bounds__(WARP ? kRowWarps * 32 : kMaxThreads) block_norm_kernel(const NormParams p, int tokens) {
   __shared__ float sums[2][32];
   pdl_wait();
   pdl_launch_dependents();
-  const long long row = blockIdx.x;
+  const long long row = WARP ? static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && row >= tokens) return;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, n = WARP ? 32 : blockDim.x;
   const int vecs = p.hidden / 8;
+  auto row_sum = [&](float v, float* to) { return WARP ? warp_sum(v) : cta_sum(v, to); };
   uint4 xv[VECS], bv[VECS], gv[VECS];
 #pragma unroll
   for (int j = 0; j < VECS; ++j) {
-    const int at = (j * blockDim.x + threadIdx.x) * 8;
+    const int at = (j * n + tid) * 8;
     xv[j] = bv[j] = gv[j] = make_uint4(0u, 0u, 0u, 0u);
     if (at >= p.hidden) continue;
     xv[j] = *reinterpret_cast<const uint4*>(p.x + row * p.x_stride + at);
@@ -101,12 +113,12 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormParam
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fmaf(f[j][i], f[j][i], sum);
     }
-    r = rsqrtf(cta_sum(sum, sums[0]) / static_cast<float>(p.hidden) + p.eps);
+    r = rsqrtf(row_sum(sum, sums[0]) / static_cast<float>(p.hidden) + p.eps);
   }
   float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < VECS; ++j) {
-    const int v = j * blockDim.x + threadIdx.x;
+    const int v = j * n + tid;
     if (v >= vecs) continue;
     float x[8];
     unpack(xv[j], x);
@@ -130,14 +142,100 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormParam
     if (p.y) *reinterpret_cast<uint4*>(p.y + row * p.y_stride + v * 8) = pack(f[j]);
   }
   if (!p.n) return;
-  r = rsqrtf(cta_sum(sum, sums[1]) / static_cast<float>(p.hidden) + p.eps);
+  r = rsqrtf(row_sum(sum, sums[1]) / static_cast<float>(p.hidden) + p.eps);
 #pragma unroll
   for (int j = 0; j < VECS; ++j) {
-    const int v = j * blockDim.x + threadIdx.x;
+    const int v = j * n + tid;
     if (v >= vecs) continue;
     weighted(f[j], p.pre + v * 8, r);
     *reinterpret_cast<uint4*>(p.n + row * p.n_stride + v * 8) = pack(f[j]);
   }
+}
+
+constexpr int kAhead = 3;
+constexpr int kSms = 152;
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// Rows of up to 8 * THREADS values, a vector of eight to a thread. `parts`: 1, and 1 for a block and for a gate each.
+template <int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) block_norm_rows_kernel(const NormParams p, int tokens, int parts) {
+  extern __shared__ uint4 ring[];  // [kAhead + 1][parts][blockDim.x]
+  __shared__ float sums[2][2][32];
+  const int tid = threadIdx.x, n = blockDim.x, at = tid * 8;
+  const bool live = at < p.hidden;
+  pdl_wait();
+  pdl_launch_dependents();
+  auto fetch = [&](long long row, int slot) {
+    if (live && row < tokens) {
+      const uint32_t to = smem_u32(ring + slot * parts * n + tid);
+      copy16(to, p.x + row * p.x_stride + at);
+      if (p.block) copy16(to + 16 * n, p.block + row * p.block_stride + at);
+      if (p.gate) copy16(to + 32 * n, p.gate + row * p.gate_stride + at);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
+  float post[8], pre[8];  // 1 + w
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    post[i] = live && p.post ? 1.0f + p.post[at + i] : 1.0f;
+    pre[i] = live && p.pre ? 1.0f + p.pre[at + i] : 1.0f;
+  }
+  const float inv = 1.0f / static_cast<float>(p.hidden);
+  int slot = 0;
+  for (long long row = blockIdx.x, k = 0; row < tokens; row += gridDim.x, ++k) {
+    fetch(row + static_cast<long long>(kAhead) * gridDim.x, slot == 0 ? kAhead : slot - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    const uint4* mine = ring + slot * parts * n + tid;
+    if (++slot > kAhead) slot = 0;
+    float f[8], x[8];
+    unpack(live ? mine[0] : make_uint4(0u, 0u, 0u, 0u), x);
+    if (p.block) {
+      unpack(live ? mine[n] : make_uint4(0u, 0u, 0u, 0u), f);
+      if (p.post) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
+        // (Two sets of sums: a warp may be a row ahead of one that still reads.)
+        const float r = rsqrtf(cta_sum(sum, sums[k & 1][0]) * inv + p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * r * post[i];
+      }
+      if (p.gate) {
+        float g[8];
+        unpack(live ? mine[2 * n] : make_uint4(0u, 0u, 0u, 0u), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= g[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += f[i];
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] *= p.scale;
+      sum = fmaf(x[i], x[i], sum);
+    }
+    if (p.y && live) *reinterpret_cast<uint4*>(p.y + row * p.y_stride + at) = pack(x);
+    if (!p.n) continue;
+    const float r = rsqrtf(cta_sum(sum, sums[k & 1][1]) * inv + p.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * pre[i];
+    if (live) *reinterpret_cast<uint4*>(p.n + row * p.n_stride + at) = pack(x);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// CTAS of THREADS to an SM, or more of fewer.
+template <int THREADS, int CTAS>
+cudaError_t launch_rows(const NormParams& p, int tokens, int parts, dim3 block, int smem, cudaStream_t s) {
+  const auto kernel = block_norm_rows_kernel<THREADS, CTAS>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kAhead + 1) * 3 * 16 * THREADS);
+  return e == cudaSuccess ? launch_pdl(kernel, dim3(THREADS * CTAS / block.x * kSms), block, smem, s, p, tokens, parts) : e;
 }
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -208,11 +306,24 @@ extern "C" int moe_ffn_block_norm(const moe_ffn_norm* a, void* stream) {
   const dim3 grid(a->tokens), block(((vecs + per - 1) / per + 31) / 32 * 32);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  switch (per) {
-    case 1: e = launch_pdl(block_norm_kernel<1>, grid, block, 0, s, p); break;
-    case 2: e = launch_pdl(block_norm_kernel<2>, grid, block, 0, s, p); break;
-    case 3: e = launch_pdl(block_norm_kernel<3>, grid, block, 0, s, p); break;
-    default: e = launch_pdl(block_norm_kernel<kMaxVecs>, grid, block, 0, s, p); break;
+  // Which of the three, in us of two inputs without a gate. A warp to a row or a CTA: 40000 rows of 264 24 and 41, of 512 29 and
+  // 42; of 1024 the warp's loads are too few (8192 rows: 17 and 15). CTAs that stay, or one a row: 8192 rows of 2816 35 and
+  // 40, of 4096 46 and 56, of 2048 26 and 28; of 1536 21 and 21, and narrower ones with a gate lose (40000 of 768: 55 and
+  // 50). Below about eight rows to each they lose too (2000 rows of 2816: 11.6 and 10.7).
+  if (vecs <= 64) {
+    const dim3 rows((a->tokens + kRowWarps - 1) / kRowWarps), warps(kRowWarps * 32);
+    e = vecs <= 32 ? launch_pdl(block_norm_kernel<1, true>, rows, warps, 0, s, p, a->tokens)
+                   : launch_pdl(block_norm_kernel<2, true>, rows, warps, 0, s, p, a->tokens);
+  } else if (per == 1 && block.x >= 224 && static_cast<long long>(a->tokens) * block.x >= 8LL * kSms * 1152) {
+    const int parts = 1 + (a->block ? 1 : 0) + (a->gate ? 1 : 0), smem = (kAhead + 1) * parts * 16 * static_cast<int>(block.x);
+    e = block.x <= 384 ? launch_rows<384, 3>(p, a->tokens, parts, block, smem, s) : launch_rows<512, 2>(p, a->tokens, parts, block, smem, s);
+  } else {
+    switch (per) {
+      case 1: e = launch_pdl(block_norm_kernel<1, false>, grid, block, 0, s, p, a->tokens); break;
+      case 2: e = launch_pdl(block_norm_kernel<2, false>, grid, block, 0, s, p, a->tokens); break;
+      case 3: e = launch_pdl(block_norm_kernel<3, false>, grid, block, 0, s, p, a->tokens); break;
+      default: e = launch_pdl(block_norm_kernel<kMaxVecs, false>, grid, block, 0, s, p, a->tokens); break;
+    }
   }
   return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
 }

@@ -78,12 +78,12 @@ def _run(**kw):
 
 @pytest.mark.parametrize("gate", ["", "one", "token"])
 @pytest.mark.parametrize("T,H", [(1, 8), (3, 16), (5, 264), (64, 2816), (2, 4096), (3, 4104), (1, 8200), (7, 12296), (2, 16384),
-                                 (1300, 40)])
+                                 (1300, 40), (6, 512), (9, 520), (4001, 2816), (7000, 1800), (2800, 4096)])
 def test_whole_form(T, H, gate):
     _run(**_inputs(T, H, seed=T + H, gate=gate), scale=0.8)
 
 
-@pytest.mark.parametrize("T,H", [(1, 2816), (9, 72)])
+@pytest.mark.parametrize("T,H", [(1, 2816), (9, 72), (4100, 2816), (2900, 3592)])
 def test_parts(T, H):
     s = _inputs(T, H, seed=3)
     _run(x=s["x"], pre=s["pre"])
@@ -143,6 +143,14 @@ def test_strided_rows_and_places():
                         normed=wide[:, 1])
     assert torch.equal(wide[:, 0], want[0]) and torch.equal(wide[:, 1], want[1])
     assert torch.equal(wide[:, 2], s["gate"])
+
+
+@pytest.mark.parametrize("T,H", [(9, 264), (4500, 2816)])
+def test_in_place_over_many_rows(T, H):
+    s = _inputs(T, H, seed=11, gate="one")
+    want = B.block_norm(**s)
+    y, n = B.block_norm(**s, out=s["x"], normed=s["block"])
+    assert y is s["x"] and torch.equal(y, want[0]) and torch.equal(n, want[1])
 
 
 def test_no_tokens():
