@@ -1131,11 +1131,11 @@ class BeamSearch:
         if logits.device != device:
             raise ValueError("logits must be on %s" % device)
         out = torch.empty((U, C), dtype=torch.float32, device=device)
-        ids = torch.empty((2, U, C), dtype=torch.int32, device=device)
-        at = ids.data_ptr()
+        beams = torch.empty((U, C), dtype=torch.int32, device=device)
+        tokens = torch.empty((U, C), dtype=torch.int32, device=device)
         a = _PACK_BEAM(logits.data_ptr(), stride if U * K > 1 else V, scores.data_ptr(),
-                       0 if finished is None else finished.data_ptr(), out.data_ptr(), at, at + 4 * U * C, wide, end_token, U, K, V,
-                       C)
+                       0 if finished is None else finished.data_ptr(), out.data_ptr(), beams.data_ptr(), tokens.data_ptr(), wide,
+                       end_token, U, K, V, C)
         raw = torch._C._cuda_getCurrentRawStream(device.index)
         if raw != self._last_raw and not torch.cuda.is_current_stream_capturing():
             stream = torch.cuda.current_stream(device)
@@ -1144,7 +1144,6 @@ class BeamSearch:
             self.workspace.record_stream(stream)  # dropped early, it stays until the stream is done with it
             self._last, self._last_raw = stream, raw
         _check("moe_ffn_beam_select", _launch(lib().moe_ffn_beam_select, device, a, self._workspace, self.nbytes))
-        beams, tokens = ids.unbind(0)
         return out, beams, tokens
 
 
