@@ -21,6 +21,12 @@
 //
 // fp64 is slow here (an operation takes a warp 16 cycles or more, and its result some 60): only the last comparisons
 // are made in it.
+//
+// Times, 262144 bf16 logits to a row: 160 rows (32 users of 5 beams, the 10 best) 31 us, of which the pass takes 24 at 3.5 TB/s
+// with 56% of the issue slots busy (exponentials, sums and comparisons, not HBM), and the join the rest: a chain of
+// barriers and small steps of one CTA to a user. 4 rows, the 8 best: 9.3 us in a graph, of which the bytes are 0.3. The join in
+// fp64 throughout took 40 us. A form that found its thresholds by bisection, a barrier for each step, and summed in fp64 took
+// 136 for the 160 rows and 44 for the 4.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -810,7 +816,9 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   }
 }
 
-// Parts of a row: enough for four CTAs on each SM, of a tile at least. (Tiles of bf16 logits, which have the larger ones: one workspace serves both types.)
+// Parts of a row: enough for four CTAs on each SM, which are as many as run there at once (160 rows of 262144: 31 us, 38 with
+// two, 34 with three, 34 with six, 33 with eight), of a tile at least. (Tiles of bf16 logits, which have the larger ones: one
+// workspace serves both types.)
 int beam_splits(int rows, int vocab, int count) {
   constexpr int kTile = kThreads * kVecs * 8;
   const int tiles = (vocab + kTile - 1) / kTile;
