@@ -374,14 +374,27 @@ int kv_arguments(const moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_
   return MOE_FFN_OK;
 }
 
-// Several layers' caches.
+// Several layers' caches, which a call moves rows of: one that is given twice would move its rows twice, at once.
 int kv_layers_ok(const moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n) {
   if (!caches) return MOE_FFN_EINVAL;
-  const bool q8 = kv->cfg.format == MOE_FFN_KV_E4M3;
+  const KvCache shape = kv_shape(kv);
+  const bool q8 = shape.e4m3 != 0;
+  const size_t rows = (static_cast<size_t>(shape.n_pages) * shape.kv_heads) << shape.page_log2;
+  const size_t values = rows * shape.head_dim * (q8 ? 1 : 2), scales = rows * 4;
   for (int i = 0; i < n; ++i) {
     const moe_ffn_kv_cache& c = caches[i];
     if (!c.k || !c.v || (q8 && (!c.k_scale || !c.v_scale))) return MOE_FFN_EINVAL;
     if (off16(c.k) || off16(c.v) || (q8 && (off16(c.k_scale) || off16(c.v_scale)))) return MOE_FFN_EALIGN;
+    if (meet(c.k, values, c.v, values) || (q8 && meet(c.k_scale, scales, c.v_scale, scales))) return MOE_FFN_EINVAL;
+    for (int j = 0; j < i; ++j) {
+      const moe_ffn_kv_cache& o = caches[j];
+      if (meet(c.k, values, o.k, values) || meet(c.k, values, o.v, values) || meet(c.v, values, o.k, values) ||
+          meet(c.v, values, o.v, values))
+        return MOE_FFN_EINVAL;
+      if (q8 && (meet(c.k_scale, scales, o.k_scale, scales) || meet(c.k_scale, scales, o.v_scale, scales) ||
+                 meet(c.v_scale, scales, o.k_scale, scales) || meet(c.v_scale, scales, o.v_scale, scales)))
+        return MOE_FFN_EINVAL;
+    }
   }
   return MOE_FFN_OK;
 }

@@ -199,3 +199,18 @@ def test_refusals():
             B.block_norm(**kw)
     with pytest.raises(B.MoeFFNError):  # too wide
         B.block_norm(torch.zeros(1, 16392, dtype=torch.bfloat16, device="cuda"), scale=2.0)
+
+
+def test_places_past_32_bits():
+    T, H = 800_000, 2816  # 2.25e9 elements
+    rows = [0, 1, 762_599, 762_600, 799_999]  # (2^31 elements end in row 762600)
+    small = _inputs(len(rows), H, seed=9, gate="one")
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    n = torch.empty_like(x)
+    x[rows] = small["x"]
+    block = small["block"][:1].expand(T, H)
+    B.block_norm(x, block, post=small["post"], gate=small["gate"][:1].expand(T, H), pre=small["pre"], out=x, normed=n)
+    wy, wn, ty, tn = _wanted(**dict(small, block=small["block"][:1].expand(len(rows), H)))
+    _check(x[rows], wy, ty)
+    _check(n[rows], wn, tn)
+    assert torch.equal(x[2], x[T - 2]) and torch.equal(n[2], n[T - 2])

@@ -216,3 +216,14 @@ def test_refusals():
     x = _rows(5, 2, 64)
     with pytest.raises(B.MoeFFNError):  # each in place, but over the other
         r.apply(x[:4], x[1:], pos, inplace=True)
+
+
+def test_places_past_32_bits():
+    T, heads, D = 270_000, 16, 512  # 2.2e9 elements
+    q = torch.empty(T, heads, D, dtype=torch.bfloat16, device="cuda").normal_()
+    positions = torch.arange(T, dtype=torch.int32, device="cuda")
+    freqs = _freqs(D // 2)
+    rows = torch.tensor([0, 1, 262_143, 262_144, T - 1], device="cuda")  # (2^31 elements end with row 262143)
+    before = q[rows]
+    B.Rotary(freqs).apply(q, None, positions, inplace=True)
+    _check(q[rows], before, freqs, [0] * (D // 2), positions[rows])

@@ -599,3 +599,58 @@ def test_refusals():
                  lambda: kv.keep(cache, batch, nodes, counts)):
         with pytest.raises(B.MoeFFNError):
             call()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_caches_given_twice_are_refused(fmt):
+    case = U.Case(fmt, 2, 2, 128, 16, [4, 5], [20, 30], seed=31)
+    kv = case.handle()
+    a, b = _random_cache(kv, 1), _random_cache(kv, 2)
+    was = {n: t.clone() for n, t in _bits(a).items()}
+    batch, counts = case.batch(), torch.ones(2, dtype=torch.int32, device="cuda")
+    nodes = torch.full((2, 1), 3, dtype=torch.int32, device="cuda")
+    scales = dict(k_scale=a.k_scale, v_scale=a.v_scale) if fmt == "e4m3" else {}
+    lists = [[a, b, a], [a, dict(k=b.k, v=a.k, **scales)], [dict(k=a.k, v=a.k, **scales)]]
+    if fmt == "e4m3":
+        lists += [[dict(k=a.k, v=a.v, k_scale=a.k_scale, v_scale=a.k_scale)],
+                  [b, dict(k=a.k, v=a.v, k_scale=a.k_scale, v_scale=b.k_scale)]]
+    for caches in lists:
+        with pytest.raises(B.MoeFFNError):
+            kv.keep(caches, batch, nodes, counts)
+        with pytest.raises(B.MoeFFNError):
+            kv.reorder(caches, batch.tensors[2].contiguous(), torch.full((1,), 5, dtype=torch.int32, device="cuda"),
+                       torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"))
+    _ok(kv)
+    assert all(torch.equal(t, was[n]) for n, t in _bits(a).items())
+
+
+def test_moves_past_32_bits():
+    hkv, d, page, n_pages = 8, 512, 64, 8448  # 2.2e9 elements
+    kv = B.PagedKV(hkv, hkv, d, page, n_pages, "bf16", max_tokens=64, max_seqs=2)
+    c = kv.new_cache()
+    last = [n_pages - 1, n_pages - 2, n_pages - 3, n_pages - 4]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for p in last:
+        c.k[p] = torch.randn(hkv, page, d, generator=g, device="cuda").to(torch.bfloat16)
+        c.v[p] = torch.randn(hkv, page, d, generator=g, device="cuda").to(torch.bfloat16)
+    pages = torch.tensor([last[:2], last[2:]], dtype=torch.int32, device="cuda")
+    want = {n: t[last].clone() for n, t in (("k", c.k), ("v", c.v))}
+    # Beams at 70 tokens change places: 6 slots of their second pages, and the tables' first entries.
+    kv.reorder(c, pages, torch.tensor([70], dtype=torch.int32, device="cuda"),
+               torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"))
+    assert pages.tolist() == [[last[2], last[1]], [last[0], last[3]]]
+    for w in want.values():
+        w[1, :, :6], w[3, :, :6] = w[3, :, :6].clone(), w[1, :, :6].clone()
+    # Of trees of ten nodes in the slots from 60 on, nodes 2, 5 and 9 stay.
+    batch = B.KVBatch(torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda"),
+                      torch.tensor([70, 70], dtype=torch.int32, device="cuda"), pages, max_new=10)
+    left = kv.keep(c, batch, torch.tensor([[2, 5, 9]] * 2, dtype=torch.int32, device="cuda"),
+                   torch.tensor([3, 3], dtype=torch.int32, device="cuda"))
+    assert left.tolist() == [63, 63]
+    for w in want.values():
+        for first, second in ((2, 1), (0, 3)):
+            w[first, :, 60], w[first, :, 61], w[first, :, 62] = w[first, :, 62].clone(), w[second, :, 1].clone(), w[second, :, 5].clone()
+    _ok(kv)
+    for n, t in (("k", c.k), ("v", c.v)):
+        assert torch.equal(t[last], want[n]), n
+        assert not t[:n_pages - 4].any(), n
