@@ -454,8 +454,8 @@ int moe_ffn_kv_tree_attention(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, con
 /* Keeps one path of each tree: the keys and values of the nodes nodes[b * nodes_stride + i], i < counts[b], move to
  * the slots after the context, in that order, in each of the n_layers caches. What lies behind them is left
  * as it is.
- *   caches   host array of n_layers caches of the handle's shape, none of which overlaps another;
- *   batch    the trees' batch; n_tokens: at least the last value of cu_q;
+ *   caches   host array of n_layers caches of the handle's shape, none of which overlaps another (MOE_FFN_EINVAL);
+ *   batch    the trees' batch, max_new at most MOE_FFN_KV_TREE_NODES; n_tokens: at least the last value of cu_q;
  *   nodes    device pointer, [n_seqs, nodes_cols] int32, rows nodes_stride >= nodes_cols entries apart, each
  *            ascending: i <= nodes[b][i] < n_b;
  *   counts   device pointer, [n_seqs] int32, 0 <= counts[b] <= nodes_cols;
@@ -475,7 +475,7 @@ int moe_ffn_kv_keep(moe_ffn_kv* kv, const moe_ffn_kv_cache* caches, int n_layers
  *   - the table's entries of full pages are the parent's (the pages themselves are not copied);
  *   - of the page under way, the lengths[u] % page_size first slots are copied from the parent's into its own, in
  *     each of the n_layers caches.
- *   caches   host array of n_layers (>= 0) caches of the handle's shape, none of which overlaps another;
+ *   caches   host array of n_layers (>= 0) caches of the handle's shape, none of which overlaps another (MOE_FFN_EINVAL);
  *   pages    device pointer, [users * beams, pages_cols] int32, rows pages_stride >= pages_cols entries apart;
  *   lengths  device pointer, [users] int32; parents: device pointer, [users, beams] int32; neither overlaps pages;
  *   users    0..max_seqs / beams; beams: 1..MOE_FFN_BEAM_MAX.
@@ -563,7 +563,8 @@ int moe_ffn_rotary_apply(const moe_ffn_rotary* a, const moe_ffn_kv_rows* q, cons
  * best first, ties by the lower beam, then the lower token. A finished beam has one continuation, the end token, with
  * its score unchanged, and its logits are not read. A continuation of -infinity or NaN is none (a NaN or +infinity
  * among a beam's logits leaves it without any); where there are fewer than `count`, the rest have score
- * -infinity, beam -1 and token -1. The sums are formed to about 1e-8, the comparisons made in fp64. */
+ * -infinity, beam -1 and token -1. The sums are formed to about 1e-8, the comparisons made in fp64, within a beam of the
+ * logits themselves; a score that fp32 rounds to -infinity counts as such. */
 typedef struct moe_ffn_beam {
   const void* logits;      /* device pointer, [users * beams, vocab], rows logits_stride elements apart */
   long long logits_stride; /* >= 0 */

@@ -22,11 +22,12 @@
 // fp64 is slow here (an operation takes a warp 16 cycles or more, and its result some 60): only the last comparisons
 // are made in it.
 //
-// Times, 262144 bf16 logits to a row: 160 rows (32 users of 5 beams, the 10 best) 31 us, of which the pass takes 24 at 3.5 TB/s
-// with 56% of the issue slots busy (exponentials, sums and comparisons, not HBM), and the join the rest: a chain of
-// barriers and small steps of one CTA to a user. 4 rows, the 8 best: 9.3 us in a graph, of which the bytes are 0.3. The join in
-// fp64 throughout took 40 us. A form that found its thresholds by bisection, a barrier for each step, and summed in fp64 took
-// 136 for the 160 rows and 44 for the 4.
+// Times, 262144 bf16 logits to a row: 160 rows (32 users of 5 beams, some ended, the 10 best) 28 us, of which the pass takes 24
+// at 3.5 TB/s with 56% of the issue slots busy (exponentials, sums and comparisons, not HBM), and the join the rest: a chain
+// of barriers and small steps of one CTA to a user. 4 rows, the 8 best: 9.3 us in a graph, of which the bytes are 0.3. 64
+// rows, the 64 best: 57. Rows of equal logits, which no threshold parts, take two to five times as long. The join in fp64
+// throughout took 40 us. A form that found its thresholds by bisection, a barrier for each step, and summed in fp64 took 136
+// for the 160 rows and 44 for the 4.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -351,19 +352,21 @@ __device__ __forceinline__ float cta_max(Shared& s, float v) {
 }
 
 // The `count` best of the first n entries of the list (fewer if there are fewer), best first, in s.best; their
-// number. All entries differ. Few entries are ranked by comparing each with all; of many, the best is taken `count`
-// times.
+// number. All entries differ. Few entries are ranked by comparing each with all; of more, those within a distance from the
+// best that `count` are within, copied over the noted vectors, which are done with; of many such, the best is taken
+// `count` times.
 __device__ int select_best(Shared& s, int n, int count) {
   const int tid = threadIdx.x, found = min(n, count);
-  if (n <= kThreads) {
-    const unsigned long long mine = tid < n ? s.list[tid] : 0ull;
+  auto rank_all = [&](const unsigned long long* from, int m) {
+    const unsigned long long mine = tid < m ? from[tid] : 0ull;
     int rank = 0;
-    if ((tid & ~31) < n)
-      for (int i = 0; i < n; ++i) rank += s.list[i] > mine ? 1 : 0;
-    if (tid < n && rank < count) s.best[rank] = mine;
+    if ((tid & ~31) < m)
+      for (int i = 0; i < m; ++i) rank += from[i] > mine ? 1 : 0;
+    if (tid < m && rank < count) s.best[rank] = mine;
     __syncthreads();
     return found;
-  }
+  };
+  if (n <= kThreads) return rank_all(s.list, n);
   constexpr int kOwn = kList / kThreads;
   unsigned long long own[kOwn], top = 0ull;
 #pragma unroll
@@ -371,6 +374,24 @@ __device__ int select_best(Shared& s, int n, int count) {
     own[i] = i * kThreads + tid < n ? s.list[i * kThreads + tid] : 0ull;
     top = max(top, own[i]);
   }
+  // (No entry is NaN or -infinity; where one is +infinity there is no distance that says anything.)
+  s.bins[tid] = 0;
+  if (tid == 0) s.n_noted = 0;
+  const float most = cta_max(s, entry_x(top));
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i)
+    if (own[i] != 0ull) atomicAdd(&s.bins[bin_of(most - entry_x(own[i]))], 1);
+  __syncthreads();
+  const float far = bin_end(bin_reached(s.bins, count));
+  unsigned long long* close = reinterpret_cast<unsigned long long*>(s.noted);
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    if (own[i] == 0ull || far == INFINITY || !(most - entry_x(own[i]) < far)) continue;
+    const int to = atomicAdd(&s.n_noted, 1);
+    if (to < kThreads) close[to] = own[i];
+  }
+  __syncthreads();
+  if (far < INFINITY && s.n_noted <= kThreads) return rank_all(close, s.n_noted);
   for (int c = 0; c < found; ++c) {
     unsigned long long m = top;
 #pragma unroll
@@ -600,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
   }
 }
 
-// A candidate in the order of unsigned integers: its value in fp64, of equal ones (-0 is 0) the lower beam, then the
-// lower token.
+// A candidate in the order of unsigned integers: its value in fp64; of equal ones the lower beam, then the larger logit (-0 is
+// 0), then the lower token.
 struct Candidate {
   unsigned long long value;  // 0: none
-  uint32_t place;            // beam << 24 | token
+  unsigned long long place;  // beam << 56 | (complement of the logit's order) << 24 | token
 };
 static_assert(MOE_FFN_BEAM_MAX_VOCAB <= 1 << 24 && MOE_FFN_BEAM_MAX <= 1 << 8, "places");
 __device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
@@ -617,33 +638,39 @@ __device__ __forceinline__ double value_of(unsigned long long o) {
 
 // A CTA per user: the beams' log sum exp, then the best of all parts' candidates, found as in a part: a distance from the
 // largest value within which there are `count`, a list of these, and the order by comparing each with all. Candidates
-// have their values formed in fp32 first, with a bound of what that loses.
+// have their values formed in fp32 first, with a bound of what that loses. The distance is that of all candidates where
+// they have been copied into shared memory, else of the first ones of each part, which is sorted; then a part is looked
+// through only where its first one is within it. (64 beams, the 64 best: 640 parts of 64 candidates each, 39 us here,
+// and 175 to look through them all.) Where more are that close together than the list holds, equal ones for
+// instance, the best of the parts' first ones is taken `count` times.
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParams p) {
   // A continuation's value is (x - ref) + shift: the sum of exp(x - ref) is what has been formed. NaN: none.
   __shared__ double shift[MOE_FFN_BEAM_MAX];
   __shared__ float rough_shift[MOE_FFN_BEAM_MAX], beam_ref[MOE_FFN_BEAM_MAX];
   __shared__ bool ended[MOE_FFN_BEAM_MAX];
-  __shared__ float held[kJoinHeld], held_x[kJoinHeld];
+  __shared__ float held_x[kJoinHeld];
   __shared__ int held_token[kJoinHeld];
   __shared__ Candidate list[kJoinList];
-  __shared__ float warp_top[kJoinWarps], warp_off[kJoinWarps];
+  __shared__ uint8_t taken[MOE_FFN_BEAM_MAX * kMaxSplits];  // of a part's candidates
+  __shared__ float warp_top[kJoinWarps];
   __shared__ alignas(16) int bins[kBins];
-  __shared__ int found;
+  __shared__ int found, live;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, user = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
   const long long row0 = static_cast<long long>(user) * p.beams;
-  const int per_beam = p.splits * p.count, n = p.beams * per_beam;
+  const int n_parts = p.beams * p.splits, per_beam = p.splits * p.count, n = p.beams * per_beam;
   const float* xs = p.part_x + row0 * per_beam;
   const int32_t* tokens = p.part_token + row0 * per_beam;
   static_assert(kJoinThreads == kBins && kThreads == kBins, "a bin to a thread");
   bins[tid] = 0;
-  if (tid == 0) found = 0;
+  if (tid == 0) found = live = 0;
   // The candidates are on their way while the sums are formed.
+  const bool all = n <= kJoinHeld;
 #pragma unroll
   for (int j = 0; j < kJoinHeld / kJoinThreads; ++j) {
     const int i = tid + j * kJoinThreads;
-    if (i >= n) break;
+    if (!all || i >= n) break;
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&held_x[i])), "l"(xs + i) : "memory");
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&held_token[i])), "l"(tokens + i) : "memory");
   }
@@ -694,12 +721,13 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  auto x_of = [&](int i) { return i < kJoinHeld ? held_x[i] : xs[i]; };
-  auto token_of = [&](int i) { return i < kJoinHeld ? held_token[i] : tokens[i]; };
+  auto x_of = [&](int i) { return all ? held_x[i] : xs[i]; };
+  auto token_of = [&](int i) { return all ? held_token[i] : tokens[i]; };
   const float per_beam_inv = 1.0f / static_cast<float>(per_beam);
   // (n is at most 2^18: the product is off by less than the distance of i + 1/2 from a multiple.)
   auto beam_of = [&](int i) { return static_cast<int>((static_cast<float>(i) + 0.5f) * per_beam_inv); };
-  // A candidate's value in fp32, and what it may be off by: half a step of each of two operations and of shift.
+  // A candidate's value in fp32 (-infinity or NaN: none), and what it may be off by: half a step of each of two operations
+  // and of shift.
   auto rough = [&](int i, float& off) {
     const int k = beam_of(i);
     const float t = rough_shift[k];
@@ -714,59 +742,81 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   auto exact = [&](int i) {
     const int k = beam_of(i);
     double v = shift[k];
+    float x = 0.0f;
     int token = p.end_token;
     if (!ended[k]) {
-      v += static_cast<double>(x_of(i)) - static_cast<double>(beam_ref[k]);
+      x = x_of(i);
+      v += static_cast<double>(x) - static_cast<double>(beam_ref[k]);
       token = token_of(i);
     } else if (i != k * per_beam) {
       token = -1;
     }
     Candidate c;
-    c.value = token >= 0 && v > -INFINITY ? ordered(v + 0.0) : 0ull;
-    c.place = static_cast<uint32_t>(k) << 24 | static_cast<uint32_t>(token & 0xffffff);
+    c.value = token >= 0 && static_cast<float>(v) > -INFINITY ? ordered(v + 0.0) : 0ull;
+    c.place = static_cast<unsigned long long>(k) << 56 | static_cast<unsigned long long>(~ordered(x + 0.0f)) << 24 |
+              static_cast<unsigned long long>(token & 0xffffff);
     return c;
   };
-  float top = -INFINITY, off = 0.0f;
+  // The first `firsts` candidates of each part, as many that `count` of all can be among them.
+  int firsts = p.count;
+  if (!all) {
+    int mine = 0;
+    for (int i = tid; i < n_parts; i += kJoinThreads) {
+      float off;
+      mine += rough(i * p.count, off) > -INFINITY ? 1 : 0;
+    }
+    if (mine > 0) atomicAdd(&live, mine);
+    __syncthreads();
+    firsts = live > 0 ? (p.count + live - 1) / live : 1;
+  }
+  const int n_firsts = n_parts * firsts;
+  auto at_first = [&](int h) { return firsts == p.count ? h : h / firsts * p.count + h % firsts; };
+  // At least as large as what is found below: `count` of the firsts, less what they may be off by.
+  float top = -INFINITY;
 #pragma unroll 4
-  for (int i = tid; i < n; i += kJoinThreads) {
-    float o;
-    const float v = rough(i, o);
-    if (i < kJoinHeld) held[i] = v;
-    top = fmaxf(top, v);
-    if (v > -INFINITY) off = fmaxf(off, o);
+  for (int h = tid; h < n_firsts; h += kJoinThreads) {
+    float off;
+    const float v = rough(at_first(h), off);
+    if (v > -INFINITY) top = fmaxf(top, __fsub_rd(v, off));
   }
-  auto value = [&](int i) {
-    float o;
-    return i < kJoinHeld ? held[i] : rough(i, o);
-  };
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, o));
-  }
-  if (lane == 0) {
-    warp_top[warp] = top;
-    warp_off[warp] = off;
-  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) warp_top[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    top = fmaxf(top, warp_top[w]);
-    off = fmaxf(off, warp_off[w]);
-  }
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const float v = value(i);
-    if (v > -INFINITY) atomicAdd(&bins[bin_of(top - v)], 1);
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, warp_top[w]);
+#pragma unroll 4
+  for (int h = tid; h < n_firsts; h += kJoinThreads) {
+    float off;
+    const float v = rough(at_first(h), off);
+    if (v > -INFINITY) atomicAdd(&bins[bin_of(top - __fsub_rd(v, off))], 1);
   }
   __syncthreads();
   float least = -INFINITY;
   const float d = bin_end(bin_reached(bins, p.count));
-  if (top < INFINITY && d < INFINITY) least = __fsub_rd(top, fmaf(2.0f, off, d * 1.000001f));
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const float v = value(i);
-    if (v > -INFINITY && v >= least) {
-      const int to = atomicAdd(&found, 1);
-      if (to < kJoinList) list[to].place = i;
+  if (top < INFINITY && d < INFINITY) least = __fsub_rd(top, d * 1.000001f);
+  auto close = [&](int i) {
+    float off;
+    const float v = rough(i, off);
+    return v > -INFINITY && __fadd_ru(v, off) >= least;
+  };
+  auto note = [&](int i) {
+    const int to = atomicAdd(&found, 1);
+    if (to < kJoinList) list[to].place = static_cast<unsigned long long>(i);
+  };
+  if (all) {
+    for (int i = tid; i < n; i += kJoinThreads)
+      if (close(i)) note(i);
+  } else {
+    // What comes after a part's first one is no larger.
+    for (int base = warp * 32; base < n_parts; base += kJoinThreads) {
+      const int part = base + lane;
+      unsigned which = __ballot_sync(0xffffffffu, part < n_parts && close(part * p.count));
+      for (; which != 0; which &= which - 1) {
+        const int first = (base + __ffs(which) - 1) * p.count;
+        for (int j = lane; j < p.count; j += 32)
+          if (close(first + j)) note(first + j);
+      }
     }
   }
   __syncthreads();
@@ -775,8 +825,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     const unsigned long long u = a.value;
     const bool some = u != 0ull;
     p.out_scores[o] = some ? static_cast<float>(value_of(u)) : -INFINITY;
-    p.out_beams[o] = some ? static_cast<int>(a.place >> 24) : -1;
-    p.out_tokens[o] = some ? static_cast<int>(a.place & 0xffffff) : -1;
+    p.out_beams[o] = some ? static_cast<int>(a.place >> 56) : -1;
+    p.out_tokens[o] = some ? static_cast<int>(a.place & 0xffffffull) : -1;
   };
   const int have = found;
   if (have <= kJoinList) {
@@ -791,40 +841,54 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     for (int c = have + tid; c < p.count; c += kJoinThreads) answer(c, Candidate{0ull, 0u});
     return;
   }
-  // More than that, where many values lie close together. The best after the last one is taken `count` times.
-  Candidate last = {~0ull, 0u};
-  for (int c = 0; c < p.count; ++c) {
-    Candidate a = {0ull, 0xffffffffu};
-    for (int i = tid; i < n; i += kJoinThreads) {
-      const float v = value(i);
-      if (!(v > -INFINITY && v >= least)) continue;
-      const Candidate b = exact(i);
-      if (b.value != 0ull && before(last, b) && before(b, a)) a = b;
+  // A thread keeps the best that is left of its parts.
+  for (int i = tid; i < n_parts; i += kJoinThreads) taken[i] = 0;
+  Candidate mine;
+  int mine_of = -1;
+  auto look = [&] {
+    mine = Candidate{0ull, ~0ull};
+#pragma unroll 4
+    for (int i = tid; i < n_parts; i += kJoinThreads) {
+      if (taken[i] >= p.count) continue;
+      const Candidate b = exact(i * p.count + taken[i]);
+      if (b.value == 0ull || !before(b, mine)) continue;
+      mine = b;
+      mine_of = i;
     }
+  };
+  look();
+  for (int c = 0; c < p.count; ++c) {
+    Candidate a = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const Candidate b = {__shfl_xor_sync(0xffffffffu, a.value, o), __shfl_xor_sync(0xffffffffu, a.place, o)};
       if (before(b, a)) a = b;
     }
+    Candidate* best = list + (c & 1) * kJoinWarps;  // (a warp may be a step ahead of one that still reads)
+    if (lane == 0) best[warp] = a;
     __syncthreads();
-    if (lane == 0) list[warp] = a;
-    __syncthreads();
+#pragma unroll
     for (int w = 0; w < kJoinWarps; ++w)
-      if (before(list[w], a)) a = list[w];
+      if (before(best[w], a)) a = best[w];
     if (tid == 0) answer(c, a);
-    last = a;
+    if (a.value != 0ull && a.value == mine.value && a.place == mine.place) {
+      ++taken[mine_of];
+      look();
+    }
   }
 }
 
-// Parts of a row: enough for four CTAs on each SM, which are as many as run there at once (160 rows of 262144: 31 us, 38 with
-// two, 34 with three, 34 with six, 33 with eight), of a tile at least. (Tiles of bf16 logits, which have the larger ones: one
-// workspace serves both types.)
+// Parts of a row: as many as four CTAs on each SM, which run there at once, of a tile at least. Rounded up where a part is then
+// still of eight tiles (160 rows of 262144: 30 us, 32 rounded down), else down, as a few CTAs more take as long as all before
+// (64 rows of 128256, 9 parts or 10: 16 and 20 us). And small enough that the vectors that it notes, one or two times
+// `count` of a tile, have room: of 400 rows of 262144, the 8 best take 61 us in 2 parts and 55 in 3; the 64 best of 32 rows 129
+// in 8 and 51 in 10. (Tiles of bf16 logits, which have the larger ones: one workspace serves both types.)
 int beam_splits(int rows, int vocab, int count) {
-  constexpr int kTile = kThreads * kVecs * 8;
+  constexpr int kTile = kThreads * kVecs * 8, kCtas = 4 * 152;
   const int tiles = (vocab + kTile - 1) / kTile;
-  int splits = (4 * 152 + rows - 1) / (rows > 0 ? rows : 1);
-  // (Few tiles: those that note as many vectors, a few more than `count` each, as there is room for.)
-  const int least = count > 20 ? (tiles * count + 319) / 320 : (tiles + 15) / 16;
+  int splits = rows > 0 ? (kCtas + rows - 1) / rows : kCtas;
+  if (rows <= kCtas && splits * rows > kCtas && tiles < 8 * splits) --splits;
+  const int least = (tiles * (count > 13 ? count : 13) + 159) / 160;
   if (splits < least) splits = least;
   if (splits > tiles) splits = tiles;
   if (splits > kMaxSplits) splits = kMaxSplits;

@@ -105,6 +105,33 @@ def test_ties():
     _check(z.to(torch.bfloat16), torch.zeros(1, 2, device="cuda"), 40)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K,V,C", [(64, 20000, 64), (8, 262144, 64), (37, 33001, 41)])
+def test_many_candidates(K, V, C, dtype):
+    """More parts and candidates than are compared at once: of random rows, of equal ones, of few values; one beam alone,
+    one far ahead, most of them ended, few tokens allowed."""
+    logits, scores = _inputs(2, K, V, seed=C, dtype=dtype)
+    search = B.BeamSearch(2, K, V, C)
+    _check(logits, scores, C, search=search)
+    first = scores.clone()
+    first[:, 1:] = -math.inf
+    _check(logits, first, C, search=search)
+    ahead = scores.clone()
+    ahead[:, K // 2] = 50.0
+    _check(logits, ahead, C, search=search)
+    ended = (torch.arange(2 * K, device="cuda") % 5 != 0).view(2, K)
+    _check(logits, scores, C, ended, 3, search=search)
+    for share in (2e-5, 5e-4):
+        g = torch.Generator(device="cuda").manual_seed(C)
+        allowed = torch.rand(logits.shape, generator=g, device="cuda") < share
+        _check(torch.where(allowed, logits, -math.inf), scores, C, search=search)
+        _check(torch.where(allowed, logits, torch.finfo(dtype).min), scores, C, search=search)
+    few = (logits[:1] * 0.7).round().expand(2 * K, V).contiguous()  # equal rows: ties over all beams
+    for level in (torch.full_like(scores, -1.5), scores):
+        _check(few, level, C, search=search)
+        _check(torch.zeros_like(logits), level, C, search=search)
+
+
 def test_first_step_and_finished_beams():
     logits, scores = _inputs(3, 4, 9000, seed=5)
     scores[:, 1:] = -math.inf
@@ -225,3 +252,43 @@ def test_refusals():
             search.select(logits, scores, done, end)
     empty = B.BeamSearch(0, 4, 100, 8).select(logits[:0], scores[:0])
     assert all(t.shape == (0, 8) for t in empty)
+
+
+def test_rows_past_32_bits():
+    U, K, V, C = 13, 10, 1 << 24, 6
+    logits = torch.zeros(U * K, V, dtype=torch.bfloat16, device="cuda")  # 2.2e9 logits
+    g = torch.Generator().manual_seed(4)
+    rows = torch.arange(U * K).repeat_interleave(3)
+    places = (torch.randint(0, V // 3, (U * K, 3), generator=g) + torch.arange(3) * (V // 3)).view(-1)
+    places[-1] = V - 1
+    values = (torch.rand(U * K * 3, generator=g) * 8 + 1).to(torch.bfloat16)
+    logits[rows.cuda(), places.cuda()] = values.cuda()
+    scores = -torch.rand(U, K, generator=g)
+    got = B.BeamSearch(U, K, V, C).select(logits, scores.cuda())
+    x = values.double().view(U * K, 3)
+    x = x - (V - 3 + x.exp().sum(1, keepdim=True)).log() + scores.double().view(-1, 1)
+    beams = torch.arange(K).repeat_interleave(3)
+    for u in range(U):
+        mine, token = x[u * K:(u + 1) * K].reshape(-1), places.view(U, -1)[u]
+        order = sorted(range(3 * K), key=lambda i: (-float(mine[i]), int(beams[i]), int(token[i])))[:C]
+        assert got[1][u].tolist() == beams[order].tolist() and got[2][u].tolist() == token[order].tolist()
+        assert ((got[0][u].cpu().double() - mine[order]).abs() <= 2.0 ** -24 * mine[order].abs() + 1e-7).all()
+
+
+def test_two_searches_at_once():
+    # Objects of their own, on streams of their own.
+    both = []
+    for seed in (1, 2):
+        logits, scores = _inputs(8, 5, 50_001, seed=seed)
+        both.append((B.BeamSearch(8, 5, 50_001, 10), torch.cuda.Stream(), logits, scores))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for search, stream, logits, scores in both:
+            with torch.cuda.stream(stream):
+                got.append(search.select(logits, scores))
+    torch.cuda.synchronize()
+    for i, (_, _, logits, scores) in enumerate(both):
+        want = _wanted(logits, scores, 10)
+        for g in got[i::2]:
+            assert torch.equal(g[1], want[1]) and torch.equal(g[2], want[2])
