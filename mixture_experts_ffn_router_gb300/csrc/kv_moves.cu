@@ -150,6 +150,10 @@ __global__ void __launch_bounds__(kKeepThreads)
 }
 
 constexpr int kReorderThreads = 128;
+// Blocks in all, each with as many vectors as it takes. A page is seldom nearly full: 18 users' 2 beams of 6 to 31 tokens on
+// pages of 128, 6 layers, take 33 us with a block for each vector that there could be, 12 with these (14 with a quarter, 16
+// with four times as many).
+constexpr int kReorderCtas = 16 * 152;
 constexpr int kReorderRegs = 8;  // beams whose vectors a thread holds in registers (5 beams: 14.2 us, in shared memory 14.7)
 
 // Blocks of a user and plane, then (of the first plane) one for the user's table. A thread takes one vector of one
@@ -206,43 +210,47 @@ __global__ void __launch_bounds__(kReorderThreads)
     }
     return;
   }
-  const int item = blockIdx.y * kReorderThreads + tid;
-  if (item >= items) return;
-  const int v = item & ((1 << vecs_log2) - 1), row = item >> vecs_log2;  // (a head's slots lie next to each other)
-  const int head = row / rest, slot = row - head * rest;
   const Plane p = plane_of(l, blockIdx.z);
   uint4* rows = reinterpret_cast<uint4*>(p.rows);
-  auto place = [&](int k) { return (static_cast<long long>(page[k] * c.kv_heads + head) << c.page_log2) + slot; };
   auto moves = [&](int k) { return source[k] >= 0 && page[k] >= 0 && page[source[k]] >= 0; };
-  const bool scaled = v == 0 && p.scales;
-  if constexpr (REGS) {
-    uint4 x[kReorderRegs];
-    float sc[kReorderRegs];
+  for (int item = blockIdx.y * kReorderThreads + tid; item < items; item += move_blocks * kReorderThreads) {
+    const int v = item & ((1 << vecs_log2) - 1), row = item >> vecs_log2;  // (a head's slots lie next to each other)
+    const int head = row / rest, slot = row - head * rest;
+    auto place = [&](int k) { return (static_cast<long long>(page[k] * c.kv_heads + head) << c.page_log2) + slot; };
+    const bool scaled = v == 0 && p.scales;
+    if constexpr (REGS) {
+      uint4 x[kReorderRegs];
+      float sc[kReorderRegs];
 #pragma unroll
-    for (int k = 0; k < kReorderRegs; ++k) {
-      if (k >= beams || !moves(k)) continue;
-      const long long from = place(source[k]);
-      x[k] = rows[(from << vecs_log2) + v];
-      if (scaled) sc[k] = p.scales[from];
-    }
+      for (int k = 0; k < kReorderRegs; ++k) {
+        if (k >= beams || !moves(k)) continue;
+        const long long from = place(source[k]);
+        x[k] = rows[(from << vecs_log2) + v];
+        if (scaled) sc[k] = p.scales[from];
+      }
 #pragma unroll
-    for (int k = 0; k < kReorderRegs; ++k) {
-      if (k >= beams || !moves(k)) continue;
-      const long long to = place(k);
-      rows[(to << vecs_log2) + v] = x[k];
-      if (scaled) p.scales[to] = sc[k];
+      for (int k = 0; k < kReorderRegs; ++k) {
+        if (k >= beams || !moves(k)) continue;
+        const long long to = place(k);
+        rows[(to << vecs_log2) + v] = x[k];
+        if (scaled) p.scales[to] = sc[k];
+      }
+    } else {
+      uint4* mine = held + tid;
+      for (int k = 0; k < beams; ++k)
+        if (moves(k))
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(mine + k * kReorderThreads)),
+                       "l"(rows + (place(source[k]) << vecs_log2) + v)
+                       : "memory");
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int k = 0; k < beams; ++k)
+        if (moves(k)) rows[(place(k) << vecs_log2) + v] = mine[k * kReorderThreads];
+      if (!scaled) continue;
+      for (int k = 0; k < beams; ++k)
+        if (moves(k)) mine[k * kReorderThreads].x = __float_as_uint(p.scales[place(source[k])]);
+      for (int k = 0; k < beams; ++k)
+        if (moves(k)) p.scales[place(k)] = __uint_as_float(mine[k * kReorderThreads].x);
     }
-  } else {
-    uint4* mine = held + tid;
-    for (int k = 0; k < beams; ++k)
-      if (moves(k)) mine[k * kReorderThreads] = rows[(place(source[k]) << vecs_log2) + v];
-    for (int k = 0; k < beams; ++k)
-      if (moves(k)) rows[(place(k) << vecs_log2) + v] = mine[k * kReorderThreads];
-    if (!scaled) return;
-    for (int k = 0; k < beams; ++k)
-      if (moves(k)) mine[k * kReorderThreads].x = __float_as_uint(p.scales[place(source[k])]);
-    for (int k = 0; k < beams; ++k)
-      if (moves(k)) p.scales[place(k)] = __uint_as_float(mine[k * kReorderThreads].x);
   }
 }
 
@@ -269,7 +277,8 @@ cudaError_t launch_kv_reorder(const KvCache& c, const KvLayers& l, int n_layers,
                               bool first_group, unsigned int* status, cudaStream_t s) {
   const int vecs = c.head_dim * (c.e4m3 ? 1 : 2) / 16;
   const int most = (((1 << c.page_log2) - 1) * c.kv_heads * vecs + kReorderThreads - 1) / kReorderThreads;
-  const int move_blocks = n_layers > 0 ? most : 0;
+  const int planes = 2 * n_layers, share = planes > 0 ? (kReorderCtas + users * planes - 1) / (users * planes) : 0;
+  const int move_blocks = share < most ? share : most;
   const dim3 grid(users, move_blocks + 1, n_layers > 0 ? 2 * n_layers : 1);
   const size_t smem = static_cast<size_t>(beams) * kReorderThreads * (beams <= kReorderRegs ? 4 : 16);
   const int first = first_group ? 1 : 0;

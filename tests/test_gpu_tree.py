@@ -654,3 +654,20 @@ def test_moves_past_32_bits():
     for n, t in (("k", c.k), ("v", c.v)):
         assert torch.equal(t[last], want[n]), n
         assert not t[:n_pages - 4].any(), n
+
+
+@pytest.mark.parametrize("fmt,beams", [("bf16", 3), ("e4m3", 20)])
+def test_reordered_pages_of_many_rows(fmt, beams):
+    """More rows to a block than it has threads."""
+    page, lengths = 128, [127, 100, 255, 129, 128, 60] * 3
+    table, n_pages = _beams(len(lengths), beams, page, lengths, seed=beams)
+    kv = B.PagedKV(8, 8, 256, page, n_pages, fmt, max_seqs=len(lengths) * beams)
+    layers = [_random_cache(kv, i) for i in range(2)]
+    parents = torch.randint(0, beams, (len(lengths), beams), generator=torch.Generator().manual_seed(beams))
+    want_table, want = _reordered(table, lengths, parents.tolist(), page, layers)
+    pages = table.cuda()
+    kv.reorder(layers, pages, torch.tensor(lengths, dtype=torch.int32, device="cuda"), parents.to(torch.int32).cuda())
+    _ok(kv)
+    assert torch.equal(pages.cpu(), want_table)
+    for c, w in zip(layers, want):
+        assert all(torch.equal(t, w[n]) for n, t in _bits(c).items())
