@@ -25,9 +25,10 @@
 // Times, 262144 bf16 logits to a row: 160 rows (32 users of 5 beams, some ended, the 10 best) 28 us, of which the pass takes 24
 // at 3.5 TB/s with 56% of the issue slots busy (exponentials, sums and comparisons, not HBM), and the join the rest: a chain
 // of barriers and small steps of one CTA to a user. 4 rows, the 8 best: 9.3 us in a graph, of which the bytes are 0.3. 64
-// rows, the 64 best: 57. Rows of equal logits, which no threshold parts, take two to five times as long. The join in fp64
-// throughout took 40 us. A form that found its thresholds by bisection, a barrier for each step, and summed in fp64 took 136
-// for the 160 rows and 44 for the 4.
+// rows, the 64 best: 57; in fp32, 180 rows of 116508, the 20 best: 37 (84 MB). One token far above all others takes no longer,
+// as coarse distances are cut again (160 rows 73 us otherwise). Rows of equal logits, which no threshold parts, take two to
+// seven times as long. The join in fp64 throughout took 40 us. A form that found its thresholds by bisection, a barrier for
+// each step, and summed in fp64 took 136 for the 160 rows and 44 for the 4.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -43,8 +44,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;                     // 16-byte vectors of a thread in a tile
-constexpr int kNoted = 512;                  // vectors
-constexpr int kList = 4096;
+constexpr int kNoted = 1024;                 // vectors
+constexpr int kList = 2560;
 constexpr int kListLong = kList - kThreads * 8 - 32;  // what still has room for a vector of each thread, and the ends
 constexpr int kMaxSplits = 64;
 constexpr int kMaxCount = MOE_FFN_BEAM_MAX;
@@ -126,8 +127,10 @@ __device__ __forceinline__ void terms(const float (&x)[8], float ref, float (&e)
 }
 
 // Distances below a maximum in 256 bins, eight to a factor of two, from 2^-20 to 2^12; NaN and what is further is in the last.
+// Where one is far above all others these are coarse, and each is cut into 256 again.
 constexpr int kBins = 256;
 constexpr int kBinShift = 20, kBinFirst = (127 - 20) << 3;
+constexpr int kFineShift = kBinShift - 8;
 __device__ __forceinline__ int bin_of(float d) {
   return min(max(static_cast<int>(__float_as_uint(d) >> kBinShift) - kBinFirst, 0), kBins - 1);
 }
@@ -135,8 +138,8 @@ __device__ __forceinline__ int bin_of(float d) {
 __device__ __forceinline__ float bin_end(int b) {
   return b == kBins - 1 ? INFINITY : __uint_as_float(static_cast<uint32_t>(b + 1 + kBinFirst) << kBinShift);
 }
-// The first bin up to which there are at least `count`, or the last; for a whole warp.
-__device__ __forceinline__ int bin_reached(const int* bins, int count) {
+// The first bin up to which there are at least `count`, or the last, and how many come before it; for a whole warp.
+__device__ __forceinline__ int bin_reached(const int* bins, int count, int& before) {
   const int lane = threadIdx.x & 31;
   const int4 a = reinterpret_cast<const int4*>(bins)[2 * lane], b = reinterpret_cast<const int4*>(bins)[2 * lane + 1];
   const int n[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -150,15 +153,40 @@ __device__ __forceinline__ int bin_reached(const int* bins, int count) {
     if (lane >= o) upto += up;
   }
   int at = upto - mine, bin = 0;
+  before = at;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     at += n[i];
-    bin += at < count ? 1 : 0;
+    if (at >= count) continue;
+    ++bin;
+    before = at;
   }
   const unsigned reached = __ballot_sync(0xffffffffu, upto >= count);
   if (reached == 0) return kBins - 1;
   const int which = __ffs(reached) - 1;
+  before = __shfl_sync(0xffffffffu, before, which);
   return __shfl_sync(0xffffffffu, 8 * lane + bin, which);
+}
+// What at least `count` of the CTA's distances are below, and no more than `room` where bins can tell them apart; infinity
+// where there are fewer. each(f) calls f with each of a thread's. The bins are zero.
+struct Bins {
+  alignas(16) int coarse[kBins];
+  alignas(16) int fine[kBins];
+};
+template <typename Each>
+__device__ __forceinline__ float distance_reached(Bins& bins, int count, int room, Each each) {
+  each([&](float d) { atomicAdd(&bins.coarse[bin_of(d)], 1); });
+  __syncthreads();
+  int before;
+  const int b = bin_reached(bins.coarse, count, before);
+  if (b == 0 || b == kBins - 1 || before + bins.coarse[b] <= room) return bin_end(b);
+  each([&](float d) {
+    if (bin_of(d) == b) atomicAdd(&bins.fine[__float_as_uint(d) >> kFineShift & (kBins - 1)], 1);
+  });
+  __syncthreads();
+  int none;
+  const uint32_t sub = static_cast<uint32_t>(bin_reached(bins.fine, count - before, none)) + 1;
+  return __uint_as_float((static_cast<uint32_t>(b + kBinFirst) << kBinShift) + (sub << kFineShift));
 }
 
 // A number in two of fp32, the second what the first leaves of it; and operations that lose about 2^-46.
@@ -333,7 +361,7 @@ struct Shared {
   unsigned long long warp_best[2][kWarps];
   uint4 noted[kNoted];
   int noted_at[kNoted];
-  alignas(16) int bins[kBins];
+  Bins bins;
   Sum warp_sum[kWarps];
   long long warp_fixed[kWarps];
   float warp_max[kWarps];
@@ -375,14 +403,14 @@ __device__ int select_best(Shared& s, int n, int count) {
     top = max(top, own[i]);
   }
   // (No entry is NaN or -infinity; where one is +infinity there is no distance that says anything.)
-  s.bins[tid] = 0;
+  s.bins.coarse[tid] = s.bins.fine[tid] = 0;
   if (tid == 0) s.n_noted = 0;
   const float most = cta_max(s, entry_x(top));
+  const float far = distance_reached(s.bins, count, kThreads, [&](auto&& take) {
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i)
-    if (own[i] != 0ull) atomicAdd(&s.bins[bin_of(most - entry_x(own[i]))], 1);
-  __syncthreads();
-  const float far = bin_end(bin_reached(s.bins, count));
+    for (int i = 0; i < kOwn; ++i)
+      if (own[i] != 0ull) take(most - entry_x(own[i]));
+  });
   unsigned long long* close = reinterpret_cast<unsigned long long*>(s.noted);
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
@@ -437,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
   if (split == 0) side = tid < head ? tid : end > 1 && end * N + tid - head < p.vocab ? end * N + tid - head : -1;
   const float x_side = side < 0 ? -INFINITY : L::value(logits[side]);
   if (tid == 0) s.n = s.n_noted = 0;
-  s.bins[tid] = 0;
+  s.bins.coarse[tid] = s.bins.fine[tid] = 0;
 
   Raw<SHIFTED> v[kVecs];
 #pragma unroll
@@ -453,11 +481,9 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
     for (int i = 0; i < N; ++i) m = fmaxf(m, f[i]);
   }
   float ref = cta_max(s, m);
-  atomicAdd(&s.bins[bin_of(ref - m)], 1);
-  __syncthreads();
   // (Rounded down, and by more than the distances' rounding: what is in the bins is above it.)
   float above = -INFINITY;
-  const float d = bin_end(bin_reached(s.bins, p.count));
+  const float d = distance_reached(s.bins, p.count, p.count + p.count / 2 + 8, [&](auto&& take) { take(ref - m); });
   if (ref < INFINITY && d < INFINITY) above = __fsub_rd(ref, d * 1.000001f);
   float unit = ref == -INFINITY ? 0.0f : ref;
 
@@ -488,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
         for (int i = 0; i < 8; ++i) e[i] = f[i] > above ? 0.0f : e[i];
 #pragma unroll
         for (int k = 0; k < 8 / N; ++k) {
+          if (N < 8 && !(fmaxf(fmaxf(f[k * N], f[k * N + 1]), fmaxf(f[k * N + 2], f[k * N + 3])) > above)) continue;
           const int to = atomicAdd(&s.n_noted, 1);
           if (to >= kNoted) continue;
           s.noted[to] = now[k];
@@ -638,11 +665,11 @@ __device__ __forceinline__ double value_of(unsigned long long o) {
 
 // A CTA per user: the beams' log sum exp, then the best of all parts' candidates, found as in a part: a distance from the
 // largest value within which there are `count`, a list of these, and the order by comparing each with all. Candidates
-// have their values formed in fp32 first, with a bound of what that loses. The distance is that of all candidates where
-// they have been copied into shared memory, else of the first ones of each part, which is sorted; then a part is looked
-// through only where its first one is within it. (64 beams, the 64 best: 640 parts of 64 candidates each, 39 us here,
-// and 175 to look through them all.) Where more are that close together than the list holds, equal ones for
-// instance, the best of the parts' first ones is taken `count` times.
+// have their values formed in fp32 first, with a bound of what that loses. Where there are too many to be copied into shared
+// memory, the first ones of each part, which is sorted, give a distance, and only the parts whose first one is within it are
+// looked through. (64 beams, the 64 best, 832 parts of 64 candidates each: 38 us; 175 to look through 640 such parts.) Where
+// more are close together than the list holds, equal ones for instance, the best of the parts' first ones is taken `count`
+// times. Loops over candidates are not unrolled: fetching instructions costs more here (4 us more in all where they were).
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParams p) {
   // A continuation's value is (x - ref) + shift: the sum of exp(x - ref) is what has been formed. NaN: none.
   __shared__ double shift[MOE_FFN_BEAM_MAX];
@@ -653,7 +680,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   __shared__ Candidate list[kJoinList];
   __shared__ uint8_t taken[MOE_FFN_BEAM_MAX * kMaxSplits];  // of a part's candidates
   __shared__ float warp_top[kJoinWarps];
-  __shared__ alignas(16) int bins[kBins];
+  __shared__ Bins bins;
   __shared__ int found, live;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, user = blockIdx.x;
   pdl_wait();
@@ -663,7 +690,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   const float* xs = p.part_x + row0 * per_beam;
   const int32_t* tokens = p.part_token + row0 * per_beam;
   static_assert(kJoinThreads == kBins && kThreads == kBins, "a bin to a thread");
-  bins[tid] = 0;
+  bins.coarse[tid] = bins.fine[tid] = 0;
   if (tid == 0) found = live = 0;
   // The candidates are on their way while the sums are formed.
   const bool all = n <= kJoinHeld;
@@ -674,47 +701,48 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&held_x[i])), "l"(xs + i) : "memory");
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&held_token[i])), "l"(tokens + i) : "memory");
   }
-  for (int k = warp; k < p.beams; k += kJoinWarps) {
-    const long long row = row0 + k;
-    static_assert(kMaxSplits == 64, "two parts of a row to a lane");
-    const bool end = p.finished && p.finished[row];
+  {
+    // All beams at once, 4 to 32 lanes to each.
+    static_assert(kJoinThreads >= 4 * MOE_FFN_BEAM_MAX, "lanes for all beams");
+    const int lanes = p.beams <= kJoinThreads / 32 ? 32 : p.beams <= kJoinThreads / 16 ? 16 : p.beams <= kJoinThreads / 8 ? 8 : 4;
+    const int k = tid / lanes, l = tid & (lanes - 1);
+    const bool live_beam = k < p.beams;
+    const long long row = row0 + (live_beam ? k : 0);
+    const bool end = !live_beam || (p.finished && p.finished[row]);
     const float score = p.scores[row];
-    float r[2] = {-INFINITY, -INFINITY};
-    float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = lane + 32 * j;
-      if (end || i >= p.splits) continue;
-      r[j] = p.part_ref[row * p.splits + i];
-      part[j] = p.part_sum[row * p.splits + i];
-    }
-    float top = fmaxf(r[0], r[1]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float* refs = p.part_ref + row * p.splits;
+    const float2* sums = p.part_sum + row * p.splits;
+    const int splits = end ? 0 : p.splits;
+    float2 first = make_float2(0.0f, 0.0f);
+    if (l < splits) first = sums[l];
+    float top = -INFINITY;
+    for (int i = l; i < splits; i += lanes) top = fmaxf(top, refs[i]);
+    for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     Sum sum;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (j > 0 && p.splits <= 32) break;
+#pragma unroll 1
+    for (int i = l; i < splits; i += lanes) {
+      const float r = refs[i];
+      const float2 part = i == l ? first : sums[i];
       Sum a;
-      a.hi = part[j].x;
-      a.lo = part[j].y;
-      if (r[j] != top) a.times(exp_pair(difference(r[j], top)));
+      a.hi = part.x;
+      a.lo = part.y;
+      if (r != top) a.times(exp_pair(difference(r, top)));
       sum.add(a);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll 1
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
       Sum other;
       other.hi = __shfl_xor_sync(0xffffffffu, sum.hi, o);
       other.lo = __shfl_xor_sync(0xffffffffu, sum.lo, o);
       sum.add(other);
       sum.settle();
     }
-    const Sum l = log_pair(sum);
-    if (lane == 0) {
+    const Sum log_sum = log_pair(sum);
+    if (live_beam && l == 0) {
       ended[k] = end;
       beam_ref[k] = top;
       const double sh = end ? static_cast<double>(score)
-                            : static_cast<double>(score) - (static_cast<double>(l.hi) + static_cast<double>(l.lo));
+                            : static_cast<double>(score) - (static_cast<double>(log_sum.hi) + static_cast<double>(log_sum.lo));
       shift[k] = sh;
       rough_shift[k] = static_cast<float>(sh);
     }
@@ -757,67 +785,75 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
               static_cast<unsigned long long>(token & 0xffffff);
     return c;
   };
-  // The first `firsts` candidates of each part, as many that `count` of all can be among them.
-  int firsts = p.count;
-  if (!all) {
-    int mine = 0;
-    for (int i = tid; i < n_parts; i += kJoinThreads) {
-      float off;
-      mine += rough(i * p.count, off) > -INFINITY ? 1 : 0;
-    }
-    if (mine > 0) atomicAdd(&live, mine);
-    __syncthreads();
-    firsts = live > 0 ? (p.count + live - 1) / live : 1;
-  }
-  const int n_firsts = n_parts * firsts;
-  auto at_first = [&](int h) { return firsts == p.count ? h : h / firsts * p.count + h % firsts; };
-  // At least as large as what is found below: `count` of the firsts, less what they may be off by.
+  // The parts' first candidates: their largest value, and how many there are.
   float top = -INFINITY;
-#pragma unroll 4
-  for (int h = tid; h < n_firsts; h += kJoinThreads) {
+  int mine_live = 0;
+#pragma unroll 1
+  for (int i = tid; i < n_parts; i += kJoinThreads) {
     float off;
-    const float v = rough(at_first(h), off);
-    if (v > -INFINITY) top = fmaxf(top, __fsub_rd(v, off));
+    const float v = rough(i * p.count, off);
+    if (!(v > -INFINITY)) continue;
+    ++mine_live;
+    top = fmaxf(top, __fsub_rd(v, off));
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) warp_top[warp] = top;
+  for (int o = 16; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    mine_live += __shfl_xor_sync(0xffffffffu, mine_live, o);
+  }
+  if (lane == 0) {
+    warp_top[warp] = top;
+    atomicAdd(&live, mine_live);
+  }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, warp_top[w]);
-#pragma unroll 4
-  for (int h = tid; h < n_firsts; h += kJoinThreads) {
-    float off;
-    const float v = rough(at_first(h), off);
-    if (v > -INFINITY) atomicAdd(&bins[bin_of(top - __fsub_rd(v, off))], 1);
-  }
-  __syncthreads();
+  // What is looked through: all candidates, or first as many of each part that `count` of all can be among them, and then all of
+  // the parts whose first one is near enough (what comes after it is no larger).
+  uint16_t* near = reinterpret_cast<uint16_t*>(held_x);
+  static_assert(sizeof(held_x) >= 2 * MOE_FFN_BEAM_MAX * kMaxSplits, "all parts");
+  int per = all ? p.count : live > 0 ? (p.count + live - 1) / live : 1;
+  int m = n_parts * per;
+  bool last = all;
   float least = -INFINITY;
-  const float d = bin_end(bin_reached(bins, p.count));
-  if (top < INFINITY && d < INFINITY) least = __fsub_rd(top, d * 1.000001f);
-  auto close = [&](int i) {
-    float off;
-    const float v = rough(i, off);
-    return v > -INFINITY && __fadd_ru(v, off) >= least;
+  auto at = [&](int h) {
+    if (all) return h;
+    const int part = h / per;
+    return (last ? near[part] : part) * p.count + h - part * per;
   };
-  auto note = [&](int i) {
-    const int to = atomicAdd(&found, 1);
-    if (to < kJoinList) list[to].place = static_cast<unsigned long long>(i);
-  };
-  if (all) {
-    for (int i = tid; i < n; i += kJoinThreads)
-      if (close(i)) note(i);
-  } else {
-    // What comes after a part's first one is no larger.
-    for (int base = warp * 32; base < n_parts; base += kJoinThreads) {
-      const int part = base + lane;
-      unsigned which = __ballot_sync(0xffffffffu, part < n_parts && close(part * p.count));
-      for (; which != 0; which &= which - 1) {
-        const int first = (base + __ffs(which) - 1) * p.count;
-        for (int j = lane; j < p.count; j += 32)
-          if (close(first + j)) note(first + j);
+#pragma unroll 1
+  for (;;) {
+    const float d = distance_reached(bins, p.count, last ? kJoinList : p.count + p.count / 2 + 8, [&](auto&& take) {
+#pragma unroll 1
+      for (int h = tid; h < m; h += kJoinThreads) {
+        float off;
+        const float v = rough(at(h), off);
+        if (v > -INFINITY) take(top - __fsub_rd(v, off));
+      }
+    });
+    if (top < INFINITY && d < INFINITY) least = fmaxf(least, __fsub_rd(top, d * 1.000001f));
+    if (!last && tid == 0) live = 0;
+    if (!last) __syncthreads();
+#pragma unroll 1
+    for (int h = tid; h < m; h += kJoinThreads) {
+      const int i = at(h);
+      float off;
+      const float v = rough(i, off);
+      if (!(v > -INFINITY && __fadd_ru(v, off) >= least)) continue;
+      if (last) {
+        const int to = atomicAdd(&found, 1);
+        if (to < kJoinList) list[to].place = static_cast<unsigned long long>(i);
+      } else if (h % per == 0) {
+        near[atomicAdd(&live, 1)] = static_cast<uint16_t>(h / per);
       }
     }
+    if (last) break;
+    __syncthreads();
+    bins.coarse[tid] = bins.fine[tid] = 0;
+    last = true;
+    per = p.count;
+    m = live * per;
+    __syncthreads();
   }
   __syncthreads();
   auto answer = [&](int c, const Candidate& a) {

@@ -76,6 +76,17 @@ def test_spreads(dtype, spread):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lift", [10.0, 40.0, 1e4, 1e9])
+def test_one_far_above_the_rest(dtype, lift):
+    for U, K, V, C in ((2, 4, 128256, 16), (1, 3, 262144, 1), (1, 12, 50001, 22)):
+        logits, scores = _inputs(U, K, V, seed=C, dtype=dtype)
+        logits[torch.arange(U * K), torch.arange(U * K) * 37 % V] = lift
+        _check(logits, scores, C)
+        logits[::2, V - 1] = 0.75 * lift
+        _check(logits, scores, C)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("count", [1, 7, 64])
 def test_orders_that_fill_the_list(dtype, count):
     """Logits that ascend (each tile's are above all before), descend, or are mostly equal."""
