@@ -14,9 +14,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_ffn.so")
 SOURCES = ["moe_ffn.cu", "route.cu", "router.cu", "gemm.cu", "gemm_pair.cu", "quant.cu", "noalloc.cu",
-           "selftest.cu", "kv.cu", "kv_decode.cu", "kv_chunk.cu", "kv_tree.cu", "kv_moves.cu", "norm.cu", "rotary.cu",
-           "beam.cu"]
-HEADERS = ["internal.h", "kv.h", "ptx.cuh"]
+           "selftest.cu", "kv.cu", "kv_decode.cu", "kv_chunk.cu", "kv_tree.cu", "kv_tree_few.cu",
+           "kv_moves.cu", "norm.cu", "rotary.cu", "beam.cu"]
+HEADERS = ["internal.h", "kv.h", "kv_mma.cuh", "kv_tree.cuh", "ptx.cuh"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-I" + INCLUDE]

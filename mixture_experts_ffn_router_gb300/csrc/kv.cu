@@ -523,9 +523,13 @@ int kv_attend(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_ba
   // kernel computes tiles of 256 rows of which it would fill `group`. Single tokens through the one and the other:
   // one short sequence 14 and 20 us, 64 e4m3 sequences (width 512) 78 and 226, 256 windows 217 and 360,
   // one long bf16 sequence 96 and 124.
-  // (A tree of one node is a single token.)
+  // (A tree of one node is a single token.) Trees of up to kFewRows rows to a kv head over e4m3: a kernel of their own, 120 us
+  // against the chunk kernel's 264 for 64 sequences of 1000 to 4000 tokens (width 256), 10 and 20 for one short one. Over bf16 the chunk
+  // kernel is within 8% of the bytes there, and at width 512 of e4m3 their queries and outputs leave too little room.
   cudaError_t e;
   if (a.b.max_new <= 1 && a.group <= kDecodeHeads) e = launch_kv_decode(a, ctas, s);
+  else if (masks && a.c.e4m3 && a.c.head_dim <= 256 && a.b.max_new * a.group <= kFewRows)
+    e = launch_kv_tree_few(a, ctas, s);
   else if (masks) e = launch_kv_tree_chunk(a, kv->tree_pairs, s);
   else e = launch_kv_chunk(a, kv->chunk_pairs, s);
   return e == cudaSuccess ? MOE_FFN_OK : MOE_FFN_ECUDA;
@@ -577,7 +581,7 @@ int moe_ffn_kv_init(moe_ffn_kv** out, const moe_ffn_kv_config* cfg, void* worksp
   // The workspace may be memory that work still queued on some stream writes: that ends before the control words
   // are cleared, and the clearing before any call.
   if (kv_decode_setup() != cudaSuccess || kv_chunk_setup(&kv->chunk_pairs) != cudaSuccess ||
-      kv_tree_chunk_setup(&kv->tree_pairs) != cudaSuccess || kv_moves_setup() != cudaSuccess ||
+      kv_tree_chunk_setup(&kv->tree_pairs) != cudaSuccess || kv_tree_few_setup() != cudaSuccess || kv_moves_setup() != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess || cudaMemset(kv->ws, 0, l.partial) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     delete kv;

@@ -113,6 +113,7 @@ struct KvAttn {
 // their running maxima and sums.
 constexpr int kDecodeMaxCtas = 304;
 constexpr int kDecodeHeads = 8;
+constexpr int kFewRows = 16;  // of small trees: (node, query head) to a kv head
 __host__ __device__ constexpr long long decode_piece_floats(int head_dim) {
   return static_cast<long long>(kDecodeHeads) * head_dim + 2 * kDecodeHeads;
 }
@@ -136,6 +137,8 @@ cudaError_t kv_chunk_setup(int* pairs);
 cudaError_t launch_kv_chunk(const KvAttn& a, int pairs, cudaStream_t s);
 cudaError_t kv_tree_chunk_setup(int* pairs);
 cudaError_t launch_kv_tree_chunk(const KvAttn& a, int pairs, cudaStream_t s);
+cudaError_t kv_tree_few_setup();
+cudaError_t launch_kv_tree_few(const KvAttn& a, int ctas, cudaStream_t s);
 cudaError_t kv_moves_setup();
 cudaError_t launch_kv_tree(const KvBatch& b, const KvCache& c, const int32_t* parents, uint32_t* masks, int32_t* depth,
                            unsigned int* status, cudaStream_t s);

@@ -138,6 +138,28 @@ def test_long_caches(fmt, hq, hkv, d, page, new, kv, window, sinks):
     _check(case, _trees(case), window, sinks)
 
 
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("hq,hkv,most", [(2, 2, 16), (3, 1, 5), (8, 4, 8), (16, 2, 2), (16, 1, 1), (12, 4, 4)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5, 2), (130, 0), (300, 140)])
+def test_few_rows(d, hq, hkv, most, window, sinks):
+    """At most 16 rows to a kv head, over pages of every size, contexts that end anywhere in a tile, empty sequences."""
+    new = [most, 1, 0, max(1, most // 2), most, most, 1, most]
+    kv = [most, 1, 17, 127, 128 + most, 700, 129, 1500]
+    for page in (16, 64, 128):
+        case = U.Case("e4m3", hq, hkv, d, page, new, kv, pad_rows=2, seed=page + most)
+        for shape in ("random", "chain", "star"):
+            _check(case, _trees(case, shape), window, sinks)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_few_rows_of_many_and_long_sequences(d):
+    _check(*(lambda c: (c, _trees(c)))(U.Case("e4m3", 4, 2, d, 16, [2, 1, 8, 3] * 100, [9, 1, 150, 30] * 100, seed=d)))
+    case = U.Case("e4m3", 2, 1, d, 64, [8], [40_000], seed=d + 1)  # its pieces are joined in groups
+    _check(case, _trees(case))
+    case = U.Case("e4m3", 4, 2, d, 128, [3, 4, 2], [9_000, 70, 20_000], seed=d + 2)
+    _check(case, _trees(case), 8_000, 3)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_a_chain_is_the_causal_rule(fmt):
     case = U.Case(fmt, 8, 2, 256, 32, [30, 1, 64], [200, 50, 64], seed=6)
