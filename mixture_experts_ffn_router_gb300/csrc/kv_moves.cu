@@ -5,7 +5,7 @@
 // all layers' in a launch, so the launch and the chain of small loads before the first row (lengths, path, page
 // ids, rows) bound it; only many beams' pages in many layers come near HBM's rate. In a graph, the path of one tree in one
 // layer takes 1.7 us and a user's beams 1.9; from Python the calls take 10 and 7. The pages under way of 16 users' 5 beams in
-// 6 layers: 14.2 us, 4.4 TB/s.
+// 6 layers: 12.2 us, 5.1 TB/s.
 #include "internal.h"
 #include "kv.h"
 #include "ptx.cuh"
@@ -154,7 +154,7 @@ constexpr int kReorderThreads = 128;
 // pages of 128, 6 layers, take 33 us with a block for each vector that there could be, 12 with these (14 with a quarter, 16
 // with four times as many).
 constexpr int kReorderCtas = 16 * 152;
-constexpr int kReorderRegs = 8;  // beams whose vectors a thread holds in registers (5 beams: 14.2 us, in shared memory 14.7)
+constexpr int kReorderRegs = 8;  // beams whose vectors a thread holds in registers (8 beams: 24.6 us, in shared memory 26.6)
 
 // Blocks of a user and plane, then (of the first plane) one for the user's table. A thread takes one vector of one
 // slot and head, of all the user's beams: it reads what any beam takes from another, then writes, so no other

@@ -231,6 +231,90 @@ def test_values_of_far_apart_sizes(d, big):
     _check(case, _trees(case, "roots"), 60, 1)
 
 
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (4, 2), (40, 0)])
+def test_few_rows_and_hidden_values(d, window, sinks):
+    """As above, of up to 16 rows: what a node holds reaches only those below it, whatever its size, and bytes behind the
+    last node reach nobody."""
+    def case():
+        return U.Case("e4m3", 4, 2, d, 16, [8, 5], [150, 40], seed=d + window)
+    trees = _trees(case(), "comb")
+    kv = case().handle()
+    want, wl, tol, ltol = W.attention(case(), trees, window, sinks)
+    for name, value in (("k", math.nan), ("k", math.inf), ("v", math.nan), ("v", -math.inf)):
+        other = case()
+        for leaf in (3, 7):  # leaves: seen by themselves alone
+            getattr(other, name)[0][142 + leaf, :, 5] = value
+        cache = other.filled(kv)
+        for t in (cache.k, cache.v):  # the slots behind the second sequence's last node
+            t.view(torch.uint8)[int(other.pages[1, 2]), :, 8:] = 0x7f
+        for t in (cache.k_scale, cache.v_scale):
+            t[int(other.pages[1, 2]), :, 8:] = math.nan
+        tree = kv.tree(other.batch(), _flat(other, trees))
+        out, lse = kv.tree_attention(cache, other.batch(), tree, other.q.cuda(), window=window, sinks=sinks)
+        _ok(kv)
+        seen = torch.zeros(other.T, dtype=torch.bool)
+        seen[[3, 7]] = True
+        U.check_close(out[~seen.cuda()], want[~seen], tol[~seen], name)
+        U.check_close(lse[~seen.cuda()], wl[~seen], ltol[~seen], name)
+        assert not torch.isfinite(out[seen.cuda()]).all(-1).any()
+    for big in (2.0 ** -30, 2.0 ** 30):
+        other = case()
+        other.v[0][145] = (other.v[0][145].float() * big).to(torch.bfloat16)
+        other.v[0][3] = (other.v[0][3].float() * big).to(torch.bfloat16)
+        other.v[1][20:] = (other.v[1][20:].float() * big).to(torch.bfloat16)
+        _check(other, _trees(other, "binary"), window, sinks)
+        _check(other, _trees(other, "roots"), window, sinks)
+
+
+def test_few_rows_captured_and_repeated():
+    case = U.Case("e4m3", 8, 4, 256, 32, [8, 3, 8], [9000, 39, 600], seed=13)
+    kv = case.handle()
+    cache, batch = case.filled(kv), case.batch()
+    p, q = _flat(case, _trees(case)), case.q.cuda()
+    first = kv.tree_attention(cache, batch, kv.tree(batch, p), q)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out, lse = kv.tree_attention(cache, batch, kv.tree(batch, p), q)
+    for _ in range(5):
+        graph.replay()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    for shape in ("chain", "star"):
+        p.copy_(_flat(case, _trees(case, shape, 3)))
+        graph.replay()
+        _ok(kv)
+        want, wl, tol, ltol = W.attention(case, _trees(case, shape, 3))
+        U.check_close(out, want, tol, shape)
+        U.check_close(lse, wl, ltol, shape)
+
+
+def test_few_rows_with_bad_batches():
+    """Sequences with more nodes than cached tokens, and pages that are none: status, and the others as they should be."""
+    case = U.Case("e4m3", 4, 2, 128, 16, [4, 4, 4], [40, 40, 40], seed=14)
+    kv = case.handle()
+    cache = case.filled(kv)
+    batch, q = case.batch(), case.q.cuda()
+    tree = kv.tree(batch, _flat(case, _trees(case)))
+    want = kv.tree_attention(cache, batch, tree, q)
+    _ok(kv)
+    short = batch.tensors[1].clone()
+    short[1] = 3
+    out, lse = kv.tree_attention(cache, B.KVBatch(batch.tensors[0], short, batch.tensors[2], max_new=4), tree, q)
+    torch.cuda.synchronize()
+    assert kv.status() == (B.MOE_FFN_EDEVICE, BAD)
+    assert (out[4:8] == 0).all() and (lse[4:8] == -math.inf).all()
+    for i in (slice(0, 4), slice(8, 12)):
+        assert torch.equal(out[i], want[0][i]) and torch.equal(lse[i], want[1][i])
+    none = batch.tensors[2].clone()
+    none[1, 0] = 10 ** 6
+    out, lse = kv.tree_attention(cache, B.KVBatch(batch.tensors[0], batch.tensors[1], none, max_new=4), tree, q)
+    torch.cuda.synchronize()
+    assert kv.status() == (B.MOE_FFN_EDEVICE, BAD)
+    for i in (slice(0, 4), slice(8, 12)):
+        assert torch.equal(out[i], want[0][i]) and torch.equal(lse[i], want[1][i])
+
+
 def test_rows_far_apart_and_strided_queries():
     case = U.Case("bf16", 8, 2, 128, 32, [6, 9], [100, 9], seed=9)
     fused = torch.zeros(case.T, 12, 128, dtype=torch.bfloat16, device="cuda")
