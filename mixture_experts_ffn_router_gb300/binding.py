@@ -1094,6 +1094,10 @@ class BeamSearch:
             raise ValueError("invalid configuration")
         self.device = torch.device("cuda", int(device))
         self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+        # It may be memory that work still queued on this stream writes; the first call may come on another one, or be
+        # captured, and then waits for nothing. (Allocated within a capture it is the graph's own.)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()
         self._workspace = self.workspace.data_ptr()
         self._shapes = tuple(torch.Size(t) for t in ((self.users * self.beams, self.vocab), (self.users, self.beams, self.vocab),
                                                      (self.users, self.beams)))

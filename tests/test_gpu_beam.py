@@ -303,3 +303,26 @@ def test_two_searches_at_once():
         want = _wanted(logits, scores, 10)
         for g in got[i::2]:
             assert torch.equal(g[1], want[1]) and torch.equal(g[2], want[2])
+
+
+def test_a_search_made_while_its_memory_is_written():
+    """Its workspace was another tensor's, which work queued on the stream it is made on still writes; the first call
+    comes on another stream."""
+    logits, scores = _inputs(8, 5, 50_001, seed=3)
+    want = B.BeamSearch(8, 5, 50_001, 10).select(logits, scores)
+    nbytes = B.moe_ffn_beam_workspace_bytes(8, 5, 50_001, 10)
+    before, after = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(before):
+        large = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+        was = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(before):
+        for i in range(40):
+            large.fill_(i)
+            was.fill_(0x7f)
+        del was
+        search = B.BeamSearch(8, 5, 50_001, 10)
+    with torch.cuda.stream(after):
+        got = search.select(logits, scores)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -177,6 +177,35 @@ def test_selection_alignment_and_room():
     assert B.moe_ffn_beam_workspace_bytes(4096, 64, 1 << 24, 64) > 4096 * 64 * 64 * 8
 
 
+class _Streams:
+    """In the place of torch's streams: what is done with the current one, in order."""
+
+    def __init__(self, monkeypatch, capturing=False):
+        self.done = []
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+
+    def synchronize(self):
+        self.done.append("synchronize")
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_search_waits_for_what_its_workspace_was(monkeypatch, capturing):
+    """Work queued before on the stream that a search is made on may still write the memory that it gets; no call on
+    another stream would wait for that."""
+    streams = _Streams(monkeypatch, capturing)
+    empty = torch.empty
+
+    def allocate(*size, device=None, **kw):
+        assert device == torch.device("cuda", 0)
+        streams.done.append("allocate")
+        return empty(*size, **kw)
+
+    monkeypatch.setattr(torch, "empty", allocate)
+    B.BeamSearch(2, 4, 100, 8)
+    assert streams.done == (["allocate"] if capturing else ["allocate", "synchronize"])
+
+
 # ------------------------------------------------------------------ the cache's calls
 
 def test_calls_without_a_handle():
