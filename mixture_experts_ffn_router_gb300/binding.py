@@ -1014,7 +1014,8 @@ def block_norm(x, block=None, post=None, gate=None, scale: float = 1.0, pre=None
 class Rotary:
     """Rotary positions with one or several axes. freqs: each pair's radians per position; axes: the axis whose
     position turns it (all 0 if not given). Pair i of a head is (i, pairs + i), or (2i, 2i + 1) where interleaved;
-    elements after the pairs stay as they are. scale multiplies the turned elements."""
+    elements after the pairs stay as they are. scale multiplies the turned elements. Keep the object as long as a graph
+    that captured it."""
 
     def __init__(self, freqs, axes=None, interleaved: bool = False, scale: float = 1.0, device: int = 0):
         import torch
@@ -1029,6 +1030,7 @@ class Rotary:
         self.interleaved, self.scale = bool(interleaved), float(scale)
         self.table = torch.tensor(signed, dtype=torch.int64).to(self.device)
         self._table = self.table.data_ptr()
+        self._last_raw = None
 
     def _rows(self, what, t, T, D, bf16):
         """A tensor's address and strides, packed, and its heads."""
@@ -1075,6 +1077,10 @@ class Rotary:
             if k is not None:
                 k = torch.empty((T, k_heads, D), dtype=bf16, device=device)
                 k_to = _PACK_ROWS(k.data_ptr(), k_heads * D if T > 1 else 0, D if k_heads > 1 else 0)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        if raw != self._last_raw and not torch.cuda.is_current_stream_capturing():
+            self.table.record_stream(torch.cuda.current_stream(device))  # dropped early, it stays until the stream is done with it
+            self._last_raw = raw
         a = _PACK_ROTARY(self._table, positions.data_ptr(), steps[0] if self.axes > 1 else 0, self.scale, self.pairs, self.axes,
                          self.interleaved, inverse, T, D, q_heads, k_heads)
         _check("moe_ffn_rotary_apply", _launch(lib().moe_ffn_rotary_apply, device, a, q_rows, k_rows, q_to, k_to))

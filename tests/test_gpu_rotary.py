@@ -227,3 +227,24 @@ def test_places_past_32_bits():
     before = q[rows]
     B.Rotary(freqs).apply(q, None, positions, inplace=True)
     _check(q[rows], before, freqs, [0] * (D // 2), positions[rows])
+
+
+def test_dropped_while_another_stream_still_turns():
+    """The table's memory goes to new tensors of the stream it was made on only after the queued call."""
+    T = 64
+    q = _rows(T, 16, 256)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 7
+    want = B.Rotary(_freqs(128)).apply(q, None, pos)[0]
+    side = torch.cuda.Stream()
+    large = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    r = B.Rotary(_freqs(128))
+    nbytes = r.table.numel() * 8
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(40):
+            large.fill_(i)
+        got = r.apply(q, None, pos)[0]
+    del r
+    over = [torch.full((nbytes,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(200)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(over) == 200

@@ -104,6 +104,46 @@ def test_tables_are_checked():
             B.Rotary([1.0] * n)
 
 
+class _OnGpu:
+    """In the place of a class's tensor argument: on a GPU as far as it says."""
+
+    def __init__(self, *shape, dtype):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", 0)
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return torch.empty(self.shape, device="meta").stride()
+
+    def data_ptr(self):
+        return AT
+
+
+def test_a_table_stays_until_every_stream_is_done_with_it(monkeypatch):
+    """The table belongs to the stream it was made on. Dropped while another one's call is queued, its memory must not
+    go to new work before that; a call that is captured runs later, and says so nowhere."""
+    raw, capturing, recorded = [1], [False], []
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: raw[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: raw[0])
+    monkeypatch.setattr(B, "_launch", lambda call, device, *args: B.MOE_FFN_OK)
+    monkeypatch.setattr(torch.Tensor, "to", lambda self, device: _Table())
+
+    class _Table:
+        def data_ptr(self):
+            return AT
+
+        def record_stream(self, stream):
+            recorded.append(stream)
+
+    r = B.Rotary([1.0] * 4)
+    q, positions = _OnGpu(3, 2, 8, dtype=torch.bfloat16), _OnGpu(3, dtype=torch.int32)
+    for raw[0], capturing[0] in ((1, False), (1, False), (2, False), (3, True), (3, True), (3, False), (1, False)):
+        r.apply(q, None, positions, inplace=True)
+    assert recorded == [1, 2, 3, 1]
+
+
 def _rotary(rows=None, **change):
     a = dict(table=AT, positions=2 * AT, positions_stride=4, scale=1.0, pairs=32, axes=1, interleaved=0, inverse=0, tokens=4,
              head_dim=64, q_heads=2, k_heads=1)
