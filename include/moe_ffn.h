@@ -530,8 +530,8 @@ int moe_ffn_block_norm(const moe_ffn_norm* a, void* stream);
 #define MOE_FFN_ROTARY_MAX_PAIRS 512
 
 typedef struct moe_ffn_rotary_pair {
-  uint64_t turn;  /* freq / 2 pi modulo 1, times 2^64: a product with a position wraps at whole turns, so that an
-                     angle is off by 2^-33 turns and its fp32 rounding at any position */
+  uint64_t turn;  /* freq / 2 pi modulo 1, times 2^64, rounded to nearest: a product with a position wraps at whole
+                     turns, so that an angle is off by less than 2^-32 turns and its fp32 rounding at any position */
   uint64_t axis;
 } moe_ffn_rotary_pair;
 

@@ -8,9 +8,9 @@
 // 94% of the copy rate.) 64 tokens of 24 heads take 2.3 us in a graph, and the call from Python 12.
 //
 // Angles. In fp32 a position of a million leaves a tenth of a radian unknown, and in fp64 an angle would cost more
-// than the rest. Here a frequency is a fraction of a turn in 64-bit fixed point: its product with the position, modulo
-// 2^64, is the angle modulo a turn, and its upper 32 bits, as a signed number, the angle in (-1/2, 1/2] turns to
-// 2^-33, which sincospif takes.
+// than the rest. Here a frequency is a fraction of a turn in 64-bit fixed point, rounded from the exact quotient (to 2^-65):
+// its product with the position, modulo 2^64, is the angle modulo a turn to 2^-34, and its upper 32 bits, as a signed
+// number and rounded to nearest (to 2^-33), the angle in (-1/2, 1/2] turns, which sincospif takes.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -216,6 +216,55 @@ bool apart(const Extent& a, int a_heads, const Extent& b, int b_heads, int token
   return a_heads > 1 && b_heads > 1 && a.head == b.head && a.head > 0 && apart_modulo(a.at, at + row, b.at, bt + row, a.head);
 }
 
+// 2 pi / 8 in binary, a fraction of 1280 bits, the highest word first.
+constexpr uint64_t kEighthOfTurn[20] = {
+    0xc90fdaa22168c234ull, 0xc4c6628b80dc1cd1ull, 0x29024e088a67cc74ull, 0x020bbea63b139b22ull,
+    0x514a08798e3404ddull, 0xef9519b3cd3a431bull, 0x302b0a6df25f1437ull, 0x4fe1356d6d51c245ull,
+    0xe485b576625e7ec6ull, 0xf44c42e9a637ed6bull, 0x0bff5cb6f406b7edull, 0xee386bfb5a899fa5ull,
+    0xae9f24117c4b1fe6ull, 0x49286651ece45b3dull, 0xc2007cb8a163bf05ull, 0x98da48361c55d39aull,
+    0x69163fa8fd24cf5full, 0x83655d23dca3ad96ull, 0x1c62f356208552bbull, 0x9ed529077096966dull};
+
+// x / 2 pi modulo 1, times 2^64, of x >= 0, rounded to nearest: a long division, a bit at a time. (A quotient in fp64 is
+// known to 2^-53 of itself, which a position of 2^31 makes 2^-25 turns at x = 1, and a large x a part of a turn.)
+uint64_t turn_of(double x) {
+  if (x == 0.0) return 0;
+  int exponent;
+  const double f = std::frexp(x, &exponent);  // [1/2, 1)
+  const int last = exponent + 61;              // x / 2 pi 2^64 = f / (2 pi / 8) 2^last
+  if (last < -1) return 0;
+  // The divisor's words after these change the quotient by less than 2^-64 of its last bit.
+  const int n = (last + 64) / 64 + 1;
+  static_assert((1024 + 61 + 64) / 64 + 1 <= 20, "words");
+  uint64_t r[20] = {static_cast<uint64_t>(std::ldexp(f, 64))}, q = 0;
+  for (int bit = 0; bit <= last + 1; ++bit) {
+    uint64_t carry = 0;
+    if (bit > 0)
+      for (int i = n - 1; i >= 0; --i) {
+        const uint64_t out = r[i] >> 63;
+        r[i] = r[i] << 1 | carry;
+        carry = out;
+      }
+    bool less = false;
+    if (carry == 0)
+      for (int i = 0; i < n; ++i)
+        if (r[i] != kEighthOfTurn[i]) {
+          less = r[i] < kEighthOfTurn[i];
+          break;
+        }
+    if (!less) {
+      uint64_t borrow = 0;
+      for (int i = n - 1; i >= 0; --i) {
+        const uint64_t was = r[i], d = kEighthOfTurn[i];
+        r[i] = was - d - borrow;
+        borrow = was < d || (was == d && borrow != 0) ? 1 : 0;
+      }
+    }
+    // The bits up to the last, as many as 64 hold, then the one that rounds.
+    q = bit <= last ? q << 1 | (less ? 0 : 1) : q + (less ? 0 : 1);
+  }
+  return q;
+}
+
 bool own_rows_apart(const Extent& e, int tokens, int heads, int dim) {
   const long long row = 2LL * dim;
   if (heads > 1 && e.head < row) return false;
@@ -232,8 +281,7 @@ extern "C" int moe_ffn_rotary_table(const double* freq, const int* axis, int pai
   for (int i = 0; i < pairs; ++i)
     if (!std::isfinite(freq[i]) || axis[i] < 0 || axis[i] >= MOE_FFN_ROTARY_MAX_AXES) return MOE_FFN_EINVAL;
   for (int i = 0; i < pairs; ++i) {
-    const double turns = std::fmod(std::fabs(freq[i]) / 6.283185307179586476925, 1.0);  // in [0, 1)
-    const uint64_t t = static_cast<uint64_t>(std::ldexp(turns, 64));
+    const uint64_t t = moe::turn_of(std::fabs(freq[i]));
     table[i].turn = freq[i] < 0.0 ? 0 - t : t;
     table[i].axis = static_cast<uint64_t>(axis[i]);
   }

@@ -5,6 +5,7 @@ good to two units in the last place (2^-23): together 2^-21 of either at most. I
 itself known to 2^-51 a (a frequency's quotient and the product). The two products and their sum lose 3 * 2^-24 of their
 magnitudes, and the result is rounded to bf16 once (2^-8)."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -248,3 +249,18 @@ def test_dropped_while_another_stream_still_turns():
     over = [torch.full((nbytes,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(200)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(over) == 200
+
+
+def test_far_positions_and_fast_turns():
+    """Angles of up to 10^15 radians, against their exact remainders: off by 2^-32 turns and the fp32 rounding, whatever the
+    position and the frequency (together with the sine's, 2^-21 as above)."""
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    freqs = [1.0, -0.3, 12345.678, 1e6, 333333.3, 7654321.0, 1e-3, 2.0 ** 20]
+    at = [2 ** 31 - 1, -2 ** 31, 2 ** 24, 10 ** 6, -10 ** 6 - 3, 2 ** 30 + 12345, 1, 0]
+    angle = torch.tensor([[float(Fraction(f) * p % two_pi) for f in freqs] for p in at], dtype=torch.float64)[:, None]
+    q = _rows(len(at), 16, 16)
+    got = B.Rotary(freqs).apply(q, None, torch.tensor(at, dtype=torch.int64).to(torch.int32).cuda())[0].double().cpu()
+    a, b = q.double().cpu().split(8, -1)
+    d = (a.abs() + b.abs()) * (2.0 ** -21 + 3 * F32)
+    for r, g in ((a * angle.cos() - b * angle.sin(), got[..., :8]), (b * angle.cos() + a * angle.sin(), got[..., 8:])):
+        assert ((g - r).abs() <= d + BF * (r.abs() + d)).all()

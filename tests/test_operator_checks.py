@@ -3,6 +3,7 @@ without a GPU: every call here fails its checks before it touches a pointer."""
 import ctypes
 import math
 import os
+import random
 import subprocess
 from fractions import Fraction
 
@@ -91,6 +92,34 @@ def test_turns_are_exact_fractions():
         off = (Fraction(turn, 1 << 64) - exact) % 1
         off = min(off, 1 - off)
         assert off <= abs(exact) / (1 << 51) + Fraction(1, 1 << 64)
+
+
+def _two_pi(bits):
+    """2 pi to that many bits, by Machin's formula."""
+    def arctan_of_inverse(n):
+        total = power = (1 << (bits + 32)) // n
+        k = sign = 1
+        while power:
+            power //= n * n
+            k, sign = k + 2, -sign
+            total += sign * (power // k)
+        return total
+    return Fraction(8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239)), 1 << (bits + 32))
+
+
+def test_turns_are_rounded_once():
+    """Every frequency's fraction of a turn is the exact quotient's, rounded to the nearest of 2^64."""
+    two_pi = _two_pi(1400)
+    rng = random.Random(5)
+    freqs = [1.0, 1e4 ** -0.5, 1e-6, -0.3, 6.283185307179586, 12345.678, 1e6, 0.0, 1e300, -1.7976931348623157e308, 5e-324, -1e-9]
+    freqs += [math.ldexp(f, e) for e in (-62, -61, -60, -59, -2, 2, 3, 64, 130) for f in (0.5, 0.75, 0.7853981633974482, 0.7853981633974483,
+                                                                                         0.7853981633974484, 0.9999999999999999)]
+    freqs += [math.ldexp(0.5 + rng.random() / 2, rng.randint(-70, 40)) for _ in range(200)]
+    freqs += [math.ldexp(0.5 + rng.random() / 2, rng.randint(40, 1024)) for _ in range(100)]
+    table = B.moe_ffn_rotary_table(freqs, [0] * len(freqs))
+    for f, (turn, _) in zip(freqs, table):
+        off = (Fraction(turn, 1 << 64) - Fraction(f) / two_pi) % 1
+        assert min(off, 1 - off) <= Fraction(1, 1 << 65) * (1 + Fraction(1, 1 << 60)), f
 
 
 def test_tables_are_checked():
