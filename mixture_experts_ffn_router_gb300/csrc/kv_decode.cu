@@ -89,6 +89,7 @@ struct SeqTiles {
 template <int KT>
 __device__ __forceinline__ SeqTiles seq_tiles(const KvAttn& a, int seq) {
   const KvSeq s = kv_sequence(a.b, a.c, seq, a.status);
+  if (a.tree && s.len < s.n) atomicOr(a.status, kStatusBadIndex);  // a drafted token that the cache does not hold
   SeqTiles t;
   t.row = s.row0;
   t.span = kv_span(s.n > 0 ? s.len - 1 : -1, a.window, a.sinks);

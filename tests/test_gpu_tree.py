@@ -777,3 +777,25 @@ def test_reordered_pages_of_many_rows(fmt, beams):
     assert torch.equal(pages.cpu(), want_table)
     for c, w in zip(layers, want):
         assert all(torch.equal(t, w[n]) for n, t in _bits(c).items())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq", [2, 8, 16, 24])
+def test_single_nodes_without_room_are_reported(fmt, hq):
+    """A sequence of one node of which the cache holds nothing, whichever kernel takes the batch."""
+    case = U.Case(fmt, hq, 1, 128, 16, [1, 1, 1], [30, 1, 50], seed=12)
+    kv = case.handle()
+    cache = case.filled(kv)
+    batch = case.batch()
+    tree = kv.tree(batch, torch.full((3,), -1, dtype=torch.int32, device="cuda"))
+    want, want_lse = kv.tree_attention(cache, batch, tree, case.q.cuda())
+    _ok(kv)
+    batch.tensors[1][1] = 0
+    out, lse = kv.tree_attention(cache, batch, tree, case.q.cuda(), out=torch.ones_like(want))
+    torch.cuda.synchronize()
+    assert kv.status() == (B.MOE_FFN_EDEVICE, BAD)
+    assert not out[1].any() and (lse[1] == -math.inf).all()
+    assert torch.equal(out[::2], want[::2]) and torch.equal(lse[::2], want_lse[::2])
+    # Of tokens that are no tree the same is no error.
+    kv.attention(cache, batch, case.q.cuda())
+    _ok(kv)
