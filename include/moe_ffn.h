@@ -563,8 +563,9 @@ int moe_ffn_rotary_apply(const moe_ffn_rotary* a, const moe_ffn_kv_rows* q, cons
  * best first, ties by the lower beam, then the lower token. A finished beam has one continuation, the end token, with
  * its score unchanged, and its logits are not read. A continuation of -infinity or NaN is none (a NaN or +infinity
  * among a beam's logits leaves it without any); where there are fewer than `count`, the rest have score
- * -infinity, beam -1 and token -1. The sums are formed to about 1e-8, the comparisons made in fp64, within a beam of the
- * logits themselves; a score that fp32 rounds to -infinity counts as such. */
+ * -infinity, beam -1 and token -1. The sums are formed to about 1e-8 where few logits or many different ones carry the
+ * weight, and to 2^-20 where 10^5 equal ones do; the comparisons are made in fp64, within a beam of the logits themselves;
+ * a score that fp32 rounds to -infinity counts as such. */
 typedef struct moe_ffn_beam {
   const void* logits;      /* device pointer, [users * beams, vocab], rows logits_stride elements apart */
   long long logits_stride; /* >= 0 */

@@ -13,11 +13,17 @@
 // in steps that the list has room for: when it is long, it is cut to the `count` best, which raise the threshold.
 //
 // Sums. What is at most the threshold is added as exp(x - R) with R the first tile's maximum, by the hardware's
-// 2^x: that is off by up to 2^-22 of a term, which averages out over many small ones, and sums of 16 go into a pair of
-// fp32 numbers that keeps the rounding (D. E. Knuth, "The Art of Computer Programming" 2, 4.2.2, Theorem B). What is above
-// it may outweigh all else: the selected logits' terms are formed in such pairs, by the exponential's series, the
-// others' are added as integers, whose sum does not depend on the order in which they were noted. log sum exp is then
-// good to about 1e-8, below which values of different beams seldom lie, and equal rows have equal sums wherever they lie.
+// 2^x, and sums of 16 go into a pair of fp32 numbers that keeps the rounding (D. E. Knuth, "The Art of Computer
+// Programming" 2, 4.2.2, Theorem B). What is above it may outweigh all else: these terms are formed in such pairs, by the
+// exponential's series, to 2^-30; the selected logits' are added in the order of their ranks, the others' as integers, whose
+// sum does not depend on the order in which they were noted. So that few large logits are above it however few are asked
+// for, the threshold is lowered to the kExact-th of the threads' maxima where `count` is less (and only what is above
+// the count-th is ranked). (160 rows, the best 32.2 us, 30.0 without; with 16 of them instead of 8 33.5, and the 10 best
+// 30.3 instead of 28.6.)
+//   A term below the threshold is off by 2^-22 of itself, and by half a step of the exponent, log2 e of its distance from
+// R. Over many different ones that averages out: log sum exp is good to about 1e-8, below which values of different
+// beams seldom lie. Many equal ones are all off alike, by up to 2^-20 if it takes 10^5 of them to outweigh the
+// largest. Equal rows have equal sums wherever they lie.
 //
 // fp64 is slow here (an operation takes a warp 16 cycles or more, and its result some 60): only the last comparisons
 // are made in it.
@@ -49,6 +55,11 @@ constexpr int kList = 2560;
 constexpr int kListLong = kList - kThreads * 8 - 32;  // what still has room for a vector of each thread, and the ends
 constexpr int kMaxSplits = 64;
 constexpr int kMaxCount = MOE_FFN_BEAM_MAX;
+// As many of a part's largest logits at least have their terms formed in two numbers, as far as they lie within kNear of
+// the first tile's maximum (one that is further weighs at most e^-4 of it, and 2^-22 of that is 4e-9), and unless there are more
+// than kNearMost in the distance of the last (many like it: rather none of these, as there would be no room for them).
+constexpr int kExact = 8, kNearMost = 48;
+constexpr float kNear = 4.0f;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinHeld = 2048;  // candidates
@@ -93,10 +104,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 constexpr float kLog2eHigh = 1.44269502f;          // log2 e, and what fp32 leaves of it
 constexpr float kLog2eLow = 1.92596303e-8f;
 
-// exp(x - ref).
+// exp(x - ref). (The small product first: the exponent is rounded once.)
 __device__ __forceinline__ float term(float x, float ref) {
   const float d = __fsub_rn(x, ref);
-  return exp2_approx(fmaf(d, kLog2eLow, __fmul_rn(d, kLog2eHigh)));
+  return exp2_approx(fmaf(d, kLog2eHigh, __fmul_rn(d, kLog2eLow)));
 }
 
 __device__ __forceinline__ unsigned long long two(float a, float b) {
@@ -117,8 +128,8 @@ __device__ __forceinline__ void terms(const float (&x)[8], float ref, float (&e)
   for (int i = 0; i < 8; i += 2) {
     const unsigned long long d = add2(two(x[i], x[i + 1]), r2);
     unsigned long long t;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(d), "l"(high));
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(d), "l"(low), "l"(t));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(d), "l"(low));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(d), "l"(high), "l"(t));
     float a, b;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(t));
     e[i] = exp2_approx(a);
@@ -481,10 +492,18 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
     for (int i = 0; i < N; ++i) m = fmaxf(m, f[i]);
   }
   float ref = cta_max(s, m);
-  // (Rounded down, and by more than the distances' rounding: what is in the bins is above it.)
-  float above = -INFINITY;
+  // (Rounded down, and by more than the distances' rounding: what is in the bins is above it.) What may be selected is above
+  // `listed`; what is above `above` alone has its term formed in two numbers.
+  float above = -INFINITY, listed = -INFINITY;
   const float d = distance_reached(s.bins, p.count, p.count + p.count / 2 + 8, [&](auto&& take) { take(ref - m); });
-  if (ref < INFINITY && d < INFINITY) above = __fsub_rd(ref, d * 1.000001f);
+  if (ref < INFINITY && d < INFINITY) {
+    listed = above = __fsub_rd(ref, d * 1.000001f);
+    if (p.count < kExact) {
+      int less;
+      const int b = bin_reached(s.bins.coarse, kExact, less);
+      if (b > 0) above = fminf(above, __fsub_rd(ref, fminf(bin_end(less + s.bins.coarse[b] <= kNearMost ? b : b - 1), kNear)));
+    }
+  }
   float unit = ref == -INFINITY ? 0.0f : ref;
 
   Sum sum;
@@ -532,23 +551,35 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
   }
   __syncthreads();
   const int noted = s.n_noted;
+  long long fixed = 0;
+  // A logit that is too small to be selected, and the same of what is listed but not selected below: added in units of
+  // 2^-36 exp(ref), as long as it is no more than e^10 of these.
+  auto add_fixed = [&](float x) {
+    const Sum t = exp_pair(difference(x, unit));
+    fixed += __float2ll_rn(t.hi * 0x1p36f) + __float2ll_rn(t.lo * 0x1p36f);
+  };
   for (int i = tid; i < min(noted, kNoted); i += kThreads) {
     const int at = s.noted_at[i];
     float f[N];
     L::unpack(s.noted[i], f);
+    uint32_t near = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       if (!(f[k] > above)) continue;
+      if (!(f[k] > listed)) {
+        near |= 1u << k;
+        continue;
+      }
       const int to = atomicAdd(&s.n, 1);
       if (to < kList) s.list[to] = entry(f[k], at * N + k);
     }
+#pragma unroll 1
+    for (; near != 0u; near &= near - 1u) add_fixed(L::value(reinterpret_cast<const T*>(&s.noted[i])[__ffs(near) - 1]));
   }
   __syncthreads();
   int found = -1;
-  long long fixed = 0;
   if (__builtin_expect(noted <= kNoted && s.n <= kList, 1)) {
-    // What is listed but not selected is added in units of 2^-36 exp(ref), as long as it is no more than e^10 of these (or
-    // there are more than `count` such: then in the other way).
+    // (Where there are more than `count` above e^10 of these: in the other way.)
     const int n = s.n;
     found = select_best(s, n, p.count);
     bool large = false;
@@ -557,11 +588,12 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
       if (e >= s.best[found - 1]) continue;
       const float x = entry_x(e);
       large |= x > ref + 10.0f;
-      fixed += __float2ll_rn(term(x, unit) * 0x1p36f);
+      add_fixed(x);
     }
     if (__syncthreads_or(large)) found = -1;
   }
   if (found < 0) {
+    const int exact = max(p.count, kExact);
     float m = x_side;
     for (int i = lo + tid; i < hi; i += kThreads) {
       float f[N];
@@ -583,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
       __syncthreads();
       if (at == lo && side < head && x_side > above) s.list[atomicAdd(&s.n, 1)] = entry(x_side, side);
       if (n > kListLong) {
-        const int best = select_best(s, n, p.count);
+        const int best = select_best(s, n, exact);
         if (tid < best) s.list[tid] = s.best[tid];
         if (tid == 0) s.n = best;
         above = fmaxf(above, entry_x(s.best[best - 1]));  // (as many as are asked for: of equal ones the earlier win)
@@ -600,9 +632,11 @@ __global__ void __launch_bounds__(kThreads, SHIFTED ? 3 : 4) beam_part_kernel(co
     }
     if (side >= head && x_side > above) s.list[atomicAdd(&s.n, 1)] = entry(x_side, side);
     __syncthreads();
-    found = select_best(s, s.n, p.count);
+    found = select_best(s, s.n, exact);
     // (These terms were added by the hardware's exponential.)
     if (tid < found) sum.add(-term(entry_x(s.best[tid]), unit));
+    if (tid >= p.count && tid < found) sum.add(exp_pair(difference(entry_x(s.best[tid]), unit)));
+    found = min(found, p.count);
   }
   // The sum in units of the largest logit's exponential: the selected ones' terms in the order of their ranks.
   const float most = found > 0 ? entry_x(s.best[0]) : ref;

@@ -326,3 +326,43 @@ def test_a_search_made_while_its_memory_is_written():
         got = search.select(logits, scores)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [4000, 60001])
+@pytest.mark.parametrize("count,large", [(1, 2), (1, 3), (2, 2), (1, 12), (5, 14)])
+def test_few_large_logits_weigh_exactly(dtype, V, count, large):
+    """Pairs of beams whose best values lie 2e-8 to 6e-8 apart. A few logits carry the weight of a row: their terms are
+    good to 2^-30 of the sum (1e-9, of each of the two rows). The others weigh less than 60000 e^-30, 6e-9, of which 2^-22
+    is nothing. So the order is the exact one."""
+    U = 200
+    g = torch.Generator().manual_seed(V + count + large)
+    x = (-30 - 8 * torch.rand(U * 2, V, generator=g)).to(dtype)
+    at = torch.rand(U * 2, V, generator=g).argsort(1)[:, :large]
+    x.scatter_(1, at, (-2.5 * torch.rand(U * 2, large, generator=g)).to(dtype))
+    x[torch.arange(U * 2), at[:, 0]] = 0
+    lse = torch.logsumexp(x.double(), -1).view(U, 2)
+    # The first beam's score in steps of 2^-30, so that of many the second's can be rounded near any distance.
+    first = torch.rand(U, 4096, generator=g) / 64
+    gap = (2e-8 + 4e-8 * torch.rand(U, 1, generator=g).double()) * (torch.arange(U) % 2 * 2 - 1).view(U, 1)
+    second = (first.double() - lse[:, :1] + lse[:, 1:] + gap).float()
+    found = second.double() - lse[:, 1:] - (first.double() - lse[:, :1])
+    best = (found - gap).abs().argmin(1, keepdim=True)
+    assert (found.gather(1, best) - gap).abs().max() < 2e-9
+    scores = torch.cat((first.gather(1, best), second.gather(1, best)), 1)
+    _check(x.cuda(), scores.cuda(), count)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_equal_logits_that_carry_the_weight(dtype):
+    """All terms but one are off alike, by 2^-22 of each for the exponential and by half a step of the exponent, which is
+    below 32 (2^-20 ln 2): together less than 2^-20."""
+    V = 262_144
+    far = torch.tensor([0.3, 1.7, 3.1, 5.9, 9.2, 11.3, 12.4], device="cuda").to(dtype).float()
+    x = -far.view(-1, 1).expand(-1, V).clone()
+    x[:, 4321] = 0.0
+    scores = torch.zeros(7, 1, device="cuda")
+    got = B.BeamSearch(7, 1, V, 1).select(x.to(dtype), scores)
+    want = -torch.log1p((V - 1) * torch.exp(-far.double()))
+    assert (got[2] == 4321).all()
+    assert ((got[0][:, 0].double() - want).abs() <= 2.0 ** -20 + 2.0 ** -24 * want.abs()).all()
