@@ -364,7 +364,8 @@ typedef struct moe_ffn_kv_batch {
   int pages_cols;          /* >= 0 */
   int n_seqs;              /* 0..max_seqs */
   int n_tokens;            /* token rows of the batch's tensors, 0..max_tokens */
-  int max_new;             /* at least the largest n_b */
+  int max_new;             /* at least the largest n_b; which kernel attends goes by it, so a loose one costs time:
+                              small trees over e4m3 take twice as long with 256 */
 } moe_ffn_kv_batch;
 
 /* A bf16 tensor [n_tokens, heads, head_dim] whose last dimension is contiguous: element (t, h, d) is

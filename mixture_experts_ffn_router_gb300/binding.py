@@ -617,7 +617,7 @@ class KVBatch:
     """The new tokens of a step, for PagedKV: device int32 tensors cu_q [n_seqs + 1] (first token row
     of each sequence), kv_len [n_seqs] (cached tokens, the new ones included) and pages [n_seqs, cols]
     (page ids; rows may be strided), and max_new, at least the largest number of new tokens of one
-    sequence. The tensors may be rewritten between calls (a captured graph reads them anew); their
+    sequence, by which the kernels are chosen: a loose one costs time. The tensors may be rewritten between calls (a captured graph reads them anew); their
     values are checked on the device."""
 
     def __init__(self, cu_q, kv_len, pages, max_new: int):

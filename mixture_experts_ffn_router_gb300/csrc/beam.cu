@@ -28,13 +28,17 @@
 // fp64 is slow here (an operation takes a warp 16 cycles or more, and its result some 60): only the last comparisons
 // are made in it.
 //
-// Times, 262144 bf16 logits to a row: 160 rows (32 users of 5 beams, some ended, the 10 best) 28 us, of which the pass takes 24
-// at 3.5 TB/s with 56% of the issue slots busy (exponentials, sums and comparisons, not HBM), and the join the rest: a chain
-// of barriers and small steps of one CTA to a user. 4 rows, the 8 best: 9.3 us in a graph, of which the bytes are 0.3. 64
-// rows, the 64 best: 57; in fp32, 180 rows of 116508, the 20 best: 37 (84 MB). One token far above all others takes no longer,
-// as coarse distances are cut again (160 rows 73 us otherwise). Rows of equal logits, which no threshold parts, take two to
-// seven times as long. The join in fp64 throughout took 40 us. A form that found its thresholds by bisection, a barrier for
-// each step, and summed in fp64 took 136 for the 160 rows and 44 for the 4.
+// Times in a graph, 262144 bf16 logits to a row, each call's logits from HBM. 160 rows, the 10 best: 35.4 us, of which the
+// bytes are 12.6. The same with 32 users of 5 beams of which a fifth has ended: 28.4 (10.2). There the pass takes 24 at
+// 2.6 TB/s, a third of HBM's, with 54% of the issue slots busy, so neither bounds it: its parts run in one wave and in step,
+// and HBM waits while all form their thresholds, and again while all list, rank and sum. The join is a chain of barriers and
+// small steps of one CTA to a user. 4 rows, the 8 best: 10.1, of which the bytes are 0.3. 64 rows, the 64 best: 56.5 (5.0); in fp32, 180 rows of
+// 116508, the 20 best: 30.2 (12.6). One token far above all others takes 41 for the 160 rows (73 if coarse distances were not cut
+// again), -infinity in place of all but 0.1% of the logits 33. Where no threshold parts a row, because most logits are equal
+// or are the type's lowest value, parts are gone through twice: equal rows take two to five times as long as others (160 rows
+// 101 us, 64 rows and the 64 best 269), rows with 0.1% above the lowest value two to three times (83 and 140). The join in
+// fp64 throughout took 40 us. A form that found its thresholds by bisection, a barrier for each step, and summed in fp64 took
+// 136 for the 160 rows with ended ones and 44 for the 4.
 #include <cuda_bf16.h>
 
 #include <cmath>

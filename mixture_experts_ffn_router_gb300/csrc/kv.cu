@@ -523,9 +523,11 @@ int kv_attend(moe_ffn_kv* kv, const moe_ffn_kv_cache* cache, const moe_ffn_kv_ba
   // kernel computes tiles of 256 rows of which it would fill `group`. Single tokens through the one and the other:
   // one short sequence 14 and 20 us, 64 e4m3 sequences (width 512) 78 and 226, 256 windows 217 and 360,
   // one long bf16 sequence 96 and 124.
-  // (A tree of one node is a single token.) Trees of up to kFewRows rows to a kv head over e4m3: a kernel of their own, 120 us
-  // against the chunk kernel's 264 for 64 sequences of 1000 to 4000 tokens (width 256), 10 and 20 for one short one. Over bf16 the chunk
-  // kernel is within 8% of the bytes there, and at width 512 of e4m3 their queries and outputs leave too little room.
+  // (A tree of one node is a single token.) Trees of up to kFewRows rows to a kv head over e4m3: a kernel of their own, 122 us
+  // against the chunk kernel's 264 for 64 sequences of 1000 to 4000 tokens (16 heads on 8 of width 256, 8 nodes), 56 and 112
+  // at width 128 (16 on 4, 4 nodes), 10 and 20 for one short one. At width 512 of e4m3 their queries and outputs leave too
+  // little room. Over bf16 there is no such form: the chunk kernel takes 209 us for the first of these batches, 1.2 times its
+  // bytes, 86 for the second, 2.0 times, and 166 at width 512 (16 on 2, 2 nodes), 1.9 times.
   cudaError_t e;
   if (a.b.max_new <= 1 && a.group <= kDecodeHeads) e = launch_kv_decode(a, ctas, s);
   else if (masks && a.c.e4m3 && a.c.head_dim <= 256 && a.b.max_new * a.group <= kFewRows)

@@ -4,8 +4,8 @@
 // What moves is little (a few tokens of each sequence, a fraction of a page of each beam) and is read and written once,
 // all layers' in a launch, so the launch and the chain of small loads before the first row (lengths, path, page
 // ids, rows) bound it; only many beams' pages in many layers come near HBM's rate. In a graph, the path of one tree in one
-// layer takes 1.7 us and a user's beams 1.9; from Python the calls take 10 and 7. The pages under way of 16 users' 5 beams in
-// 6 layers: 12.2 us, 5.1 TB/s.
+// layer takes 1.8 us and a user's beams 2.2; from Python the calls take 10 and 7. The pages under way of 16 users' 5 beams in
+// 6 layers, of which two in five move (50 MB read and written): 12.2 us, 4.1 TB/s.
 #include "internal.h"
 #include "kv.h"
 #include "ptx.cuh"

@@ -12,8 +12,9 @@
 // memory; elsewhere every row sees every key. A tile's values that no row sees are cleared, whatever they are.
 //
 // Measured, in a graph, against the kernel for chunks, trees of 4 nodes, 16 heads on 8 of width 256: 64 sequences
-// of 1000 to 4000 tokens 120 and 264 us (the bytes 86), of 250 to 1000 51 and 120, 1 of 4000 23 and 28; 16 heads on 4 of width
-// 128: 58 and 112 us, 31 and 53, 19 and 23. A chain of barriers per tile bounds it, as for single tokens. Tiles of 64 keys, which leave room
+// of 1000 to 4000 tokens 118 and 262 us (the bytes 87.5), of 250 to 1000 51 and 120 (22.5), 1 of 4000 23 and 28; 16 heads
+// on 4 of width 128: 56 and 112 us (22.4), 30 and 53 (5.9), 19 and 23. A chain of barriers per tile bounds it, as for single
+// tokens, and a tile of width 128 has the same chain for half the bytes. Tiles of 64 keys, which leave room
 // for more of them on their way but double the barriers, took 144 us for the first. With 32 rows, four blocks, the outputs
 // and references no longer fit two CTAs' registers: 98 us against 127 for 64 sequences of 1000, but 45 against 27 for one of
 // 4000, so these stay with the kernel for chunks.

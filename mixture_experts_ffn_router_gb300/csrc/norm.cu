@@ -5,8 +5,8 @@
 // 8 to 10 bytes per value meet a dozen operations, so HBM bounds it, or the launch where tokens are few. A CTA takes
 // a row at a time, whose values stay in its registers from the only load to the stores: a thread holds up to kMaxVecs
 // vectors of eight of x, block and gate. The two sums of squares are a reduction over the CTA each. The row's statistics
-// and y are fp32; y and n are rounded once. 8192 rows of 2816 with a gate take 38.1 us, 91% of the copy rate; 64 rows 2.2
-// in a graph (from Python the call itself takes 12).
+// and y are fp32; y and n are rounded once. 8192 rows of 2816 with a gate take 38.1 us, 91% of the copy rate; 64 rows 2.4
+// in a graph (from Python the call itself takes 11 to 16).
 //
 // Narrow rows: a warp for each, whose sums need no barrier. Others, where they are few or very wide: a CTA for each, all its
 // loads before the first use. Many rows: CTAs that stay, each with every gridDim-th row, the weights in registers and the
@@ -310,7 +310,8 @@ extern "C" int moe_ffn_block_norm(const moe_ffn_norm* a, void* stream) {
   // Which of the three, in us of two inputs without a gate. A warp to a row or a CTA: 40000 rows of 264 24 and 41, of 512 29 and
   // 42; of 1024 the warp's loads are too few (8192 rows: 17 and 15). CTAs that stay, or one a row: 8192 rows of 2816 35 and
   // 40, of 4096 46 and 56, of 2048 26 and 28; of 1536 21 and 21, and narrower ones with a gate lose (40000 of 768: 55 and
-  // 50). Below about eight rows to each they lose too (2000 rows of 2816: 11.6 and 10.7).
+  // 50). Below about eight rows to each they lose too (2000 rows of 2816: 11.6 and 10.7). Above 4096 a CTA for each row is all
+  // there is: 8192 rows of 4104 60 us, of 5376 84, of 8192 104, of 16384 256 (1.5, 1.6, 1.3 and 1.6 times the bytes).
   if (vecs <= 64) {
     const dim3 rows((a->tokens + kRowWarps - 1) / kRowWarps), warps(kRowWarps * 32);
     e = vecs <= 32 ? launch_pdl(block_norm_kernel<1, true>, rows, warps, 0, s, p, a->tokens)
