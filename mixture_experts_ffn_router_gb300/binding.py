@@ -660,10 +660,11 @@ class KVBatch:
 class KVTree:
     """The trees of a batch as PagedKV.tree_attention reads them (PagedKV.tree makes it): masks, int32
     [tokens, 8], and depth, int32 [tokens], each node's number of ancestors: its position is the context's length
-    plus that."""
+    plus that. Keep it as long as a graph that captured its attention."""
 
-    def __init__(self, masks, depth):
+    def __init__(self, masks, depth, raw=None):
         self.masks, self.depth = masks, depth
+        self._raw = raw  # the stream whose memory these are
         self.device = masks.device
         self.n_tokens = masks.shape[0]
 
@@ -824,6 +825,8 @@ class PagedKV:
             _check("moe_ffn_kv_attention", moe_ffn_kv_attention(self._handle, c, batch.of(T), qr, scale, window, sinks,
                                                                 out.data_ptr(), lse.data_ptr(), s))
         else:
+            if s != tree._raw and tree._raw is not None and not torch.cuda.is_current_stream_capturing():
+                tree.masks.record_stream(torch.cuda.current_stream(self.device))  # dropped early, they stay until it is done
             _check("moe_ffn_kv_tree_attention",
                    moe_ffn_kv_tree_attention(self._handle, c, batch.of(T), tree.masks.data_ptr(), qr, scale, window, sinks,
                                              out.data_ptr(), lse.data_ptr(), s))
@@ -864,7 +867,7 @@ class PagedKV:
         s = self._stream(batch)
         _check("moe_ffn_kv_tree", moe_ffn_kv_tree(self._handle, batch.of(T), parents.data_ptr(), masks.data_ptr(),
                                                   depth.data_ptr(), s))
-        return KVTree(masks, depth)
+        return KVTree(masks, depth, s)
 
     def tree_attention(self, cache, batch: KVBatch, tree: KVTree, q, window: int = 0, sinks: int = 0, scale=None, out=None):
         """Attention of drafted tokens' queries, bf16 [tokens, q_heads, head_dim], over the cache, which holds their

@@ -799,3 +799,27 @@ def test_single_nodes_without_room_are_reported(fmt, hq):
     # Of tokens that are no tree the same is no error.
     kv.attention(cache, batch, case.q.cuda())
     _ok(kv)
+
+
+def test_a_tree_dropped_while_another_stream_still_attends():
+    """The memory of its masks goes to new tensors of the stream that made them only after the queued attention."""
+    case = U.Case("bf16", 4, 2, 256, 16, [10, 20], [40, 50], seed=14)
+    kv = case.handle()
+    cache = case.filled(kv)
+    batch = case.batch()
+    q, parents = case.q.cuda(), _flat(case, _trees(case))
+    want, _ = kv.tree_attention(cache, batch, kv.tree(batch, parents), q)
+    large = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    tree = kv.tree(batch, parents)
+    nbytes = tree.masks.numel() * 4
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(40):
+            large.fill_(i)
+        got, _ = kv.tree_attention(cache, batch, tree, q)
+    del tree
+    over = [torch.zeros(nbytes, dtype=torch.uint8, device="cuda") for _ in range(200)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(over) == 200
+    _ok(kv)

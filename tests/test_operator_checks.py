@@ -296,6 +296,32 @@ def _stub():
     return kv
 
 
+def test_masks_stay_until_every_stream_is_done_with_them(monkeypatch):
+    """A tree's masks belong to the stream that made them; its attention may be queued on another one when it is dropped."""
+    raw, capturing, recorded = [1], [False], []
+
+    class Masks(_OnGpu):
+        def record_stream(self, stream):
+            recorded.append(stream)
+
+    kv = _stub()
+    kv._handle, kv.default_scale = None, 1.0
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *size, dtype=None, device=None: empty(*size, dtype=dtype))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: raw[0])
+    monkeypatch.setattr(kv, "_rows", lambda *a: None, raising=False)
+    monkeypatch.setattr(kv, "_begin", lambda cache, batch: (None, raw[0]), raising=False)
+    monkeypatch.setattr(B, "moe_ffn_kv_tree_attention", lambda *a: B.MOE_FFN_OK)
+    batch = B.KVBatch.__new__(B.KVBatch)
+    batch.of = lambda n: None
+    tree = B.KVTree(Masks(4, 8, dtype=torch.int32), None, 1)
+    q = torch.zeros(4, 16, 256, dtype=torch.bfloat16)
+    for raw[0], capturing[0] in ((1, False), (2, False), (3, True), (3, False), (1, False)):
+        kv.tree_attention(None, batch, tree, q)
+    assert recorded == [2, 3]
+
+
 def test_arguments_of_the_cache_are_checked():
     kv = _stub()
     ids = lambda *shape: torch.zeros(shape, dtype=torch.int32)  # noqa: E731
